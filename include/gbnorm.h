@@ -13,8 +13,10 @@
  *   "Implementation:NVIDIA TransformerEngine Ops Fused Backward Add RMSNorm"
  *     (sections Description, I/O Contract): the backward with the residual
  *     gradient added to the input gradient in the same kernel.
- * The softmax entry points (end of this file) follow "Migrate norms and
- * softmax kernels to NVRTC" (Description, JIT cost table), which names them.
+ * The softmax entry points follow "Migrate norms and softmax kernels to
+ * NVRTC" (Description, JIT cost table), which names them.  Rotary positions
+ * and the paged key/value cache (end of this file) have no page: they are what
+ * stands between the norms and the softmax's use, in this library's manner.
  *
  * Arithmetic (x is one row of `hidden` elements; all device math in fp32):
  *   LayerNorm: mu = mean(x); var = mean((x - mu)^2); rsigma = 1/sqrt(var + eps)
@@ -106,7 +108,7 @@ typedef enum {
   GBN_ERR_NULL = 1,      /* a pointer the chosen mode needs is NULL */
   GBN_ERR_DTYPE = 2,     /* unsupported dtype or dtype combination */
   GBN_ERR_SHAPE = 3,     /* rows/hidden out of range, or MXFP8 blocks do not tile */
-  GBN_ERR_ALIGNMENT = 4, /* reserved: misaligned pointers take the scalar path */
+  GBN_ERR_ALIGNMENT = 4, /* paged attention only: everything else takes a scalar path */
   GBN_ERR_WORKSPACE = 5, /* workspace NULL or smaller than the queried size */
   GBN_ERR_ENUM = 6,      /* norm type, scaling mode or layout out of range */
   GBN_ERR_CUDA = 7       /* a CUDA runtime call or a launch failed */
@@ -242,6 +244,10 @@ gbn_status gbn_norm_bwd_noalloc(const void* dz, const void* x, const float* mu,
  * reaches the host.  The query synchronizes with the device.  With clear != 0
  * the bits are reset after reading. */
 #define GBN_DEVICE_ERR_COPY_TIMEOUT 1u
+/*   bit 1 (GBN_DEVICE_ERR_BAD_INDEX): gbn_paged_append or gbn_paged_attention
+ *   met lengths or a page index outside what the call's sizes allow (see
+ *   there); what they point at was neither read nor written. */
+#define GBN_DEVICE_ERR_BAD_INDEX 2u
 gbn_status gbn_device_error(unsigned int* flags, int clear);
 
 /* Self-test of that failure path (no counterpart on the pages): enqueues on
@@ -287,6 +293,164 @@ gbn_status gbn_softmax_fwd(const void* x, const uint8_t* mask, void* y, int64_t 
  * Masked positions have y = 0 and so dx = 0: no mask argument. */
 gbn_status gbn_softmax_bwd(const void* dy, const void* y, void* dx, int64_t rows, int64_t sk,
                            gbn_dtype dtype, float scale, cudaStream_t stream);
+
+/* ---- Rotary positions.
+ *
+ * Of each head's head_dim elements the first rotary_dim turn in pairs, the
+ * rest is copied.  Pair i (i < rotary_dim / 2) at position t turns by the
+ * angle t * inv_freq[i]:
+ *     a' = mscale * (a cos - b sin),   b' = mscale * (a sin + b cos),
+ * (a, b) = elements (i, i + rotary_dim / 2) (HALF) or (2i, 2i + 1)
+ * (INTERLEAVED).  Scaled contexts are a matter of inv_freq and mscale.
+ * inv_freq is fp64 [rotary_dim / 2], radians per position, finite and below
+ * 2^50 in magnitude; the angle is reduced exactly (fixed point, modulo one
+ * turn), so far positions lose nothing.  fp32 arithmetic, one rounding to the
+ * tensors' type. */
+typedef enum { GBN_ROPE_HALF = 0, GBN_ROPE_INTERLEAVED = 1 } gbn_rope_layout;
+
+#define GBN_ROPE_MAX_DIM 1024 /* largest head_dim */
+
+/* Forward, q and k in one launch.
+ *
+ *   q, q_out   [batches, seq, q_heads, head_dim] dtype (F32, BF16, F16), the
+ *              elements of a head contiguous, element strides for the other
+ *              three (views of a packed projection need no copy).  q_heads = 0
+ *              or k_heads = 0 leaves that tensor out (pointers may be NULL).
+ *              q_out may be q itself (same strides); other overlaps are not
+ *              allowed.
+ *   k, k_out   [batches, seq, k_heads, head_dim], likewise
+ *   positions  int32 or int64 (position_bytes 4 or 8) [batches, seq],
+ *              contiguous along seq, position_stride elements between batches
+ *              (0: shared by all).  NULL: 0, 1, ..., seq - 1.
+ *   inv_freq   fp64 [rotary_dim / 2], device (NULL if rotary_dim is 0)
+ *
+ * GBN_ERR_SHAPE: odd rotary_dim or one beyond head_dim, head_dim outside
+ * [1, GBN_ROPE_MAX_DIM], over 4096 heads.  Sizes, strides or pointers that
+ * allow no 16- or 8-byte vectors take a scalar path. */
+gbn_status gbn_rope_fwd(const void* q, const void* k, const void* positions,
+                        const double* inv_freq, void* q_out, void* k_out, int64_t batches,
+                        int64_t seq, int64_t q_heads, int64_t k_heads, int64_t head_dim,
+                        int64_t rotary_dim, int64_t q_stride_b, int64_t q_stride_s,
+                        int64_t q_stride_h, int64_t k_stride_b, int64_t k_stride_s,
+                        int64_t k_stride_h, int64_t q_out_stride_b, int64_t q_out_stride_s,
+                        int64_t q_out_stride_h, int64_t k_out_stride_b, int64_t k_out_stride_s,
+                        int64_t k_out_stride_h, int64_t position_stride, int position_bytes,
+                        gbn_dtype dtype, gbn_rope_layout layout, float mscale,
+                        cudaStream_t stream);
+
+/* Backward: the transpose (the angle negated, the same mscale) applied to the
+ * output gradients dq, dk; arguments as in the forward. */
+gbn_status gbn_rope_bwd(const void* dq, const void* dk, const void* positions,
+                        const double* inv_freq, void* dq_out, void* dk_out, int64_t batches,
+                        int64_t seq, int64_t q_heads, int64_t k_heads, int64_t head_dim,
+                        int64_t rotary_dim, int64_t q_stride_b, int64_t q_stride_s,
+                        int64_t q_stride_h, int64_t k_stride_b, int64_t k_stride_s,
+                        int64_t k_stride_h, int64_t q_out_stride_b, int64_t q_out_stride_s,
+                        int64_t q_out_stride_h, int64_t k_out_stride_b, int64_t k_out_stride_s,
+                        int64_t k_out_stride_h, int64_t position_stride, int position_bytes,
+                        gbn_dtype dtype, gbn_rope_layout layout, float mscale,
+                        cudaStream_t stream);
+
+/* ---- Paged key/value cache.
+ *
+ * A batch of sequences, each with some new tokens, packed: sequence b owns
+ * the token rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (int32, batches + 1
+ * entries, ascending; rows before the first and behind the last sequence are
+ * padding, neither read nor written).  kv_lens[b] (int32) counts the
+ * sequence's keys INCLUDING its new tokens, so new token i of q_len stands at
+ * key position kv_lens[b] - q_len + i.  Position t lives in slot
+ * t % page_size of page block_table[b][t / page_size] (int32, table_pages
+ * entries per sequence, table_stride between sequences; entries that no key
+ * of the call needs are not looked at).  k_cache and v_cache have num_pages
+ * pages of page_size slots (a power of two up to GBN_PAGED_MAX_PAGE) of
+ * kv_heads heads of head_dim contiguous elements, element strides for page,
+ * slot and head (any order of the dimensions, K and V in one tensor or two).
+ * The cache's type is the tensors' (BF16 or F16) or E4M3.
+ *
+ * The lengths and the table live on the device and are not read by the host.
+ * The kernels check every index against the call's sizes: what does not fit
+ * (a token before position 0, a page outside [0, num_pages), a length beyond
+ * the table, max_q or max_kv) is left out, read as zero or not written, and
+ * GBN_DEVICE_ERR_BAD_INDEX is set; the rows concerned are then unspecified. */
+#define GBN_PAGED_MAX_BATCHES (1 << 20)
+#define GBN_PAGED_MAX_PAGE 65536
+#define GBN_PAGED_MAX_DIM 256 /* largest head_dim of the attention */
+
+/* Appends the new tokens' keys and values to the cache, the keys (and, with
+ * q_heads > 0, the queries, into q_out) rotated to their key positions as in
+ * gbn_rope_fwd.  rotary_dim = 0: no rotation.
+ *
+ *   q, q_out   [tokens, q_heads, head_dim] dtype (BF16 or F16), element
+ *              strides for token and head; q_out may be q.
+ *   k, v       [tokens, kv_heads, head_dim], likewise
+ *   k_scale, v_scale   fp32 [1], device, E4M3 caches only: the multiplier
+ *              before the saturating cast, as in delayed scaling.
+ * The pages that receive tokens must be distinct within the call (two tokens
+ * for one slot: either may stay). */
+gbn_status gbn_paged_append(const void* q, const void* k, const void* v, void* q_out,
+                            void* k_cache, void* v_cache, const double* inv_freq,
+                            const float* k_scale, const float* v_scale,
+                            const int32_t* cu_seqlens, const int32_t* kv_lens,
+                            const int32_t* block_table, int64_t tokens, int64_t batches,
+                            int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                            int64_t rotary_dim, int64_t num_pages, int64_t page_size,
+                            int64_t table_pages, int64_t table_stride, int64_t q_stride_t,
+                            int64_t q_stride_h, int64_t k_stride_t, int64_t k_stride_h,
+                            int64_t v_stride_t, int64_t v_stride_h, int64_t q_out_stride_t,
+                            int64_t q_out_stride_h, int64_t k_cache_stride_page,
+                            int64_t k_cache_stride_slot, int64_t k_cache_stride_head,
+                            int64_t v_cache_stride_page, int64_t v_cache_stride_slot,
+                            int64_t v_cache_stride_head, gbn_dtype dtype, gbn_dtype cache_dtype,
+                            gbn_rope_layout layout, float mscale, cudaStream_t stream);
+
+/* Attention of the new tokens over the cache (which holds their own keys and
+ * values already): for each token and query head, over the kept keys j,
+ *     s_j = scale * q . k_j,   out = sum_j softmax(s)_j v_j,
+ *     lse = log sum_j exp(s_j)   (natural logarithm).
+ * The token at key position t keeps j <= t if causal (bottom-right aligned,
+ * the softmax's GBN_SOFTMAX_CAUSAL_ALIGNED), else every key of its sequence;
+ * with window > 0 only j > t - window.  A row that keeps nothing gets out = 0,
+ * lse = -inf.  Query head n reads kv head n / (q_heads / kv_heads).
+ *
+ *   q, out     [tokens, q_heads, head_dim] dtype (BF16 or F16), element
+ *              strides for token and head
+ *   lse        fp32 [tokens, q_heads] contiguous, or NULL
+ *   k_scale_inv, v_scale_inv  fp32 [1], device, E4M3 caches only: what the
+ *              codes are multiplied by
+ *   max_q      upper bound of the new tokens per sequence; max_kv: of kv_lens.
+ *              They size the grid and the workspace (any bounds work, tight
+ *              ones are faster).
+ *   workspace  gbn_paged_attention_workspace_size() bytes (same arguments,
+ *              same device), 16-byte aligned: partial results of split key
+ *              ranges.  Needs no initialization; calls that may overlap on the
+ *              GPU need one each.
+ * fp32 scores, sums and outputs, probabilities rounded to the values' type
+ * (f16 for E4M3 caches) for the product with the values.  Deterministic.
+ * head_dim: a multiple of 16 up to GBN_PAGED_MAX_DIM; scale finite and
+ * positive; q_heads a multiple of kv_heads; tokens * q_heads < 2^31; max_kv
+ * up to 2^30 (else GBN_ERR_SHAPE).  All base pointers 16-byte aligned and all
+ * strides multiples of 16 bytes (else GBN_ERR_ALIGNMENT). */
+gbn_status gbn_paged_attention_workspace_size(int64_t tokens, int64_t batches, int64_t q_heads,
+                                              int64_t kv_heads, int64_t head_dim,
+                                              int64_t page_size, int64_t table_pages,
+                                              int64_t max_q, int64_t max_kv, int64_t window,
+                                              int causal, gbn_dtype dtype, gbn_dtype cache_dtype,
+                                              size_t* bytes);
+gbn_status gbn_paged_attention(const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* cu_seqlens, const int32_t* kv_lens,
+                               const int32_t* block_table, const float* k_scale_inv,
+                               const float* v_scale_inv, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, int64_t tokens, int64_t batches,
+                               int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                               int64_t num_pages, int64_t page_size, int64_t table_pages,
+                               int64_t table_stride, int64_t max_q, int64_t max_kv,
+                               int64_t q_stride_t, int64_t q_stride_h, int64_t out_stride_t,
+                               int64_t out_stride_h, int64_t k_cache_stride_page,
+                               int64_t k_cache_stride_slot, int64_t k_cache_stride_head,
+                               int64_t v_cache_stride_page, int64_t v_cache_stride_slot,
+                               int64_t v_cache_stride_head, gbn_dtype dtype,
+                               gbn_dtype cache_dtype, int causal, int64_t window, float scale,
+                               cudaStream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* gbn_status_string(gbn_status status);

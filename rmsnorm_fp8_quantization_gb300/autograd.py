@@ -9,7 +9,11 @@ separate add ("Implementation:NVIDIA TransformerEngine Ops Fused Backward Add
 RMSNorm", Description and I/O Contract: grad_input = norm backward +
 residual gradient, plus grad_weight).
 
-Shapes: x is [..., hidden], contiguous, on a CUDA device; gamma (and beta)
+``rope`` rotates q and k to their positions in one launch; its backward is
+the transposed rotation of both gradients in one launch, and saves nothing but
+the positions and frequencies.
+
+Shapes (norms): x is [..., hidden], contiguous, on a CUDA device; gamma (and beta)
 [hidden].  The outputs have x's dtype; weight gradients have the weights'
 dtype.  Every step runs in the library's kernels; this module only reshapes
 and marshals.
@@ -17,10 +21,11 @@ and marshals.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import ops
 
-__all__ = ["layer_norm", "rms_norm", "layer_norm_with_residual", "rms_norm_with_residual"]
+__all__ = ["layer_norm", "rms_norm", "layer_norm_with_residual", "rms_norm_with_residual", "rope"]
 
 
 def _rows(x: torch.Tensor, hidden: int) -> torch.Tensor:
@@ -85,3 +90,32 @@ def rms_norm_with_residual(x, gamma, eps=1e-6, zero_centered_gamma=False, sm_mar
     """(rms_norm(x), x); the backward adds the second output's gradient to dx
     inside the norm's backward kernel (the fused backward-add)."""
     return _Norm.apply(x, gamma, None, "rmsnorm", eps, zero_centered_gamma, sm_margin, True)
+
+
+class _Rope(torch.autograd.Function):
+    """(q, k) rotated; k may be None."""
+
+    @staticmethod
+    def forward(ctx, q, k, inv_freq, positions, layout, mscale):
+        ctx.save_for_backward(inv_freq, positions)
+        ctx.layout, ctx.mscale = layout, mscale
+        ctx.set_materialize_grads(False)  # an unused output costs nothing
+        return ops.rope_fwd(q, k, inv_freq, positions, layout=layout, mscale=mscale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        inv_freq, positions = ctx.saved_tensors
+        # A gradient whose head elements are not contiguous (an expanded or
+        # transposed view) is copied; other strides are taken as they are.
+        dq, dk = (t if t is None or t.stride(-1) == 1 else t.contiguous() for t in (dq, dk))
+        if dq is None and dk is None:
+            return (None,) * 6
+        dq, dk = ops.rope_bwd(dq, dk, inv_freq, positions, layout=ctx.layout, mscale=ctx.mscale)
+        return dq, dk, None, None, None, None
+
+
+def rope(q, k, inv_freq, positions=None, layout="half", mscale=1.0):
+    """Rotary positions of q and k [batch, seq, heads, head_dim] (k may be
+    None): ``ops.rope_fwd`` with its gradient."""
+    return _Rope.apply(q, k, inv_freq, positions, layout, mscale)

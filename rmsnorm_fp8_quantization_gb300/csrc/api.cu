@@ -13,6 +13,7 @@
 #include <tuple>
 
 #include "gbn_internal.h"
+#include "paged_attn.h"
 #include "gbnorm.h"
 
 namespace {
@@ -756,7 +757,11 @@ gbn_status gbn_device_error(unsigned int* flags, int clear) {
       kernels_bf16().read_device_error(&b, clear != 0) != cudaSuccess ||
       kernels_f16().read_device_error(&c, clear != 0) != cudaSuccess)
     return GBN_ERR_CUDA;
-  *flags = a | b | c;
+  unsigned int r = 0, s = 0;
+  if (read_rope_error(&r, clear != 0) != cudaSuccess ||
+      read_attention_error(&s, clear != 0) != cudaSuccess)
+    return GBN_ERR_CUDA;
+  *flags = a | b | c | r | s;
   return GBN_OK;
 }
 

@@ -1,0 +1,832 @@
+// Attention of new tokens over a paged key/value cache: the kernel for few
+// rows per kv head (single tokens, a few tokens to verify; and any chunk with
+// heads wider than 128), the merge of split key ranges, and the C entry.
+//
+//   s_j = scale * q . k_j over the keys the row keeps,
+//   o = sum_j 2^(s_j log2 e - m) v_j / sum_j 2^(s_j log2 e - m),  m the
+//   running maximum: one pass over the keys, rescaling what is summed so far
+//   when the maximum grows.
+//
+// What bounds it: with few rows each key and value is read from HBM once and
+// used for a handful of rows, so the bytes of the cache.  A CTA of four warps
+// streams tiles of 64 keys through a ring of cp.async copies (16 bytes a
+// thread, a page looked up per row; rows past the range are zero-filled, so
+// what stands in their slots never enters).  The rows of the kv head's whole
+// group share the tile.  With up to 16 rows the four warps take 16 keys each
+// and keep maxima, sums and outputs of their own, merged once at the end;
+// with 32 rows they are 2 x 2, with 64 each warp has its own 16 rows and all
+// keys.  The products run on mma.sync m16n8k16: the tensor work per byte is
+// far below what tcgen05 is for, and the accumulators stay in registers next
+// to the softmax.  Long key ranges are split over CTAs (fp32 partial outputs,
+// merged by a second kernel), so that a few sequences fill the GPU.
+//
+// E4M3 caches: a thread reads 16 bytes of a key row and converts in
+// registers.  The head elements of Q K^T may be summed in any order, and the
+// columns of the output may be computed in any order, so the fragments take
+// whatever elements those 16 bytes hold and no byte is shuffled between lanes.
+// Keys become q's type (an E4M3 value is exact in both), values become f16,
+// and so do the probabilities next to them.
+#include <type_traits>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "paged_rows.cuh"
+
+namespace gbn {
+namespace {
+
+constexpr int kStepThreads = 128;
+constexpr int kStepKeys = 64;          // keys per tile
+constexpr int kSplitPages = 1024;      // page entries a CTA holds
+constexpr int kMaxSplits = 512;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two E4M3 codes (low 16 bits) to a pair of f16, exact; NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+      : "=r"(r)
+      : "r"(c));
+  return r;
+}
+// ... to a pair of T.
+template <typename T>
+__device__ __forceinline__ uint32_t e4m3x2_to(uint32_t c) {
+  const uint32_t h = e4m3x2_to_f16x2(c);
+  if constexpr (std::is_same<T, __half>::value) return h;
+  else return narrow2<__nv_bfloat16>(widen2<__half>(h));
+}
+
+// Column (16-byte chunk) permutation of the tiles in shared memory.  Two-byte
+// rows: the eight rows of an ldmatrix phase in eight chunks.  E4M3 rows: a
+// 16-byte load's phase reads four chunks of two neighbouring rows (keys) or
+// two chunks of four rows two apart (values); both land in distinct banks.
+template <bool FP8, int CHUNKS>
+__device__ __forceinline__ int swz(int row, int chunk) {
+  if constexpr (!FP8) return chunk ^ (row & 7);
+  else if constexpr (CHUNKS >= 8) return chunk ^ ((((row >> 1) & 3) << 1) ^ ((row & 1) << 2));
+  else return chunk ^ ((row >> 1) & 3);
+}
+
+template <typename T, bool FP8, int DP>
+struct StepShape {
+  static constexpr int kRowBytes = DP * (FP8 ? 1 : 2);
+  static constexpr int kChunks = kRowBytes / 16;
+  static constexpr int kTileBytes = kStepKeys * kRowBytes;  // keys or values of one tile
+  // Bytes in flight: 96 KB a CTA of two-byte 128-wide heads, two CTAs an SM.
+  static constexpr int kStages = kRowBytes >= 512 ? 2 : kRowBytes >= 256 ? 3 : 4;
+  static constexpr int kRing = kStages * 2 * kTileBytes;
+  static constexpr int kMerge = 4 * 16 * DP * 4;  // outputs of the four warps, over the ring
+  static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kQPitch = DP * 2 + 16;
+  static constexpr int smem(int mt) {
+    return kBody + 16 * mt * kQPitch + kSplitPages * 4 + 4 * 16 * 8;
+  }
+};
+
+// T: q's type.  MT: 16-row tiles (1, 2, 4).
+template <typename T, bool FP8, int DP, int MT>
+__global__ void __launch_bounds__(kStepThreads)
+    paged_step_kernel(const __grid_constant__ AttnParams p) {
+  using Shape = StepShape<T, FP8, DP>;
+  constexpr int WN = 4 / MT;                 // warps over the keys
+  constexpr int KW = kStepKeys / WN;         // keys per warp and tile
+  constexpr int NT = KW / 8;                 // score tiles of 8 keys
+  constexpr int DT = DP / 8;                 // output tiles of 8 columns
+  constexpr int KS = DP / 16;                // steps of 16 head elements
+  constexpr bool kQReg = DP <= 128;          // q's fragments stay in registers
+  using TP = typename std::conditional<FP8, __half, T>::type;  // type of the P V product
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* s_q = smem + Shape::kBody;
+  int32_t* s_page = reinterpret_cast<int32_t*>(s_q + 16 * MT * Shape::kQPitch);
+  float2* s_ml = reinterpret_cast<float2*>(s_page + kSplitPages);
+
+  pdl_begin();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int wm = warp / WN, wn = warp % WN;
+  const int qr = lane >> 2, qc = lane & 3;
+  uint32_t x = blockIdx.x;
+  const int h = x % p.hkv;
+  x /= p.hkv;
+  const int rt = x % p.row_tiles;
+  x /= p.row_tiles;
+  const int split = x % p.splits;
+  const int b = x / p.splits;
+
+  const SeqRange s = seq_range(p, b, tid == 0 && split == 0 && rt == 0 && h == 0);
+  const int r0 = rt * 16 * MT;
+  const int rows = min(16 * MT, s.qlen * p.group - r0);
+  if (rows <= 0) return;
+  const int i0 = r0 / p.group, i1 = (r0 + rows - 1) / p.group;
+  const int lo = row_low(p, s, i0), hi = row_high(p, s, i1);
+  const int64_t start = lo + static_cast<int64_t>(split) * p.split_len;
+  const int k0 = static_cast<int>(min(start, static_cast<int64_t>(max(hi, 0))));
+  const int k1 = static_cast<int>(min(start + p.split_len, static_cast<int64_t>(max(hi, 0))));
+  const int ntiles = k1 > k0 ? (k1 - k0 + kStepKeys - 1) / kStepKeys : 0;
+  if (ntiles == 0 && split > 0) {
+    // Nothing here: say so (the merge reads every split's maximum and sum).
+    for (int r = tid; r < rows; r += kStepThreads) {
+      const int gr = r0 + r;
+      const int64_t o = static_cast<int64_t>(s.q0 + gr / p.group) * p.hq + h * p.group + gr % p.group;
+      p.part_ml[o * p.splits + split] = make_float2(-INFINITY, 0.f);
+    }
+    return;
+  }
+
+  // Pages of this range, checked once.
+  const int page0 = k0 >> p.page_shift;
+  if (ntiles > 0) {
+    const int pages = ((k1 - 1) >> p.page_shift) - page0 + 1;
+    for (int i = tid; i < pages; i += kStepThreads) {
+      int pg = p.table[b * p.table_stride + page0 + i];
+      if (pg < 0 || pg >= p.num_pages) {
+        flag_bad_index();
+        pg = -1;  // its keys read as zero
+      }
+      s_page[i] = pg;
+    }
+  }
+  // q's rows into shared memory (rows past the end and columns past d: zero).
+  {
+    constexpr int C = DP / 8;
+    const T* q = reinterpret_cast<const T*>(p.q);
+    for (int i = tid; i < 16 * MT * C; i += kStepThreads) {
+      const int r = i / C, c = i % C;
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows && c * 8 < p.d) {
+        const int gr = r0 + r;
+        w = *reinterpret_cast<const uint4*>(q + (s.q0 + gr / p.group) * p.qt +
+                                            (h * p.group + gr % p.group) * p.qh + c * 8);
+      }
+      *reinterpret_cast<uint4*>(s_q + r * Shape::kQPitch + c * 16) = w;
+    }
+  }
+  __syncthreads();
+
+  const uint32_t ring = smem_u32(smem);
+  const uint8_t* kbase = reinterpret_cast<const uint8_t*>(p.k) + h * p.kh * (FP8 ? 1 : 2);
+  const uint8_t* vbase = reinterpret_cast<const uint8_t*>(p.v) + h * p.vh * (FP8 ? 1 : 2);
+  auto load_tile = [&](int t) {
+    if (t < ntiles) {
+      const uint32_t kd = ring + (t % Shape::kStages) * 2 * Shape::kTileBytes;
+      const uint32_t vd = kd + Shape::kTileBytes;
+      const int base = k0 + t * kStepKeys;
+#pragma unroll
+      for (int i = 0; i < kStepKeys * Shape::kChunks / kStepThreads; ++i) {
+        const int id = tid + i * kStepThreads;
+        const int r = id / Shape::kChunks, c = id % Shape::kChunks;
+        const int j = base + r;
+        const int pg = j < k1 ? s_page[(j >> p.page_shift) - page0] : -1;
+        const bool live = pg >= 0 && c * 16 < p.d * (FP8 ? 1 : 2);
+        const int slot = j & ((1 << p.page_shift) - 1);
+        const uint32_t at = r * Shape::kRowBytes + swz<FP8, Shape::kChunks>(r, c) * 16;
+        const int64_t ko = live ? (pg * p.kp + slot * p.ks) * (FP8 ? 1 : 2) + c * 16 : 0;
+        const int64_t vo = live ? (pg * p.vp + slot * p.vs) * (FP8 ? 1 : 2) + c * 16 : 0;
+        cp_async16(kd + at, kbase + ko, live);
+        cp_async16(vd + at, vbase + vo, live);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int t = 0; t < Shape::kStages - 1; ++t) load_tile(t);
+
+  // q fragments.  Two-byte caches: the standard order.  E4M3: step ks of the
+  // 64-column block takes, for lane column qc, elements 16 qc + 4 (ks % 4).. + 3.
+  const uint32_t qbase = smem_u32(s_q) + wm * 16 * Shape::kQPitch;
+  auto load_q = [&](int ks, uint32_t* a) {
+    if constexpr (!FP8) {
+      ldsm4(a, qbase + (lane & 15) * Shape::kQPitch + ks * 32 + (lane >> 4) * 16);
+    } else {
+      const uint32_t col = ((ks / 4) * 64 + qc * 16 + (ks % 4) * 4) * 2;
+      const uint2 u = lds8(qbase + qr * Shape::kQPitch + col);
+      const uint2 w = lds8(qbase + (qr + 8) * Shape::kQPitch + col);
+      a[0] = u.x;
+      a[1] = w.x;
+      a[2] = u.y;
+      a[3] = w.y;
+    }
+  };
+  uint32_t qf[kQReg ? KS : 1][4];
+  if constexpr (kQReg) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) load_q(ks, qf[ks]);
+  }
+
+  // Key limits of this thread's two rows.
+  int rlo[2], rhi[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = wm * 16 + qr + 8 * e;
+    const int i = (r0 + min(r, rows - 1)) / p.group;
+    rlo[e] = row_low(p, s, i);
+    rhi[e] = row_high(p, s, i);
+  }
+  // Keys that every row of the CTA keeps need no test.
+  const int all_lo = row_low(p, s, i1), all_hi = min(row_high(p, s, i0), k1);
+
+  float scale = p.scale_log2;
+  if constexpr (FP8) scale *= *p.k_scale_inv;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float o[DT][4];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+
+  for (int t = 0; t < ntiles; ++t) {
+    cp_async_wait<Shape::kStages - 2>();
+    __syncthreads();  // tile t is here, and every warp is done with tile t - 1
+    load_tile(t + Shape::kStages - 1);
+    const uint32_t kd = ring + (t % Shape::kStages) * 2 * Shape::kTileBytes;
+    const uint32_t vd = kd + Shape::kTileBytes;
+    const int kw = wn * KW;  // this warp's first key row in the tile
+    float sc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
+    if constexpr (!FP8) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t a[4];
+        if constexpr (!kQReg) load_q(ks, a);
+        const uint32_t* af = kQReg ? qf[kQReg ? ks : 0] : a;
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          const int row = kw + n * 8 + (lane & 7) + ((lane >> 4) << 3);
+          const int ch = ks * 2 + ((lane >> 3) & 1);
+          uint32_t kb[4];
+          ldsm4(kb, kd + row * Shape::kRowBytes + swz<FP8, Shape::kChunks>(row, ch) * 16);
+          mma16816<T>(sc[n], af, kb[0], kb[1]);
+          mma16816<T>(sc[n + 1], af, kb[2], kb[3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int blk = 0; blk < DP / 64; ++blk) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int row = kw + n * 8 + qr;
+          const uint4 u = lds16(kd + row * Shape::kRowBytes +
+                                swz<FP8, Shape::kChunks>(row, blk * 4 + qc) * 16);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int s4 = 0; s4 < 4; ++s4) {
+            uint32_t a[4];
+            if constexpr (!kQReg) load_q(blk * 4 + s4, a);
+            const uint32_t* af = kQReg ? qf[kQReg ? blk * 4 + s4 : 0] : a;
+            mma16816<T>(sc[n], af, e4m3x2_to<T>(w[s4] & 0xFFFFu), e4m3x2_to<T>(w[s4] >> 16));
+          }
+        }
+      }
+    }
+
+    // Scale, mask, running maximum.
+    const int jbase = k0 + t * kStepKeys + kw;
+    float mx[2] = {m[0], m[1]};
+    if (jbase >= all_lo && jbase + KW <= all_hi) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sc[n][e] *= scale;
+          mx[e >> 1] = fmaxf(mx[e >> 1], sc[n][e]);
+        }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = jbase + n * 8 + qc * 2 + (e & 1);
+          const bool keep = j >= rlo[e >> 1] && j < rhi[e >> 1] && j < k1;
+          sc[n][e] = keep ? sc[n][e] * scale : -INFINITY;
+          mx[e >> 1] = fmaxf(mx[e >> 1], sc[n][e]);
+        }
+    }
+    float base[2];
+    bool grew = false;
+    float al[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));
+      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 2));
+      base[e] = mx[e] == -INFINITY ? 0.f : mx[e];
+      al[e] = ex2(m[e] - base[e]);  // m = -inf: 0, and the sums are still 0
+      grew |= mx[e] != m[e];
+      m[e] = mx[e];
+    }
+    if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) l[e] *= al[e];
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[d][e] *= al[e >> 1];
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sc[n][e] = ex2(sc[n][e] - base[e >> 1]);
+        l[e >> 1] += sc[n][e];
+      }
+    // P V.  P is rounded to the values' type (at most half a step relative:
+    // the sums l keep it unrounded).
+#pragma unroll
+    for (int kk = 0; kk < NT / 2; ++kk) {
+      uint32_t a[4];
+      a[0] = narrow2<TP>(p2(sc[2 * kk][0], sc[2 * kk][1]));
+      a[1] = narrow2<TP>(p2(sc[2 * kk][2], sc[2 * kk][3]));
+      a[2] = narrow2<TP>(p2(sc[2 * kk + 1][0], sc[2 * kk + 1][1]));
+      a[3] = narrow2<TP>(p2(sc[2 * kk + 1][2], sc[2 * kk + 1][3]));
+      const int kr = kw + kk * 16;
+      if constexpr (!FP8) {
+#pragma unroll
+        for (int d = 0; d < DT; d += 2) {
+          const int row = kr + (lane & 15);
+          uint32_t vb[4];
+          ldsm4t(vb, vd + row * Shape::kRowBytes +
+                         swz<FP8, Shape::kChunks>(row, d + (lane >> 4)) * 16);
+          mma16816<TP>(o[d], a, vb[0], vb[1]);
+          mma16816<TP>(o[d + 1], a, vb[2], vb[3]);
+        }
+      } else {
+        // Output tile d of a block of 128 (64) columns holds, for lane row qr,
+        // column 16 qr + d (8 qr + d).
+        constexpr int CB = DP >= 128 ? 16 : 8;  // bytes per load
+#pragma unroll
+        for (int blk = 0; blk < DP / (CB * 8); ++blk) {
+          uint32_t w[4][CB / 4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = kr + qc * 2 + (e & 1) + (e >> 1) * 8;
+            if constexpr (CB == 16) {
+              const uint4 u = lds16(vd + row * Shape::kRowBytes +
+                                    swz<FP8, Shape::kChunks>(row, blk * 8 + qr) * 16);
+              w[e][0] = u.x; w[e][1] = u.y; w[e][2] = u.z; w[e][3] = u.w;
+            } else {
+              const uint2 u = lds8(vd + row * Shape::kRowBytes +
+                                   swz<FP8, Shape::kChunks>(row, qr >> 1) * 16 + (qr & 1) * 8);
+              w[e][0] = u.x; w[e][1] = u.y;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < CB / 4; ++i) {
+            const uint32_t x0 = __byte_perm(w[0][i], w[1][i], 0x5140);  // bytes 0, 1 of both keys
+            const uint32_t x1 = __byte_perm(w[0][i], w[1][i], 0x7362);
+            const uint32_t y0 = __byte_perm(w[2][i], w[3][i], 0x5140);
+            const uint32_t y1 = __byte_perm(w[2][i], w[3][i], 0x7362);
+            const int d = blk * CB + i * 4;
+            mma16816<TP>(o[d], a, e4m3x2_to_f16x2(x0 & 0xFFFFu), e4m3x2_to_f16x2(y0 & 0xFFFFu));
+            mma16816<TP>(o[d + 1], a, e4m3x2_to_f16x2(x0 >> 16), e4m3x2_to_f16x2(y0 >> 16));
+            mma16816<TP>(o[d + 2], a, e4m3x2_to_f16x2(x1 & 0xFFFFu), e4m3x2_to_f16x2(y1 & 0xFFFFu));
+            mma16816<TP>(o[d + 3], a, e4m3x2_to_f16x2(x1 >> 16), e4m3x2_to_f16x2(y1 >> 16));
+          }
+        }
+      }
+    }
+  }
+
+  // Merge the warps of each row tile through shared memory.
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
+    l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
+  }
+  cp_async_wait<0>();
+  __syncthreads();  // the ring is free
+  float* s_o = reinterpret_cast<float*>(smem) + warp * 16 * DP;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = qr + 8 * (e >> 1);
+      int col;
+      if constexpr (!FP8) {
+        col = d * 8 + qc * 2 + (e & 1);
+      } else {
+        constexpr int CB = DP >= 128 ? 16 : 8;
+        col = (d / CB) * CB * 8 + (qc * 2 + (e & 1)) * CB + d % CB;
+      }
+      s_o[r * DP + col] = o[d][e];
+    }
+  if (qc == 0) {
+    s_ml[warp * 16 + qr] = make_float2(m[0], l[0]);
+    s_ml[warp * 16 + qr + 8] = make_float2(m[1], l[1]);
+  }
+  __syncthreads();
+  const float vscale = FP8 ? *p.v_scale_inv : 1.f;
+  constexpr int Q4 = DP / 8;  // groups of 8 columns per row
+  for (int i = tid; i < rows * Q4; i += kStepThreads) {
+    const int r = i / Q4, c = (i % Q4) * 8;
+    if (c >= p.d) continue;
+    const int w0 = (r / 16) * WN;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WN; ++w) mm = fmaxf(mm, s_ml[(w0 + w) * 16 + r % 16].x);
+    const float mb = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f, acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WN; ++w) {
+      const float2 ml = s_ml[(w0 + w) * 16 + r % 16];
+      const float f = ex2(ml.x - mb);
+      ll += ml.y * f;
+      const float* src = reinterpret_cast<const float*>(smem) + ((w0 + w) * 16 + r % 16) * DP + c;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(src[e], f, acc[e]);
+    }
+    const int gr = r0 + r;
+    const int token = s.q0 + gr / p.group, head = h * p.group + gr % p.group;
+    const int64_t ro = static_cast<int64_t>(token) * p.hq + head;
+    if (p.splits > 1) {
+      float* dst = p.part_o + (static_cast<int64_t>(split) * p.tokens * p.hq + ro) * p.d + c;
+      *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      *reinterpret_cast<float4*>(dst + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      if (c == 0) p.part_ml[ro * p.splits + split] = make_float2(mm, ll);
+    } else {
+      const float inv = ll == 0.f ? 0.f : vscale / ll;
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = narrow2<T>(p2(acc[2 * e] * inv, acc[2 * e + 1] * inv));
+      st_words<4>(reinterpret_cast<T*>(p.out) + token * p.ot + head * p.oh + c, w);
+      if (c == 0 && p.lse) p.lse[ro] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+    }
+  }
+}
+
+// Merge of split key ranges: one CTA per (token, query head).
+//   o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s
+// in the order of the splits within each of the CTA's split groups, the
+// groups added in order: the same bits every time.
+constexpr int kMergeThreads = 128;
+template <typename T>
+__global__ void __launch_bounds__(kMergeThreads)
+    paged_merge_kernel(const __grid_constant__ AttnParams p, int fp8) {
+  pdl_begin();
+  __shared__ float s_w[kMaxSplits];
+  __shared__ float s_red[kMergeThreads / 32];
+  __shared__ float4 s_o[kMergeThreads];
+  const int64_t ro = blockIdx.x;
+  const int token = static_cast<int>(ro / p.hq), head = static_cast<int>(ro % p.hq);
+  // Padding rows behind the last sequence are left alone.
+  if (token >= p.cu[p.batches] || token < p.cu[0]) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float2* ml = p.part_ml + ro * p.splits;
+  float m = -INFINITY;
+  for (int s = tid; s < p.splits; s += kMergeThreads) m = fmaxf(m, ml[s].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if (lane == 0) s_red[warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  __syncthreads();
+  const float mb = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  for (int s = tid; s < p.splits; s += kMergeThreads) {
+    const float2 v = ml[s];
+    // A split without a kept key wrote no partial output: weight exactly 0,
+    // and its slot is skipped below.
+    const float w = v.y == 0.f ? 0.f : ex2(v.x - mb);
+    s_w[s] = w;
+    l += v.y == 0.f ? 0.f : v.y * w;
+  }
+  l = warp_sum(l);
+  if (lane == 0) s_red[warp] = l;
+  __syncthreads();
+  l = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+
+  const int cols = p.d / 4;                       // float4 columns (4 .. 64)
+  const int groups = kMergeThreads / cols;        // split groups (2 .. 32)
+  const int col = tid % cols, grp = tid / cols;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (grp < groups) {
+    const float* src = p.part_o + ro * p.d + col * 4;
+    const int64_t step = static_cast<int64_t>(p.tokens) * p.hq * p.d;
+#pragma unroll 4
+    for (int s = grp; s < p.splits; s += groups) {
+      const float w = s_w[s];
+      if (w != 0.f) {
+        const float4 v = *reinterpret_cast<const float4*>(src + s * step);
+        acc.x = fmaf(v.x, w, acc.x);
+        acc.y = fmaf(v.y, w, acc.y);
+        acc.z = fmaf(v.z, w, acc.z);
+        acc.w = fmaf(v.w, w, acc.w);
+      }
+    }
+  }
+  s_o[tid] = acc;
+  __syncthreads();
+  if (tid < cols) {
+    for (int g = 1; g < groups; ++g) {
+      const float4 v = s_o[g * cols + tid];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+    const float inv = l == 0.f ? 0.f : (fp8 ? *p.v_scale_inv : 1.f) / l;
+    uint32_t w[2] = {narrow2<T>(p2(acc.x * inv, acc.y * inv)),
+                     narrow2<T>(p2(acc.z * inv, acc.w * inv))};
+    st_words<2>(reinterpret_cast<T*>(p.out) + token * p.ot + head * p.oh + tid * 4, w);
+    if (tid == 0 && p.lse) p.lse[ro] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+}
+
+// ---- host side
+
+template <typename T, bool FP8, int DP, int MT>
+cudaError_t launch_step(const AttnParams& p, int64_t grid, cudaStream_t st) {
+  constexpr int smem = StepShape<T, FP8, DP>::smem(MT);
+  auto k = paged_step_kernel<T, FP8, DP, MT>;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(kStepThreads), smem, st, p);
+}
+template <typename T, bool FP8, int DP>
+cudaError_t launch_step_mt(const AttnParams& p, int mt, int64_t grid, cudaStream_t st) {
+  if (mt == 1) return launch_step<T, FP8, DP, 1>(p, grid, st);
+  if (mt == 2) return launch_step<T, FP8, DP, 2>(p, grid, st);
+  return launch_step<T, FP8, DP, 4>(p, grid, st);
+}
+template <typename T, bool FP8>
+cudaError_t launch_step_d(const AttnParams& p, int mt, int64_t grid, cudaStream_t st) {
+  if (p.d <= 64) return launch_step_mt<T, FP8, 64>(p, mt, grid, st);
+  if (p.d <= 128) return launch_step_mt<T, FP8, 128>(p, mt, grid, st);
+  return launch_step_mt<T, FP8, 256>(p, mt, grid, st);
+}
+
+// How a call is carried out: a function of sizes that the host knows.
+struct AttnPlan {
+  int rows;       // rows per CTA (16, 32, 64: the step kernel)
+  int row_tiles;
+  int splits;
+  int split_len;
+  int64_t ctas;
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t max_q, int64_t max_kv,
+                   int64_t window, int causal, int page_shift, int sms) {
+  AttnPlan a;
+  const int64_t r = max_q * group;
+  a.rows = r <= 16 ? 16 : r <= 32 ? 32 : 64;
+  a.row_tiles = static_cast<int>(ceil_div(r, a.rows));
+  // Longest key range of a row tile.
+  int64_t range = max_kv;
+  if (window > 0 && causal) {
+    const int64_t tile_tokens = ceil_div(a.rows, group) + 1;
+    const int64_t w = window + (tile_tokens < max_q ? tile_tokens : max_q);
+    if (w < range) range = w;
+  }
+  // Splits: enough CTAs for several rounds of two per SM, at least 256 keys each.
+  const int64_t tiles = batches * hkv * a.row_tiles;
+  const int64_t want = 8ll * sms;
+  int64_t splits = tiles >= want ? 1 : ceil_div(want, tiles > 0 ? tiles : 1);
+  const int64_t most = ceil_div(range, 256);
+  if (splits > most) splits = most;
+  const int64_t pages_least = ceil_div(range, (int64_t(kSplitPages) - 1) << page_shift);
+  if (splits < pages_least) splits = pages_least;
+  if (splits < 1) splits = 1;
+  int64_t len = ceil_div(ceil_div(range, splits), kStepKeys) * kStepKeys;
+  const int64_t cap = (int64_t(kSplitPages) - 1) << page_shift;
+  if (len > cap) len = cap;
+  if (len < 1) len = 1;
+  a.split_len = static_cast<int>(len);
+  a.splits = static_cast<int>(range > 0 ? ceil_div(range, len) : 1);
+  a.ctas = tiles * a.splits;
+  return a;
+}
+
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+struct AttnSizes {
+  int64_t tokens, batches, hq, hkv, d, page, table_pages, max_q, max_kv, window;
+};
+
+gbn_status check_sizes(const AttnSizes& z, gbn_dtype dtype, gbn_dtype cache_dtype) {
+  if (dtype != GBN_BF16 && dtype != GBN_F16) return GBN_ERR_DTYPE;
+  if (cache_dtype != dtype && cache_dtype != GBN_E4M3) return GBN_ERR_DTYPE;
+  if (z.tokens < 0 || z.tokens > INT32_MAX || z.batches < 0 || z.batches > GBN_PAGED_MAX_BATCHES ||
+      z.hkv < 1 || z.hkv > 4096 || z.hq < z.hkv || z.hq > 4096 || z.hq % z.hkv || z.d < 16 ||
+      z.d > GBN_PAGED_MAX_DIM || z.d % 16 || z.page < 1 || z.page > GBN_PAGED_MAX_PAGE ||
+      (z.page & (z.page - 1)) || z.table_pages < 0 || z.table_pages > INT32_MAX || z.max_q < 0 ||
+      z.max_kv < 0 || z.max_kv > (1 << 30) || z.window < 0 ||
+      z.window > INT32_MAX || z.tokens * z.hq > INT32_MAX)
+    return GBN_ERR_SHAPE;
+  return GBN_OK;
+}
+
+int log2_of(int64_t v) {
+  int s = 0;
+  while ((int64_t(1) << s) < v) ++s;
+  return s;
+}
+
+gbn_status plan_for(const AttnSizes& z, int causal, AttnPlan* a) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return GBN_ERR_CUDA;
+  const int64_t room = z.table_pages * z.page;
+  const int64_t kv = z.max_kv < room ? z.max_kv : room;
+  const int64_t mq = z.max_q < z.tokens ? z.max_q : z.tokens;
+  *a = attn_plan(z.batches, z.hkv, z.hq / z.hkv, mq, kv, z.window, causal, log2_of(z.page),
+                 sms);
+  if (a->splits > kMaxSplits || a->ctas > 0x7FFFFFFF) return GBN_ERR_SHAPE;
+  return GBN_OK;
+}
+
+size_t plan_bytes(const AttnSizes& z, const AttnPlan& a) {
+  if (a.splits <= 1) return 0;
+  const int64_t rows = z.tokens * z.hq;
+  return static_cast<size_t>(align256(rows * a.splits * 8) + rows * a.splits * z.d * 4);
+}
+
+}  // namespace
+
+cudaError_t read_attention_error(unsigned int* v, bool clear) { return read_paged_error(v, clear); }
+
+}  // namespace gbn
+
+using namespace gbn;
+
+extern "C" {
+
+gbn_status gbn_paged_attention_workspace_size(int64_t tokens, int64_t batches, int64_t q_heads,
+                                              int64_t kv_heads, int64_t head_dim,
+                                              int64_t page_size, int64_t table_pages,
+                                              int64_t max_q, int64_t max_kv, int64_t window,
+                                              int causal, gbn_dtype dtype, gbn_dtype cache_dtype,
+                                              size_t* bytes) {
+  if (!bytes) return GBN_ERR_NULL;
+  const AttnSizes z{tokens, batches, q_heads, kv_heads, head_dim,
+                    page_size, table_pages, max_q, max_kv, window};
+  gbn_status st = check_sizes(z, dtype, cache_dtype);
+  if (st != GBN_OK) return st;
+  *bytes = 0;
+  if (tokens == 0 || batches == 0 || max_q == 0) return GBN_OK;
+  AttnPlan a;
+  st = plan_for(z, causal, &a);
+  if (st != GBN_OK) return st;
+  *bytes = plan_bytes(z, a);
+  return GBN_OK;
+}
+
+gbn_status gbn_paged_attention(const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* cu_seqlens, const int32_t* kv_lens,
+                               const int32_t* block_table, const float* k_scale_inv,
+                               const float* v_scale_inv, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, int64_t tokens, int64_t batches,
+                               int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                               int64_t num_pages, int64_t page_size, int64_t table_pages,
+                               int64_t table_stride, int64_t max_q, int64_t max_kv,
+                               int64_t q_stride_t, int64_t q_stride_h, int64_t out_stride_t,
+                               int64_t out_stride_h, int64_t k_cache_stride_page,
+                               int64_t k_cache_stride_slot, int64_t k_cache_stride_head,
+                               int64_t v_cache_stride_page, int64_t v_cache_stride_slot,
+                               int64_t v_cache_stride_head, gbn_dtype dtype,
+                               gbn_dtype cache_dtype, int causal, int64_t window, float scale,
+                               cudaStream_t stream) {
+  const AttnSizes z{tokens, batches, q_heads, kv_heads, head_dim,
+                    page_size, table_pages, max_q, max_kv, window};
+  gbn_status st = check_sizes(z, dtype, cache_dtype);
+  if (st != GBN_OK) return st;
+  if (num_pages < 0 || num_pages > INT32_MAX || table_stride < 0 || !(scale > 0.f) ||
+      scale > 3.0e38f)
+    return GBN_ERR_SHAPE;
+  if (tokens == 0 || batches == 0 || max_q == 0) return GBN_OK;
+  if (!q || !k_cache || !v_cache || !cu_seqlens || !kv_lens || !block_table || !out)
+    return GBN_ERR_NULL;
+  const bool fp8 = cache_dtype == GBN_E4M3;
+  if (fp8 && (!k_scale_inv || !v_scale_inv)) return GBN_ERR_NULL;
+  const int ce = fp8 ? 1 : 2;
+  auto aligned = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; };
+  if (!aligned(q) || !aligned(out) || !aligned(k_cache) || !aligned(v_cache) ||
+      (tokens > 1 && (q_stride_t % 8 || out_stride_t % 8)) ||
+      (q_heads > 1 && (q_stride_h % 8 || out_stride_h % 8)) ||
+      (num_pages > 1 && (k_cache_stride_page * ce % 16 || v_cache_stride_page * ce % 16)) ||
+      (page_size > 1 && (k_cache_stride_slot * ce % 16 || v_cache_stride_slot * ce % 16)) ||
+      (kv_heads > 1 && (k_cache_stride_head * ce % 16 || v_cache_stride_head * ce % 16)))
+    return GBN_ERR_ALIGNMENT;
+  AttnPlan a;
+  st = plan_for(z, causal, &a);
+  if (st != GBN_OK) return st;
+  if (plan_bytes(z, a) > 0 &&
+      (!workspace || workspace_bytes < plan_bytes(z, a) || !aligned(workspace)))
+    return GBN_ERR_WORKSPACE;
+
+  AttnParams p = {};
+  p.q = q;
+  p.k = k_cache;
+  p.v = v_cache;
+  p.out = out;
+  p.lse = lse;
+  p.cu = cu_seqlens;
+  p.kv_lens = kv_lens;
+  p.table = block_table;
+  p.k_scale_inv = k_scale_inv;
+  p.v_scale_inv = v_scale_inv;
+  p.part_ml = reinterpret_cast<float2*>(workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                      align256(tokens * q_heads * a.splits * 8));
+  p.qt = q_stride_t;
+  p.qh = q_stride_h;
+  p.ot = out_stride_t;
+  p.oh = out_stride_h;
+  p.kp = k_cache_stride_page;
+  p.ks = k_cache_stride_slot;
+  p.kh = k_cache_stride_head;
+  p.vp = v_cache_stride_page;
+  p.vs = v_cache_stride_slot;
+  p.vh = v_cache_stride_head;
+  p.table_stride = table_stride;
+  p.num_pages = num_pages;
+  p.tokens = static_cast<int>(tokens);
+  p.batches = static_cast<int>(batches);
+  p.hq = static_cast<int>(q_heads);
+  p.hkv = static_cast<int>(kv_heads);
+  p.group = p.hq / p.hkv;
+  p.d = static_cast<int>(head_dim);
+  p.page_shift = log2_of(page_size);
+  p.table_pages = static_cast<int>(table_pages);
+  p.max_q = static_cast<int>(max_q < tokens ? max_q : tokens);
+  p.max_kv = static_cast<int>(max_kv);
+  p.causal = causal != 0;
+  p.window = static_cast<int>(window);
+  p.row_tiles = a.row_tiles;
+  p.splits = a.splits;
+  p.split_len = a.split_len;
+  p.scale_log2 = scale * kAttnLog2e;
+
+  const int mt = a.rows / 16;
+  cudaError_t e;
+  if (dtype == GBN_BF16)
+    e = fp8 ? launch_step_d<__nv_bfloat16, true>(p, mt, a.ctas, stream)
+            : launch_step_d<__nv_bfloat16, false>(p, mt, a.ctas, stream);
+  else
+    e = fp8 ? launch_step_d<__half, true>(p, mt, a.ctas, stream)
+            : launch_step_d<__half, false>(p, mt, a.ctas, stream);
+  if (e != cudaSuccess) return GBN_ERR_CUDA;
+  if (a.splits > 1) {
+    const dim3 g(static_cast<unsigned>(tokens * q_heads)), t(kMergeThreads);
+    e = dtype == GBN_BF16 ? launch_pdl(paged_merge_kernel<__nv_bfloat16>, g, t, 0, stream, p, int(fp8))
+                          : launch_pdl(paged_merge_kernel<__half>, g, t, 0, stream, p, int(fp8));
+    if (e != cudaSuccess) return GBN_ERR_CUDA;
+  }
+  return GBN_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,56 @@
+// Rows, masks and key ranges of the paged attention.
+//
+// The rows of one (sequence, kv head) are its new tokens times the group's
+// query heads: row r is token r / group, head kvh * group + r % group, so
+// the heads that share keys share a tile and the keys are read once for all
+// of them.  Token i stands at key position off + i (off = kv_len - q_len) and
+// keeps the keys j in [low(i), high(i)):
+//   high = off + i + 1 (causal) or kv_len, low = off + i - window + 1 or 0.
+#pragma once
+
+#include "paged.cuh"
+#include "paged_attn.h"
+
+namespace gbn {
+
+struct SeqRange {
+  int q0;    // first token
+  int qlen;  // new tokens
+  int kv;    // keys with them
+  int off;   // kv - qlen (negative: the first tokens keep nothing)
+};
+
+// Sequence b's lengths, bounded by the buffers whatever the values are; what
+// does not fit is flagged.
+__device__ __forceinline__ SeqRange seq_range(const AttnParams& p, int b, bool flag) {
+  SeqRange s;
+  const int c0 = p.cu[b], c1 = p.cu[b + 1], kv = p.kv_lens[b];
+  s.q0 = min(max(c0, 0), p.tokens);
+  s.qlen = min(max(c1, s.q0), p.tokens) - s.q0;
+  const int64_t room = static_cast<int64_t>(p.table_pages) << p.page_shift;
+  s.kv = static_cast<int>(min(static_cast<int64_t>(min(max(kv, 0), p.max_kv)), room));
+  s.off = s.kv - s.qlen;
+  if (flag && (s.q0 != c0 || s.q0 + s.qlen != c1 || s.kv != kv || s.qlen > p.max_q))
+    flag_bad_index();
+  return s;
+}
+
+__device__ __forceinline__ int row_high(const AttnParams& p, const SeqRange& s, int i) {
+  return p.causal ? min(max(s.off + i + 1, 0), s.kv) : s.kv;
+}
+__device__ __forceinline__ int row_low(const AttnParams& p, const SeqRange& s, int i) {
+  // 64-bit: a window near 2^31 must not wrap.
+  if (p.window <= 0) return 0;
+  const int64_t l = static_cast<int64_t>(s.off) + i - p.window + 1;
+  return l > 0 ? static_cast<int>(min(l, static_cast<int64_t>(s.kv))) : 0;
+}
+
+__device__ __forceinline__ float ex2(float a) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+  return r;
+}
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kAttnLog2e = 1.4426950408889634f;
+
+}  // namespace gbn

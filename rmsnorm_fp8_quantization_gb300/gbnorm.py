@@ -29,11 +29,16 @@ TORCH_DTYPE = {torch.float32: GBN_F32, torch.bfloat16: GBN_BF16, torch.float16: 
 
 FUNCTIONS = ("gbn_norm_fwd_workspace_size", "gbn_norm_fwd", "gbn_norm_bwd_workspace_size",
              "gbn_norm_bwd", "gbn_norm_bwd_noalloc", "gbn_device_error", "gbn_status_string",
-             "gbn_softmax_fwd", "gbn_softmax_bwd", "gbn_selftest_copy_timeout")
+             "gbn_softmax_fwd", "gbn_softmax_bwd", "gbn_selftest_copy_timeout", "gbn_rope_fwd",
+             "gbn_rope_bwd", "gbn_paged_append", "gbn_paged_attention_workspace_size",
+             "gbn_paged_attention")
 (GBN_SOFTMAX_NO_MASK, GBN_SOFTMAX_PADDING, GBN_SOFTMAX_CAUSAL_UPPER,
  GBN_SOFTMAX_CAUSAL_ALIGNED) = range(4)
 GBN_SOFTMAX_MAX_KEYS = 16384
-GBN_DEVICE_ERR_COPY_TIMEOUT = 1
+GBN_DEVICE_ERR_COPY_TIMEOUT, GBN_DEVICE_ERR_BAD_INDEX = 1, 2
+GBN_ROPE_HALF, GBN_ROPE_INTERLEAVED = 0, 1
+GBN_ROPE_MAX_DIM = 1024
+GBN_PAGED_MAX_BATCHES, GBN_PAGED_MAX_PAGE, GBN_PAGED_MAX_DIM = 1 << 20, 65536, 256
 
 
 class GbnError(RuntimeError):
@@ -68,6 +73,15 @@ def _load():
     lib.gbn_softmax_fwd.restype = I
     lib.gbn_softmax_bwd.argtypes = [P, P, P, I64, I64, I, F, P]
     lib.gbn_softmax_bwd.restype = I
+    for f in (lib.gbn_rope_fwd, lib.gbn_rope_bwd):
+        f.argtypes = [P] * 6 + [I64] * 19 + [I, I, I, F, P]
+        f.restype = I
+    lib.gbn_paged_append.argtypes = [P] * 12 + [I64] * 24 + [I, I, I, F, P]
+    lib.gbn_paged_append.restype = I
+    lib.gbn_paged_attention_workspace_size.argtypes = [I64] * 10 + [I, I, I, ctypes.POINTER(SZ)]
+    lib.gbn_paged_attention_workspace_size.restype = I
+    lib.gbn_paged_attention.argtypes = [P] * 11 + [SZ] + [I64] * 21 + [I, I, I, I64, F, P]
+    lib.gbn_paged_attention.restype = I
     lib.gbn_selftest_copy_timeout.argtypes = [ctypes.c_uint, P]
     lib.gbn_selftest_copy_timeout.restype = I
     lib.gbn_status_string.argtypes = [I]
@@ -182,6 +196,71 @@ def gbn_softmax_fwd(x, mask, y, batches, heads, sq, sk, mask_batches, dtype, mas
 def gbn_softmax_bwd(dy, y, dx, rows, sk, dtype, scale, stream=None) -> int:
     return _lib.gbn_softmax_bwd(_ptr(dy), _ptr(y), _ptr(dx), rows, sk, dtype, float(scale),
                                 _stream(stream))
+
+
+def gbn_rope_fwd(q, k, positions, inv_freq, q_out, k_out, batches, seq, q_heads, k_heads, head_dim,
+                 rotary_dim, q_strides, k_strides, q_out_strides, k_out_strides, position_stride,
+                 position_bytes, dtype, layout, mscale, stream=None) -> int:
+    """Strides: (batch, seq, head) triples in elements (one argument each in C)."""
+    return _lib.gbn_rope_fwd(_ptr(q), _ptr(k), _ptr(positions), _ptr(inv_freq), _ptr(q_out),
+                             _ptr(k_out), batches, seq, q_heads, k_heads, head_dim, rotary_dim,
+                             *q_strides, *k_strides, *q_out_strides, *k_out_strides,
+                             position_stride, position_bytes, dtype, layout, mscale,
+                             _stream(stream))
+
+
+def gbn_rope_bwd(dq, dk, positions, inv_freq, dq_out, dk_out, batches, seq, q_heads, k_heads,
+                 head_dim, rotary_dim, q_strides, k_strides, q_out_strides, k_out_strides,
+                 position_stride, position_bytes, dtype, layout, mscale, stream=None) -> int:
+    return _lib.gbn_rope_bwd(_ptr(dq), _ptr(dk), _ptr(positions), _ptr(inv_freq), _ptr(dq_out),
+                             _ptr(dk_out), batches, seq, q_heads, k_heads, head_dim, rotary_dim,
+                             *q_strides, *k_strides, *q_out_strides, *k_out_strides,
+                             position_stride, position_bytes, dtype, layout, mscale,
+                             _stream(stream))
+
+
+def gbn_paged_append(q, k, v, q_out, k_cache, v_cache, inv_freq, k_scale, v_scale, cu_seqlens,
+                     kv_lens, block_table, tokens, batches, q_heads, kv_heads, head_dim,
+                     rotary_dim, num_pages, page_size, table_pages, table_stride, q_strides,
+                     k_strides, v_strides, q_out_strides, k_cache_strides, v_cache_strides, dtype,
+                     cache_dtype, layout, mscale, stream=None) -> int:
+    """Strides in elements: (token, head) pairs, and (page, slot, head) triples of the caches."""
+    return _lib.gbn_paged_append(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_cache),
+                                 _ptr(v_cache), _ptr(inv_freq), _ptr(k_scale), _ptr(v_scale),
+                                 _ptr(cu_seqlens), _ptr(kv_lens), _ptr(block_table), tokens,
+                                 batches, q_heads, kv_heads, head_dim, rotary_dim, num_pages,
+                                 page_size, table_pages, table_stride, *q_strides, *k_strides,
+                                 *v_strides, *q_out_strides, *k_cache_strides, *v_cache_strides,
+                                 dtype, cache_dtype, layout, mscale, _stream(stream))
+
+
+def gbn_paged_attention_workspace_size(tokens, batches, q_heads, kv_heads, head_dim, page_size,
+                                       table_pages, max_q, max_kv, window, causal, dtype,
+                                       cache_dtype):
+    """Returns (status, bytes)."""
+    n = ctypes.c_size_t(0)
+    st = _lib.gbn_paged_attention_workspace_size(tokens, batches, q_heads, kv_heads, head_dim,
+                                                 page_size, table_pages, max_q, max_kv, window,
+                                                 int(bool(causal)), dtype, cache_dtype,
+                                                 ctypes.byref(n))
+    return st, n.value
+
+
+def gbn_paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, k_scale_inv,
+                        v_scale_inv, out, lse, workspace, workspace_bytes, tokens, batches,
+                        q_heads, kv_heads, head_dim, num_pages, page_size, table_pages,
+                        table_stride, max_q, max_kv, q_strides, out_strides, k_cache_strides,
+                        v_cache_strides, dtype, cache_dtype, causal, window, scale,
+                        stream=None) -> int:
+    """Strides in elements: (token, head) pairs, and (page, slot, head) triples of the caches."""
+    return _lib.gbn_paged_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens),
+                                    _ptr(kv_lens), _ptr(block_table), _ptr(k_scale_inv),
+                                    _ptr(v_scale_inv), _ptr(out), _ptr(lse), _ptr(workspace),
+                                    workspace_bytes, tokens, batches, q_heads, kv_heads, head_dim,
+                                    num_pages, page_size, table_pages, table_stride, max_q,
+                                    max_kv, *q_strides, *out_strides, *k_cache_strides,
+                                    *v_cache_strides, dtype, cache_dtype, int(bool(causal)),
+                                    window, scale, _stream(stream))
 
 
 def gbn_selftest_copy_timeout(timeout_us, stream=None) -> int:

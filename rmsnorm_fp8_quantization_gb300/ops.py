@@ -1,10 +1,13 @@
 """Allocating wrappers over the C ABI: build the output tensors with torch,
-call ``gbn_norm_fwd`` / ``gbn_norm_bwd`` and raise on a non-OK status.
+call ``gbn_norm_fwd`` / ``gbn_norm_bwd`` (and the softmax, rotary position and
+paged cache entry points) and raise on a non-OK status.
 
-The norm itself runs in the library's CUDA kernels; these functions only
+The work itself runs in the library's CUDA kernels; these functions only
 allocate device memory and marshal arguments.
 """
 from __future__ import annotations
+
+import math
 
 import torch
 
@@ -153,3 +156,339 @@ def softmax_bwd(dy, y, scale=1.0, out=None, stream=None):
     st = G.gbn_softmax_bwd(dy, y, dx, y.numel() // sk, sk, G.TORCH_DTYPE[y.dtype], scale, stream)
     _check(st, "gbn_softmax_bwd")
     return dx
+
+
+# ---- rotary positions and the paged key/value cache
+
+_ROPE_LAYOUT = {"half": G.GBN_ROPE_HALF, "interleaved": G.GBN_ROPE_INTERLEAVED}
+_NO_STRIDES = (0, 0, 0)
+
+
+class _on:
+    """Makes the tensor's device current for the call (the launch and the
+    current stream go by it); nothing to do when it already is."""
+
+    __slots__ = ("dev", "guard")
+
+    def __init__(self, t):
+        if t.device.type != "cuda":
+            raise ValueError(f"expected CUDA tensors, got one on {t.device}")
+        self.dev, self.guard = t.device, None
+
+    def __enter__(self):
+        if self.dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.dev)
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _same(name, t, dtype, device, dims=None):
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if dims is not None and t.dim() != dims:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected {dims}")
+
+
+def _inner(name, t):
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+
+
+def rope_frequencies(rotary_dim, base=10000.0, *, scaling="none", factor=1.0,
+                     original_length=None, fast_turns=32.0, slow_turns=1.0, device="cuda"):
+    """Radians per position of each pair: base^(-2i / rotary_dim), fp64
+    [rotary_dim / 2], scaled for contexts ``factor`` times longer:
+
+    * "linear": every frequency divided by ``factor``;
+    * "ntk": the base enlarged so that the slowest pair slows down by
+      ``factor`` and the fastest not at all;
+    * "yarn": by how often a pair turns within ``original_length`` positions:
+      kept from ``fast_turns`` on, divided by ``factor`` up to ``slow_turns``, a
+      linear ramp over the pair's index between (``rope_mscale`` goes with it).
+    """
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError(f"rotary_dim must be even and positive, got {rotary_dim}")
+    if not base > 0 or not factor >= 1.0:
+        raise ValueError("base must be positive and factor at least 1")
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64)
+    if scaling == "ntk" and rotary_dim > 2:
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = torch.pow(torch.tensor(float(base), dtype=torch.float64), -2.0 * i / rotary_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if original_length is None:
+            raise ValueError('"yarn" needs original_length')
+        if not base > 1.0 or not fast_turns > slow_turns > 0:
+            raise ValueError("base must exceed 1 and fast_turns slow_turns")
+
+        def index_of(turns):  # the (fractional) pair that turns this often
+            return (rotary_dim * math.log(original_length / (turns * 2 * math.pi))
+                    / (2 * math.log(base)))
+
+        lo = max(0.0, math.floor(index_of(fast_turns)))
+        hi = min(rotary_dim // 2 - 1.0, math.ceil(index_of(slow_turns)))
+        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        f = f * (1 - ramp) + f / factor * ramp
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(device)
+
+
+def rope_mscale(factor):
+    """The amplitude that goes with "yarn" frequencies: 0.1 ln(factor) + 1."""
+    return 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
+
+
+def _rope(call, where, q, k, inv_freq, positions, layout, mscale, q_out, k_out, stream):
+    if q is None and k is None:
+        raise ValueError("q and k are both None")
+    x = q if q is not None else k
+    if x.dim() != 4:
+        raise ValueError(f"expected [batch, seq, heads, head_dim], got {tuple(x.shape)}")
+    b, s, _, d = x.shape
+    dev = x.device
+    _same("inv_freq", inv_freq, torch.float64, dev, 1)
+    if not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be contiguous")
+    ptrs, heads, strides = [], [], []
+    for name, t, o in (("q", q, q_out), ("k", k, k_out)):
+        if t is None:
+            ptrs.append((None, None))
+            heads.append(0)
+            strides.append((_NO_STRIDES, _NO_STRIDES))
+            continue
+        _same(name, t, x.dtype, dev, 4)
+        if t.shape[0] != b or t.shape[1] != s or t.shape[3] != d:
+            raise ValueError(f"{name}: shape {tuple(t.shape)} does not go with {tuple(x.shape)}")
+        _inner(name, t)
+        if o is None:
+            o = torch.empty(t.shape, dtype=t.dtype, device=dev)
+        else:
+            _same(name + "_out", o, x.dtype, dev)
+            if o.shape != t.shape:
+                raise ValueError(f"{name}_out: shape {tuple(o.shape)}, expected {tuple(t.shape)}")
+            _inner(name + "_out", o)
+        ptrs.append((t, o))
+        heads.append(t.shape[2])
+        strides.append((t.stride()[:3], o.stride()[:3]))
+    pos_stride, pos_bytes = 0, 8
+    if positions is not None:
+        if positions.dtype not in (torch.int32, torch.int64) or positions.device != dev:
+            raise ValueError("positions: int32 or int64 on the tensors' device")
+        if positions.shape not in ((s,), (1, s), (b, s)):
+            raise ValueError(f"positions: shape {tuple(positions.shape)}, expected "
+                             f"({s},), (1, {s}) or ({b}, {s})")
+        if positions.stride(-1) != 1 and s > 1:
+            raise ValueError("positions must be contiguous along the sequence")
+        pos_bytes = positions.element_size()
+        if positions.dim() == 2 and positions.shape[0] > 1:
+            pos_stride = positions.stride(0)
+    if x.dtype not in G.TORCH_DTYPE:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    with _on(x):
+        st = call(ptrs[0][0], ptrs[1][0], positions, inv_freq, ptrs[0][1], ptrs[1][1], b, s,
+                  heads[0], heads[1], d, 2 * inv_freq.shape[0], strides[0][0], strides[1][0],
+                  strides[0][1], strides[1][1], pos_stride, pos_bytes, G.TORCH_DTYPE[x.dtype],
+                  _ROPE_LAYOUT[layout], mscale, stream)
+    _check(st, where)
+    return ptrs[0][1], ptrs[1][1]
+
+
+def rope_fwd(q, k, inv_freq, positions=None, *, layout="half", mscale=1.0, q_out=None, k_out=None,
+             stream=None):
+    """Rotates q and k [batch, seq, heads, head_dim] (either may be None) to
+    their positions ([seq], [1, seq] or [batch, seq] int32 / int64; None: 0, 1,
+    ...) and returns (q_out, k_out), new tensors unless given (q and k
+    themselves may be).  ``inv_freq``: ``rope_frequencies(rotary_dim)``; of the
+    head's elements the first rotary_dim = 2 * len(inv_freq) turn.  ``layout``:
+    pairs (i, i + rotary_dim / 2) ("half") or (2i, 2i + 1) ("interleaved")."""
+    return _rope(G.gbn_rope_fwd, "gbn_rope_fwd", q, k, inv_freq, positions, layout, mscale, q_out,
+                 k_out, stream)
+
+
+def rope_bwd(dq, dk, inv_freq, positions=None, *, layout="half", mscale=1.0, dq_out=None,
+             dk_out=None, stream=None):
+    """Gradients of ``rope_fwd``'s inputs from those of its outputs."""
+    return _rope(G.gbn_rope_bwd, "gbn_rope_bwd", dq, dk, inv_freq, positions, layout, mscale,
+                 dq_out, dk_out, stream)
+
+
+_E4M3_DTYPES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _cache_dtype(k_cache, v_cache, dtype):
+    c = k_cache.dtype
+    if c in _E4M3_DTYPES and v_cache.dtype in _E4M3_DTYPES:
+        return G.GBN_E4M3
+    if v_cache.dtype != c:
+        raise ValueError(f"v_cache: dtype {v_cache.dtype}, expected {c}")
+    if c != dtype:
+        raise ValueError(f"cache dtype {c}: expected {dtype}, or E4M3 codes (uint8, float8_e4m3fn)")
+    return G.TORCH_DTYPE[c]
+
+
+def _paged_args(x, k_cache, v_cache, cu_seqlens, kv_lens, block_table):
+    """Checks what both paged calls share; (cache dtype, kv heads, head_dim)."""
+    dev = x.device
+    if x.dim() != 3:
+        raise ValueError(f"expected [tokens, heads, head_dim], got {tuple(x.shape)}")
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"unsupported dtype {x.dtype}: bfloat16 or float16")
+    cdt = _cache_dtype(k_cache, v_cache, x.dtype)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("caches: [pages, page_size, kv_heads, head_dim], the same for both; got "
+                         f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+    if k_cache.shape[3] != x.shape[2]:
+        raise ValueError(f"caches: head_dim {k_cache.shape[3]}, expected {x.shape[2]}")
+    if k_cache.device != dev or v_cache.device != dev:
+        raise ValueError(f"caches: not on {dev}")
+    _inner("k_cache", k_cache)
+    _inner("v_cache", v_cache)
+    _same("cu_seqlens", cu_seqlens, torch.int32, dev, 1)
+    _same("kv_lens", kv_lens, torch.int32, dev, 1)
+    _same("block_table", block_table, torch.int32, dev, 2)
+    n = kv_lens.shape[0]
+    if cu_seqlens.shape[0] != n + 1 or block_table.shape[0] != n:
+        raise ValueError(f"{n} kv_lens need {n + 1} cu_seqlens and {n} block_table rows, got "
+                         f"{cu_seqlens.shape[0]} and {block_table.shape[0]}")
+    if not (cu_seqlens.is_contiguous() and kv_lens.is_contiguous()):
+        raise ValueError("cu_seqlens and kv_lens must be contiguous")
+    _inner("block_table", block_table)
+    return cdt, k_cache.shape[2], k_cache.shape[3]
+
+
+def _scalar(name, t, dev):
+    _same(name, t, torch.float32, dev)
+    if t.numel() != 1:
+        raise ValueError(f"{name}: one element, got {t.numel()}")
+
+
+def paged_append(k, v, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, q=None,
+                 inv_freq=None, layout="half", mscale=1.0, k_scale=None, v_scale=None, q_out=None,
+                 stream=None):
+    """Writes the new tokens' k and v [tokens, kv_heads, head_dim] into the
+    paged caches [pages, page_size, kv_heads, head_dim] (bf16 / f16 like k, or
+    E4M3 codes as uint8 / float8_e4m3fn, then with k_scale and v_scale, fp32
+    [1]).  Sequence b's tokens are rows cu_seqlens[b] .. cu_seqlens[b+1] - 1
+    and become its last keys: kv_lens[b] counts them.  With ``inv_freq`` the
+    keys are rotated to their positions on the way, and ``q`` [tokens, heads,
+    head_dim], if given, into ``q_out`` (returned; a new tensor unless given,
+    and then with unwritten padding rows)."""
+    cdt, hk, d = _paged_args(k, k_cache, v_cache, cu_seqlens, kv_lens, block_table)
+    dev = k.device
+    _same("v", v, k.dtype, dev, 3)
+    if v.shape != k.shape or k.shape[1] != hk:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)}: expected "
+                         f"[tokens, {hk}, {d}]")
+    _inner("k", k)
+    _inner("v", v)
+    hq, qs, qo = 0, (0, 0), (0, 0)
+    if q is not None:
+        _same("q", q, k.dtype, dev, 3)
+        if q.shape[0] != k.shape[0] or q.shape[2] != d:
+            raise ValueError(f"q: shape {tuple(q.shape)} does not go with k {tuple(k.shape)}")
+        _inner("q", q)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        else:
+            _same("q_out", q_out, k.dtype, dev, 3)
+            if q_out.shape != q.shape:
+                raise ValueError(f"q_out: shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
+            _inner("q_out", q_out)
+        hq, qs, qo = q.shape[1], q.stride()[:2], q_out.stride()[:2]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot = 0
+    if inv_freq is not None:
+        _same("inv_freq", inv_freq, torch.float64, dev, 1)
+        if not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be contiguous")
+        rot = 2 * inv_freq.shape[0]
+    if cdt == G.GBN_E4M3:
+        if k_scale is None or v_scale is None:
+            raise ValueError("E4M3 caches need k_scale and v_scale")
+        _scalar("k_scale", k_scale, dev)
+        _scalar("v_scale", v_scale, dev)
+    with _on(k):
+        st = G.gbn_paged_append(q, k, v, q_out, k_cache, v_cache, inv_freq, k_scale, v_scale,
+                                cu_seqlens, kv_lens, block_table, k.shape[0], kv_lens.shape[0],
+                                hq, hk, d, rot, k_cache.shape[0], k_cache.shape[1],
+                                block_table.shape[1], block_table.stride(0), qs, k.stride()[:2],
+                                v.stride()[:2], qo, k_cache.stride()[:3], v_cache.stride()[:3],
+                                G.TORCH_DTYPE[k.dtype], cdt, _ROPE_LAYOUT[layout], mscale, stream)
+    _check(st, "gbn_paged_append")
+    return q_out
+
+
+def paged_attention_workspace(q, k_cache, block_table, *, max_q, max_kv=None, causal=True,
+                              window=0):
+    """A workspace for ``paged_attention`` calls of these sizes (None: they need none)."""
+    cdt = _cache_dtype(k_cache, k_cache, q.dtype)
+    mkv = block_table.shape[1] * k_cache.shape[1] if max_kv is None else max_kv
+    with _on(q):
+        st, n = G.gbn_paged_attention_workspace_size(
+            q.shape[0], block_table.shape[0], q.shape[1], k_cache.shape[2], q.shape[2],
+            k_cache.shape[1], block_table.shape[1], max_q, mkv, window, causal,
+            G.TORCH_DTYPE[q.dtype], cdt)
+        _check(st, "gbn_paged_attention_workspace_size")
+        return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+
+
+def paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, max_q, max_kv=None,
+                    scale=None, causal=True, window=0, k_scale_inv=None, v_scale_inv=None,
+                    return_lse=False, out=None, lse=None, workspace=None, stream=None):
+    """Attention of the new tokens q [tokens, heads, head_dim] over the paged
+    caches (arguments as in ``paged_append``, which has run before).  max_q and
+    max_kv bound the new tokens per sequence and kv_lens (max_kv: by default
+    the table's room).  ``scale``: 1 / sqrt(head_dim) by default.  ``causal``:
+    bottom-right aligned; ``window`` > 0: only the last ``window`` positions up
+    to the token's own.  Returns out, or (out, lse) with ``return_lse``; both
+    are new tensors unless given (padding rows are not written).
+    ``workspace``: ``paged_attention_workspace``; allocated here when needed."""
+    cdt, hk, d = _paged_args(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table)
+    dev, t, hq = q.device, q.shape[0], q.shape[1]
+    _inner("q", q)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        _same("out", out, q.dtype, dev, 3)
+        if out.shape != q.shape:
+            raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+        _inner("out", out)
+    if return_lse and lse is None:
+        lse = torch.empty(t, hq, dtype=torch.float32, device=dev)
+    elif lse is not None:
+        _same("lse", lse, torch.float32, dev)
+        if lse.shape != (t, hq) or not lse.is_contiguous():
+            raise ValueError(f"lse: contiguous [{t}, {hq}] expected")
+    if cdt == G.GBN_E4M3:
+        if k_scale_inv is None or v_scale_inv is None:
+            raise ValueError("E4M3 caches need k_scale_inv and v_scale_inv")
+        _scalar("k_scale_inv", k_scale_inv, dev)
+        _scalar("v_scale_inv", v_scale_inv, dev)
+    page, pages = k_cache.shape[1], block_table.shape[1]
+    mkv = pages * page if max_kv is None else max_kv
+    dt = G.TORCH_DTYPE[q.dtype]
+    n = kv_lens.shape[0]
+    with _on(q):
+        if workspace is None:
+            st, need = G.gbn_paged_attention_workspace_size(t, n, hq, hk, d, page, pages, max_q,
+                                                            mkv, window, causal, dt, cdt)
+            _check(st, "gbn_paged_attention_workspace_size")
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        st = G.gbn_paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table,
+                                   k_scale_inv, v_scale_inv, out, lse, workspace,
+                                   workspace.numel() if workspace is not None else 0, t, n, hq,
+                                   hk, d, k_cache.shape[0], page, pages, block_table.stride(0),
+                                   max_q, mkv, q.stride()[:2], out.stride()[:2],
+                                   k_cache.stride()[:3], v_cache.stride()[:3], dt, cdt, causal,
+                                   window, d ** -0.5 if scale is None else scale, stream)
+    _check(st, "gbn_paged_attention")
+    return (out, lse) if return_lse else out
