@@ -19,7 +19,8 @@ LIB = os.path.join(PKG, "libgbnorm.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "kernels_f32.cu", "kernels_bf16.cu", "kernels_f16.cu", "finalize.cu",
-           "noalloc.cu", "softmax.cu", "rope.cu", "paged_attention.cu"]
+           "noalloc.cu", "softmax.cu", "rope.cu", "paged_attention.cu",
+           "paged_prefill.cu"]
 
 
 def _nvcc() -> str:

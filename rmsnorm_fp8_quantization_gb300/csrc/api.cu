@@ -757,11 +757,12 @@ gbn_status gbn_device_error(unsigned int* flags, int clear) {
       kernels_bf16().read_device_error(&b, clear != 0) != cudaSuccess ||
       kernels_f16().read_device_error(&c, clear != 0) != cudaSuccess)
     return GBN_ERR_CUDA;
-  unsigned int r = 0, s = 0;
+  unsigned int r = 0, s = 0, t = 0;
   if (read_rope_error(&r, clear != 0) != cudaSuccess ||
-      read_attention_error(&s, clear != 0) != cudaSuccess)
+      read_attention_error(&s, clear != 0) != cudaSuccess ||
+      read_prefill_error(&t, clear != 0) != cudaSuccess)
     return GBN_ERR_CUDA;
-  *flags = a | b | c | r | s;
+  *flags = a | b | c | r | s | t;
   return GBN_OK;
 }
 

@@ -609,7 +609,8 @@ cudaError_t launch_step_d(const AttnParams& p, int mt, int64_t grid, cudaStream_
 
 // How a call is carried out: a function of sizes that the host knows.
 struct AttnPlan {
-  int rows;       // rows per CTA (16, 32, 64: the step kernel)
+  bool prefill;   // the tcgen05 kernel
+  int rows;       // rows per CTA (16, 32, 64; prefill: 256)
   int row_tiles;
   int splits;
   int split_len;
@@ -618,11 +619,14 @@ struct AttnPlan {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t max_q, int64_t max_kv,
-                   int64_t window, int causal, int page_shift, int sms) {
+AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t d, int64_t max_q,
+                   int64_t max_kv, int64_t window, int causal, int page_shift, int sms) {
   AttnPlan a;
   const int64_t r = max_q * group;
-  a.rows = r <= 16 ? 16 : r <= 32 ? 32 : 64;
+  // The tcgen05 kernel from the first size on that fills half a tile of it;
+  // its boxes are at least 8 slots (one swizzle atom).
+  a.prefill = r > 64 && d <= 128 && page_shift >= 3;
+  a.rows = a.prefill ? kPrefillRows : r <= 16 ? 16 : r <= 32 ? 32 : 64;
   a.row_tiles = static_cast<int>(ceil_div(r, a.rows));
   // Longest key range of a row tile.
   int64_t range = max_kv;
@@ -631,17 +635,19 @@ AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t max_q, i
     const int64_t w = window + (tile_tokens < max_q ? tile_tokens : max_q);
     if (w < range) range = w;
   }
-  // Splits: enough CTAs for several rounds of two per SM, at least 256 keys each.
   const int64_t tiles = batches * hkv * a.row_tiles;
-  const int64_t want = 8ll * sms;
+  const int64_t step = a.prefill ? kPrefillKeys : kStepKeys;
+  // Splits.  Few rows: enough CTAs for several rounds of two per SM, at least
+  // 256 keys each.  Prefill (one CTA per SM): two rounds where the row tiles
+  // alone do not fill one, at least 512 keys each.
+  const int64_t want = a.prefill ? (tiles < sms ? 2ll * sms : 0) : 8ll * sms;
   int64_t splits = tiles >= want ? 1 : ceil_div(want, tiles > 0 ? tiles : 1);
-  const int64_t most = ceil_div(range, 256);
+  const int64_t most = ceil_div(range, a.prefill ? 512 : 256);
   if (splits > most) splits = most;
-  const int64_t pages_least = ceil_div(range, (int64_t(kSplitPages) - 1) << page_shift);
-  if (splits < pages_least) splits = pages_least;
+  const int64_t cap = a.prefill ? int64_t(1) << 30 : (int64_t(kSplitPages) - 1) << page_shift;
+  if (splits < ceil_div(range, cap)) splits = ceil_div(range, cap);
   if (splits < 1) splits = 1;
-  int64_t len = ceil_div(ceil_div(range, splits), kStepKeys) * kStepKeys;
-  const int64_t cap = (int64_t(kSplitPages) - 1) << page_shift;
+  int64_t len = ceil_div(ceil_div(range, splits), step) * step;
   if (len > cap) len = cap;
   if (len < 1) len = 1;
   a.split_len = static_cast<int>(len);
@@ -683,7 +689,7 @@ gbn_status plan_for(const AttnSizes& z, int causal, AttnPlan* a) {
   const int64_t room = z.table_pages * z.page;
   const int64_t kv = z.max_kv < room ? z.max_kv : room;
   const int64_t mq = z.max_q < z.tokens ? z.max_q : z.tokens;
-  *a = attn_plan(z.batches, z.hkv, z.hq / z.hkv, mq, kv, z.window, causal, log2_of(z.page),
+  *a = attn_plan(z.batches, z.hkv, z.hq / z.hkv, z.d, mq, kv, z.window, causal, log2_of(z.page),
                  sms);
   if (a->splits > kMaxSplits || a->ctas > 0x7FFFFFFF) return GBN_ERR_SHAPE;
   return GBN_OK;
@@ -813,7 +819,9 @@ gbn_status gbn_paged_attention(const void* q, const void* k_cache, const void* v
 
   const int mt = a.rows / 16;
   cudaError_t e;
-  if (dtype == GBN_BF16)
+  if (a.prefill)
+    e = launch_paged_prefill(p, dtype, cache_dtype, stream);
+  else if (dtype == GBN_BF16)
     e = fp8 ? launch_step_d<__nv_bfloat16, true>(p, mt, a.ctas, stream)
             : launch_step_d<__nv_bfloat16, false>(p, mt, a.ctas, stream);
   else

@@ -1,0 +1,729 @@
+// Paged attention for many rows per kv head: prompts and chunks of prompts on
+// the 5th-generation tensor cores.  Same mathematics as the kernel for few
+// rows (paged_attention.cu); here the matrix products bound it: 4 d flops per
+// kept (row, key) against the bytes of a key shared by 256 rows.
+//
+// A CTA holds two tiles of 128 rows (token x head of the kv head's group) and
+// streams tiles of 128 keys past both.  Roles:
+//   warps 0-3, 4-7   softmax of row tile 0 and 1, one thread per row
+//   warp 8           issues every tcgen05.mma (one lane)
+//   warp 9           issues the TMA loads, one lane per page box
+//   warps 12-15      E4M3 caches only: load, convert, store keys and values
+// Tensor memory (512 columns): scores S0, S1 (128 fp32 columns each) and
+// outputs O0, O1.  S = Q K^T reads both operands from shared memory; the
+// probabilities go back into S's columns as 16-bit pairs and are the A operand
+// of O += P V straight from tensor memory, so they never pass through shared
+// memory.  While the tensor core works on one tile (P V of key tile j, then
+// Q K^T of tile j + 1), the other tile's softmax runs: the two alternate.
+//
+// The outputs stay in tensor memory for the whole key range.  A row's
+// reference maximum moves only when the running maximum has grown by more
+// than 2^8 over it: until then the probabilities, at most 256, lose nothing in
+// fp32 sums or 16-bit mantissas, and O is not touched; when it moves the
+// row's own threads rescale O (a few times per row, mostly in the first
+// tiles).
+//
+// K and V tiles: [128 keys][64 elements] panels with 128-byte rows in the
+// 128-byte swizzle, written by TMA boxes of one page (or 128 slots of a larger
+// one) each; K is read K-major, V MN-major from the same layout.  A box whose
+// keys all lie outside the range is fetched from the page index one past the
+// cache, which TMA fills with zeros: the byte count stays the same and nothing
+// is read.  Rows of a box that the range cuts are zeroed in shared memory for
+// V (a weight of 0 times what stands in such a slot must be 0); for K the mask
+// replaces the score.
+#include <type_traits>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "paged_rows.cuh"
+
+namespace gbn {
+namespace {
+
+constexpr int kRowsT = 128;                // rows per tile
+constexpr int kKeys = kPrefillKeys;        // keys per tile
+constexpr int kPanel = kKeys * 128;        // bytes of [128][64] 16-bit elements
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescale = 8.f;            // log2 growth before the reference moves
+
+template <bool FP8, int DP>
+struct PrefillShape {
+  static constexpr int kPanels = DP / 64;
+  static constexpr int kSlot = kPanels * kPanel;   // one K or V tile
+  static constexpr int kSlots = DP == 128 ? 5 : 8; // K and V alternate
+  static constexpr int kQ = 2 * kSlot;
+  static constexpr int kSmem = kQ + kSlots * kSlot + 1024;  // + alignment
+  static constexpr int kThreads = FP8 ? 512 : 384;
+  // Registers a thread: launched with 65536 / kThreads (128, 168), moved from
+  // the other warps to the softmax.  2 x 128 x softmax + the rest x other =
+  // kThreads x launch, exactly.
+  static constexpr int kRegsLaunch = FP8 ? 128 : 168;
+  static constexpr int kRegsSoftmax = FP8 ? 184 : 208;
+  static constexpr int kRegsOther = FP8 ? 72 : 88;
+  static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther == kThreads * kRegsLaunch, "");
+};
+
+struct Barriers {
+  uint64_t full[8], empty[8], s_full[2], p_full[2], o_full[2], q_full;
+  uint32_t tmem;
+};
+
+// ---- tcgen05
+
+__device__ __forceinline__ void tc_alloc(uint32_t* dst) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(dst)),
+               "r"(kTmemCols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_dealloc(uint32_t t) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(kTmemCols)
+               : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_u32(bar))
+               : "memory");
+}
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// 32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// The loaded registers pass through, so that nothing uses them earlier.
+__device__ __forceinline__ void tc_loaded(uint32_t* r) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                 "+r"(r[31])::"memory");
+}
+template <int N>
+__device__ __forceinline__ void tc_wait_ld(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; i += 32) tc_loaded(r + i);
+}
+__device__ __forceinline__ void tc_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle, 8-row groups 1024 bytes
+// apart; `panel` the distance of the next 64 elements (MN-major only).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t panel) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) |
+         (static_cast<uint64_t>(panel >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor: fp32 accumulator, A and B f16 (0) or bf16 (1), M x N;
+// bmn: B is MN-major.
+__host__ __device__ constexpr uint32_t instr_desc(int type, int m, int n, int bmn) {
+  return (1u << 4) | (static_cast<uint32_t>(type) << 7) | (static_cast<uint32_t>(type) << 10) |
+         (static_cast<uint32_t>(bmn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                        int c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
+}
+
+__device__ __forceinline__ uint32_t e4m3_pair_f16(uint32_t c) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+      : "=r"(r)
+      : "r"(c));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t c) {
+  const uint32_t h = e4m3_pair_f16(c);
+  if constexpr (BF16) return narrow2<__nv_bfloat16>(widen2<__half>(h));
+  else return h;
+}
+
+template <int N>
+__device__ __forceinline__ void set_regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <typename T, bool FP8, int DP>
+__global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
+    paged_prefill_kernel(const __grid_constant__ AttnParams p,
+                         const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap) {
+  using Shape = PrefillShape<FP8, DP>;
+  using TP = typename std::conditional<FP8, __half, T>::type;
+  constexpr int kTypeQ = std::is_same<T, __half>::value ? 0 : 1;
+  constexpr int kTypeP = std::is_same<TP, __half>::value ? 0 : 1;
+  extern __shared__ uint8_t raw[];
+  __shared__ Barriers bars;
+
+  pdl_begin();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // Row blocks from the last one down: causal rows late in a sequence have the
+  // most keys.
+  uint32_t x = blockIdx.x;
+  const int h = x % p.hkv;
+  x /= p.hkv;
+  const int split = x % p.splits;
+  x /= p.splits;
+  const int b = x % p.batches;
+  const int rt = p.row_tiles - 1 - static_cast<int>(x / p.batches);
+
+  const SeqRange s = seq_range(p, b, tid == 0 && split == 0 && rt == 0 && h == 0);
+  const int r0 = rt * kPrefillRows;
+  const int rows = min(kPrefillRows, s.qlen * p.group - r0);
+  if (rows <= 0) return;
+
+  // Key range of this CTA [k0, k1), first key of its tiles, tiles per row tile.
+  const int i_last = (r0 + rows - 1) / p.group;
+  const int lo = row_low(p, s, r0 / p.group), hi = row_high(p, s, i_last);
+  const int64_t start = lo + static_cast<int64_t>(split) * p.split_len;
+  const int k0 = static_cast<int>(min(start, static_cast<int64_t>(hi)));
+  const int k1 = static_cast<int>(min(start + p.split_len, static_cast<int64_t>(hi)));
+  const int base = k0 & ~(kKeys - 1);
+  int nt[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int last = min(r0 + kRowsT * (t + 1), r0 + rows) - 1;  // last row of the tile
+    const int end = last < r0 + kRowsT * t ? 0 : min(row_high(p, s, last / p.group), k1);
+    nt[t] = k1 > k0 && end > base ? (end - base + kKeys - 1) / kKeys : 0;
+  }
+  const int nmax = max(nt[0], nt[1]);
+
+  const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t qs = smem0, ring = smem0 + Shape::kQ;
+  uint8_t* const gen0 = raw + (smem0 - smem_u32(raw));  // the same, generic
+
+  if (tid == 0) {
+    for (int i = 0; i < Shape::kSlots; ++i) {
+      mbar_init(&bars.full[i], FP8 ? 128 : 1);
+      mbar_init(&bars.empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars.s_full[t], 1);
+      mbar_init(&bars.p_full[t], 128);
+      mbar_init(&bars.o_full[t], 1);
+    }
+    mbar_init(&bars.q_full, 256);
+    fence_mbar_init();
+  }
+  if (warp == 8) tc_alloc(&bars.tmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  bool ok = true;
+
+  float kscale = 1.f, vscale = 1.f;
+  if constexpr (FP8) {
+    kscale = *p.k_scale_inv;
+    vscale = *p.v_scale_inv;
+  }
+
+  if (warp >= 8) {
+    set_regs_dec<Shape::kRegsOther>();
+    if (warp == 8) {
+      // ------------------------------------------------ tensor core issue
+      constexpr uint32_t kIdQK = instr_desc(kTypeQ, kRowsT, kKeys, 0);
+      constexpr uint32_t kIdPV = instr_desc(kTypeP, kRowsT, DP, 1);
+      auto qk = [&](int t, int slot) {
+        if (lane == 0) {
+#pragma unroll
+          for (int kk = 0; kk < DP / 16; ++kk) {
+            const uint32_t at = (kk / 4) * kPanel + (kk % 4) * 32;
+            tc_mma_ss(tmem + t * 128, smem_desc(qs + t * Shape::kSlot + at, 16),
+                      smem_desc(ring + slot * Shape::kSlot + at, 16), kIdQK, kk > 0);
+          }
+          tc_commit(&bars.s_full[t]);
+        }
+      };
+      int it = 0;  // ring position
+      if (nmax > 0) {
+        ok = warp_wait(&bars.q_full, 0) && warp_wait(&bars.full[0], 0);
+        if (ok) {
+          tc_fence_after();
+          for (int t = 0; t < 2; ++t)
+            if (nt[t] > 0) qk(t, 0);
+          if (lane == 0) tc_commit(&bars.empty[0]);
+          it = 1;
+        }
+      }
+      for (int j = 0; ok && j < nmax; ++j) {
+        const int vs = it % Shape::kSlots;
+        ok = warp_wait(&bars.full[vs], (it / Shape::kSlots) & 1);
+        if (!ok) break;
+        ++it;
+        if constexpr (!FP8) {
+          // Values of slots outside the range become zero.
+          const int tb = base + j * kKeys;
+          const int za = max(0, k0 - tb), zb = min(kKeys, k1 - tb);
+          if (za > 0 || zb < kKeys) {
+            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+            const int outside = za + kKeys - zb;
+            for (int i = lane; i < outside * 8 * Shape::kPanels; i += 32) {
+              const int c = i & 7, pr = i >> 3;
+              const int pn = pr % Shape::kPanels, o = pr / Shape::kPanels;
+              const int r = o < za ? o : zb + (o - za);
+              *reinterpret_cast<uint4*>(gen0 + Shape::kQ + vs * Shape::kSlot + pn * kPanel +
+                                        r * 128 + c * 16) = z;
+            }
+            fence_async_smem();
+            __syncwarp();
+          }
+        }
+        int ks = -1;
+        if (j + 1 < nmax) {
+          ks = it % Shape::kSlots;
+          ok = warp_wait(&bars.full[ks], (it / Shape::kSlots) & 1);
+          if (!ok) break;
+          ++it;
+        }
+        for (int t = 0; t < 2; ++t) {
+          if (j >= nt[t]) continue;
+          ok = warp_wait(&bars.p_full[t], j & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
+                        smem_desc(ring + vs * Shape::kSlot + kk * 2048, kPanel), kIdPV,
+                        j > 0 || kk > 0);
+            tc_commit(&bars.o_full[t]);
+          }
+          if (j + 1 < nt[t]) qk(t, ks);
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          tc_commit(&bars.empty[vs]);
+          if (ks >= 0) tc_commit(&bars.empty[ks]);
+        }
+        __syncwarp();
+      }
+      // The last of this warp's arrivals has landed before the CTA ends.
+      if (ok && nmax > 0) {
+        const int last = 2 * nmax - 1;
+        ok = warp_wait(&bars.empty[last % Shape::kSlots], (last / Shape::kSlots) & 1);
+      }
+    } else if (!FP8 && warp == 9) {
+      // ------------------------------------------------ TMA loads
+      if constexpr (!FP8) {
+        const int page = 1 << p.page_shift;
+        const int box = min(page, kKeys);           // keys per box
+        const int boxes = kKeys / box;              // per panel, at most 16
+        const int32_t* tab = p.table + b * p.table_stride;
+        const int e_last = k1 > 0 ? (k1 - 1) >> p.page_shift : 0;
+        // Page of this lane's box of key tile j; one past the map's pages: zeros.
+        const int zero_page = max(1, static_cast<int>(p.num_pages));
+        auto page_of = [&](int j) {
+          const int key = base + j * kKeys + lane * box;
+          int pg = zero_page;
+          if (lane < boxes && key < k1 && key + box > k0) {
+            const int v = tab[min(key >> p.page_shift, e_last)];
+            if (v >= 0 && v < p.num_pages) pg = v;
+            else flag_bad_index();
+          }
+          return pg;
+        };
+        int issued = 0;
+        int pg = nmax > 0 ? page_of(0) : 0;
+        for (int j = 0; ok && j < nmax; ++j) {
+          const int next = j + 1 < nmax ? page_of(j + 1) : 0;
+          for (int kv = 0; kv < 2; ++kv) {
+            const int it = 2 * j + kv, slot = it % Shape::kSlots, use = it / Shape::kSlots;
+            if (use > 0) ok = warp_wait(&bars.empty[slot], (use - 1) & 1);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bars.full[slot], Shape::kSlot);
+            __syncwarp();
+            if (lane < boxes) {
+              const int key = base + j * kKeys + lane * box;
+#pragma unroll
+              for (int pn = 0; pn < Shape::kPanels; ++pn)
+                tma_box(ring + slot * Shape::kSlot + pn * kPanel + lane * box * 128,
+                        kv ? &vmap : &kmap, pn * 64, h, key & (page - 1), pg, &bars.full[slot]);
+            }
+            issued = it + 1;
+          }
+          pg = next;
+        }
+        if (!ok) {
+          // Leave no copy in flight behind.
+          for (int i = max(0, issued - Shape::kSlots); i < issued; ++i)
+            warp_wait(&bars.full[i % Shape::kSlots], (i / Shape::kSlots) & 1);
+        }
+      }
+    } else if (FP8 && warp >= 12) {
+      // ------------------------------------------------ E4M3: load and convert
+      if constexpr (FP8) {
+        constexpr int kChunks = DP / 16;                    // 16-byte chunks per key
+        constexpr int kPer = kKeys * kChunks / 128;         // per thread and tile
+        const int lt = tid - 384;
+        const int32_t* tab = p.table + b * p.table_stride;
+        const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k) + h * p.kh;
+        const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v) + h * p.vh;
+        const int c = lt % kChunks;                         // the same chunk of every row
+        uint4 w[kPer];
+        auto fetch = [&](int it) {
+          const int tb = base + (it >> 1) * kKeys;
+          const bool is_v = it & 1;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int key = tb + (lt + i * 128) / kChunks;
+            w[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (key >= k0 && key < k1 && c * 16 < p.d) {
+              const int pg = tab[key >> p.page_shift];
+              const int slot = key & ((1 << p.page_shift) - 1);
+              if (pg >= 0 && pg < p.num_pages)
+                w[i] = ld_stream16(is_v ? vb + pg * p.vp + slot * p.vs + c * 16
+                                        : kb + pg * p.kp + slot * p.ks + c * 16);
+              else
+                flag_bad_index();
+            }
+          }
+        };
+        if (nmax > 0) fetch(0);
+        for (int it = 0; ok && it < 2 * nmax; ++it) {
+          const int slot = it % Shape::kSlots, use = it / Shape::kSlots;
+          if (use > 0) ok = warp_wait(&bars.empty[slot], (use - 1) & 1);
+          if (!ok) break;
+          uint8_t* dst = gen0 + Shape::kQ + slot * Shape::kSlot + (c / 4) * kPanel;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int r = (lt + i * 128) / kChunks;
+            const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t o[8];
+            if (it & 1) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                o[2 * e] = e4m3_pair<false>(a[e] & 0xFFFFu);
+                o[2 * e + 1] = e4m3_pair<false>(a[e] >> 16);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                o[2 * e] = e4m3_pair<kTypeQ == 1>(a[e] & 0xFFFFu);
+                o[2 * e + 1] = e4m3_pair<kTypeQ == 1>(a[e] >> 16);
+              }
+            }
+            const int c2 = (c % 4) * 2;
+            *reinterpret_cast<uint4*>(dst + r * 128 + ((c2 ^ (r & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((c2 + 1) ^ (r & 7)) << 4)) =
+                make_uint4(o[4], o[5], o[6], o[7]);
+          }
+          if (it + 1 < 2 * nmax) fetch(it + 1);
+          fence_async_smem();
+          mbar_arrive(&bars.full[slot]);
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------- softmax
+    set_regs_inc<Shape::kRegsSoftmax>();
+    const int t = warp >> 2;
+    const int r = tid & 127;
+    const int gr = r0 + t * kRowsT + r;          // row of the (sequence, kv head)
+    const bool live = t * kRowsT + r < rows;
+    const int token_i = live ? gr / p.group : i_last;
+    const int head = h * p.group + (live ? gr % p.group : 0);
+    // q's row, by whole warps: a row's 16-byte chunks by neighbouring lanes.
+    {
+      constexpr int C = DP / 8;
+      const T* q = reinterpret_cast<const T*>(p.q);
+      // A negative factor of the keys turns q's sign, a factor of 0 clears it:
+      // what is left multiplies the scores by something positive.
+      const uint32_t flip = kscale < 0.f ? 0x80008000u : 0u, keep = kscale == 0.f ? 0u : ~0u;
+      for (int i = lane; i < 32 * C; i += 32) {
+        const int rr = (warp & 3) * 32 + i / C, c = i % C;
+        const int row = t * kRowsT + rr;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (row < rows && c * 8 < p.d) {
+          const int g = r0 + row;
+          w = *reinterpret_cast<const uint4*>(q + (s.q0 + g / p.group) * p.qt +
+                                              (h * p.group + g % p.group) * p.qh + c * 8);
+          if constexpr (FP8) {
+            w.x = (w.x ^ flip) & keep;
+            w.y = (w.y ^ flip) & keep;
+            w.z = (w.z ^ flip) & keep;
+            w.w = (w.w ^ flip) & keep;
+          }
+        }
+        *reinterpret_cast<uint4*>(gen0 + t * Shape::kSlot + (c / 8) * kPanel + rr * 128 +
+                                  (((c & 7) ^ (rr & 7)) << 4)) = w;
+      }
+      fence_async_smem();
+      mbar_arrive(&bars.q_full);
+    }
+    const int rlo = max(row_low(p, s, token_i), k0), rhi = min(row_high(p, s, token_i), k1);
+    const float scale = p.scale_log2 * (kscale == 0.f ? 1.f : fabsf(kscale));
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+    float m = -INFINITY;   // the row's reference maximum (log2 units)
+    float l = 0.f;
+    const int n = nt[t];
+    for (int j = 0; j < n; ++j) {
+      ok = warp_wait(&bars.s_full[t], j & 1);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sc[128];
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) tc_ld32(ts + q4 * 32, sc + q4 * 32);
+      tc_wait_ld<128>(sc);
+      const int tb = base + j * kKeys;
+      if (__any_sync(0xFFFFFFFFu, tb < rlo || tb + kKeys > rhi)) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i)
+          if (tb + i < rlo || tb + i >= rhi) sc[i] = 0xFF800000u;  // -inf
+      }
+      float mx[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(sc[e]);
+#pragma unroll
+      for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(sc[i]));
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+      // -inf - -inf is not a number: no growth.
+      if (__any_sync(0xFFFFFFFFu, mt - m > kRescale)) {
+        const float mn = fmaxf(m, mt);
+        const float al = mn == -INFINITY ? 1.f : ex2(m - mn);
+        l *= al;
+        m = mn;
+        if (j > 0) {
+          ok = warp_wait(&bars.o_full[t], (j - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int q4 = 0; q4 < DP / 32; ++q4) {
+            uint32_t o[32];
+            tc_ld32(to + q4 * 32, o);
+            tc_wait_ld<32>(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+            tc_st32(to + q4 * 32, o);
+          }
+        }
+      }
+      const float mb = m == -INFINITY ? 0.f : m;
+      const uint64_t sc2 = p2(scale, scale), mb2 = p2(-mb, -mb);
+      uint64_t l2[2] = {p2(l, 0.f), 0ull};
+      uint32_t pk[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        const float2 a = u2(fma2(p2(__uint_as_float(sc[2 * i]), __uint_as_float(sc[2 * i + 1])), sc2, mb2));
+        const uint64_t e = p2(ex2(a.x), ex2(a.y));
+        l2[i & 1] = add2(l2[i & 1], e);
+        pk[i] = narrow2<TP>(e);
+        if (i == 31) tc_st32(ts, pk);
+      }
+      tc_st32(ts + 32, pk + 32);
+      const float2 la = u2(add2(l2[0], l2[1]));
+      l = la.x + la.y;
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(&bars.p_full[t]);
+    }
+    // Output.
+    if (ok && n > 0) {
+      ok = warp_wait(&bars.o_full[t], (n - 1) & 1);
+      tc_fence_after();
+    }
+    if (ok) {
+      const int64_t token = s.q0 + token_i;
+      const int64_t ro = token * p.hq + head;
+      const bool part = p.splits > 1;
+      const float inv = part ? 1.f : l == 0.f ? 0.f : vscale / l;
+      if (live) {
+        if (part) p.part_ml[ro * p.splits + split] = make_float2(m, l);
+        else if (p.lse) p.lse[ro] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
+#pragma unroll
+      for (int q4 = 0; q4 < DP / 32; ++q4) {
+        uint32_t o[32];
+        if (n > 0) {
+          tc_ld32(to + q4 * 32, o);
+          tc_wait_ld<32>(o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        if (live && part) {
+          float* dst = p.part_o + (static_cast<int64_t>(split) * p.tokens * p.hq + ro) * p.d;
+          if (l != 0.f) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              if (q4 * 32 + i < p.d)
+                *reinterpret_cast<uint4*>(dst + q4 * 32 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        } else if (live) {
+          T* dst = reinterpret_cast<T*>(p.out) + token * p.ot + head * p.oh;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = narrow2<T>(p2(l == 0.f ? 0.f : __uint_as_float(o[i + 2 * e]) * inv,
+                                   l == 0.f ? 0.f : __uint_as_float(o[i + 2 * e + 1]) * inv));
+            if (q4 * 32 + i < p.d) st_words<4>(dst + q4 * 32 + i, w);
+          }
+        }
+        __syncwarp();  // the loads of tensor memory take the whole warp
+      }
+    }
+  }
+
+  if (!ok && lane == 0) flag_wait_timeout();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tc_dealloc(tmem);
+}
+
+// ---- host side
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor map encoder (looked up once; no link against libcuda).
+EncodeFn encoder() {
+  static const EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &st) != cudaSuccess ||
+        st != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// A cache as [pages][slots][heads][d] 16-bit elements, boxes of 64 elements of
+// one head in min(page, 128) slots.
+bool make_map(CUtensorMap* map, const void* base, bool bf16, const AttnParams& p, int64_t sp,
+              int64_t ss, int64_t sh) {
+  EncodeFn enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t page = cuuint64_t(1) << p.page_shift;
+  const cuuint64_t dims[4] = {cuuint64_t(p.d), cuuint64_t(p.hkv), page,
+                              cuuint64_t(p.num_pages > 0 ? p.num_pages : 1)};
+  // Dimensions of one element may have any stride: give those a valid one.
+  const cuuint64_t strides[3] = {p.hkv > 1 ? cuuint64_t(sh) * 2 : 16, page > 1 ? cuuint64_t(ss) * 2 : 16,
+                                 p.num_pages > 1 ? cuuint64_t(sp) * 2 : 16};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(page < 128 ? page : 128), 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+             const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, bool FP8, int DP>
+cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm,
+                   cudaStream_t st) {
+  using Shape = PrefillShape<FP8, DP>;
+  auto k = paged_prefill_kernel<T, FP8, DP>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = int64_t(p.row_tiles) * p.batches * p.splits * p.hkv;
+  return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(Shape::kThreads), Shape::kSmem, st, p,
+                    km, vm);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_prefill(const AttnParams& p, gbn_dtype dtype, gbn_dtype cache_dtype,
+                                 cudaStream_t stream) {
+  const bool fp8 = cache_dtype == GBN_E4M3, bf16 = dtype == GBN_BF16;
+  CUtensorMap km = {}, vm = {};
+  if (!fp8 && (!make_map(&km, p.k, bf16, p, p.kp, p.ks, p.kh) ||
+               !make_map(&vm, p.v, bf16, p, p.vp, p.vs, p.vh)))
+    return cudaErrorInvalidValue;
+  if (p.d <= 64) {
+    if (fp8)
+      return bf16 ? launch<__nv_bfloat16, true, 64>(p, km, vm, stream)
+                  : launch<__half, true, 64>(p, km, vm, stream);
+    return bf16 ? launch<__nv_bfloat16, false, 64>(p, km, vm, stream)
+                : launch<__half, false, 64>(p, km, vm, stream);
+  }
+  if (fp8)
+    return bf16 ? launch<__nv_bfloat16, true, 128>(p, km, vm, stream)
+                : launch<__half, true, 128>(p, km, vm, stream);
+  return bf16 ? launch<__nv_bfloat16, false, 128>(p, km, vm, stream)
+              : launch<__half, false, 128>(p, km, vm, stream);
+}
+
+cudaError_t read_prefill_error(unsigned int* v, bool clear) { return read_paged_error(v, clear); }
+
+}  // namespace gbn
