@@ -310,6 +310,28 @@ typedef enum { GBN_ROPE_HALF = 0, GBN_ROPE_INTERLEAVED = 1 } gbn_rope_layout;
 
 #define GBN_ROPE_MAX_DIM 1024 /* largest head_dim */
 
+/* The calls from here on take their arguments as a struct (host memory, read
+ * during the call): at thirty-odd of them it is what keeps the cost of a call
+ * from another language near that of the launch.  Strides are in elements. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* positions;
+  const double* inv_freq;
+  void* q_out;
+  void* k_out;
+  int64_t batches, seq, q_heads, k_heads, head_dim, rotary_dim;
+  int64_t q_strides[3]; /* batch, position, head */
+  int64_t k_strides[3];
+  int64_t q_out_strides[3];
+  int64_t k_out_strides[3];
+  int64_t position_stride;
+  int32_t position_bytes;
+  int32_t dtype;  /* gbn_dtype */
+  int32_t layout; /* gbn_rope_layout */
+  float mscale;
+} gbn_rope_args;
+
 /* Forward, q and k in one launch.
  *
  *   q, q_out   [batches, seq, q_heads, head_dim] dtype (F32, BF16, F16), the
@@ -327,29 +349,11 @@ typedef enum { GBN_ROPE_HALF = 0, GBN_ROPE_INTERLEAVED = 1 } gbn_rope_layout;
  * GBN_ERR_SHAPE: odd rotary_dim or one beyond head_dim, head_dim outside
  * [1, GBN_ROPE_MAX_DIM], over 4096 heads.  Sizes, strides or pointers that
  * allow no 16- or 8-byte vectors take a scalar path. */
-gbn_status gbn_rope_fwd(const void* q, const void* k, const void* positions,
-                        const double* inv_freq, void* q_out, void* k_out, int64_t batches,
-                        int64_t seq, int64_t q_heads, int64_t k_heads, int64_t head_dim,
-                        int64_t rotary_dim, int64_t q_stride_b, int64_t q_stride_s,
-                        int64_t q_stride_h, int64_t k_stride_b, int64_t k_stride_s,
-                        int64_t k_stride_h, int64_t q_out_stride_b, int64_t q_out_stride_s,
-                        int64_t q_out_stride_h, int64_t k_out_stride_b, int64_t k_out_stride_s,
-                        int64_t k_out_stride_h, int64_t position_stride, int position_bytes,
-                        gbn_dtype dtype, gbn_rope_layout layout, float mscale,
-                        cudaStream_t stream);
+gbn_status gbn_rope_fwd(const gbn_rope_args* args, cudaStream_t stream);
 
 /* Backward: the transpose (the angle negated, the same mscale) applied to the
- * output gradients dq, dk; arguments as in the forward. */
-gbn_status gbn_rope_bwd(const void* dq, const void* dk, const void* positions,
-                        const double* inv_freq, void* dq_out, void* dk_out, int64_t batches,
-                        int64_t seq, int64_t q_heads, int64_t k_heads, int64_t head_dim,
-                        int64_t rotary_dim, int64_t q_stride_b, int64_t q_stride_s,
-                        int64_t q_stride_h, int64_t k_stride_b, int64_t k_stride_s,
-                        int64_t k_stride_h, int64_t q_out_stride_b, int64_t q_out_stride_s,
-                        int64_t q_out_stride_h, int64_t k_out_stride_b, int64_t k_out_stride_s,
-                        int64_t k_out_stride_h, int64_t position_stride, int position_bytes,
-                        gbn_dtype dtype, gbn_rope_layout layout, float mscale,
-                        cudaStream_t stream);
+ * output gradients in q and k; arguments as in the forward. */
+gbn_status gbn_rope_bwd(const gbn_rope_args* args, cudaStream_t stream);
 
 /* ---- Paged key/value cache.
  *
@@ -387,21 +391,32 @@ gbn_status gbn_rope_bwd(const void* dq, const void* dk, const void* positions,
  *              before the saturating cast, as in delayed scaling.
  * The pages that receive tokens must be distinct within the call (two tokens
  * for one slot: either may stay). */
-gbn_status gbn_paged_append(const void* q, const void* k, const void* v, void* q_out,
-                            void* k_cache, void* v_cache, const double* inv_freq,
-                            const float* k_scale, const float* v_scale,
-                            const int32_t* cu_seqlens, const int32_t* kv_lens,
-                            const int32_t* block_table, int64_t tokens, int64_t batches,
-                            int64_t q_heads, int64_t kv_heads, int64_t head_dim,
-                            int64_t rotary_dim, int64_t num_pages, int64_t page_size,
-                            int64_t table_pages, int64_t table_stride, int64_t q_stride_t,
-                            int64_t q_stride_h, int64_t k_stride_t, int64_t k_stride_h,
-                            int64_t v_stride_t, int64_t v_stride_h, int64_t q_out_stride_t,
-                            int64_t q_out_stride_h, int64_t k_cache_stride_page,
-                            int64_t k_cache_stride_slot, int64_t k_cache_stride_head,
-                            int64_t v_cache_stride_page, int64_t v_cache_stride_slot,
-                            int64_t v_cache_stride_head, gbn_dtype dtype, gbn_dtype cache_dtype,
-                            gbn_rope_layout layout, float mscale, cudaStream_t stream);
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_cache;
+  void* v_cache;
+  const double* inv_freq;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* cu_seqlens;
+  const int32_t* kv_lens;
+  const int32_t* block_table;
+  int64_t tokens, batches, q_heads, kv_heads, head_dim, rotary_dim;
+  int64_t num_pages, page_size, table_pages, table_stride;
+  int64_t q_strides[2]; /* token, head */
+  int64_t k_strides[2];
+  int64_t v_strides[2];
+  int64_t q_out_strides[2];
+  int64_t k_cache_strides[3]; /* page, slot, head */
+  int64_t v_cache_strides[3];
+  int32_t dtype, cache_dtype; /* gbn_dtype */
+  int32_t layout;             /* gbn_rope_layout */
+  float mscale;
+} gbn_paged_append_args;
+gbn_status gbn_paged_append(const gbn_paged_append_args* args, cudaStream_t stream);
 
 /* Attention of the new tokens over the cache (which holds their own keys and
  * values already): for each token and query head, over the kept keys j,
@@ -436,21 +451,31 @@ gbn_status gbn_paged_attention_workspace_size(int64_t tokens, int64_t batches, i
                                               int64_t max_q, int64_t max_kv, int64_t window,
                                               int causal, gbn_dtype dtype, gbn_dtype cache_dtype,
                                               size_t* bytes);
-gbn_status gbn_paged_attention(const void* q, const void* k_cache, const void* v_cache,
-                               const int32_t* cu_seqlens, const int32_t* kv_lens,
-                               const int32_t* block_table, const float* k_scale_inv,
-                               const float* v_scale_inv, void* out, float* lse, void* workspace,
-                               size_t workspace_bytes, int64_t tokens, int64_t batches,
-                               int64_t q_heads, int64_t kv_heads, int64_t head_dim,
-                               int64_t num_pages, int64_t page_size, int64_t table_pages,
-                               int64_t table_stride, int64_t max_q, int64_t max_kv,
-                               int64_t q_stride_t, int64_t q_stride_h, int64_t out_stride_t,
-                               int64_t out_stride_h, int64_t k_cache_stride_page,
-                               int64_t k_cache_stride_slot, int64_t k_cache_stride_head,
-                               int64_t v_cache_stride_page, int64_t v_cache_stride_slot,
-                               int64_t v_cache_stride_head, gbn_dtype dtype,
-                               gbn_dtype cache_dtype, int causal, int64_t window, float scale,
-                               cudaStream_t stream);
+typedef struct {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* cu_seqlens;
+  const int32_t* kv_lens;
+  const int32_t* block_table;
+  const float* k_scale_inv;
+  const float* v_scale_inv;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t tokens, batches, q_heads, kv_heads, head_dim;
+  int64_t num_pages, page_size, table_pages, table_stride, max_q, max_kv;
+  int64_t q_strides[2]; /* token, head */
+  int64_t out_strides[2];
+  int64_t k_cache_strides[3]; /* page, slot, head */
+  int64_t v_cache_strides[3];
+  int64_t window;
+  int32_t dtype, cache_dtype; /* gbn_dtype */
+  int32_t causal;
+  float scale;
+} gbn_paged_attention_args;
+gbn_status gbn_paged_attention(const gbn_paged_attention_args* args, cudaStream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* gbn_status_string(gbn_status status);

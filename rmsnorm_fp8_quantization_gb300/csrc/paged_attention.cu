@@ -36,6 +36,9 @@
 namespace gbn {
 namespace {
 
+// What a caller in another language lays out by hand.
+static_assert(sizeof(gbn_paged_attention_args) == 12 * 8 + 22 * 8 + 4 * 4, "");
+
 constexpr int kStepThreads = 128;
 constexpr int kStepKeys = 64;          // keys per tile
 constexpr int kSplitPages = 1024;      // page entries a CTA holds
@@ -731,91 +734,84 @@ gbn_status gbn_paged_attention_workspace_size(int64_t tokens, int64_t batches, i
   return GBN_OK;
 }
 
-gbn_status gbn_paged_attention(const void* q, const void* k_cache, const void* v_cache,
-                               const int32_t* cu_seqlens, const int32_t* kv_lens,
-                               const int32_t* block_table, const float* k_scale_inv,
-                               const float* v_scale_inv, void* out, float* lse, void* workspace,
-                               size_t workspace_bytes, int64_t tokens, int64_t batches,
-                               int64_t q_heads, int64_t kv_heads, int64_t head_dim,
-                               int64_t num_pages, int64_t page_size, int64_t table_pages,
-                               int64_t table_stride, int64_t max_q, int64_t max_kv,
-                               int64_t q_stride_t, int64_t q_stride_h, int64_t out_stride_t,
-                               int64_t out_stride_h, int64_t k_cache_stride_page,
-                               int64_t k_cache_stride_slot, int64_t k_cache_stride_head,
-                               int64_t v_cache_stride_page, int64_t v_cache_stride_slot,
-                               int64_t v_cache_stride_head, gbn_dtype dtype,
-                               gbn_dtype cache_dtype, int causal, int64_t window, float scale,
-                               cudaStream_t stream) {
-  const AttnSizes z{tokens, batches, q_heads, kv_heads, head_dim,
-                    page_size, table_pages, max_q, max_kv, window};
+gbn_status gbn_paged_attention(const gbn_paged_attention_args* args, cudaStream_t stream) {
+  if (!args) return GBN_ERR_NULL;
+  const gbn_paged_attention_args& c = *args;
+  const gbn_dtype dtype = static_cast<gbn_dtype>(c.dtype);
+  const gbn_dtype cache_dtype = static_cast<gbn_dtype>(c.cache_dtype);
+  const AttnSizes z{c.tokens,    c.batches,     c.q_heads, c.kv_heads, c.head_dim,
+                    c.page_size, c.table_pages, c.max_q,   c.max_kv,   c.window};
   gbn_status st = check_sizes(z, dtype, cache_dtype);
   if (st != GBN_OK) return st;
-  if (num_pages < 0 || num_pages > INT32_MAX || table_stride < 0 || !(scale > 0.f) ||
-      scale > 3.0e38f)
+  if (c.num_pages < 0 || c.num_pages > INT32_MAX || c.table_stride < 0 || !(c.scale > 0.f) ||
+      c.scale > 3.0e38f)
     return GBN_ERR_SHAPE;
-  if (tokens == 0 || batches == 0 || max_q == 0) return GBN_OK;
-  if (!q || !k_cache || !v_cache || !cu_seqlens || !kv_lens || !block_table || !out)
+  if (c.tokens == 0 || c.batches == 0 || c.max_q == 0) return GBN_OK;
+  if (!c.q || !c.k_cache || !c.v_cache || !c.cu_seqlens || !c.kv_lens || !c.block_table || !c.out)
     return GBN_ERR_NULL;
   const bool fp8 = cache_dtype == GBN_E4M3;
-  if (fp8 && (!k_scale_inv || !v_scale_inv)) return GBN_ERR_NULL;
+  if (fp8 && (!c.k_scale_inv || !c.v_scale_inv)) return GBN_ERR_NULL;
   const int ce = fp8 ? 1 : 2;
   auto aligned = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; };
-  if (!aligned(q) || !aligned(out) || !aligned(k_cache) || !aligned(v_cache) ||
-      (tokens > 1 && (q_stride_t % 8 || out_stride_t % 8)) ||
-      (q_heads > 1 && (q_stride_h % 8 || out_stride_h % 8)) ||
-      (num_pages > 1 && (k_cache_stride_page * ce % 16 || v_cache_stride_page * ce % 16)) ||
-      (page_size > 1 && (k_cache_stride_slot * ce % 16 || v_cache_stride_slot * ce % 16)) ||
-      (kv_heads > 1 && (k_cache_stride_head * ce % 16 || v_cache_stride_head * ce % 16)))
+  auto off = [](int64_t extent, int64_t stride, int esize) {
+    return extent > 1 && stride * esize % 16 != 0;
+  };
+  if (!aligned(c.q) || !aligned(c.out) || !aligned(c.k_cache) || !aligned(c.v_cache) ||
+      off(c.tokens, c.q_strides[0], 2) || off(c.tokens, c.out_strides[0], 2) ||
+      off(c.q_heads, c.q_strides[1], 2) || off(c.q_heads, c.out_strides[1], 2) ||
+      off(c.num_pages, c.k_cache_strides[0], ce) || off(c.num_pages, c.v_cache_strides[0], ce) ||
+      off(c.page_size, c.k_cache_strides[1], ce) || off(c.page_size, c.v_cache_strides[1], ce) ||
+      off(c.kv_heads, c.k_cache_strides[2], ce) || off(c.kv_heads, c.v_cache_strides[2], ce))
     return GBN_ERR_ALIGNMENT;
   AttnPlan a;
-  st = plan_for(z, causal, &a);
+  st = plan_for(z, c.causal, &a);
   if (st != GBN_OK) return st;
   if (plan_bytes(z, a) > 0 &&
-      (!workspace || workspace_bytes < plan_bytes(z, a) || !aligned(workspace)))
+      (!c.workspace || c.workspace_bytes < plan_bytes(z, a) || !aligned(c.workspace)))
     return GBN_ERR_WORKSPACE;
 
   AttnParams p = {};
-  p.q = q;
-  p.k = k_cache;
-  p.v = v_cache;
-  p.out = out;
-  p.lse = lse;
-  p.cu = cu_seqlens;
-  p.kv_lens = kv_lens;
-  p.table = block_table;
-  p.k_scale_inv = k_scale_inv;
-  p.v_scale_inv = v_scale_inv;
-  p.part_ml = reinterpret_cast<float2*>(workspace);
-  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                      align256(tokens * q_heads * a.splits * 8));
-  p.qt = q_stride_t;
-  p.qh = q_stride_h;
-  p.ot = out_stride_t;
-  p.oh = out_stride_h;
-  p.kp = k_cache_stride_page;
-  p.ks = k_cache_stride_slot;
-  p.kh = k_cache_stride_head;
-  p.vp = v_cache_stride_page;
-  p.vs = v_cache_stride_slot;
-  p.vh = v_cache_stride_head;
-  p.table_stride = table_stride;
-  p.num_pages = num_pages;
-  p.tokens = static_cast<int>(tokens);
-  p.batches = static_cast<int>(batches);
-  p.hq = static_cast<int>(q_heads);
-  p.hkv = static_cast<int>(kv_heads);
+  p.q = c.q;
+  p.k = c.k_cache;
+  p.v = c.v_cache;
+  p.out = c.out;
+  p.lse = c.lse;
+  p.cu = c.cu_seqlens;
+  p.kv_lens = c.kv_lens;
+  p.table = c.block_table;
+  p.k_scale_inv = c.k_scale_inv;
+  p.v_scale_inv = c.v_scale_inv;
+  p.part_ml = reinterpret_cast<float2*>(c.workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(c.workspace) +
+                                      align256(c.tokens * c.q_heads * a.splits * 8));
+  p.qt = c.q_strides[0];
+  p.qh = c.q_strides[1];
+  p.ot = c.out_strides[0];
+  p.oh = c.out_strides[1];
+  p.kp = c.k_cache_strides[0];
+  p.ks = c.k_cache_strides[1];
+  p.kh = c.k_cache_strides[2];
+  p.vp = c.v_cache_strides[0];
+  p.vs = c.v_cache_strides[1];
+  p.vh = c.v_cache_strides[2];
+  p.table_stride = c.table_stride;
+  p.num_pages = c.num_pages;
+  p.tokens = static_cast<int>(c.tokens);
+  p.batches = static_cast<int>(c.batches);
+  p.hq = static_cast<int>(c.q_heads);
+  p.hkv = static_cast<int>(c.kv_heads);
   p.group = p.hq / p.hkv;
-  p.d = static_cast<int>(head_dim);
-  p.page_shift = log2_of(page_size);
-  p.table_pages = static_cast<int>(table_pages);
-  p.max_q = static_cast<int>(max_q < tokens ? max_q : tokens);
-  p.max_kv = static_cast<int>(max_kv);
-  p.causal = causal != 0;
-  p.window = static_cast<int>(window);
+  p.d = static_cast<int>(c.head_dim);
+  p.page_shift = log2_of(c.page_size);
+  p.table_pages = static_cast<int>(c.table_pages);
+  p.max_q = static_cast<int>(c.max_q < c.tokens ? c.max_q : c.tokens);
+  p.max_kv = static_cast<int>(c.max_kv);
+  p.causal = c.causal != 0;
+  p.window = static_cast<int>(c.window);
   p.row_tiles = a.row_tiles;
   p.splits = a.splits;
   p.split_len = a.split_len;
-  p.scale_log2 = scale * kAttnLog2e;
+  p.scale_log2 = c.scale * kAttnLog2e;
 
   const int mt = a.rows / 16;
   cudaError_t e;
@@ -829,7 +825,7 @@ gbn_status gbn_paged_attention(const void* q, const void* k_cache, const void* v
             : launch_step_d<__half, false>(p, mt, a.ctas, stream);
   if (e != cudaSuccess) return GBN_ERR_CUDA;
   if (a.splits > 1) {
-    const dim3 g(static_cast<unsigned>(tokens * q_heads)), t(kMergeThreads);
+    const dim3 g(static_cast<unsigned>(c.tokens * c.q_heads)), t(kMergeThreads);
     e = dtype == GBN_BF16 ? launch_pdl(paged_merge_kernel<__nv_bfloat16>, g, t, 0, stream, p, int(fp8))
                           : launch_pdl(paged_merge_kernel<__half>, g, t, 0, stream, p, int(fp8));
     if (e != cudaSuccess) return GBN_ERR_CUDA;

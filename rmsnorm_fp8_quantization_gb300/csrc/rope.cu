@@ -31,6 +31,10 @@
 namespace gbn {
 namespace {
 
+// What a caller in another language lays out by hand.
+static_assert(sizeof(gbn_rope_args) == 6 * 8 + 19 * 8 + 4 * 4, "");
+static_assert(sizeof(gbn_paged_append_args) == 12 * 8 + 24 * 8 + 4 * 4, "");
+
 constexpr int kRopeThreads = 256;
 constexpr int kRopeUnits = 4;                       // units per thread
 constexpr int kRopeItems = kRopeThreads * kRopeUnits;
@@ -459,15 +463,17 @@ gbn_status rope_launch(RopeParams& p, cudaStream_t stream) {
   return e == cudaSuccess ? GBN_OK : GBN_ERR_CUDA;
 }
 
-gbn_status rope_call(const void* q, const void* k, const void* positions, const double* inv_freq,
-                     void* q_out, void* k_out, int64_t batches, int64_t seq, int64_t q_heads,
-                     int64_t k_heads, int64_t head_dim, int64_t rotary_dim, Strided qs,
-                     Strided ks, Strided qo, Strided ko, int64_t position_stride,
-                     int position_bytes, gbn_dtype dtype, gbn_rope_layout layout, float mscale,
-                     float sign, cudaStream_t stream) {
+Strided strides3(const int64_t* s) { return {s[0], s[1], s[2]}; }
+Strided strides2(const int64_t* s) { return {0, s[0], s[1]}; }
+
+gbn_status rope_call(const gbn_rope_args* a, float sign, cudaStream_t stream) {
+  if (!a) return GBN_ERR_NULL;
+  const int dtype = a->dtype, layout = a->layout;
+  const int64_t batches = a->batches, seq = a->seq, q_heads = a->q_heads, k_heads = a->k_heads,
+                head_dim = a->head_dim, rotary_dim = a->rotary_dim;
   if (dtype != GBN_F32 && dtype != GBN_BF16 && dtype != GBN_F16) return GBN_ERR_DTYPE;
   if (layout != GBN_ROPE_HALF && layout != GBN_ROPE_INTERLEAVED) return GBN_ERR_ENUM;
-  if (position_bytes != 4 && position_bytes != 8) return GBN_ERR_DTYPE;
+  if (a->position_bytes != 4 && a->position_bytes != 8) return GBN_ERR_DTYPE;
   if (batches < 0 || seq < 0 || q_heads < 0 || k_heads < 0 || q_heads > 4096 || k_heads > 4096 ||
       head_dim < 1 || head_dim > GBN_ROPE_MAX_DIM || rotary_dim < 0 || rotary_dim > head_dim ||
       rotary_dim % 2)
@@ -476,27 +482,28 @@ gbn_status rope_call(const void* q, const void* k, const void* positions, const 
   RopeParams p = {};
   p.tokens = batches * seq;
   if (p.tokens == 0 || q_heads + k_heads == 0) return GBN_OK;
-  if ((q_heads && (!q || !q_out)) || (k_heads && (!k || !k_out)) || (rotary_dim && !inv_freq))
+  if ((q_heads && (!a->q || !a->q_out)) || (k_heads && (!a->k || !a->k_out)) ||
+      (rotary_dim && !a->inv_freq))
     return GBN_ERR_NULL;
-  p.q = q;
-  p.k = k;
-  p.q_out = q_out;
-  p.k_out = k_out;
-  p.qs = qs;
-  p.ks = ks;
-  p.qo = qo;
-  p.ko = ko;
-  p.inv_freq = inv_freq;
-  p.positions = positions;
-  p.pos_stride = position_stride;
-  p.pos_bytes = position_bytes;
+  p.q = a->q;
+  p.k = a->k;
+  p.q_out = a->q_out;
+  p.k_out = a->k_out;
+  p.qs = strides3(a->q_strides);
+  p.ks = strides3(a->k_strides);
+  p.qo = strides3(a->q_out_strides);
+  p.ko = strides3(a->k_out_strides);
+  p.inv_freq = rotary_dim ? a->inv_freq : nullptr;
+  p.positions = a->positions;
+  p.pos_stride = a->position_stride;
+  p.pos_bytes = a->position_bytes;
   p.seq = seq;
   p.hq = static_cast<int>(q_heads);
   p.hk = static_cast<int>(k_heads);
   p.d = static_cast<int>(head_dim);
   p.rot = static_cast<int>(rotary_dim);
   p.layout = layout;
-  p.mscale = mscale;
+  p.mscale = a->mscale;
   p.sign = sign;
   if (dtype == GBN_F32) return rope_launch<float, false, false>(p, stream);
   if (dtype == GBN_BF16) return rope_launch<__nv_bfloat16, false, false>(p, stream);
@@ -513,106 +520,68 @@ using namespace gbn;
 
 extern "C" {
 
-gbn_status gbn_rope_fwd(const void* q, const void* k, const void* positions,
-                        const double* inv_freq, void* q_out, void* k_out, int64_t batches,
-                        int64_t seq, int64_t q_heads, int64_t k_heads, int64_t head_dim,
-                        int64_t rotary_dim, int64_t q_stride_b, int64_t q_stride_s,
-                        int64_t q_stride_h, int64_t k_stride_b, int64_t k_stride_s,
-                        int64_t k_stride_h, int64_t q_out_stride_b, int64_t q_out_stride_s,
-                        int64_t q_out_stride_h, int64_t k_out_stride_b, int64_t k_out_stride_s,
-                        int64_t k_out_stride_h, int64_t position_stride, int position_bytes,
-                        gbn_dtype dtype, gbn_rope_layout layout, float mscale,
-                        cudaStream_t stream) {
-  return rope_call(q, k, positions, inv_freq, q_out, k_out, batches, seq, q_heads, k_heads,
-                   head_dim, rotary_dim, {q_stride_b, q_stride_s, q_stride_h},
-                   {k_stride_b, k_stride_s, k_stride_h},
-                   {q_out_stride_b, q_out_stride_s, q_out_stride_h},
-                   {k_out_stride_b, k_out_stride_s, k_out_stride_h}, position_stride,
-                   position_bytes, dtype, layout, mscale, 1.f, stream);
+gbn_status gbn_rope_fwd(const gbn_rope_args* args, cudaStream_t stream) {
+  return rope_call(args, 1.f, stream);
 }
 
-gbn_status gbn_rope_bwd(const void* dq, const void* dk, const void* positions,
-                        const double* inv_freq, void* dq_out, void* dk_out, int64_t batches,
-                        int64_t seq, int64_t q_heads, int64_t k_heads, int64_t head_dim,
-                        int64_t rotary_dim, int64_t q_stride_b, int64_t q_stride_s,
-                        int64_t q_stride_h, int64_t k_stride_b, int64_t k_stride_s,
-                        int64_t k_stride_h, int64_t q_out_stride_b, int64_t q_out_stride_s,
-                        int64_t q_out_stride_h, int64_t k_out_stride_b, int64_t k_out_stride_s,
-                        int64_t k_out_stride_h, int64_t position_stride, int position_bytes,
-                        gbn_dtype dtype, gbn_rope_layout layout, float mscale,
-                        cudaStream_t stream) {
-  return rope_call(dq, dk, positions, inv_freq, dq_out, dk_out, batches, seq, q_heads, k_heads,
-                   head_dim, rotary_dim, {q_stride_b, q_stride_s, q_stride_h},
-                   {k_stride_b, k_stride_s, k_stride_h},
-                   {q_out_stride_b, q_out_stride_s, q_out_stride_h},
-                   {k_out_stride_b, k_out_stride_s, k_out_stride_h}, position_stride,
-                   position_bytes, dtype, layout, mscale, -1.f, stream);
+gbn_status gbn_rope_bwd(const gbn_rope_args* args, cudaStream_t stream) {
+  return rope_call(args, -1.f, stream);
 }
 
-gbn_status gbn_paged_append(const void* q, const void* k, const void* v, void* q_out,
-                            void* k_cache, void* v_cache, const double* inv_freq,
-                            const float* k_scale, const float* v_scale,
-                            const int32_t* cu_seqlens, const int32_t* kv_lens,
-                            const int32_t* block_table, int64_t tokens, int64_t batches,
-                            int64_t q_heads, int64_t kv_heads, int64_t head_dim,
-                            int64_t rotary_dim, int64_t num_pages, int64_t page_size,
-                            int64_t table_pages, int64_t table_stride, int64_t q_stride_t,
-                            int64_t q_stride_h, int64_t k_stride_t, int64_t k_stride_h,
-                            int64_t v_stride_t, int64_t v_stride_h, int64_t q_out_stride_t,
-                            int64_t q_out_stride_h, int64_t k_cache_stride_page,
-                            int64_t k_cache_stride_slot, int64_t k_cache_stride_head,
-                            int64_t v_cache_stride_page, int64_t v_cache_stride_slot,
-                            int64_t v_cache_stride_head, gbn_dtype dtype, gbn_dtype cache_dtype,
-                            gbn_rope_layout layout, float mscale, cudaStream_t stream) {
+gbn_status gbn_paged_append(const gbn_paged_append_args* a, cudaStream_t stream) {
+  if (!a) return GBN_ERR_NULL;
+  const int dtype = a->dtype, cache_dtype = a->cache_dtype, layout = a->layout;
+  const int64_t page_size = a->page_size, rot = a->rotary_dim;
   if (dtype != GBN_BF16 && dtype != GBN_F16) return GBN_ERR_DTYPE;
   if (cache_dtype != dtype && cache_dtype != GBN_E4M3) return GBN_ERR_DTYPE;
   if (layout != GBN_ROPE_HALF && layout != GBN_ROPE_INTERLEAVED) return GBN_ERR_ENUM;
-  if (tokens < 0 || tokens > INT32_MAX || batches < 0 || batches > GBN_PAGED_MAX_BATCHES ||
-      q_heads < 0 || q_heads > 4096 || kv_heads < 1 || kv_heads > 4096 || head_dim < 1 ||
-      head_dim > GBN_ROPE_MAX_DIM || rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 2 ||
-      num_pages < 0 || num_pages > INT32_MAX || page_size < 1 ||
-      page_size > GBN_PAGED_MAX_PAGE || (page_size & (page_size - 1)) || table_pages < 0 ||
-      table_pages > INT32_MAX || table_stride < 0)
+  if (a->tokens < 0 || a->tokens > INT32_MAX || a->batches < 0 ||
+      a->batches > GBN_PAGED_MAX_BATCHES || a->q_heads < 0 || a->q_heads > 4096 ||
+      a->kv_heads < 1 || a->kv_heads > 4096 || a->head_dim < 1 ||
+      a->head_dim > GBN_ROPE_MAX_DIM || rot < 0 || rot > a->head_dim || rot % 2 ||
+      a->num_pages < 0 || a->num_pages > INT32_MAX || page_size < 1 ||
+      page_size > GBN_PAGED_MAX_PAGE || (page_size & (page_size - 1)) || a->table_pages < 0 ||
+      a->table_pages > INT32_MAX || a->table_stride < 0)
     return GBN_ERR_SHAPE;
-  if (tokens == 0 || batches == 0) return GBN_OK;
-  if (!k || !v || !k_cache || !v_cache || !cu_seqlens || !kv_lens || !block_table ||
-      (q_heads && (!q || !q_out)) || (rotary_dim && !inv_freq))
+  if (a->tokens == 0 || a->batches == 0) return GBN_OK;
+  if (!a->k || !a->v || !a->k_cache || !a->v_cache || !a->cu_seqlens || !a->kv_lens ||
+      !a->block_table || (a->q_heads && (!a->q || !a->q_out)) || (rot && !a->inv_freq))
     return GBN_ERR_NULL;
   const bool fp8 = cache_dtype == GBN_E4M3;
-  if (fp8 && (!k_scale || !v_scale)) return GBN_ERR_NULL;
+  if (fp8 && (!a->k_scale || !a->v_scale)) return GBN_ERR_NULL;
   RopeParams p = {};
-  p.tokens = tokens;
-  p.seq = tokens;
-  p.q = q;
-  p.k = k;
-  p.v = v;
-  p.q_out = q_out;
-  p.k_out = k_cache;
-  p.v_out = v_cache;
-  p.qs = {0, q_stride_t, q_stride_h};
-  p.ks = {0, k_stride_t, k_stride_h};
-  p.vs = {0, v_stride_t, v_stride_h};
-  p.qo = {0, q_out_stride_t, q_out_stride_h};
-  p.ko = {k_cache_stride_page, k_cache_stride_slot, k_cache_stride_head};
-  p.vo = {v_cache_stride_page, v_cache_stride_slot, v_cache_stride_head};
-  p.inv_freq = rotary_dim ? inv_freq : nullptr;
-  p.hq = static_cast<int>(q_heads);
-  p.hk = p.hv = static_cast<int>(kv_heads);
-  p.d = static_cast<int>(head_dim);
-  p.rot = static_cast<int>(rotary_dim);
+  p.tokens = a->tokens;
+  p.seq = a->tokens;
+  p.q = a->q;
+  p.k = a->k;
+  p.v = a->v;
+  p.q_out = a->q_out;
+  p.k_out = a->k_cache;
+  p.v_out = a->v_cache;
+  p.qs = strides2(a->q_strides);
+  p.ks = strides2(a->k_strides);
+  p.vs = strides2(a->v_strides);
+  p.qo = strides2(a->q_out_strides);
+  p.ko = strides3(a->k_cache_strides);
+  p.vo = strides3(a->v_cache_strides);
+  p.inv_freq = rot ? a->inv_freq : nullptr;
+  p.hq = static_cast<int>(a->q_heads);
+  p.hk = p.hv = static_cast<int>(a->kv_heads);
+  p.d = static_cast<int>(a->head_dim);
+  p.rot = static_cast<int>(rot);
   p.layout = layout;
-  p.mscale = mscale;
+  p.mscale = a->mscale;
   p.sign = 1.f;
-  p.cu = cu_seqlens;
-  p.kv_lens = kv_lens;
-  p.table = block_table;
-  p.table_stride = table_stride;
-  p.batches = static_cast<int>(batches);
-  p.table_pages = static_cast<int>(table_pages);
-  p.num_pages = num_pages;
+  p.cu = a->cu_seqlens;
+  p.kv_lens = a->kv_lens;
+  p.table = a->block_table;
+  p.table_stride = a->table_stride;
+  p.batches = static_cast<int>(a->batches);
+  p.table_pages = static_cast<int>(a->table_pages);
+  p.num_pages = a->num_pages;
   while ((int64_t(1) << p.page_shift) < page_size) ++p.page_shift;
-  p.k_scale = k_scale;
-  p.v_scale = v_scale;
+  p.k_scale = a->k_scale;
+  p.v_scale = a->v_scale;
   if (dtype == GBN_BF16)
     return fp8 ? rope_launch<__nv_bfloat16, true, true>(p, stream)
                : rope_launch<__nv_bfloat16, true, false>(p, stream);

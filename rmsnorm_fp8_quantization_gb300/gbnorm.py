@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -73,15 +74,11 @@ def _load():
     lib.gbn_softmax_fwd.restype = I
     lib.gbn_softmax_bwd.argtypes = [P, P, P, I64, I64, I, F, P]
     lib.gbn_softmax_bwd.restype = I
-    for f in (lib.gbn_rope_fwd, lib.gbn_rope_bwd):
-        f.argtypes = [P] * 6 + [I64] * 19 + [I, I, I, F, P]
+    for f in (lib.gbn_rope_fwd, lib.gbn_rope_bwd, lib.gbn_paged_append, lib.gbn_paged_attention):
+        f.argtypes = [P, P]  # the argument struct (packed bytes), the stream
         f.restype = I
-    lib.gbn_paged_append.argtypes = [P] * 12 + [I64] * 24 + [I, I, I, F, P]
-    lib.gbn_paged_append.restype = I
     lib.gbn_paged_attention_workspace_size.argtypes = [I64] * 10 + [I, I, I, ctypes.POINTER(SZ)]
     lib.gbn_paged_attention_workspace_size.restype = I
-    lib.gbn_paged_attention.argtypes = [P] * 11 + [SZ] + [I64] * 21 + [I, I, I, I64, F, P]
-    lib.gbn_paged_attention.restype = I
     lib.gbn_selftest_copy_timeout.argtypes = [ctypes.c_uint, P]
     lib.gbn_selftest_copy_timeout.restype = I
     lib.gbn_status_string.argtypes = [I]
@@ -198,25 +195,39 @@ def gbn_softmax_bwd(dy, y, dx, rows, sk, dtype, scale, stream=None) -> int:
                                 _stream(stream))
 
 
+# The argument structs of include/gbnorm.h, as packed bytes (native layout:
+# pointers, 64-bit sizes and strides, then 32-bit fields; no padding).
+_rope_args = struct.Struct("=6Q19q3if").pack
+_append_args = struct.Struct("=12Q24q3if").pack
+_attention_args = struct.Struct("=12Q22q3if").pack
+
+
+def _addr(t):
+    """Address of a tensor, an address itself, or 0 for None."""
+    if t is None:
+        return 0
+    return t if isinstance(t, int) else t.data_ptr()
+
+
 def gbn_rope_fwd(q, k, positions, inv_freq, q_out, k_out, batches, seq, q_heads, k_heads, head_dim,
                  rotary_dim, q_strides, k_strides, q_out_strides, k_out_strides, position_stride,
                  position_bytes, dtype, layout, mscale, stream=None) -> int:
-    """Strides: (batch, seq, head) triples in elements (one argument each in C)."""
-    return _lib.gbn_rope_fwd(_ptr(q), _ptr(k), _ptr(positions), _ptr(inv_freq), _ptr(q_out),
-                             _ptr(k_out), batches, seq, q_heads, k_heads, head_dim, rotary_dim,
-                             *q_strides, *k_strides, *q_out_strides, *k_out_strides,
-                             position_stride, position_bytes, dtype, layout, mscale,
-                             _stream(stream))
+    """Strides: (batch, position, head) triples in elements."""
+    return _lib.gbn_rope_fwd(
+        _rope_args(_addr(q), _addr(k), _addr(positions), _addr(inv_freq), _addr(q_out),
+                   _addr(k_out), batches, seq, q_heads, k_heads, head_dim, rotary_dim, *q_strides,
+                   *k_strides, *q_out_strides, *k_out_strides, position_stride, position_bytes,
+                   dtype, layout, mscale), _stream(stream))
 
 
 def gbn_rope_bwd(dq, dk, positions, inv_freq, dq_out, dk_out, batches, seq, q_heads, k_heads,
                  head_dim, rotary_dim, q_strides, k_strides, q_out_strides, k_out_strides,
                  position_stride, position_bytes, dtype, layout, mscale, stream=None) -> int:
-    return _lib.gbn_rope_bwd(_ptr(dq), _ptr(dk), _ptr(positions), _ptr(inv_freq), _ptr(dq_out),
-                             _ptr(dk_out), batches, seq, q_heads, k_heads, head_dim, rotary_dim,
-                             *q_strides, *k_strides, *q_out_strides, *k_out_strides,
-                             position_stride, position_bytes, dtype, layout, mscale,
-                             _stream(stream))
+    return _lib.gbn_rope_bwd(
+        _rope_args(_addr(dq), _addr(dk), _addr(positions), _addr(inv_freq), _addr(dq_out),
+                   _addr(dk_out), batches, seq, q_heads, k_heads, head_dim, rotary_dim, *q_strides,
+                   *k_strides, *q_out_strides, *k_out_strides, position_stride, position_bytes,
+                   dtype, layout, mscale), _stream(stream))
 
 
 def gbn_paged_append(q, k, v, q_out, k_cache, v_cache, inv_freq, k_scale, v_scale, cu_seqlens,
@@ -225,13 +236,13 @@ def gbn_paged_append(q, k, v, q_out, k_cache, v_cache, inv_freq, k_scale, v_scal
                      k_strides, v_strides, q_out_strides, k_cache_strides, v_cache_strides, dtype,
                      cache_dtype, layout, mscale, stream=None) -> int:
     """Strides in elements: (token, head) pairs, and (page, slot, head) triples of the caches."""
-    return _lib.gbn_paged_append(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_cache),
-                                 _ptr(v_cache), _ptr(inv_freq), _ptr(k_scale), _ptr(v_scale),
-                                 _ptr(cu_seqlens), _ptr(kv_lens), _ptr(block_table), tokens,
-                                 batches, q_heads, kv_heads, head_dim, rotary_dim, num_pages,
-                                 page_size, table_pages, table_stride, *q_strides, *k_strides,
-                                 *v_strides, *q_out_strides, *k_cache_strides, *v_cache_strides,
-                                 dtype, cache_dtype, layout, mscale, _stream(stream))
+    return _lib.gbn_paged_append(
+        _append_args(_addr(q), _addr(k), _addr(v), _addr(q_out), _addr(k_cache), _addr(v_cache),
+                     _addr(inv_freq), _addr(k_scale), _addr(v_scale), _addr(cu_seqlens),
+                     _addr(kv_lens), _addr(block_table), tokens, batches, q_heads, kv_heads,
+                     head_dim, rotary_dim, num_pages, page_size, table_pages, table_stride,
+                     *q_strides, *k_strides, *v_strides, *q_out_strides, *k_cache_strides,
+                     *v_cache_strides, dtype, cache_dtype, layout, mscale), _stream(stream))
 
 
 def gbn_paged_attention_workspace_size(tokens, batches, q_heads, kv_heads, head_dim, page_size,
@@ -253,14 +264,14 @@ def gbn_paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, k
                         v_cache_strides, dtype, cache_dtype, causal, window, scale,
                         stream=None) -> int:
     """Strides in elements: (token, head) pairs, and (page, slot, head) triples of the caches."""
-    return _lib.gbn_paged_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens),
-                                    _ptr(kv_lens), _ptr(block_table), _ptr(k_scale_inv),
-                                    _ptr(v_scale_inv), _ptr(out), _ptr(lse), _ptr(workspace),
-                                    workspace_bytes, tokens, batches, q_heads, kv_heads, head_dim,
-                                    num_pages, page_size, table_pages, table_stride, max_q,
-                                    max_kv, *q_strides, *out_strides, *k_cache_strides,
-                                    *v_cache_strides, dtype, cache_dtype, int(bool(causal)),
-                                    window, scale, _stream(stream))
+    return _lib.gbn_paged_attention(
+        _attention_args(_addr(q), _addr(k_cache), _addr(v_cache), _addr(cu_seqlens),
+                        _addr(kv_lens), _addr(block_table), _addr(k_scale_inv),
+                        _addr(v_scale_inv), _addr(out), _addr(lse), _addr(workspace),
+                        workspace_bytes, tokens, batches, q_heads, kv_heads, head_dim, num_pages,
+                        page_size, table_pages, table_stride, max_q, max_kv, *q_strides,
+                        *out_strides, *k_cache_strides, *v_cache_strides, window, dtype,
+                        cache_dtype, 1 if causal else 0, scale), _stream(stream))
 
 
 def gbn_selftest_copy_timeout(timeout_us, stream=None) -> int:

@@ -7,6 +7,7 @@ allocate device memory and marshal arguments.
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -162,31 +163,25 @@ def softmax_bwd(dy, y, scale=1.0, out=None, stream=None):
 
 _ROPE_LAYOUT = {"half": G.GBN_ROPE_HALF, "interleaved": G.GBN_ROPE_INTERLEAVED}
 _NO_STRIDES = (0, 0, 0)
+_INT_DTYPES = (torch.int32, torch.int64)
 
 
-class _on:
-    """Makes the tensor's device current for the call (the launch and the
-    current stream go by it); nothing to do when it already is."""
+def _call(dev, fn, *args):
+    """fn(*args) with ``dev`` the current device (the launch and the current
+    stream go by it)."""
+    if dev.index == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
-    __slots__ = ("dev", "guard")
 
-    def __init__(self, t):
-        if t.device.type != "cuda":
-            raise ValueError(f"expected CUDA tensors, got one on {t.device}")
-        self.dev, self.guard = t.device, None
-
-    def __enter__(self):
-        if self.dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _on_gpu(t):
+    if t.device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got one on {t.device}")
 
 
 def _same(name, t, dtype, device, dims=None):
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
@@ -245,59 +240,77 @@ def rope_mscale(factor):
     return 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
 
 
-def _rope(call, where, q, k, inv_freq, positions, layout, mscale, q_out, k_out, stream):
+def _rope_tensor(name, t, o, x):
+    """Checks q or k against x (whichever of them is given first), and its output."""
+    if t.dim() != 4:
+        raise ValueError(f"{name}: expected [batch, seq, heads, head_dim], got {tuple(t.shape)}")
+    _same(name, t, x.dtype, x.device)
+    if t.shape[:2] != x.shape[:2] or t.shape[3] != x.shape[3]:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} does not go with {tuple(x.shape)}")
+    _inner(name, t)
+    if o is not None:
+        _same(name + "_out", o, x.dtype, x.device)
+        if o.shape != t.shape:
+            raise ValueError(f"{name}_out: shape {tuple(o.shape)}, expected {tuple(t.shape)}")
+        _inner(name + "_out", o)
+
+
+def _check_rope(q, k, inv_freq, positions, q_out, k_out):
     if q is None and k is None:
         raise ValueError("q and k are both None")
     x = q if q is not None else k
-    if x.dim() != 4:
-        raise ValueError(f"expected [batch, seq, heads, head_dim], got {tuple(x.shape)}")
-    b, s, _, d = x.shape
-    dev = x.device
-    _same("inv_freq", inv_freq, torch.float64, dev, 1)
+    for name, t, o in (("q", q, q_out), ("k", k, k_out)):
+        if t is not None:
+            _rope_tensor(name, t, o, x)
+    if x.dtype not in G.TORCH_DTYPE:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    _same("inv_freq", inv_freq, torch.float64, x.device, 1)
     if not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be contiguous")
-    ptrs, heads, strides = [], [], []
-    for name, t, o in (("q", q, q_out), ("k", k, k_out)):
-        if t is None:
-            ptrs.append((None, None))
-            heads.append(0)
-            strides.append((_NO_STRIDES, _NO_STRIDES))
-            continue
-        _same(name, t, x.dtype, dev, 4)
-        if t.shape[0] != b or t.shape[1] != s or t.shape[3] != d:
-            raise ValueError(f"{name}: shape {tuple(t.shape)} does not go with {tuple(x.shape)}")
-        _inner(name, t)
-        if o is None:
-            o = torch.empty(t.shape, dtype=t.dtype, device=dev)
-        else:
-            _same(name + "_out", o, x.dtype, dev)
-            if o.shape != t.shape:
-                raise ValueError(f"{name}_out: shape {tuple(o.shape)}, expected {tuple(t.shape)}")
-            _inner(name + "_out", o)
-        ptrs.append((t, o))
-        heads.append(t.shape[2])
-        strides.append((t.stride()[:3], o.stride()[:3]))
-    pos_stride, pos_bytes = 0, 8
     if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64) or positions.device != dev:
+        b, s = x.shape[:2]
+        if positions.dtype not in _INT_DTYPES or positions.device != x.device:
             raise ValueError("positions: int32 or int64 on the tensors' device")
         if positions.shape not in ((s,), (1, s), (b, s)):
             raise ValueError(f"positions: shape {tuple(positions.shape)}, expected "
                              f"({s},), (1, {s}) or ({b}, {s})")
-        if positions.stride(-1) != 1 and s > 1:
+        if s > 1 and positions.stride(-1) != 1:
             raise ValueError("positions must be contiguous along the sequence")
-        pos_bytes = positions.element_size()
+    _on_gpu(x)
+
+
+def _rope(call, where, q, k, inv_freq, positions, layout, mscale, q_out, k_out, stream):
+    # The usual call in one expression; anything else goes through the checks one by one.
+    if not (q is not None and k is not None and q_out is None and k_out is None
+            and positions is not None and q.is_contiguous() and k.is_contiguous()
+            and positions.is_contiguous() and q.dim() == 4 and q.shape[:2] == positions.shape
+            and k.shape[:2] == positions.shape and q.shape[3] == k.shape[3]
+            and q.dtype is k.dtype and q.dtype in G.TORCH_DTYPE and positions.dtype in _INT_DTYPES
+            and inv_freq.dtype is torch.float64 and inv_freq.dim() == 1
+            and inv_freq.is_contiguous() and q.is_cuda and q.get_device() == k.get_device()
+            == positions.get_device() == inv_freq.get_device()):
+        _check_rope(q, k, inv_freq, positions, q_out, k_out)
+    b, s, _, d = (k if q is None else q).shape
+    hq = hk = 0
+    qs = ks = qo = ko = _NO_STRIDES
+    if q is not None:
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        hq, qs, qo = q.shape[2], q.stride()[:3], q_out.stride()[:3]
+    if k is not None:
+        k_out = torch.empty_like(k) if k_out is None else k_out
+        hk, ks, ko = k.shape[2], k.stride()[:3], k_out.stride()[:3]
+    pos_stride, pos_bytes = 0, 8
+    if positions is not None:
+        pos_bytes = positions.itemsize
         if positions.dim() == 2 and positions.shape[0] > 1:
             pos_stride = positions.stride(0)
-    if x.dtype not in G.TORCH_DTYPE:
-        raise ValueError(f"unsupported dtype {x.dtype}")
-    with _on(x):
-        st = call(ptrs[0][0], ptrs[1][0], positions, inv_freq, ptrs[0][1], ptrs[1][1], b, s,
-                  heads[0], heads[1], d, 2 * inv_freq.shape[0], strides[0][0], strides[1][0],
-                  strides[0][1], strides[1][1], pos_stride, pos_bytes, G.TORCH_DTYPE[x.dtype],
-                  _ROPE_LAYOUT[layout], mscale, stream)
-    _check(st, where)
-    return ptrs[0][1], ptrs[1][1]
+    x = k if q is None else q
+    st = _call(x.device, call, q, k, positions, inv_freq, q_out, k_out, b, s, hq, hk, d,
+               2 * inv_freq.shape[0], qs, ks, qo, ko, pos_stride, pos_bytes,
+               G.TORCH_DTYPE[x.dtype], _ROPE_LAYOUT[layout], mscale, stream)
+    if st:
+        _check(st, where)
+    return q_out, k_out
 
 
 def rope_fwd(q, k, inv_freq, positions=None, *, layout="half", mscale=1.0, q_out=None, k_out=None,
@@ -333,14 +346,14 @@ def _cache_dtype(k_cache, v_cache, dtype):
     return G.TORCH_DTYPE[c]
 
 
-def _paged_args(x, k_cache, v_cache, cu_seqlens, kv_lens, block_table):
-    """Checks what both paged calls share; (cache dtype, kv heads, head_dim)."""
+def _check_paged(x, k_cache, v_cache, cu_seqlens, kv_lens, block_table):
+    """What both paged calls need of their tensors, one by one."""
     dev = x.device
     if x.dim() != 3:
         raise ValueError(f"expected [tokens, heads, head_dim], got {tuple(x.shape)}")
     if x.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"unsupported dtype {x.dtype}: bfloat16 or float16")
-    cdt = _cache_dtype(k_cache, v_cache, x.dtype)
+    _cache_dtype(k_cache, v_cache, x.dtype)
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
         raise ValueError("caches: [pages, page_size, kv_heads, head_dim], the same for both; got "
                          f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
@@ -360,6 +373,25 @@ def _paged_args(x, k_cache, v_cache, cu_seqlens, kv_lens, block_table):
     if not (cu_seqlens.is_contiguous() and kv_lens.is_contiguous()):
         raise ValueError("cu_seqlens and kv_lens must be contiguous")
     _inner("block_table", block_table)
+
+
+def _paged_args(x, k_cache, v_cache, cu_seqlens, kv_lens, block_table):
+    """Checks what both paged calls share; (cache dtype, kv heads, head_dim)."""
+    dt, i32 = x.dtype, torch.int32
+    # The usual call in one expression; anything else goes through the checks one by one.
+    if not (x.dim() == 3 and (dt is torch.bfloat16 or dt is torch.float16)
+            and k_cache.dtype is v_cache.dtype and k_cache.dim() == 4
+            and k_cache.shape == v_cache.shape and k_cache.shape[3] == x.shape[2]
+            and k_cache.stride(3) == 1 == v_cache.stride(3)
+            and cu_seqlens.dtype is i32 and kv_lens.dtype is i32 and block_table.dtype is i32
+            and cu_seqlens.is_contiguous() and kv_lens.is_contiguous()
+            and block_table.is_contiguous() and cu_seqlens.dim() == 1 == kv_lens.dim()
+            and block_table.dim() == 2 and cu_seqlens.shape[0] - 1 == kv_lens.shape[0]
+            == block_table.shape[0]
+            and x.get_device() == k_cache.get_device() == v_cache.get_device()
+            == cu_seqlens.get_device() == kv_lens.get_device() == block_table.get_device()):
+        _check_paged(x, k_cache, v_cache, cu_seqlens, kv_lens, block_table)
+    cdt = G.TORCH_DTYPE[dt] if k_cache.dtype is dt else _cache_dtype(k_cache, v_cache, dt)
     return cdt, k_cache.shape[2], k_cache.shape[3]
 
 
@@ -395,7 +427,7 @@ def paged_append(k, v, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, q=
             raise ValueError(f"q: shape {tuple(q.shape)} does not go with k {tuple(k.shape)}")
         _inner("q", q)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = torch.empty_like(q)
         else:
             _same("q_out", q_out, k.dtype, dev, 3)
             if q_out.shape != q.shape:
@@ -415,15 +447,25 @@ def paged_append(k, v, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, q=
             raise ValueError("E4M3 caches need k_scale and v_scale")
         _scalar("k_scale", k_scale, dev)
         _scalar("v_scale", v_scale, dev)
-    with _on(k):
-        st = G.gbn_paged_append(q, k, v, q_out, k_cache, v_cache, inv_freq, k_scale, v_scale,
-                                cu_seqlens, kv_lens, block_table, k.shape[0], kv_lens.shape[0],
-                                hq, hk, d, rot, k_cache.shape[0], k_cache.shape[1],
-                                block_table.shape[1], block_table.stride(0), qs, k.stride()[:2],
-                                v.stride()[:2], qo, k_cache.stride()[:3], v_cache.stride()[:3],
-                                G.TORCH_DTYPE[k.dtype], cdt, _ROPE_LAYOUT[layout], mscale, stream)
-    _check(st, "gbn_paged_append")
+    _on_gpu(k)
+    st = _call(dev, G.gbn_paged_append, q, k, v, q_out, k_cache, v_cache, inv_freq, k_scale,
+               v_scale, cu_seqlens, kv_lens, block_table, k.shape[0], kv_lens.shape[0], hq, hk, d,
+               rot, k_cache.shape[0], k_cache.shape[1], block_table.shape[1],
+               block_table.stride(0), qs, k.stride()[:2], v.stride()[:2], qo,
+               k_cache.stride()[:3], v_cache.stride()[:3], G.TORCH_DTYPE[k.dtype], cdt,
+               _ROPE_LAYOUT[layout], mscale, stream)
+    if st:
+        _check(st, "gbn_paged_append")
     return q_out
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_bytes(device_index, *sizes):
+    """Workspace bytes of an attention call, by its sizes (and the device's)."""
+    with torch.cuda.device(device_index):
+        st, n = G.gbn_paged_attention_workspace_size(*sizes)
+    _check(st, "gbn_paged_attention_workspace_size")
+    return n
 
 
 def paged_attention_workspace(q, k_cache, block_table, *, max_q, max_kv=None, causal=True,
@@ -431,13 +473,11 @@ def paged_attention_workspace(q, k_cache, block_table, *, max_q, max_kv=None, ca
     """A workspace for ``paged_attention`` calls of these sizes (None: they need none)."""
     cdt = _cache_dtype(k_cache, k_cache, q.dtype)
     mkv = block_table.shape[1] * k_cache.shape[1] if max_kv is None else max_kv
-    with _on(q):
-        st, n = G.gbn_paged_attention_workspace_size(
-            q.shape[0], block_table.shape[0], q.shape[1], k_cache.shape[2], q.shape[2],
-            k_cache.shape[1], block_table.shape[1], max_q, mkv, window, causal,
-            G.TORCH_DTYPE[q.dtype], cdt)
-        _check(st, "gbn_paged_attention_workspace_size")
-        return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    _on_gpu(q)
+    n = _attention_bytes(q.get_device(), q.shape[0], block_table.shape[0], q.shape[1],
+                         k_cache.shape[2], q.shape[2], k_cache.shape[1], block_table.shape[1],
+                         max_q, mkv, window, bool(causal), G.TORCH_DTYPE[q.dtype], cdt)
+    return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
 
 
 def paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, max_q, max_kv=None,
@@ -455,7 +495,7 @@ def paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, ma
     dev, t, hq = q.device, q.shape[0], q.shape[1]
     _inner("q", q)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = torch.empty_like(q)
     else:
         _same("out", out, q.dtype, dev, 3)
         if out.shape != q.shape:
@@ -476,19 +516,20 @@ def paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, ma
     mkv = pages * page if max_kv is None else max_kv
     dt = G.TORCH_DTYPE[q.dtype]
     n = kv_lens.shape[0]
-    with _on(q):
-        if workspace is None:
-            st, need = G.gbn_paged_attention_workspace_size(t, n, hq, hk, d, page, pages, max_q,
-                                                            mkv, window, causal, dt, cdt)
-            _check(st, "gbn_paged_attention_workspace_size")
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        st = G.gbn_paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table,
-                                   k_scale_inv, v_scale_inv, out, lse, workspace,
-                                   workspace.numel() if workspace is not None else 0, t, n, hq,
-                                   hk, d, k_cache.shape[0], page, pages, block_table.stride(0),
-                                   max_q, mkv, q.stride()[:2], out.stride()[:2],
-                                   k_cache.stride()[:3], v_cache.stride()[:3], dt, cdt, causal,
-                                   window, d ** -0.5 if scale is None else scale, stream)
-    _check(st, "gbn_paged_attention")
+    _on_gpu(q)
+    size = 0
+    if workspace is not None:
+        size = workspace.numel()
+    else:
+        size = _attention_bytes(q.get_device(), t, n, hq, hk, d, page, pages, max_q, mkv, window,
+                                bool(causal), dt, cdt)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    st = _call(dev, G.gbn_paged_attention, q, k_cache, v_cache, cu_seqlens, kv_lens, block_table,
+               k_scale_inv, v_scale_inv, out, lse, workspace, size, t, n, hq, hk, d,
+               k_cache.shape[0], page, pages, block_table.stride(0), max_q, mkv, q.stride()[:2],
+               out.stride()[:2], k_cache.stride()[:3], v_cache.stride()[:3], dt, cdt, causal,
+               window, d ** -0.5 if scale is None else scale, stream)
+    if st:
+        _check(st, "gbn_paged_attention")
     return (out, lse) if return_lse else out
