@@ -66,7 +66,7 @@ struct PrefillShape {
 };
 
 struct Barriers {
-  uint64_t full[8], empty[8], s_full[2], p_full[2], o_full[2], q_full;
+  uint64_t full[8], empty[8], s_full[2], p_full[2][2], o_full[2], q_full;
   uint32_t tmem;
 };
 
@@ -94,22 +94,26 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
                    smem_u32(bar))
                : "memory");
 }
-// D[tmem] (+)= A[smem] B[smem]
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                          uint32_t acc) {
+// D[tmem] (+)= A[smem] B[smem].  Descriptors as (low, high) words: the high one
+// is a constant and the low one the address, so a step costs one addition --
+// the issuing thread has to stay ahead of the tensor core (64 cycles a step).
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                          uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                          uint32_t acc) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                          uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 // 32 columns of this warp's 32 lanes.
@@ -165,11 +169,11 @@ __device__ __forceinline__ void fence_async_smem() {
 }
 
 // Shared-memory operand descriptor, 128-byte swizzle, 8-row groups 1024 bytes
-// apart; `panel` the distance of the next 64 elements (MN-major only).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t panel) {
-  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) |
-         (static_cast<uint64_t>(panel >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
+// apart (high word); low word: the address and, MN-major only, the distance
+// `panel` of the next 64 elements.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t panel) {
+  return ((addr & 0x3FFFFu) >> 4) | ((panel >> 4) << 16);
 }
 // Instruction descriptor: fp32 accumulator, A and B f16 (0) or bf16 (1), M x N;
 // bmn: B is MN-major.
@@ -186,6 +190,13 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
       : "memory");
+}
+
+// Three-input maximum (a number wins over NaN, as fmaxf).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
@@ -271,7 +282,8 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars.s_full[t], 1);
-      mbar_init(&bars.p_full[t], 128);
+      mbar_init(&bars.p_full[t][0], 128);
+      mbar_init(&bars.p_full[t][1], 128);
       mbar_init(&bars.o_full[t], 1);
     }
     mbar_init(&bars.q_full, 256);
@@ -296,13 +308,18 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
       // ------------------------------------------------ tensor core issue
       constexpr uint32_t kIdQK = instr_desc(kTypeQ, kRowsT, kKeys, 0);
       constexpr uint32_t kIdPV = instr_desc(kTypeP, kRowsT, DP, 1);
+      // Uniform across the warp, and known to be.
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      const uint32_t q_lo = __shfl_sync(0xFFFFFFFFu, desc_lo(qs, 16), 0);
+      const uint32_t k_lo = __shfl_sync(0xFFFFFFFFu, desc_lo(ring, 16), 0);
+      const uint32_t v_lo = __shfl_sync(0xFFFFFFFFu, desc_lo(ring, kPanel), 0);
       auto qk = [&](int t, int slot) {
         if (lane == 0) {
+          const uint32_t a = q_lo + t * (Shape::kSlot >> 4), b = k_lo + slot * (Shape::kSlot >> 4);
 #pragma unroll
           for (int kk = 0; kk < DP / 16; ++kk) {
-            const uint32_t at = (kk / 4) * kPanel + (kk % 4) * 32;
-            tc_mma_ss(tmem + t * 128, smem_desc(qs + t * Shape::kSlot + at, 16),
-                      smem_desc(ring + slot * Shape::kSlot + at, 16), kIdQK, kk > 0);
+            const uint32_t at = ((kk / 4) * kPanel + (kk % 4) * 32) >> 4;
+            tc_mma_ss(tm + t * 128, a + at, b + at, kDescHi, kIdQK, kk > 0);
           }
           tc_commit(&bars.s_full[t]);
         }
@@ -312,6 +329,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
         ok = warp_wait(&bars.q_full, 0) && warp_wait(&bars.full[0], 0);
         if (ok) {
           tc_fence_after();
+#pragma unroll
           for (int t = 0; t < 2; ++t)
             if (nt[t] > 0) qk(t, 0);
           if (lane == 0) tc_commit(&bars.empty[0]);
@@ -348,26 +366,34 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
           if (!ok) break;
           ++it;
         }
+        const int last_t = j < nt[1] ? 1 : 0;  // the last row tile that uses this key tile
+#pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (j >= nt[t]) continue;
-          ok = warp_wait(&bars.p_full[t], j & 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
+          // P arrives in halves of 64 keys: the first half's product runs while
+          // the softmax still computes the second.
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
-                        smem_desc(ring + vs * Shape::kSlot + kk * 2048, kPanel), kIdPV,
-                        j > 0 || kk > 0);
+          for (int hf = 0; hf < 2; ++hf) {
+            ok = ok && warp_wait(&bars.p_full[t][hf], j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int kk = hf * 4; kk < hf * 4 + 4; ++kk)
+                tc_mma_ts(tm + 256 + t * 128, tm + t * 128 + kk * 8,
+                          v_lo + vs * (Shape::kSlot >> 4) + kk * (2048 >> 4), kDescHi, kIdPV,
+                          kk > 0 ? 1u : static_cast<uint32_t>(j > 0));
+            }
+          }
+          if (!ok) break;
+          if (lane == 0) {
             tc_commit(&bars.o_full[t]);
+            if (t == last_t) tc_commit(&bars.empty[vs]);
           }
           if (j + 1 < nt[t]) qk(t, ks);
         }
         if (!ok) break;
-        if (lane == 0) {
-          tc_commit(&bars.empty[vs]);
-          if (ks >= 0) tc_commit(&bars.empty[ks]);
-        }
+        if (lane == 0 && ks >= 0) tc_commit(&bars.empty[ks]);
         __syncwarp();
       }
       // The last of this warp's arrivals has landed before the CTA ends.
@@ -383,22 +409,27 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
         const int boxes = kKeys / box;              // per panel, at most 16
         const int32_t* tab = p.table + b * p.table_stride;
         const int e_last = k1 > 0 ? (k1 - 1) >> p.page_shift : 0;
-        // Page of this lane's box of key tile j; one past the map's pages: zeros.
-        const int zero_page = max(1, static_cast<int>(p.num_pages));
-        auto page_of = [&](int j) {
+        // This lane's box of key tile j: its table entry, read one tile ahead
+        // and looked at only when the tile's turn comes.
+        const int zero_page = max(1, static_cast<int>(p.num_pages));  // one past: zeros
+        auto wanted = [&](int j) {
           const int key = base + j * kKeys + lane * box;
-          int pg = zero_page;
-          if (lane < boxes && key < k1 && key + box > k0) {
-            const int v = tab[min(key >> p.page_shift, e_last)];
-            if (v >= 0 && v < p.num_pages) pg = v;
-            else flag_bad_index();
-          }
-          return pg;
+          return lane < boxes && key < k1 && key + box > k0;
+        };
+        auto entry = [&](int j) {
+          const int key = base + j * kKeys + lane * box;
+          return wanted(j) ? tab[min(key >> p.page_shift, e_last)] : 0;
         };
         int issued = 0;
-        int pg = nmax > 0 ? page_of(0) : 0;
+        int cur = nmax > 0 ? entry(0) : 0;
         for (int j = 0; ok && j < nmax; ++j) {
-          const int next = j + 1 < nmax ? page_of(j + 1) : 0;
+          const int next = j + 1 < nmax ? entry(j + 1) : 0;
+          int pg = zero_page;
+          if (wanted(j)) {
+            if (cur >= 0 && cur < p.num_pages) pg = cur;
+            else flag_bad_index();
+          }
+          const int key = base + j * kKeys + lane * box;
           for (int kv = 0; kv < 2; ++kv) {
             const int it = 2 * j + kv, slot = it % Shape::kSlots, use = it / Shape::kSlots;
             if (use > 0) ok = warp_wait(&bars.empty[slot], (use - 1) & 1);
@@ -406,7 +437,6 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
             if (lane == 0) mbar_arrive_expect_tx(&bars.full[slot], Shape::kSlot);
             __syncwarp();
             if (lane < boxes) {
-              const int key = base + j * kKeys + lane * box;
 #pragma unroll
               for (int pn = 0; pn < Shape::kPanels; ++pn)
                 tma_box(ring + slot * Shape::kSlot + pn * kPanel + lane * box * 128,
@@ -414,7 +444,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
             }
             issued = it + 1;
           }
-          pg = next;
+          cur = next;
         }
         if (!ok) {
           // Leave no copy in flight behind.
@@ -549,7 +579,11 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(sc[e]);
 #pragma unroll
-      for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(sc[i]));
+      for (int i = 4; i + 8 <= 132; i += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          mx[e] = i + 4 + e < 128 ? max3(mx[e], __uint_as_float(sc[i + e]), __uint_as_float(sc[i + 4 + e]))
+                                  : fmaxf(mx[e], __uint_as_float(sc[i + e]));
       const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
       // -inf - -inf is not a number: no growth.
       if (__any_sync(0xFFFFFFFFu, mt - m > kRescale)) {
@@ -582,14 +616,19 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
         const uint64_t e = p2(ex2(a.x), ex2(a.y));
         l2[i & 1] = add2(l2[i & 1], e);
         pk[i] = narrow2<TP>(e);
-        if (i == 31) tc_st32(ts, pk);
+        if (i == 31) {
+          tc_st32(ts, pk);
+          tc_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars.p_full[t][0]);
+        }
       }
       tc_st32(ts + 32, pk + 32);
       const float2 la = u2(add2(l2[0], l2[1]));
       l = la.x + la.y;
       tc_wait_st();
       tc_fence_before();
-      mbar_arrive(&bars.p_full[t]);
+      mbar_arrive(&bars.p_full[t][1]);
     }
     // Output.
     if (ok && n > 0) {
