@@ -6,9 +6,10 @@
 // A CTA holds two tiles of 128 rows (token x head of the kv head's group) and
 // streams tiles of 128 keys past both.  Roles:
 //   warps 0-3, 4-7   softmax of row tile 0 and 1, one thread per row
-//   warp 8           issues every tcgen05.mma (one lane)
-//   warp 9           issues the TMA loads, one lane per page box
-//   warps 12-15      E4M3 caches only: load, convert, store keys and values
+//   warps 8, 9       issue the tcgen05.mma of row tile 0 and 1 (one thread each)
+//   warp 10          issues the TMA loads, one lane per page box
+//   warp 11          zeroes the values of slots outside the key range
+//   warps 12-15      E4M3 caches (instead of 10, 11): load, convert, store
 // Tensor memory (512 columns): scores S0, S1 (128 fp32 columns each) and
 // outputs O0, O1.  S = Q K^T reads both operands from shared memory; the
 // probabilities go back into S's columns as 16-bit pairs and are the A operand
@@ -20,7 +21,7 @@
 // reference maximum moves only when the running maximum has grown by more
 // than 2^8 over it: until then the probabilities, at most 256, lose nothing in
 // fp32 sums or 16-bit mantissas, and O is not touched; when it moves the
-// row's own threads rescale O (a few times per row, mostly in the first
+// row's own thread rescales O (a few times per row, mostly in the first
 // tiles).
 //
 // K and V tiles: [128 keys][64 elements] panels with 128-byte rows in the
@@ -46,7 +47,14 @@ constexpr int kRowsT = 128;                // rows per tile
 constexpr int kKeys = kPrefillKeys;        // keys per tile
 constexpr int kPanel = kKeys * 128;        // bytes of [128][64] 16-bit elements
 constexpr uint32_t kTmemCols = 512;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kZeroWarp = 11, kConvertWarp = 12;
+constexpr int kLoaders = 128;              // E4M3 caches: threads of warps 12-15
 constexpr float kRescale = 8.f;            // log2 growth before the reference moves
+
+struct Barriers {
+  uint64_t full[8], empty[8], s_full[2], p_full[2], o_full[2], q_full, cut, zeroed, turn[2];
+  uint32_t tmem;
+};
 
 template <bool FP8, int DP>
 struct PrefillShape {
@@ -54,20 +62,16 @@ struct PrefillShape {
   static constexpr int kSlot = kPanels * kPanel;   // one K or V tile
   static constexpr int kSlots = DP == 128 ? 5 : 8; // K and V alternate
   static constexpr int kQ = 2 * kSlot;
-  static constexpr int kSmem = kQ + kSlots * kSlot + 1024;  // + alignment
+  static constexpr int kSmem = kQ + kSlots * kSlot + (int)sizeof(Barriers);
+  static_assert(kSmem <= 232448, "");
   static constexpr int kThreads = FP8 ? 512 : 384;
   // Registers a thread: launched with 65536 / kThreads (128, 168), moved from
-  // the other warps to the softmax.  2 x 128 x softmax + the rest x other =
+  // the other warps to the softmax.  256 x softmax + the rest x other =
   // kThreads x launch, exactly.
   static constexpr int kRegsLaunch = FP8 ? 128 : 168;
   static constexpr int kRegsSoftmax = FP8 ? 184 : 208;
   static constexpr int kRegsOther = FP8 ? 72 : 88;
   static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther == kThreads * kRegsLaunch, "");
-};
-
-struct Barriers {
-  uint64_t full[8], empty[8], s_full[2], p_full[2][2], o_full[2], q_full;
-  uint32_t tmem;
 };
 
 // ---- tcgen05
@@ -130,18 +134,6 @@ __device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t* r) {
       : "r"(a)
       : "memory");
 }
-__device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 // The loaded registers pass through, so that nothing uses them earlier.
 __device__ __forceinline__ void tc_loaded(uint32_t* r) {
   asm volatile(""
@@ -157,6 +149,32 @@ __device__ __forceinline__ void tc_wait_ld(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; i += 32) tc_loaded(r + i);
+}
+__device__ __forceinline__ void tc_ld16(uint32_t a, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -235,8 +253,8 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
   using TP = typename std::conditional<FP8, __half, T>::type;
   constexpr int kTypeQ = std::is_same<T, __half>::value ? 0 : 1;
   constexpr int kTypeP = std::is_same<TP, __half>::value ? 0 : 1;
-  extern __shared__ uint8_t raw[];
-  __shared__ Barriers bars;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  Barriers& bars = *reinterpret_cast<Barriers*>(raw + Shape::kQ + Shape::kSlots * Shape::kSlot);
 
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -271,25 +289,30 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
   }
   const int nmax = max(nt[0], nt[1]);
 
-  const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
-  const uint32_t qs = smem0, ring = smem0 + Shape::kQ;
-  uint8_t* const gen0 = raw + (smem0 - smem_u32(raw));  // the same, generic
+  const uint32_t qs = smem_u32(raw), ring = qs + Shape::kQ;
+  uint8_t* const gen0 = raw;  // the same, generic
+  if (qs & 1023u) {  // the swizzle goes by address bits; the compiler's alignment holds
+    if (tid == 0) flag_wait_timeout();
+    return;
+  }
 
   if (tid == 0) {
     for (int i = 0; i < Shape::kSlots; ++i) {
-      mbar_init(&bars.full[i], FP8 ? 128 : 1);
-      mbar_init(&bars.empty[i], 1);
+      mbar_init(&bars.full[i], FP8 ? kLoaders : 1);
+      mbar_init(&bars.empty[i], 2);  // one arrival for each row tile
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars.s_full[t], 1);
-      mbar_init(&bars.p_full[t][0], 128);
-      mbar_init(&bars.p_full[t][1], 128);
+      mbar_init(&bars.p_full[t], 128);
+      mbar_init(&bars.turn[t], 1);
       mbar_init(&bars.o_full[t], 1);
     }
     mbar_init(&bars.q_full, 256);
+    mbar_init(&bars.cut, 2);
+    mbar_init(&bars.zeroed, 1);
     fence_mbar_init();
   }
-  if (warp == 8) tc_alloc(&bars.tmem);
+  if (warp == kMmaWarp) tc_alloc(&bars.tmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -302,9 +325,13 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
     vscale = *p.v_scale_inv;
   }
 
-  if (warp >= 8) {
+  // Key tiles with slots outside [k0, k1) (only the first and the last can be).
+  const bool cut_first = nmax > 0 && base < k0;
+  const bool cut_last = nmax > 0 && base + nmax * kKeys > k1 && !(nmax == 1 && cut_first);
+
+  if (warp >= kMmaWarp) {
     set_regs_dec<Shape::kRegsOther>();
-    if (warp == 8) {
+    if (warp < kMmaWarp + 2) {
       // ------------------------------------------------ tensor core issue
       constexpr uint32_t kIdQK = instr_desc(kTypeQ, kRowsT, kKeys, 0);
       constexpr uint32_t kIdPV = instr_desc(kTypeP, kRowsT, DP, 1);
@@ -313,95 +340,121 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
       const uint32_t q_lo = __shfl_sync(0xFFFFFFFFu, desc_lo(qs, 16), 0);
       const uint32_t k_lo = __shfl_sync(0xFFFFFFFFu, desc_lo(ring, 16), 0);
       const uint32_t v_lo = __shfl_sync(0xFFFFFFFFu, desc_lo(ring, kPanel), 0);
-      auto qk = [&](int t, int slot) {
-        if (lane == 0) {
-          const uint32_t a = q_lo + t * (Shape::kSlot >> 4), b = k_lo + slot * (Shape::kSlot >> 4);
+      // One thread per row tile, nothing collective.  The tensor core's queue is
+      // short: an issuing thread is held until the step before its own has
+      // begun, so what it does between two products -- a wait on a barrier that
+      // is complete already costs about 100 cycles -- leaves the tensor core
+      // idle.  With a thread per tile one waits and computes addresses while
+      // the other's products run.  They take turns (P V of a key tile, Q K^T of
+      // the next): left to themselves both tiles' products interleave and both
+      // softmaxes then run at once, with the tensor core idle (600 us for a
+      // prompt of 8192 tokens instead of the 500 of one thread for both).  The
+      // turn passes two steps before its end, so that it arrives in time.
+      if (lane == 0 && nmax > 0) {
+        const int t = warp - kMmaWarp, n = nt[t];
+        const uint32_t ts = tm + t * 128, to = tm + 256 + t * 128;
+        const uint32_t qt = q_lo + t * (Shape::kSlot >> 4);
+        constexpr int kSteps = DP / 16;
+        auto qk = [&](int slot) {
+          const uint32_t kt = k_lo + slot * (Shape::kSlot >> 4);
 #pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk) {
+          for (int kk = 0; kk < kSteps; ++kk) {
+            if (kk == kSteps - 2) mbar_arrive(&bars.turn[t ^ 1]);
             const uint32_t at = ((kk / 4) * kPanel + (kk % 4) * 32) >> 4;
-            tc_mma_ss(tm + t * 128, a + at, b + at, kDescHi, kIdQK, kk > 0);
+            tc_mma_ss(ts, qt + at, kt + at, kDescHi, kIdQK, kk > 0);
           }
           tc_commit(&bars.s_full[t]);
-        }
-      };
-      int it = 0;  // ring position
-      if (nmax > 0) {
-        ok = warp_wait(&bars.q_full, 0) && warp_wait(&bars.full[0], 0);
+        };
+        uint32_t zeros = 0;  // waits for zeroed slots so far
+        ok = mbar_wait(&bars.q_full, 0) && mbar_wait(&bars.full[0], 0) &&
+             (t == 0 || mbar_wait(&bars.turn[1], 0));
         if (ok) {
           tc_fence_after();
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (nt[t] > 0) qk(t, 0);
-          if (lane == 0) tc_commit(&bars.empty[0]);
-          it = 1;
-        }
-      }
-      for (int j = 0; ok && j < nmax; ++j) {
-        const int vs = it % Shape::kSlots;
-        ok = warp_wait(&bars.full[vs], (it / Shape::kSlots) & 1);
-        if (!ok) break;
-        ++it;
-        if constexpr (!FP8) {
-          // Values of slots outside the range become zero.
-          const int tb = base + j * kKeys;
-          const int za = max(0, k0 - tb), zb = min(kKeys, k1 - tb);
-          if (za > 0 || zb < kKeys) {
-            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-            const int outside = za + kKeys - zb;
-            for (int i = lane; i < outside * 8 * Shape::kPanels; i += 32) {
-              const int c = i & 7, pr = i >> 3;
-              const int pn = pr % Shape::kPanels, o = pr / Shape::kPanels;
-              const int r = o < za ? o : zb + (o - za);
-              *reinterpret_cast<uint4*>(gen0 + Shape::kQ + vs * Shape::kSlot + pn * kPanel +
-                                        r * 128 + c * 16) = z;
-            }
-            fence_async_smem();
-            __syncwarp();
+          if (n > 0) {
+            qk(0);
+            tc_commit(&bars.empty[0]);
+          } else {
+            // Each tile arrives once per use of a slot, in order: also one that
+            // does not read it waits until it is full.
+            mbar_arrive(&bars.turn[t ^ 1]);
+            mbar_arrive(&bars.empty[0]);
           }
         }
-        int ks = -1;
-        if (j + 1 < nmax) {
-          ks = it % Shape::kSlots;
-          ok = warp_wait(&bars.full[ks], (it / Shape::kSlots) & 1);
+        int vs = 1, vph = 0;  // V's slot in the ring and its phase
+        for (int j = 0; ok && j < nmax; ++j) {
+          int ks = vs + 1, kph = vph;
+          if (ks == Shape::kSlots) ks = 0, kph ^= 1;
+          const bool more = j + 1 < nmax, cut = (j == 0 && cut_first) || (j == nmax - 1 && cut_last);
+          ok = mbar_wait(&bars.full[vs], vph) && (!more || mbar_wait(&bars.full[ks], kph));
+          if (!FP8 && ok && cut) {
+            mbar_arrive(&bars.cut);  // its values are here: zero what lies outside
+            if (j < n) ok = mbar_wait(&bars.zeroed, zeros++ & 1);
+          }
+          if (ok && j < n) ok = mbar_wait(&bars.p_full[t], j & 1);
+          ok = ok && mbar_wait(&bars.turn[t], t == 0 ? j & 1 : (j + 1) & 1);
           if (!ok) break;
-          ++it;
-        }
-        const int last_t = j < nt[1] ? 1 : 0;  // the last row tile that uses this key tile
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (j >= nt[t]) continue;
-          // P arrives in halves of 64 keys: the first half's product runs while
-          // the softmax still computes the second.
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            ok = ok && warp_wait(&bars.p_full[t][hf], j & 1);
-            if (!ok) break;
+          if (j < n) {
             tc_fence_after();
-            if (lane == 0) {
+            const bool next = j + 1 < n;
+            const uint32_t vt = v_lo + vs * (Shape::kSlot >> 4);
 #pragma unroll
-              for (int kk = hf * 4; kk < hf * 4 + 4; ++kk)
-                tc_mma_ts(tm + 256 + t * 128, tm + t * 128 + kk * 8,
-                          v_lo + vs * (Shape::kSlot >> 4) + kk * (2048 >> 4), kDescHi, kIdPV,
-                          kk > 0 ? 1u : static_cast<uint32_t>(j > 0));
+            for (int kk = 0; kk < kKeys / 16; ++kk) {
+              if (kk == kKeys / 16 - 2 && !next) mbar_arrive(&bars.turn[t ^ 1]);
+              tc_mma_ts(to, ts + kk * 8, vt + kk * (2048 >> 4), kDescHi, kIdPV,
+                        kk > 0 ? 1u : static_cast<uint32_t>(j > 0));
             }
-          }
-          if (!ok) break;
-          if (lane == 0) {
             tc_commit(&bars.o_full[t]);
-            if (t == last_t) tc_commit(&bars.empty[vs]);
+            tc_commit(&bars.empty[vs]);
+            if (next) {
+              qk(ks);
+              tc_commit(&bars.empty[ks]);
+            } else if (more) {
+              mbar_arrive(&bars.empty[ks]);
+            }
+          } else {
+            // The other tile's key tiles go on.
+            mbar_arrive(&bars.turn[t ^ 1]);
+            mbar_arrive(&bars.empty[vs]);
+            if (more) mbar_arrive(&bars.empty[ks]);
           }
-          if (j + 1 < nt[t]) qk(t, ks);
+          vs = ks + 1;
+          vph = kph;
+          if (vs == Shape::kSlots) vs = 0, vph ^= 1;
         }
+        // The last arrivals have landed before the CTA ends.
+        if (ok) {
+          const int last = 2 * nmax - 1;
+          ok = mbar_wait(&bars.empty[last % Shape::kSlots], (last / Shape::kSlots) & 1);
+        }
+      }
+      __syncwarp();
+    } else if (!FP8 && warp == kZeroWarp) {
+      // ------------------------------------------------ slots outside the range
+      // Values of slots outside [k0, k1) become zero (a weight of 0 times what
+      // stands there must be 0).
+      uint32_t event = 0;
+      for (int e = 0; e < 2; ++e) {
+        if (e == 0 ? !cut_first : !cut_last) continue;
+        const int j = e == 0 ? 0 : nmax - 1, slot = (2 * j + 1) % Shape::kSlots;
+        // (a whole key range may lie before the last tile's turn: a longer limit)
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_for(&bars.cut, event++ & 1, 30 * kWaitLimitNs));
         if (!ok) break;
-        if (lane == 0 && ks >= 0) tc_commit(&bars.empty[ks]);
+        const int tb = base + j * kKeys;
+        const int za = max(0, k0 - tb), zb = min(kKeys, k1 - tb);
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        const int outside = za + kKeys - zb;
+        for (int i = lane; i < outside * 8 * Shape::kPanels; i += 32) {
+          const int c = i & 7, pr = i >> 3;
+          const int pn = pr % Shape::kPanels, o = pr / Shape::kPanels;
+          const int r = o < za ? o : zb + (o - za);
+          *reinterpret_cast<uint4*>(gen0 + Shape::kQ + slot * Shape::kSlot + pn * kPanel +
+                                    r * 128 + c * 16) = z;
+        }
+        fence_async_smem();
         __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.zeroed);
       }
-      // The last of this warp's arrivals has landed before the CTA ends.
-      if (ok && nmax > 0) {
-        const int last = 2 * nmax - 1;
-        ok = warp_wait(&bars.empty[last % Shape::kSlots], (last / Shape::kSlots) & 1);
-      }
-    } else if (!FP8 && warp == 9) {
+    } else if (!FP8 && warp == kLoadWarp) {
       // ------------------------------------------------ TMA loads
       if constexpr (!FP8) {
         const int page = 1 << p.page_shift;
@@ -452,45 +505,47 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
             warp_wait(&bars.full[i % Shape::kSlots], (i / Shape::kSlots) & 1);
         }
       }
-    } else if (FP8 && warp >= 12) {
+    } else if (FP8 && warp >= kConvertWarp) {
       // ------------------------------------------------ E4M3: load and convert
       if constexpr (FP8) {
-        constexpr int kChunks = DP / 16;                    // 16-byte chunks per key
-        constexpr int kPer = kKeys * kChunks / 128;         // per thread and tile
-        const int lt = tid - 384;
+        constexpr int kChunks = DP / 16;            // 16-byte chunks per key
+        constexpr int kRowsStep = kLoaders / kChunks;  // key rows per step
+        constexpr int kSteps = (kKeys + kRowsStep - 1) / kRowsStep;
+        constexpr int kBatch = kSteps;              // steps in flight
+        const int lt = tid - 32 * kConvertWarp;
+        const int c = lt % kChunks, row0 = lt / kChunks;
         const int32_t* tab = p.table + b * p.table_stride;
-        const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k) + h * p.kh;
-        const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v) + h * p.vh;
-        const int c = lt % kChunks;                         // the same chunk of every row
-        uint4 w[kPer];
-        auto fetch = [&](int it) {
-          const int tb = base + (it >> 1) * kKeys;
-          const bool is_v = it & 1;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int key = tb + (lt + i * 128) / kChunks;
-            w[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (key >= k0 && key < k1 && c * 16 < p.d) {
-              const int pg = tab[key >> p.page_shift];
-              const int slot = key & ((1 << p.page_shift) - 1);
-              if (pg >= 0 && pg < p.num_pages)
-                w[i] = ld_stream16(is_v ? vb + pg * p.vp + slot * p.vs + c * 16
-                                        : kb + pg * p.kp + slot * p.ks + c * 16);
-              else
-                flag_bad_index();
-            }
+        const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k) + h * p.kh + c * 16;
+        const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v) + h * p.vh + c * 16;
+        const bool inside = c * 16 < p.d;
+        auto fetch = [&](int it, int st) {
+          const int r = st * kRowsStep + row0, key = base + (it >> 1) * kKeys + r;
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (r < kKeys && key >= k0 && key < k1 && inside) {
+            const int pg = tab[key >> p.page_shift];
+            const int slot = key & ((1 << p.page_shift) - 1);
+            if (pg >= 0 && pg < p.num_pages)
+              w = ld_stream16(it & 1 ? vb + pg * p.vp + slot * p.vs : kb + pg * p.kp + slot * p.ks);
+            else
+              flag_bad_index();
           }
+          return w;
         };
-        if (nmax > 0) fetch(0);
+        uint4 w[kBatch];
+        if (nmax > 0) {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) w[i] = fetch(0, i);
+        }
         for (int it = 0; ok && it < 2 * nmax; ++it) {
           const int slot = it % Shape::kSlots, use = it / Shape::kSlots;
           if (use > 0) ok = warp_wait(&bars.empty[slot], (use - 1) & 1);
           if (!ok) break;
           uint8_t* dst = gen0 + Shape::kQ + slot * Shape::kSlot + (c / 4) * kPanel;
+          const int c2 = (c % 4) * 2;
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int r = (lt + i * 128) / kChunks;
-            const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          for (int st = 0; st < kSteps; ++st) {
+            const uint4 v = w[st % kBatch];
+            const uint32_t a[4] = {v.x, v.y, v.z, v.w};
             uint32_t o[8];
             if (it & 1) {
 #pragma unroll
@@ -505,13 +560,18 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
                 o[2 * e + 1] = e4m3_pair<kTypeQ == 1>(a[e] >> 16);
               }
             }
-            const int c2 = (c % 4) * 2;
-            *reinterpret_cast<uint4*>(dst + r * 128 + ((c2 ^ (r & 7)) << 4)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst + r * 128 + (((c2 + 1) ^ (r & 7)) << 4)) =
-                make_uint4(o[4], o[5], o[6], o[7]);
+            const int r = st * kRowsStep + row0;
+            if (r < kKeys) {
+              *reinterpret_cast<uint4*>(dst + r * 128 + ((c2 ^ (r & 7)) << 4)) =
+                  make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(dst + r * 128 + (((c2 + 1) ^ (r & 7)) << 4)) =
+                  make_uint4(o[4], o[5], o[6], o[7]);
+            }
           }
-          if (it + 1 < 2 * nmax) fetch(it + 1);
+          if (it + 1 < 2 * nmax) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) w[i] = fetch(it + 1, i);
+          }
           fence_async_smem();
           mbar_arrive(&bars.full[slot]);
         }
@@ -520,13 +580,13 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
   } else {
     // -------------------------------------------------- softmax
     set_regs_inc<Shape::kRegsSoftmax>();
-    const int t = warp >> 2;
-    const int r = tid & 127;
+    const int t = warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;
     const int gr = r0 + t * kRowsT + r;          // row of the (sequence, kv head)
     const bool live = t * kRowsT + r < rows;
     const int token_i = live ? gr / p.group : i_last;
     const int head = h * p.group + (live ? gr % p.group : 0);
-    // q's row, by whole warps: a row's 16-byte chunks by neighbouring lanes.
+    // q's rows, by whole warps: a row's 16-byte chunks by neighbouring lanes.
     {
       constexpr int C = DP / 8;
       const T* q = reinterpret_cast<const T*>(p.q);
@@ -534,7 +594,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
       // what is left multiplies the scores by something positive.
       const uint32_t flip = kscale < 0.f ? 0x80008000u : 0u, keep = kscale == 0.f ? 0u : ~0u;
       for (int i = lane; i < 32 * C; i += 32) {
-        const int rr = (warp & 3) * 32 + i / C, c = i % C;
+        const int rr = quad * 32 + i / C, c = i % C;
         const int row = t * kRowsT + rr;
         uint4 w = make_uint4(0u, 0u, 0u, 0u);
         if (row < rows && c * 8 < p.d) {
@@ -556,8 +616,9 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
     }
     const int rlo = max(row_low(p, s, token_i), k0), rhi = min(row_high(p, s, token_i), k1);
     const float scale = p.scale_log2 * (kscale == 0.f ? 1.f : fabsf(kscale));
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t ts = tmem + lanes + t * 128;             // S, and P over it
+    const uint32_t to = tmem + lanes + 256 + t * 128;
     float m = -INFINITY;   // the row's reference maximum (log2 units)
     float l = 0.f;
     const int n = nt[t];
@@ -575,60 +636,75 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
         for (int i = 0; i < 128; ++i)
           if (tb + i < rlo || tb + i >= rhi) sc[i] = 0xFF800000u;  // -inf
       }
-      float mx[4];
+      // The exponentials go ahead with the reference as it stands, the tile's
+      // maximum beside them (another pipe); where it turns out to have grown
+      // too far the tile is done again.  The first tile has no reference yet.
+      bool known = j == 0;  // the maximum is known
+      float mt = -INFINITY;
+      if (known) {
+        float mx[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(sc[e]);
+        for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(sc[e]);
 #pragma unroll
-      for (int i = 4; i + 8 <= 132; i += 8)
+        for (int i = 4; i < 124; i += 8)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mx[e] = i + 4 + e < 128 ? max3(mx[e], __uint_as_float(sc[i + e]), __uint_as_float(sc[i + 4 + e]))
-                                  : fmaxf(mx[e], __uint_as_float(sc[i + e]));
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-      // -inf - -inf is not a number: no growth.
-      if (__any_sync(0xFFFFFFFFu, mt - m > kRescale)) {
+          for (int e = 0; e < 4; ++e)
+            mx[e] = max3(mx[e], __uint_as_float(sc[i + e]), __uint_as_float(sc[i + 4 + e]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(sc[124 + e]));
+        mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
+        m = mt;
+      }
+      const float l_before = l;
+#pragma unroll 1
+      for (;;) {
+        const float mb = m == -INFINITY ? 0.f : m;
+        const uint64_t sc2 = p2(scale, scale), mb2 = p2(-mb, -mb);
+        uint64_t l2[2] = {p2(l, 0.f), 0ull};
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float s0 = __uint_as_float(sc[q4 * 32 + 2 * i]);
+            const float s1 = __uint_as_float(sc[q4 * 32 + 2 * i + 1]);
+            const float2 a = u2(fma2(p2(s0, s1), sc2, mb2));
+            mx[i & 3] = max3(mx[i & 3], s0, s1);
+            const uint64_t e = p2(ex2(a.x), ex2(a.y));
+            l2[i & 1] = add2(l2[i & 1], e);
+            pk[i] = narrow2<TP>(e);
+          }
+          tc_st16(ts + q4 * 16, pk);
+        }
+        const float2 la = u2(add2(l2[0], l2[1]));
+        l = la.x + la.y;
+        if (known) break;
+        mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
+        // -inf - -inf is not a number: no growth.
+        if (!__any_sync(0xFFFFFFFFu, mt - m > kRescale)) break;
         const float mn = fmaxf(m, mt);
         const float al = mn == -INFINITY ? 1.f : ex2(m - mn);
-        l *= al;
+        l = l_before * al;
         m = mn;
-        if (j > 0) {
-          ok = warp_wait(&bars.o_full[t], (j - 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
+        known = true;
+        ok = warp_wait(&bars.o_full[t], (j - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll 1
-          for (int q4 = 0; q4 < DP / 32; ++q4) {
-            uint32_t o[32];
-            tc_ld32(to + q4 * 32, o);
-            tc_wait_ld<32>(o);
+        for (int q2 = 0; q2 < DP / 16; ++q2) {
+          uint32_t o[16];
+          tc_ld16(to + q2 * 16, o);
+          tc_wait_ld16(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-            tc_st32(to + q4 * 32, o);
-          }
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+          tc_st16(to + q2 * 16, o);
         }
       }
-      const float mb = m == -INFINITY ? 0.f : m;
-      const uint64_t sc2 = p2(scale, scale), mb2 = p2(-mb, -mb);
-      uint64_t l2[2] = {p2(l, 0.f), 0ull};
-      uint32_t pk[64];
-#pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        const float2 a = u2(fma2(p2(__uint_as_float(sc[2 * i]), __uint_as_float(sc[2 * i + 1])), sc2, mb2));
-        const uint64_t e = p2(ex2(a.x), ex2(a.y));
-        l2[i & 1] = add2(l2[i & 1], e);
-        pk[i] = narrow2<TP>(e);
-        if (i == 31) {
-          tc_st32(ts, pk);
-          tc_wait_st();
-          tc_fence_before();
-          mbar_arrive(&bars.p_full[t][0]);
-        }
-      }
-      tc_st32(ts + 32, pk + 32);
-      const float2 la = u2(add2(l2[0], l2[1]));
-      l = la.x + la.y;
+      if (!ok) break;
       tc_wait_st();
       tc_fence_before();
-      mbar_arrive(&bars.p_full[t][1]);
+      mbar_arrive(&bars.p_full[t]);
     }
     // Output.
     if (ok && n > 0) {
@@ -654,13 +730,14 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
+        const int col = q4 * 32;
         if (live && part) {
           float* dst = p.part_o + (static_cast<int64_t>(split) * p.tokens * p.hq + ro) * p.d;
           if (l != 0.f) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              if (q4 * 32 + i < p.d)
-                *reinterpret_cast<uint4*>(dst + q4 * 32 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              if (col + i < p.d)
+                *reinterpret_cast<uint4*>(dst + col + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         } else if (live) {
           T* dst = reinterpret_cast<T*>(p.out) + token * p.ot + head * p.oh;
@@ -671,7 +748,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
             for (int e = 0; e < 4; ++e)
               w[e] = narrow2<T>(p2(l == 0.f ? 0.f : __uint_as_float(o[i + 2 * e]) * inv,
                                    l == 0.f ? 0.f : __uint_as_float(o[i + 2 * e + 1]) * inv));
-            if (q4 * 32 + i < p.d) st_words<4>(dst + q4 * 32 + i, w);
+            if (col + i < p.d) st_words<4>(dst + col + i, w);
           }
         }
         __syncwarp();  // the loads of tensor memory take the whole warp
@@ -683,7 +760,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tc_dealloc(tmem);
+  if (warp == kMmaWarp) tc_dealloc(tmem);
 }
 
 // ---- host side
