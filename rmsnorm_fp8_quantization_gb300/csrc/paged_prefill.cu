@@ -14,8 +14,12 @@
 // outputs O0, O1.  S = Q K^T reads both operands from shared memory; the
 // probabilities go back into S's columns as 16-bit pairs and are the A operand
 // of O += P V straight from tensor memory, so they never pass through shared
-// memory.  While the tensor core works on one tile (P V of key tile j, then
-// Q K^T of tile j + 1), the other tile's softmax runs: the two alternate.
+// memory.  While the tensor core works on one row tile (P V of a key tile, then
+// Q K^T of the next), the other's softmax runs: the two alternate.  The softmax
+// hands P over in halves of 64 keys, and the first half's product runs while it
+// computes the second.  (Scores in halves too, with four steps under way, were
+// slower: N = 64 makes Q K^T read 192 bytes of shared memory a cycle, more than
+// there are, 547 us against 468 for a prompt of 8192 tokens.)
 //
 // The outputs stay in tensor memory for the whole key range.  A row's
 // reference maximum moves only when the running maximum has grown by more
@@ -45,6 +49,7 @@ namespace {
 
 constexpr int kRowsT = 128;                // rows per tile
 constexpr int kKeys = kPrefillKeys;        // keys per tile
+constexpr int kHalf = kKeys / 2;           // keys per step of the tensor core and the softmax
 constexpr int kPanel = kKeys * 128;        // bytes of [128][64] 16-bit elements
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kZeroWarp = 11, kConvertWarp = 12;
@@ -52,7 +57,8 @@ constexpr int kLoaders = 128;              // E4M3 caches: threads of warps 12-1
 constexpr float kRescale = 8.f;            // log2 growth before the reference moves
 
 struct Barriers {
-  uint64_t full[8], empty[8], s_full[2], p_full[2], o_full[2], q_full, cut, zeroed, turn[2];
+  // p_full, o_full: [row tile][half of the keys]
+  uint64_t full[8], empty[8], s_full[2], p_full[2][2], o_full[2][2], q_full, cut, zeroed, turn[2];
   uint32_t tmem;
 };
 
@@ -134,6 +140,18 @@ __device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t* r) {
       : "r"(a)
       : "memory");
 }
+__device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
 // The loaded registers pass through, so that nothing uses them earlier.
 __device__ __forceinline__ void tc_loaded(uint32_t* r) {
   asm volatile(""
@@ -149,32 +167,6 @@ __device__ __forceinline__ void tc_wait_ld(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; i += 32) tc_loaded(r + i);
-}
-__device__ __forceinline__ void tc_ld16(uint32_t a, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(a)
-      : "memory");
-}
-__device__ __forceinline__ void tc_wait_ld16(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-  asm volatile(""
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-}
-__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
-      : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -298,16 +290,18 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < Shape::kSlots; ++i) {
-      mbar_init(&bars.full[i], FP8 ? kLoaders : 1);
+      mbar_init(&bars.full[i], FP8 ? kLoaders / 32 : 1);
       mbar_init(&bars.empty[i], 2);  // one arrival for each row tile
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars.s_full[t], 1);
-      mbar_init(&bars.p_full[t], 128);
       mbar_init(&bars.turn[t], 1);
-      mbar_init(&bars.o_full[t], 1);
+      for (int hf = 0; hf < 2; ++hf) {
+        mbar_init(&bars.p_full[t][hf], 4);  // one arrival per warp
+        mbar_init(&bars.o_full[t][hf], 1);
+      }
     }
-    mbar_init(&bars.q_full, 256);
+    mbar_init(&bars.q_full, 8);
     mbar_init(&bars.cut, 2);
     mbar_init(&bars.zeroed, 1);
     fence_mbar_init();
@@ -344,12 +338,12 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
       // short: an issuing thread is held until the step before its own has
       // begun, so what it does between two products -- a wait on a barrier that
       // is complete already costs about 100 cycles -- leaves the tensor core
-      // idle.  With a thread per tile one waits and computes addresses while
-      // the other's products run.  They take turns (P V of a key tile, Q K^T of
-      // the next): left to themselves both tiles' products interleave and both
-      // softmaxes then run at once, with the tensor core idle (600 us for a
-      // prompt of 8192 tokens instead of the 500 of one thread for both).  The
-      // turn passes two steps before its end, so that it arrives in time.
+      // idle.  With a thread per tile one waits while the other's products run.
+      // They take turns (P V of a key tile, Q K^T of the next): left to themselves
+      // both tiles' products interleave, both softmaxes then run at once and the
+      // tensor core waits (600 us for a prompt of 8192 tokens instead of the 500
+      // of one thread for both).  The turn passes two steps before its end, so
+      // that it arrives in time.
       if (lane == 0 && nmax > 0) {
         const int t = warp - kMmaWarp, n = nt[t];
         const uint32_t ts = tm + t * 128, to = tm + 256 + t * 128;
@@ -365,9 +359,15 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
           }
           tc_commit(&bars.s_full[t]);
         };
+        // This thread's turns: tile 1's i-th follows tile 0's i-th.
+        uint32_t turns = 0;
+        auto my_turn = [&]() {
+          const uint32_t i = turns++;
+          return t == 0 ? i == 0 || mbar_wait(&bars.turn[0], (i - 1) & 1)
+                        : mbar_wait(&bars.turn[1], i & 1);
+        };
         uint32_t zeros = 0;  // waits for zeroed slots so far
-        ok = mbar_wait(&bars.q_full, 0) && mbar_wait(&bars.full[0], 0) &&
-             (t == 0 || mbar_wait(&bars.turn[1], 0));
+        ok = mbar_wait(&bars.q_full, 0) && mbar_wait(&bars.full[0], 0) && my_turn();
         if (ok) {
           tc_fence_after();
           if (n > 0) {
@@ -390,20 +390,26 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
             mbar_arrive(&bars.cut);  // its values are here: zero what lies outside
             if (j < n) ok = mbar_wait(&bars.zeroed, zeros++ & 1);
           }
-          if (ok && j < n) ok = mbar_wait(&bars.p_full[t], j & 1);
-          ok = ok && mbar_wait(&bars.turn[t], t == 0 ? j & 1 : (j + 1) & 1);
+          if (ok && j < n) ok = mbar_wait(&bars.p_full[t][0], j & 1);
+          ok = ok && my_turn();
           if (!ok) break;
           if (j < n) {
-            tc_fence_after();
             const bool next = j + 1 < n;
             const uint32_t vt = v_lo + vs * (Shape::kSlot >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk) {
-              if (kk == kKeys / 16 - 2 && !next) mbar_arrive(&bars.turn[t ^ 1]);
-              tc_mma_ts(to, ts + kk * 8, vt + kk * (2048 >> 4), kDescHi, kIdPV,
-                        kk > 0 ? 1u : static_cast<uint32_t>(j > 0));
+            for (int hf = 0; hf < 2; ++hf) {
+              if (hf == 1) ok = mbar_wait(&bars.p_full[t][1], j & 1);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = hf * 4; kk < hf * 4 + 4; ++kk) {
+                if (kk == 6 && !next) mbar_arrive(&bars.turn[t ^ 1]);
+                tc_mma_ts(to, ts + hf * kHalf + (kk - hf * 4) * 8, vt + kk * (2048 >> 4), kDescHi, kIdPV,
+                          kk > 0 ? 1u : static_cast<uint32_t>(j > 0));
+              }
+              tc_commit(&bars.o_full[t][hf]);
             }
-            tc_commit(&bars.o_full[t]);
+            if (!ok) break;
             tc_commit(&bars.empty[vs]);
             if (next) {
               qk(ks);
@@ -573,7 +579,8 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
             for (int i = 0; i < kBatch; ++i) w[i] = fetch(it + 1, i);
           }
           fence_async_smem();
-          mbar_arrive(&bars.full[slot]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.full[slot]);
         }
       }
     }
@@ -612,7 +619,8 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
                                   (((c & 7) ^ (rr & 7)) << 4)) = w;
       }
       fence_async_smem();
-      mbar_arrive(&bars.q_full);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.q_full);
     }
     const int rlo = max(row_low(p, s, token_i), k0), rhi = min(row_high(p, s, token_i), k1);
     const float scale = p.scale_log2 * (kscale == 0.f ? 1.f : fabsf(kscale));
@@ -622,93 +630,108 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
     float m = -INFINITY;   // the row's reference maximum (log2 units)
     float l = 0.f;
     const int n = nt[t];
-    for (int j = 0; j < n; ++j) {
-      ok = warp_wait(&bars.s_full[t], j & 1);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t sc[128];
-#pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) tc_ld32(ts + q4 * 32, sc + q4 * 32);
-      tc_wait_ld<128>(sc);
-      const int tb = base + j * kKeys;
-      if (__any_sync(0xFFFFFFFFu, tb < rlo || tb + kKeys > rhi)) {
-#pragma unroll
-        for (int i = 0; i < 128; ++i)
-          if (tb + i < rlo || tb + i >= rhi) sc[i] = 0xFF800000u;  // -inf
+    // Step i: keys 64 i .. 64 i + 63 of the range, half i % 2 of key tile i / 2.
+    for (int i = 0; i < 2 * n; ++i) {
+      const int hf = i & 1;
+      const uint32_t th = ts + hf * kHalf;       // this half's scores, P over them
+      if (hf == 0) {
+        ok = warp_wait(&bars.s_full[t], (i >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
       }
-      // The exponentials go ahead with the reference as it stands, the tile's
-      // maximum beside them (another pipe); where it turns out to have grown
-      // too far the tile is done again.  The first tile has no reference yet.
-      bool known = j == 0;  // the maximum is known
-      float mt = -INFINITY;
-      if (known) {
-        float mx[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(sc[e]);
-#pragma unroll
-        for (int i = 4; i < 124; i += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx[e] = max3(mx[e], __uint_as_float(sc[i + e]), __uint_as_float(sc[i + 4 + e]));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(sc[124 + e]));
-        mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
-        m = mt;
-      }
-      const float l_before = l;
-#pragma unroll 1
-      for (;;) {
+      const int tb = base + i * kHalf;
+      const bool cut = __any_sync(0xFFFFFFFFu, tb < rlo || tb + kHalf > rhi);
+      bool done = false;
+      if (i > 0 && !cut) {
+        // The usual step: every key kept.  The exponentials go ahead with the
+        // reference as it stands, the step's maximum beside them (another pipe);
+        // where it turns out to have grown too far, the step is done again
+        // below.  Bound by ex2 (4.3 to 5 cycles a warp); a path that could go
+        // either way with the scores in registers would copy them.
+        uint32_t sc[64], pk[32];
+        tc_ld32(th, sc);
+        tc_ld32(th + 32, sc + 32);
+        tc_wait_ld<64>(sc);
         const float mb = m == -INFINITY ? 0.f : m;
         const uint64_t sc2 = p2(scale, scale), mb2 = p2(-mb, -mb);
         uint64_t l2[2] = {p2(l, 0.f), 0ull};
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float s0 = __uint_as_float(sc[q4 * 32 + 2 * i]);
-            const float s1 = __uint_as_float(sc[q4 * 32 + 2 * i + 1]);
-            const float2 a = u2(fma2(p2(s0, s1), sc2, mb2));
-            mx[i & 3] = max3(mx[i & 3], s0, s1);
-            const uint64_t e = p2(ex2(a.x), ex2(a.y));
-            l2[i & 1] = add2(l2[i & 1], e);
-            pk[i] = narrow2<TP>(e);
-          }
-          tc_st16(ts + q4 * 16, pk);
+        for (int e = 0; e < 32; ++e) {
+          const float s0 = __uint_as_float(sc[2 * e]), s1 = __uint_as_float(sc[2 * e + 1]);
+          const float2 a = u2(fma2(p2(s0, s1), sc2, mb2));
+          mx[e & 3] = max3(mx[e & 3], s0, s1);
+          const uint64_t x2 = p2(ex2(a.x), ex2(a.y));
+          l2[e & 1] = add2(l2[e & 1], x2);
+          pk[e] = narrow2<TP>(x2);
         }
-        const float2 la = u2(add2(l2[0], l2[1]));
-        l = la.x + la.y;
-        if (known) break;
-        mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
+        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
         // -inf - -inf is not a number: no growth.
-        if (!__any_sync(0xFFFFFFFFu, mt - m > kRescale)) break;
-        const float mn = fmaxf(m, mt);
-        const float al = mn == -INFINITY ? 1.f : ex2(m - mn);
-        l = l_before * al;
-        m = mn;
-        known = true;
-        ok = warp_wait(&bars.o_full[t], (j - 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int q2 = 0; q2 < DP / 16; ++q2) {
-          uint32_t o[16];
-          tc_ld16(to + q2 * 16, o);
-          tc_wait_ld16(o);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-          tc_st16(to + q2 * 16, o);
+        if (!__any_sync(0xFFFFFFFFu, mt - m > kRescale)) {
+          tc_st32(th, pk);
+          const float2 la = u2(add2(l2[0], l2[1]));
+          l = la.x + la.y;
+          done = true;
         }
       }
-      if (!ok) break;
+      if (!done) {
+        // The first step, one that the range or the mask cuts, and one whose
+        // maximum has grown: the maximum first, then the rest.
+        uint32_t sc[64], pk[32];
+        tc_ld32(th, sc);
+        tc_ld32(th + 32, sc + 32);
+        tc_wait_ld<64>(sc);
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {
+          if (tb + e < rlo || tb + e >= rhi) sc[e] = 0xFF800000u;  // -inf
+          mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sc[e]));
+        }
+        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
+        if (__any_sync(0xFFFFFFFFu, mt - m > kRescale)) {
+          const float mn = fmaxf(m, mt);
+          const float al = mn == -INFINITY ? 1.f : ex2(m - mn);
+          l *= al;
+          m = mn;
+          if (i > 0) {
+            // Every product of the steps before has to be in O.
+            ok = warp_wait(&bars.o_full[t][hf ^ 1], ((i - 1) >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int q2 = 0; q2 < DP / 32; ++q2) {
+              uint32_t o[32];
+              tc_ld32(to + q2 * 32, o);
+              tc_wait_ld<32>(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+              tc_st32(to + q2 * 32, o);
+            }
+          }
+        }
+        const float mb = m == -INFINITY ? 0.f : m;
+        const uint64_t sc2 = p2(scale, scale), mb2 = p2(-mb, -mb);
+        uint64_t l2[2] = {p2(l, 0.f), 0ull};
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float2 a = u2(fma2(
+              p2(__uint_as_float(sc[2 * e]), __uint_as_float(sc[2 * e + 1])), sc2, mb2));
+          const uint64_t x2 = p2(ex2(a.x), ex2(a.y));
+          l2[e & 1] = add2(l2[e & 1], x2);
+          pk[e] = narrow2<TP>(x2);
+        }
+        tc_st32(th, pk);
+        const float2 la = u2(add2(l2[0], l2[1]));
+        l = la.x + la.y;
+      }
       tc_wait_st();
       tc_fence_before();
-      mbar_arrive(&bars.p_full[t]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.p_full[t][hf]);
     }
     // Output.
     if (ok && n > 0) {
-      ok = warp_wait(&bars.o_full[t], (n - 1) & 1);
+      ok = warp_wait(&bars.o_full[t][1], (n - 1) & 1);
       tc_fence_after();
     }
     if (ok) {
