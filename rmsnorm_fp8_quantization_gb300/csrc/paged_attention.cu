@@ -24,8 +24,12 @@
 // registers.  The head elements of Q K^T may be summed in any order, and the
 // columns of the output may be computed in any order, so the fragments take
 // whatever elements those 16 bytes hold and no byte is shuffled between lanes.
-// Keys become q's type (an E4M3 value is exact in both), values become f16,
-// and so do the probabilities next to them.
+// Keys and values become f16 (an E4M3 value is exact in it, one instruction a
+// pair), the probabilities f16 next to the values, and a bf16 q becomes f16 too,
+// its row scaled by the power of two that brings its largest element near 2^8:
+// elements 2^-22 below that and smaller lose bits, 2^-33 of the row's largest.
+// (Keys in bf16 took four instructions a pair, and the kernel 133 us instead of
+// 79 us of HBM time for 262144 keys.)
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -93,22 +97,6 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two E4M3 codes (low 16 bits) to a pair of f16, exact; NaN stays NaN.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
-      : "=r"(r)
-      : "r"(c));
-  return r;
-}
-// ... to a pair of T.
-template <typename T>
-__device__ __forceinline__ uint32_t e4m3x2_to(uint32_t c) {
-  const uint32_t h = e4m3x2_to_f16x2(c);
-  if constexpr (std::is_same<T, __half>::value) return h;
-  else return narrow2<__nv_bfloat16>(widen2<__half>(h));
-}
-
 // Column (16-byte chunk) permutation of the tiles in shared memory.  Two-byte
 // rows: the eight rows of an ldmatrix phase in eight chunks.  E4M3 rows: a
 // 16-byte load's phase reads four chunks of two neighbouring rows (keys) or
@@ -132,7 +120,7 @@ struct StepShape {
   static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
   static constexpr int kQPitch = DP * 2 + 16;
   static constexpr int smem(int mt) {
-    return kBody + 16 * mt * kQPitch + kSplitPages * 4 + 4 * 16 * 8;
+    return kBody + 16 * mt * kQPitch + kSplitPages * 4 + 4 * 16 * 8 + 16 * mt * 4;
   }
 };
 
@@ -147,11 +135,12 @@ __global__ void __launch_bounds__(kStepThreads)
   constexpr int DT = DP / 8;                 // output tiles of 8 columns
   constexpr int KS = DP / 16;                // steps of 16 head elements
   constexpr bool kQReg = DP <= 128;          // q's fragments stay in registers
-  using TP = typename std::conditional<FP8, __half, T>::type;  // type of the P V product
+  using TP = typename std::conditional<FP8, __half, T>::type;  // type of both products
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* s_q = smem + Shape::kBody;
   int32_t* s_page = reinterpret_cast<int32_t*>(s_q + 16 * MT * Shape::kQPitch);
   float2* s_ml = reinterpret_cast<float2*>(s_page + kSplitPages);
+  float* s_qs = reinterpret_cast<float*>(s_ml + 4 * 16);  // E4M3: what a q row's scores are times
 
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -209,6 +198,11 @@ __global__ void __launch_bounds__(kStepThreads)
         const int gr = r0 + r;
         w = *reinterpret_cast<const uint4*>(q + (s.q0 + gr / p.group) * p.qt +
                                             (h * p.group + gr % p.group) * p.qh + c * 8);
+      }
+      if constexpr (FP8) {
+        // A row's C chunks are in C neighbouring lanes.
+        const float back = q_to_f16<T, C>(w);
+        if (c == 0) s_qs[r] = back;
       }
       *reinterpret_cast<uint4*>(s_q + r * Shape::kQPitch + c * 16) = w;
     }
@@ -277,8 +271,11 @@ __global__ void __launch_bounds__(kStepThreads)
   // Keys that every row of the CTA keeps need no test.
   const int all_lo = row_low(p, s, i1), all_hi = min(row_high(p, s, i0), k1);
 
-  float scale = p.scale_log2;
-  if constexpr (FP8) scale *= *p.k_scale_inv;
+  float scale[2] = {p.scale_log2, p.scale_log2};
+  if constexpr (FP8) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) scale[e] *= *p.k_scale_inv * s_qs[wm * 16 + qr + 8 * e];
+  }
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   float o[DT][4];
 #pragma unroll
@@ -310,8 +307,8 @@ __global__ void __launch_bounds__(kStepThreads)
           const int ch = ks * 2 + ((lane >> 3) & 1);
           uint32_t kb[4];
           ldsm4(kb, kd + row * Shape::kRowBytes + swz<FP8, Shape::kChunks>(row, ch) * 16);
-          mma16816<T>(sc[n], af, kb[0], kb[1]);
-          mma16816<T>(sc[n + 1], af, kb[2], kb[3]);
+          mma16816<TP>(sc[n], af, kb[0], kb[1]);
+          mma16816<TP>(sc[n + 1], af, kb[2], kb[3]);
         }
       }
     } else {
@@ -328,7 +325,7 @@ __global__ void __launch_bounds__(kStepThreads)
             uint32_t a[4];
             if constexpr (!kQReg) load_q(blk * 4 + s4, a);
             const uint32_t* af = kQReg ? qf[kQReg ? blk * 4 + s4 : 0] : a;
-            mma16816<T>(sc[n], af, e4m3x2_to<T>(w[s4] & 0xFFFFu), e4m3x2_to<T>(w[s4] >> 16));
+            mma16816<TP>(sc[n], af, e4m3x2_to_f16x2(w[s4] & 0xFFFFu), e4m3x2_to_f16x2(w[s4] >> 16));
           }
         }
       }
@@ -342,7 +339,7 @@ __global__ void __launch_bounds__(kStepThreads)
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          sc[n][e] *= scale;
+          sc[n][e] *= scale[e >> 1];
           mx[e >> 1] = fmaxf(mx[e >> 1], sc[n][e]);
         }
     } else {
@@ -352,7 +349,7 @@ __global__ void __launch_bounds__(kStepThreads)
         for (int e = 0; e < 4; ++e) {
           const int j = jbase + n * 8 + qc * 2 + (e & 1);
           const bool keep = j >= rlo[e >> 1] && j < rhi[e >> 1] && j < k1;
-          sc[n][e] = keep ? sc[n][e] * scale : -INFINITY;
+          sc[n][e] = keep ? sc[n][e] * scale[e >> 1] : -INFINITY;
           mx[e >> 1] = fmaxf(mx[e >> 1], sc[n][e]);
         }
     }
@@ -513,8 +510,8 @@ __global__ void __launch_bounds__(kStepThreads)
 //   o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s
 // in the order of the splits within each of the CTA's split groups, the
 // groups added in order: the same bits every time.
-constexpr int kMergeThreads = 128;
-template <typename T>
+// 128 threads, or 512 where there are many splits to add up for few rows.
+template <typename T, int kMergeThreads>
 __global__ void __launch_bounds__(kMergeThreads)
     paged_merge_kernel(const __grid_constant__ AttnParams p, int fp8) {
   pdl_begin();
@@ -533,7 +530,8 @@ __global__ void __launch_bounds__(kMergeThreads)
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   if (lane == 0) s_red[warp] = m;
   __syncthreads();
-  m = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+#pragma unroll
+  for (int w = 0; w < kMergeThreads / 32; ++w) m = fmaxf(m, s_red[w]);
   __syncthreads();
   const float mb = m == -INFINITY ? 0.f : m;
   float l = 0.f;
@@ -548,7 +546,9 @@ __global__ void __launch_bounds__(kMergeThreads)
   l = warp_sum(l);
   if (lane == 0) s_red[warp] = l;
   __syncthreads();
-  l = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeThreads / 32; ++w) l += s_red[w];
 
   const int cols = p.d / 4;                       // float4 columns (4 .. 64)
   const int groups = kMergeThreads / cols;        // split groups (2 .. 32)
@@ -608,6 +608,13 @@ cudaError_t launch_step_d(const AttnParams& p, int mt, int64_t grid, cudaStream_
   if (p.d <= 64) return launch_step_mt<T, FP8, 64>(p, mt, grid, st);
   if (p.d <= 128) return launch_step_mt<T, FP8, 128>(p, mt, grid, st);
   return launch_step_mt<T, FP8, 256>(p, mt, grid, st);
+}
+
+template <typename T>
+cudaError_t launch_merge(const AttnParams& p, bool fp8, cudaStream_t st) {
+  const dim3 g(static_cast<unsigned>(static_cast<int64_t>(p.tokens) * p.hq));
+  return p.splits > 16 ? launch_pdl(paged_merge_kernel<T, 512>, g, dim3(512), 0, st, p, int(fp8))
+                       : launch_pdl(paged_merge_kernel<T, 128>, g, dim3(128), 0, st, p, int(fp8));
 }
 
 // How a call is carried out: a function of sizes that the host knows.
@@ -825,9 +832,8 @@ gbn_status gbn_paged_attention(const gbn_paged_attention_args* args, cudaStream_
             : launch_step_d<__half, false>(p, mt, a.ctas, stream);
   if (e != cudaSuccess) return GBN_ERR_CUDA;
   if (a.splits > 1) {
-    const dim3 g(static_cast<unsigned>(c.tokens * c.q_heads)), t(kMergeThreads);
-    e = dtype == GBN_BF16 ? launch_pdl(paged_merge_kernel<__nv_bfloat16>, g, t, 0, stream, p, int(fp8))
-                          : launch_pdl(paged_merge_kernel<__half>, g, t, 0, stream, p, int(fp8));
+    e = dtype == GBN_BF16 ? launch_merge<__nv_bfloat16>(p, fp8, stream)
+                          : launch_merge<__half>(p, fp8, stream);
     if (e != cudaSuccess) return GBN_ERR_CUDA;
   }
   return GBN_OK;

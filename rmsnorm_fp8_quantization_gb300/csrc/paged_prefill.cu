@@ -9,7 +9,7 @@
 //   warps 8, 9       issue the tcgen05.mma of row tile 0 and 1 (one thread each)
 //   warp 10          issues the TMA loads, one lane per page box
 //   warp 11          zeroes the values of slots outside the key range
-//   warps 12-15      E4M3 caches (instead of 10, 11): load, convert, store
+//   warps 12-15      E4M3 caches (instead of 11): convert the loaded codes to f16
 // Tensor memory (512 columns): scores S0, S1 (128 fp32 columns each) and
 // outputs O0, O1.  S = Q K^T reads both operands from shared memory; the
 // probabilities go back into S's columns as 16-bit pairs and are the A operand
@@ -54,11 +54,14 @@ constexpr int kPanel = kKeys * 128;        // bytes of [128][64] 16-bit elements
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kZeroWarp = 11, kConvertWarp = 12;
 constexpr int kLoaders = 128;              // E4M3 caches: threads of warps 12-15
+constexpr int kStaging = 4;                // E4M3 caches: at most so many tiles of codes
 constexpr float kRescale = 8.f;            // log2 growth before the reference moves
 
 struct Barriers {
   // p_full, o_full: [row tile][half of the keys]
   uint64_t full[8], empty[8], s_full[2], p_full[2][2], o_full[2][2], q_full, cut, zeroed, turn[2];
+  uint64_t raw_full[kStaging], raw_empty[kStaging];  // E4M3 caches
+  float q_scale[2][kRowsT];  // E4M3 caches: what a q row's scores are times
   uint32_t tmem;
 };
 
@@ -66,9 +69,15 @@ template <bool FP8, int DP>
 struct PrefillShape {
   static constexpr int kPanels = DP / 64;
   static constexpr int kSlot = kPanels * kPanel;   // one K or V tile
-  static constexpr int kSlots = DP == 128 ? 5 : 8; // K and V alternate
+  // Ring slots (K and V alternate); E4M3 caches: and tiles of codes on their way
+  // to the conversion.
+  static constexpr int kSlots = DP == 128 ? (FP8 ? 4 : 5) : (FP8 ? 6 : 8);
+  static constexpr int kRaw = FP8 ? kKeys * DP : 0;
+  static constexpr int kRaws = FP8 ? (DP == 128 ? 2 : 4) : 0;
+  static_assert(kRaws <= kStaging, "");
   static constexpr int kQ = 2 * kSlot;
-  static constexpr int kSmem = kQ + kSlots * kSlot + (int)sizeof(Barriers);
+  static constexpr int kBody = kQ + kSlots * kSlot + kRaws * kRaw;
+  static constexpr int kSmem = kBody + (int)sizeof(Barriers);
   static_assert(kSmem <= 232448, "");
   static constexpr int kThreads = FP8 ? 512 : 384;
   // Registers a thread: launched with 65536 / kThreads (128, 168), moved from
@@ -213,20 +222,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
 }
 
-__device__ __forceinline__ uint32_t e4m3_pair_f16(uint32_t c) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
-      : "=r"(r)
-      : "r"(c));
-  return r;
-}
-template <bool BF16>
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t c) {
-  const uint32_t h = e4m3_pair_f16(c);
-  if constexpr (BF16) return narrow2<__nv_bfloat16>(widen2<__half>(h));
-  else return h;
-}
-
 template <int N>
 __device__ __forceinline__ void set_regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -243,10 +238,9 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
                          const __grid_constant__ CUtensorMap vmap) {
   using Shape = PrefillShape<FP8, DP>;
   using TP = typename std::conditional<FP8, __half, T>::type;
-  constexpr int kTypeQ = std::is_same<T, __half>::value ? 0 : 1;
-  constexpr int kTypeP = std::is_same<TP, __half>::value ? 0 : 1;
+  constexpr int kType = std::is_same<TP, __half>::value ? 0 : 1;  // of both products
   extern __shared__ __align__(1024) uint8_t raw[];
-  Barriers& bars = *reinterpret_cast<Barriers*>(raw + Shape::kQ + Shape::kSlots * Shape::kSlot);
+  Barriers& bars = *reinterpret_cast<Barriers*>(raw + Shape::kBody);
 
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -301,6 +295,10 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
         mbar_init(&bars.o_full[t][hf], 1);
       }
     }
+    for (int i = 0; i < Shape::kRaws; ++i) {
+      mbar_init(&bars.raw_full[i], 1);
+      mbar_init(&bars.raw_empty[i], kLoaders / 32);
+    }
     mbar_init(&bars.q_full, 8);
     mbar_init(&bars.cut, 2);
     mbar_init(&bars.zeroed, 1);
@@ -327,8 +325,8 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
     set_regs_dec<Shape::kRegsOther>();
     if (warp < kMmaWarp + 2) {
       // ------------------------------------------------ tensor core issue
-      constexpr uint32_t kIdQK = instr_desc(kTypeQ, kRowsT, kKeys, 0);
-      constexpr uint32_t kIdPV = instr_desc(kTypeP, kRowsT, DP, 1);
+      constexpr uint32_t kIdQK = instr_desc(kType, kRowsT, kKeys, 0);
+      constexpr uint32_t kIdPV = instr_desc(kType, kRowsT, DP, 1);
       // Uniform across the warp, and known to be.
       const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
       const uint32_t q_lo = __shfl_sync(0xFFFFFFFFu, desc_lo(qs, 16), 0);
@@ -460,127 +458,109 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.zeroed);
       }
-    } else if (!FP8 && warp == kLoadWarp) {
+    } else if (warp == kLoadWarp) {
       // ------------------------------------------------ TMA loads
-      if constexpr (!FP8) {
-        const int page = 1 << p.page_shift;
-        const int box = min(page, kKeys);           // keys per box
-        const int boxes = kKeys / box;              // per panel, at most 16
-        const int32_t* tab = p.table + b * p.table_stride;
-        const int e_last = k1 > 0 ? (k1 - 1) >> p.page_shift : 0;
-        // This lane's box of key tile j: its table entry, read one tile ahead
-        // and looked at only when the tile's turn comes.
-        const int zero_page = max(1, static_cast<int>(p.num_pages));  // one past: zeros
-        auto wanted = [&](int j) {
-          const int key = base + j * kKeys + lane * box;
-          return lane < boxes && key < k1 && key + box > k0;
-        };
-        auto entry = [&](int j) {
-          const int key = base + j * kKeys + lane * box;
-          return wanted(j) ? tab[min(key >> p.page_shift, e_last)] : 0;
-        };
-        int issued = 0;
-        int cur = nmax > 0 ? entry(0) : 0;
-        for (int j = 0; ok && j < nmax; ++j) {
-          const int next = j + 1 < nmax ? entry(j + 1) : 0;
-          int pg = zero_page;
-          if (wanted(j)) {
-            if (cur >= 0 && cur < p.num_pages) pg = cur;
-            else flag_bad_index();
-          }
-          const int key = base + j * kKeys + lane * box;
-          for (int kv = 0; kv < 2; ++kv) {
-            const int it = 2 * j + kv, slot = it % Shape::kSlots, use = it / Shape::kSlots;
-            if (use > 0) ok = warp_wait(&bars.empty[slot], (use - 1) & 1);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&bars.full[slot], Shape::kSlot);
-            __syncwarp();
-            if (lane < boxes) {
+      const int page = 1 << p.page_shift;
+      const int box = min(page, kKeys);           // keys per box
+      const int boxes = kKeys / box;              // per panel, at most 16
+      const int32_t* tab = p.table + b * p.table_stride;
+      const int e_last = k1 > 0 ? (k1 - 1) >> p.page_shift : 0;
+      // This lane's box of key tile j: its table entry, read one tile ahead and
+      // looked at only when the tile's turn comes.
+      const int zero_page = max(1, static_cast<int>(p.num_pages));  // one past: zeros
+      auto wanted = [&](int j) {
+        const int key = base + j * kKeys + lane * box;
+        return lane < boxes && key < k1 && key + box > k0;
+      };
+      auto entry = [&](int j) {
+        const int key = base + j * kKeys + lane * box;
+        return wanted(j) ? tab[min(key >> p.page_shift, e_last)] : 0;
+      };
+      // Two-byte caches: panels of 64 elements straight into the ring; E4M3:
+      // whole rows of codes into the staging tiles.
+      constexpr int kDeep = FP8 ? Shape::kRaws : Shape::kSlots;
+      constexpr uint32_t kBytes = FP8 ? Shape::kRaw : Shape::kSlot;
+      uint64_t* const full = FP8 ? bars.raw_full : bars.full;
+      uint64_t* const empty = FP8 ? bars.raw_empty : bars.empty;
+      const uint32_t dst0 = FP8 ? ring + Shape::kSlots * Shape::kSlot : ring;
+      int issued = 0;
+      int cur = nmax > 0 ? entry(0) : 0;
+      for (int j = 0; ok && j < nmax; ++j) {
+        const int next = j + 1 < nmax ? entry(j + 1) : 0;
+        int pg = zero_page;
+        if (wanted(j)) {
+          if (cur >= 0 && cur < p.num_pages) pg = cur;
+          else flag_bad_index();
+        }
+        const int key = base + j * kKeys + lane * box;
+        for (int kv = 0; kv < 2; ++kv) {
+          const int it = 2 * j + kv, slot = it % kDeep, use = it / kDeep;
+          if (use > 0) ok = warp_wait(&empty[slot], (use - 1) & 1);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], kBytes);
+          __syncwarp();
+          if (lane < boxes) {
 #pragma unroll
-              for (int pn = 0; pn < Shape::kPanels; ++pn)
-                tma_box(ring + slot * Shape::kSlot + pn * kPanel + lane * box * 128,
-                        kv ? &vmap : &kmap, pn * 64, h, key & (page - 1), pg, &bars.full[slot]);
-            }
-            issued = it + 1;
+            for (int pn = 0; pn < (FP8 ? 1 : Shape::kPanels); ++pn)
+              tma_box(dst0 + slot * kBytes + pn * kPanel + lane * box * (FP8 ? DP : 128),
+                      kv ? &vmap : &kmap, pn * 64, h, key & (page - 1), pg, &full[slot]);
           }
-          cur = next;
+          issued = it + 1;
         }
-        if (!ok) {
-          // Leave no copy in flight behind.
-          for (int i = max(0, issued - Shape::kSlots); i < issued; ++i)
-            warp_wait(&bars.full[i % Shape::kSlots], (i / Shape::kSlots) & 1);
-        }
+        cur = next;
+      }
+      if (!ok) {
+        // Leave no copy in flight behind.
+        for (int i = max(0, issued - kDeep); i < issued; ++i)
+          warp_wait(&full[i % kDeep], (i / kDeep) & 1);
       }
     } else if (FP8 && warp >= kConvertWarp) {
-      // ------------------------------------------------ E4M3: load and convert
+      // ------------------------------------------------ E4M3: codes to f16
       if constexpr (FP8) {
-        constexpr int kChunks = DP / 16;            // 16-byte chunks per key
+        constexpr int kChunks = DP / 16;               // 16-byte chunks per key
         constexpr int kRowsStep = kLoaders / kChunks;  // key rows per step
-        constexpr int kSteps = (kKeys + kRowsStep - 1) / kRowsStep;
-        constexpr int kBatch = kSteps;              // steps in flight
+        constexpr int kSteps = kKeys / kRowsStep;
         const int lt = tid - 32 * kConvertWarp;
         const int c = lt % kChunks, row0 = lt / kChunks;
-        const int32_t* tab = p.table + b * p.table_stride;
-        const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k) + h * p.kh + c * 16;
-        const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v) + h * p.vh + c * 16;
-        const bool inside = c * 16 < p.d;
-        auto fetch = [&](int it, int st) {
-          const int r = st * kRowsStep + row0, key = base + (it >> 1) * kKeys + r;
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (r < kKeys && key >= k0 && key < k1 && inside) {
-            const int pg = tab[key >> p.page_shift];
-            const int slot = key & ((1 << p.page_shift) - 1);
-            if (pg >= 0 && pg < p.num_pages)
-              w = ld_stream16(it & 1 ? vb + pg * p.vp + slot * p.vs : kb + pg * p.kp + slot * p.ks);
-            else
-              flag_bad_index();
-          }
-          return w;
-        };
-        uint4 w[kBatch];
-        if (nmax > 0) {
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) w[i] = fetch(0, i);
-        }
         for (int it = 0; ok && it < 2 * nmax; ++it) {
-          const int slot = it % Shape::kSlots, use = it / Shape::kSlots;
+          const int rs = it % Shape::kRaws, slot = it % Shape::kSlots, use = it / Shape::kSlots;
+          ok = warp_wait(&bars.raw_full[rs], (it / Shape::kRaws) & 1);
+          if (!ok) break;
+          const uint8_t* src = gen0 + Shape::kQ + Shape::kSlots * Shape::kSlot + rs * Shape::kRaw;
+          const int tb = base + (it >> 1) * kKeys;
+          uint4 w[kSteps];
+#pragma unroll
+          for (int st = 0; st < kSteps; ++st) {
+            const int r = st * kRowsStep + row0;
+            w[st] = *reinterpret_cast<const uint4*>(src + r * DP + c * 16);
+            // What stands outside the range must not enter.
+            if (tb + r < k0 || tb + r >= k1) w[st] = make_uint4(0u, 0u, 0u, 0u);
+          }
           if (use > 0) ok = warp_wait(&bars.empty[slot], (use - 1) & 1);
           if (!ok) break;
           uint8_t* dst = gen0 + Shape::kQ + slot * Shape::kSlot + (c / 4) * kPanel;
           const int c2 = (c % 4) * 2;
 #pragma unroll
           for (int st = 0; st < kSteps; ++st) {
-            const uint4 v = w[st % kBatch];
-            const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t a[4] = {w[st].x, w[st].y, w[st].z, w[st].w};
             uint32_t o[8];
-            if (it & 1) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                o[2 * e] = e4m3_pair<false>(a[e] & 0xFFFFu);
-                o[2 * e + 1] = e4m3_pair<false>(a[e] >> 16);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                o[2 * e] = e4m3_pair<kTypeQ == 1>(a[e] & 0xFFFFu);
-                o[2 * e + 1] = e4m3_pair<kTypeQ == 1>(a[e] >> 16);
-              }
+            for (int e = 0; e < 4; ++e) {
+              o[2 * e] = e4m3x2_to_f16x2(a[e] & 0xFFFFu);
+              o[2 * e + 1] = e4m3x2_to_f16x2(a[e] >> 16);
             }
             const int r = st * kRowsStep + row0;
-            if (r < kKeys) {
-              *reinterpret_cast<uint4*>(dst + r * 128 + ((c2 ^ (r & 7)) << 4)) =
-                  make_uint4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<uint4*>(dst + r * 128 + (((c2 + 1) ^ (r & 7)) << 4)) =
-                  make_uint4(o[4], o[5], o[6], o[7]);
-            }
-          }
-          if (it + 1 < 2 * nmax) {
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) w[i] = fetch(it + 1, i);
+            *reinterpret_cast<uint4*>(dst + r * 128 + ((c2 ^ (r & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((c2 + 1) ^ (r & 7)) << 4)) =
+                make_uint4(o[4], o[5], o[6], o[7]);
           }
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.full[slot]);
+          if (lane == 0) {
+            mbar_arrive(&bars.raw_empty[rs]);
+            mbar_arrive(&bars.full[slot]);
+          }
         }
       }
     }
@@ -608,12 +588,14 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
           const int g = r0 + row;
           w = *reinterpret_cast<const uint4*>(q + (s.q0 + g / p.group) * p.qt +
                                               (h * p.group + g % p.group) * p.qh + c * 8);
-          if constexpr (FP8) {
-            w.x = (w.x ^ flip) & keep;
-            w.y = (w.y ^ flip) & keep;
-            w.z = (w.z ^ flip) & keep;
-            w.w = (w.w ^ flip) & keep;
-          }
+        }
+        if constexpr (FP8) {
+          const float back = q_to_f16<T, C>(w);
+          if (c == 0) bars.q_scale[t][rr] = back;
+          w.x = (w.x ^ flip) & keep;
+          w.y = (w.y ^ flip) & keep;
+          w.z = (w.z ^ flip) & keep;
+          w.w = (w.w ^ flip) & keep;
         }
         *reinterpret_cast<uint4*>(gen0 + t * Shape::kSlot + (c / 8) * kPanel + rr * 128 +
                                   (((c & 7) ^ (rr & 7)) << 4)) = w;
@@ -623,7 +605,8 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
       if (lane == 0) mbar_arrive(&bars.q_full);
     }
     const int rlo = max(row_low(p, s, token_i), k0), rhi = min(row_high(p, s, token_i), k1);
-    const float scale = p.scale_log2 * (kscale == 0.f ? 1.f : fabsf(kscale));
+    float scale = p.scale_log2 * (kscale == 0.f ? 1.f : fabsf(kscale));
+    if constexpr (FP8) scale *= bars.q_scale[t][r];  // written by this warp
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128;             // S, and P over it
     const uint32_t to = tmem + lanes + 256 + t * 128;
@@ -807,23 +790,26 @@ EncodeFn encoder() {
   return fn;
 }
 
-// A cache as [pages][slots][heads][d] 16-bit elements, boxes of 64 elements of
-// one head in min(page, 128) slots.
-bool make_map(CUtensorMap* map, const void* base, bool bf16, const AttnParams& p, int64_t sp,
-              int64_t ss, int64_t sh) {
+// A cache as [pages][slots][heads][d], boxes of min(page, 128) slots of one head:
+// 64 two-byte elements, or (E4M3) dp codes.
+bool make_map(CUtensorMap* map, const void* base, int esize, bool bf16, int dp, const AttnParams& p,
+              int64_t sp, int64_t ss, int64_t sh) {
   EncodeFn enc = encoder();
   if (!enc) return false;
   const cuuint64_t page = cuuint64_t(1) << p.page_shift;
   const cuuint64_t dims[4] = {cuuint64_t(p.d), cuuint64_t(p.hkv), page,
                               cuuint64_t(p.num_pages > 0 ? p.num_pages : 1)};
   // Dimensions of one element may have any stride: give those a valid one.
-  const cuuint64_t strides[3] = {p.hkv > 1 ? cuuint64_t(sh) * 2 : 16, page > 1 ? cuuint64_t(ss) * 2 : 16,
-                                 p.num_pages > 1 ? cuuint64_t(sp) * 2 : 16};
-  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(page < 128 ? page : 128), 1};
+  const cuuint64_t strides[3] = {p.hkv > 1 ? cuuint64_t(sh) * esize : 16, page > 1 ? cuuint64_t(ss) * esize : 16,
+                                 p.num_pages > 1 ? cuuint64_t(sp) * esize : 16};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(esize == 1 ? dp : 64), 1, static_cast<cuuint32_t>(page < 128 ? page : 128), 1};
   const cuuint32_t step[4] = {1, 1, 1, 1};
-  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+  const CUtensorMapDataType type = esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : bf16     ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(map, type, 4,
              const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             esize == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -846,8 +832,9 @@ cudaError_t launch_paged_prefill(const AttnParams& p, gbn_dtype dtype, gbn_dtype
                                  cudaStream_t stream) {
   const bool fp8 = cache_dtype == GBN_E4M3, bf16 = dtype == GBN_BF16;
   CUtensorMap km = {}, vm = {};
-  if (!fp8 && (!make_map(&km, p.k, bf16, p, p.kp, p.ks, p.kh) ||
-               !make_map(&vm, p.v, bf16, p, p.vp, p.vs, p.vh)))
+  const int esize = fp8 ? 1 : 2, dp = p.d <= 64 ? 64 : 128;
+  if (!make_map(&km, p.k, esize, bf16, dp, p, p.kp, p.ks, p.kh) ||
+      !make_map(&vm, p.v, esize, bf16, dp, p, p.vp, p.vs, p.vh))
     return cudaErrorInvalidValue;
   if (p.d <= 64) {
     if (fp8)

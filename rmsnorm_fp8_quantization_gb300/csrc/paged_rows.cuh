@@ -50,6 +50,43 @@ __device__ __forceinline__ float ex2(float a) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
   return r;
 }
+// Two E4M3 codes (low 16 bits) to a pair of f16, exact; NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+      : "=r"(r)
+      : "r"(c));
+  return r;
+}
+
+// Eight elements of a q row (T) to f16 in place, next to E4M3 keys.  bf16 rows
+// are scaled by the power of two that brings the row's largest magnitude into
+// [2^8, 2^9); returns what undoes it.  The row's chunks are in C neighbouring
+// lanes (a power of two), all of which call this together.
+template <typename T, int C>
+__device__ __forceinline__ float q_to_f16(uint4& w) {
+  if constexpr (Elem<T>::kDt == DT_F16) {
+    return 1.f;
+  } else {
+    float f[8];
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    unpack<T, 8>(in, f);
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+#pragma unroll
+    for (int o = C / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    // 2^(8 - exponent), the exponent within what keeps both factors normal.
+    const int ex = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -110), 127);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - ex) << 23);
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = narrow2<__half>(p2(f[2 * e] * up, f[2 * e + 1] * up));
+    w = make_uint4(o[0], o[1], o[2], o[3]);
+    return __uint_as_float(static_cast<uint32_t>(127 - 8 + ex) << 23);
+  }
+}
+
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kAttnLog2e = 1.4426950408889634f;
 

@@ -120,6 +120,9 @@ CHUNK = [
     B([70, 33], [300, 33], heads=4, kv_heads=2, dim=192, fp8=True),
     B([100, 200], [333, 200], heads=4, kv_heads=2, dim=128, page=2),
     B([128, 129, 127], [128, 256, 384], heads=1, kv_heads=1, dim=64, page=256, heads_first=True),
+    B([200, 90], [200, 301], heads=4, kv_heads=2, dim=48),
+    B([200, 90], [200, 301], heads=4, kv_heads=2, dim=96, fp8=True),
+    B([200, 90], [200, 301], heads=4, kv_heads=2, dim=16, fp8=True, page=8),
     B([90], [1300], heads=16, kv_heads=2, dim=128, window=200, page=64),
 ]
 
