@@ -8,17 +8,21 @@
 //   when the maximum grows.
 //
 // What bounds it: with few rows each key and value is read from HBM once and
-// used for a handful of rows, so the bytes of the cache.  A CTA of four warps
-// streams tiles of 64 keys through a ring of cp.async copies (16 bytes a
-// thread, a page looked up per row; rows past the range are zero-filled, so
-// what stands in their slots never enters).  The rows of the kv head's whole
-// group share the tile.  With up to 16 rows the four warps take 16 keys each
-// and keep maxima, sums and outputs of their own, merged once at the end;
-// with 32 rows they are 2 x 2, with 64 each warp has its own 16 rows and all
-// keys.  The products run on mma.sync m16n8k16: the tensor work per byte is
-// far below what tcgen05 is for, and the accumulators stay in registers next
-// to the softmax.  Long key ranges are split over CTAs (fp32 partial outputs,
-// merged by a second kernel), so that a few sequences fill the GPU.
+// used for a handful of rows, so the bytes of the cache.  One warp of a CTA
+// fetches tiles of 64 keys into a ring in shared memory by TMA, a box per page
+// (or per 64 slots of a larger one), in the 128-byte swizzle that keeps the four
+// computing warps' reads free of bank conflicts; those wait on the ring's
+// barriers alone.  The rows of the kv head's whole group share the tile.  With up
+// to 16 rows the four warps take 16 keys each and keep maxima, sums and outputs
+// of their own, merged once at the end; with 32 rows they are 2 x 2, with 64 each
+// warp has its own 16 rows and all keys.  The products run on mma.sync m16n8k16:
+// the tensor work per byte is far below what tcgen05 is for, and the accumulators
+// stay in registers next to the softmax.  Long key ranges are split over CTAs
+// (fp32 partial outputs, merged by a second kernel), so that a few sequences fill
+// the GPU.
+//
+// Pages of fewer than 8 slots are smaller than the swizzle's pattern: the same
+// warp then copies them 16 bytes a lane (cp.async) into the same places.
 //
 // E4M3 caches: a thread reads 16 bytes of a key row and converts in
 // registers.  The head elements of Q K^T may be summed in any order, and the
@@ -31,6 +35,8 @@
 // (Keys in bf16 took four instructions a pair, and the kernel 133 us instead of
 // 79 us of HBM time for 262144 keys.)
 #include <type_traits>
+
+#include <cuda.h>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,18 +51,12 @@ static_assert(sizeof(gbn_paged_attention_args) == 12 * 8 + 22 * 8 + 4 * 4, "");
 
 constexpr int kStepThreads = 128;
 constexpr int kStepKeys = 64;          // keys per tile
-constexpr int kSplitPages = 1024;      // page entries a CTA holds
 constexpr int kMaxSplits = 512;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(live ? 16 : 0)
                : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -97,20 +97,21 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Column (16-byte chunk) permutation of the tiles in shared memory.  Two-byte
-// rows: the eight rows of an ldmatrix phase in eight chunks.  E4M3 rows: a
-// 16-byte load's phase reads four chunks of two neighbouring rows (keys) or
-// two chunks of four rows two apart (values); both land in distinct banks.
-template <bool FP8, int CHUNKS>
-__device__ __forceinline__ int swz(int row, int chunk) {
-  if constexpr (!FP8) return chunk ^ (row & 7);
-  else if constexpr (CHUNKS >= 8) return chunk ^ ((((row >> 1) & 3) << 1) ^ ((row & 1) << 2));
-  else return chunk ^ ((row >> 1) & 3);
+// Tiles in shared memory: panels of 128 bytes a row (64 for E4M3 heads of 64) and
+// 64 rows, the 16-byte chunks of a row permuted as TMA's swizzle does it.
+template <int ROW_BYTES>
+__device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
+  if constexpr (ROW_BYTES >= 128)
+    return (chunk >> 3) * (kStepKeys * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+  else
+    return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
 }
 
 template <typename T, bool FP8, int DP>
 struct StepShape {
   static constexpr int kRowBytes = DP * (FP8 ? 1 : 2);
+  static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;
+  static constexpr int kPanels = kRowBytes / kPanelBytes;
   static constexpr int kChunks = kRowBytes / 16;
   static constexpr int kTileBytes = kStepKeys * kRowBytes;  // keys or values of one tile
   // Bytes in flight: 96 KB a CTA of two-byte 128-wide heads, two CTAs an SM.
@@ -120,14 +121,16 @@ struct StepShape {
   static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
   static constexpr int kQPitch = DP * 2 + 16;
   static constexpr int smem(int mt) {
-    return kBody + 16 * mt * kQPitch + kSplitPages * 4 + 4 * 16 * 8 + 16 * mt * 4;
+    return kBody + 16 * mt * kQPitch + 4 * 16 * 8 + 16 * mt * 4 + 2 * kStages * 8;
   }
 };
 
 // T: q's type.  MT: 16-row tiles (1, 2, 4).
 template <typename T, bool FP8, int DP, int MT>
-__global__ void __launch_bounds__(kStepThreads)
-    paged_step_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kStepThreads + 32)
+    paged_step_kernel(const __grid_constant__ AttnParams p,
+                      const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap) {
   using Shape = StepShape<T, FP8, DP>;
   constexpr int WN = 4 / MT;                 // warps over the keys
   constexpr int KW = kStepKeys / WN;         // keys per warp and tile
@@ -136,11 +139,12 @@ __global__ void __launch_bounds__(kStepThreads)
   constexpr int KS = DP / 16;                // steps of 16 head elements
   constexpr bool kQReg = DP <= 128;          // q's fragments stay in registers
   using TP = typename std::conditional<FP8, __half, T>::type;  // type of both products
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* s_q = smem + Shape::kBody;
-  int32_t* s_page = reinterpret_cast<int32_t*>(s_q + 16 * MT * Shape::kQPitch);
-  float2* s_ml = reinterpret_cast<float2*>(s_page + kSplitPages);
+  float2* s_ml = reinterpret_cast<float2*>(s_q + 16 * MT * Shape::kQPitch);
   float* s_qs = reinterpret_cast<float*>(s_ml + 4 * 16);  // E4M3: what a q row's scores are times
+  uint64_t* s_full = reinterpret_cast<uint64_t*>(s_qs + 16 * MT);
+  uint64_t* s_empty = s_full + Shape::kStages;
 
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -163,10 +167,11 @@ __global__ void __launch_bounds__(kStepThreads)
   const int64_t start = lo + static_cast<int64_t>(split) * p.split_len;
   const int k0 = static_cast<int>(min(start, static_cast<int64_t>(max(hi, 0))));
   const int k1 = static_cast<int>(min(start + p.split_len, static_cast<int64_t>(max(hi, 0))));
-  const int ntiles = k1 > k0 ? (k1 - k0 + kStepKeys - 1) / kStepKeys : 0;
+  const int base = k0 & ~(kStepKeys - 1);  // first key of the tiles
+  const int ntiles = k1 > k0 ? (k1 - base + kStepKeys - 1) / kStepKeys : 0;
   if (ntiles == 0 && split > 0) {
     // Nothing here: say so (the merge reads every split's maximum and sum).
-    for (int r = tid; r < rows; r += kStepThreads) {
+    for (int r = tid; r < rows; r += kStepThreads + 32) {
       const int gr = r0 + r;
       const int64_t o = static_cast<int64_t>(s.q0 + gr / p.group) * p.hq + h * p.group + gr % p.group;
       p.part_ml[o * p.splits + split] = make_float2(-INFINITY, 0.f);
@@ -174,24 +179,20 @@ __global__ void __launch_bounds__(kStepThreads)
     return;
   }
 
-  // Pages of this range, checked once.
-  const int page0 = k0 >> p.page_shift;
-  if (ntiles > 0) {
-    const int pages = ((k1 - 1) >> p.page_shift) - page0 + 1;
-    for (int i = tid; i < pages; i += kStepThreads) {
-      int pg = p.table[b * p.table_stride + page0 + i];
-      if (pg < 0 || pg >= p.num_pages) {
-        flag_bad_index();
-        pg = -1;  // its keys read as zero
-      }
-      s_page[i] = pg;
+  const bool by_tma = p.page_shift >= 3;
+  if (tid == 0) {
+#pragma unroll
+    for (int i = 0; i < Shape::kStages; ++i) {
+      mbar_init(&s_full[i], by_tma ? 1 : 32);
+      mbar_init(&s_empty[i], 4);
     }
+    fence_mbar_init();
   }
   // q's rows into shared memory (rows past the end and columns past d: zero).
   {
     constexpr int C = DP / 8;
     const T* q = reinterpret_cast<const T*>(p.q);
-    for (int i = tid; i < 16 * MT * C; i += kStepThreads) {
+    for (int i = tid; warp < 4 && i < 16 * MT * C; i += kStepThreads) {
       const int r = i / C, c = i % C;
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
       if (r < rows && c * 8 < p.d) {
@@ -210,36 +211,94 @@ __global__ void __launch_bounds__(kStepThreads)
   __syncthreads();
 
   const uint32_t ring = smem_u32(smem);
-  const uint8_t* kbase = reinterpret_cast<const uint8_t*>(p.k) + h * p.kh * (FP8 ? 1 : 2);
-  const uint8_t* vbase = reinterpret_cast<const uint8_t*>(p.v) + h * p.vh * (FP8 ? 1 : 2);
-  auto load_tile = [&](int t) {
-    if (t < ntiles) {
-      const uint32_t kd = ring + (t % Shape::kStages) * 2 * Shape::kTileBytes;
-      const uint32_t vd = kd + Shape::kTileBytes;
-      const int base = k0 + t * kStepKeys;
+  bool ok = true;
+  if (warp == 4) {
+    // ------------------------------------------------ fetch
+    const int page = 1 << p.page_shift;
+    const int32_t* tab = p.table + b * p.table_stride;
+    const int e_last = ntiles > 0 ? (k1 - 1) >> p.page_shift : 0;
+    if (by_tma) {
+      const int box = min(page, kStepKeys), boxes = kStepKeys / box;  // at most 8
+      const int zero_page = max(1, static_cast<int>(p.num_pages));    // one past: zeros
+      // This lane's box: its table entry is read one tile ahead.
+      auto wanted = [&](int t) {
+        const int key = base + t * kStepKeys + lane * box;
+        return lane < boxes && key < k1 && key + box > k0;
+      };
+      auto entry = [&](int t) {
+        const int key = base + t * kStepKeys + lane * box;
+        return wanted(t) ? tab[min(key >> p.page_shift, e_last)] : 0;
+      };
+      int cur = ntiles > 0 ? entry(0) : 0;
+      int t = 0;
+      for (; t < ntiles; ++t) {
+        const int st = t % Shape::kStages, use = t / Shape::kStages;
+        const int next = t + 1 < ntiles ? entry(t + 1) : 0;
+        if (use > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_empty[st], (use - 1) & 1));
+        if (!ok) break;
+        int pg = zero_page;
+        if (wanted(t)) {
+          if (cur >= 0 && cur < p.num_pages) pg = cur;
+          else flag_bad_index();  // its keys read as zero
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&s_full[st], 2 * Shape::kTileBytes);
+        __syncwarp();
+        if (lane < boxes) {
+          const int slot = (base + t * kStepKeys + lane * box) & (page - 1);
+          const uint32_t dst = ring + st * 2 * Shape::kTileBytes + lane * box * Shape::kPanelBytes;
 #pragma unroll
-      for (int i = 0; i < kStepKeys * Shape::kChunks / kStepThreads; ++i) {
-        const int id = tid + i * kStepThreads;
-        const int r = id / Shape::kChunks, c = id % Shape::kChunks;
-        const int j = base + r;
-        const int pg = j < k1 ? s_page[(j >> p.page_shift) - page0] : -1;
-        const bool live = pg >= 0 && c * 16 < p.d * (FP8 ? 1 : 2);
-        const int slot = j & ((1 << p.page_shift) - 1);
-        const uint32_t at = r * Shape::kRowBytes + swz<FP8, Shape::kChunks>(r, c) * 16;
-        const int64_t ko = live ? (pg * p.kp + slot * p.ks) * (FP8 ? 1 : 2) + c * 16 : 0;
-        const int64_t vo = live ? (pg * p.vp + slot * p.vs) * (FP8 ? 1 : 2) + c * 16 : 0;
-        cp_async16(kd + at, kbase + ko, live);
-        cp_async16(vd + at, vbase + vo, live);
+          for (int pn = 0; pn < Shape::kPanels; ++pn) {
+            const int c0 = pn * (Shape::kPanelBytes / (FP8 ? 1 : 2));
+            tma_box(dst + pn * kStepKeys * 128, &kmap, c0, h, slot, pg, &s_full[st]);
+            tma_box(dst + Shape::kTileBytes + pn * kStepKeys * 128, &vmap, c0, h, slot, pg,
+                    &s_full[st]);
+          }
+        }
+        cur = next;
       }
+      if (!ok)  // leave no copy in flight behind
+        for (int i = max(0, t - Shape::kStages); i < t; ++i)
+          mbar_wait(&s_full[i % Shape::kStages], (i / Shape::kStages) & 1);
+    } else {
+      const uint8_t* kbase = reinterpret_cast<const uint8_t*>(p.k) + h * p.kh * (FP8 ? 1 : 2);
+      const uint8_t* vbase = reinterpret_cast<const uint8_t*>(p.v) + h * p.vh * (FP8 ? 1 : 2);
+      for (int t = 0; t < ntiles; ++t) {
+        const int st = t % Shape::kStages, use = t / Shape::kStages;
+        if (use > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_empty[st], (use - 1) & 1));
+        if (!ok) break;
+        const uint32_t kd = ring + st * 2 * Shape::kTileBytes;
+        for (int i = lane; i < kStepKeys * Shape::kChunks; i += 32) {
+          const int r = i / Shape::kChunks, c = i % Shape::kChunks;
+          const int j = base + t * kStepKeys + r;
+          int pg = -1;
+          if (j >= k0 && j < k1) {
+            pg = tab[j >> p.page_shift];
+            if (pg < 0 || pg >= p.num_pages) {
+              flag_bad_index();
+              pg = -1;
+            }
+          }
+          const bool live = pg >= 0 && c * 16 < p.d * (FP8 ? 1 : 2);
+          const int slot = j & (page - 1);
+          const int64_t ko = live ? (pg * p.kp + slot * p.ks) * (FP8 ? 1 : 2) + c * 16 : 0;
+          const int64_t vo = live ? (pg * p.vp + slot * p.vs) * (FP8 ? 1 : 2) + c * 16 : 0;
+          const uint32_t at = tile_at<Shape::kRowBytes>(r, c);
+          cp_async16(kd + at, kbase + ko, live);
+          cp_async16(kd + Shape::kTileBytes + at, vbase + vo, live);
+        }
+        // Arrives when this lane's copies so far have landed.
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                         smem_u32(&s_full[st]))
+                     : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int t = 0; t < Shape::kStages - 1; ++t) load_tile(t);
+    if (!ok && lane == 0) flag_wait_timeout();
+  }
 
   // q fragments.  Two-byte caches: the standard order.  E4M3: step ks of the
   // 64-column block takes, for lane column qc, elements 16 qc + 4 (ks % 4).. + 3.
-  const uint32_t qbase = smem_u32(s_q) + wm * 16 * Shape::kQPitch;
+  const uint32_t qbase = smem_u32(s_q) + (wm & (MT - 1)) * 16 * Shape::kQPitch;
   auto load_q = [&](int ks, uint32_t* a) {
     if constexpr (!FP8) {
       ldsm4(a, qbase + (lane & 15) * Shape::kQPitch + ks * 32 + (lane >> 4) * 16);
@@ -263,18 +322,18 @@ __global__ void __launch_bounds__(kStepThreads)
   int rlo[2], rhi[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const int r = wm * 16 + qr + 8 * e;
+    const int r = (wm & (MT - 1)) * 16 + qr + 8 * e;
     const int i = (r0 + min(r, rows - 1)) / p.group;
-    rlo[e] = row_low(p, s, i);
-    rhi[e] = row_high(p, s, i);
+    rlo[e] = max(row_low(p, s, i), k0);
+    rhi[e] = min(row_high(p, s, i), k1);
   }
   // Keys that every row of the CTA keeps need no test.
-  const int all_lo = row_low(p, s, i1), all_hi = min(row_high(p, s, i0), k1);
+  const int all_lo = max(row_low(p, s, i1), k0), all_hi = min(row_high(p, s, i0), k1);
 
   float scale[2] = {p.scale_log2, p.scale_log2};
   if constexpr (FP8) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) scale[e] *= *p.k_scale_inv * s_qs[wm * 16 + qr + 8 * e];
+    for (int e = 0; e < 2; ++e) scale[e] *= *p.k_scale_inv * s_qs[(wm & (MT - 1)) * 16 + qr + 8 * e];
   }
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   float o[DT][4];
@@ -283,13 +342,29 @@ __global__ void __launch_bounds__(kStepThreads)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
 
-  for (int t = 0; t < ntiles; ++t) {
-    cp_async_wait<Shape::kStages - 2>();
-    __syncthreads();  // tile t is here, and every warp is done with tile t - 1
-    load_tile(t + Shape::kStages - 1);
-    const uint32_t kd = ring + (t % Shape::kStages) * 2 * Shape::kTileBytes;
+  for (int t = 0; warp < 4 && t < ntiles; ++t) {
+    const int st = t % Shape::kStages;
+    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[st], (t / Shape::kStages) & 1));
+    if (!ok) {
+      if (lane == 0) flag_wait_timeout();
+      break;
+    }
+    const uint32_t kd = ring + st * 2 * Shape::kTileBytes;
     const uint32_t vd = kd + Shape::kTileBytes;
     const int kw = wn * KW;  // this warp's first key row in the tile
+    const bool cut = base + t * kStepKeys < k0 || base + (t + 1) * kStepKeys > k1;
+    if (cut) {
+      // A weight of 0 times what stands in a slot outside the range must be 0.
+      // (Warps that share rows all write the same zeros before they read.)
+      uint8_t* v = smem + st * 2 * Shape::kTileBytes + Shape::kTileBytes;
+      for (int i = lane; i < KW * Shape::kChunks; i += 32) {
+        const int r = kw + i / Shape::kChunks, key = base + t * kStepKeys + r;
+        if (key < k0 || key >= k1)
+          *reinterpret_cast<uint4*>(v + tile_at<Shape::kRowBytes>(r, i % Shape::kChunks)) =
+              make_uint4(0u, 0u, 0u, 0u);
+      }
+      __syncwarp();
+    }
     float sc[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -306,7 +381,7 @@ __global__ void __launch_bounds__(kStepThreads)
           const int row = kw + n * 8 + (lane & 7) + ((lane >> 4) << 3);
           const int ch = ks * 2 + ((lane >> 3) & 1);
           uint32_t kb[4];
-          ldsm4(kb, kd + row * Shape::kRowBytes + swz<FP8, Shape::kChunks>(row, ch) * 16);
+          ldsm4(kb, kd + tile_at<Shape::kRowBytes>(row, ch));
           mma16816<TP>(sc[n], af, kb[0], kb[1]);
           mma16816<TP>(sc[n + 1], af, kb[2], kb[3]);
         }
@@ -317,8 +392,7 @@ __global__ void __launch_bounds__(kStepThreads)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const int row = kw + n * 8 + qr;
-          const uint4 u = lds16(kd + row * Shape::kRowBytes +
-                                swz<FP8, Shape::kChunks>(row, blk * 4 + qc) * 16);
+          const uint4 u = lds16(kd + tile_at<Shape::kRowBytes>(row, blk * 4 + qc));
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int s4 = 0; s4 < 4; ++s4) {
@@ -332,7 +406,7 @@ __global__ void __launch_bounds__(kStepThreads)
     }
 
     // Scale, mask, running maximum.
-    const int jbase = k0 + t * kStepKeys + kw;
+    const int jbase = base + t * kStepKeys + kw;
     float mx[2] = {m[0], m[1]};
     if (jbase >= all_lo && jbase + KW <= all_hi) {
 #pragma unroll
@@ -348,7 +422,7 @@ __global__ void __launch_bounds__(kStepThreads)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = jbase + n * 8 + qc * 2 + (e & 1);
-          const bool keep = j >= rlo[e >> 1] && j < rhi[e >> 1] && j < k1;
+          const bool keep = j >= rlo[e >> 1] && j < rhi[e >> 1];
           sc[n][e] = keep ? sc[n][e] * scale[e >> 1] : -INFINITY;
           mx[e >> 1] = fmaxf(mx[e >> 1], sc[n][e]);
         }
@@ -395,8 +469,7 @@ __global__ void __launch_bounds__(kStepThreads)
         for (int d = 0; d < DT; d += 2) {
           const int row = kr + (lane & 15);
           uint32_t vb[4];
-          ldsm4t(vb, vd + row * Shape::kRowBytes +
-                         swz<FP8, Shape::kChunks>(row, d + (lane >> 4)) * 16);
+          ldsm4t(vb, vd + tile_at<Shape::kRowBytes>(row, d + (lane >> 4)));
           mma16816<TP>(o[d], a, vb[0], vb[1]);
           mma16816<TP>(o[d + 1], a, vb[2], vb[3]);
         }
@@ -411,12 +484,10 @@ __global__ void __launch_bounds__(kStepThreads)
           for (int e = 0; e < 4; ++e) {
             const int row = kr + qc * 2 + (e & 1) + (e >> 1) * 8;
             if constexpr (CB == 16) {
-              const uint4 u = lds16(vd + row * Shape::kRowBytes +
-                                    swz<FP8, Shape::kChunks>(row, blk * 8 + qr) * 16);
+              const uint4 u = lds16(vd + tile_at<Shape::kRowBytes>(row, blk * 8 + qr));
               w[e][0] = u.x; w[e][1] = u.y; w[e][2] = u.z; w[e][3] = u.w;
             } else {
-              const uint2 u = lds8(vd + row * Shape::kRowBytes +
-                                   swz<FP8, Shape::kChunks>(row, qr >> 1) * 16 + (qr & 1) * 8);
+              const uint2 u = lds8(vd + tile_at<Shape::kRowBytes>(row, qr >> 1) + (qr & 1) * 8);
               w[e][0] = u.x; w[e][1] = u.y;
             }
           }
@@ -435,6 +506,10 @@ __global__ void __launch_bounds__(kStepThreads)
         }
       }
     }
+    if (cut) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the zeros, before the next copy
+    __syncwarp();
+    if (lane == 0)
+      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&s_empty[st])) : "memory");
   }
 
   // Merge the warps of each row tile through shared memory.
@@ -443,11 +518,10 @@ __global__ void __launch_bounds__(kStepThreads)
     l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
     l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
   }
-  cp_async_wait<0>();
   __syncthreads();  // the ring is free
-  float* s_o = reinterpret_cast<float*>(smem) + warp * 16 * DP;
+  float* s_o = reinterpret_cast<float*>(smem) + (warp & 3) * 16 * DP;
 #pragma unroll
-  for (int d = 0; d < DT; ++d)
+  for (int d = 0; warp < 4 && d < DT; ++d)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int r = qr + 8 * (e >> 1);
@@ -460,14 +534,14 @@ __global__ void __launch_bounds__(kStepThreads)
       }
       s_o[r * DP + col] = o[d][e];
     }
-  if (qc == 0) {
+  if (warp < 4 && qc == 0) {
     s_ml[warp * 16 + qr] = make_float2(m[0], l[0]);
     s_ml[warp * 16 + qr + 8] = make_float2(m[1], l[1]);
   }
   __syncthreads();
   const float vscale = FP8 ? *p.v_scale_inv : 1.f;
   constexpr int Q4 = DP / 8;  // groups of 8 columns per row
-  for (int i = tid; i < rows * Q4; i += kStepThreads) {
+  for (int i = tid; i < rows * Q4; i += kStepThreads + 32) {
     const int r = i / Q4, c = (i % Q4) * 8;
     if (c >= p.d) continue;
     const int w0 = (r / 16) * WN;
@@ -591,11 +665,23 @@ __global__ void __launch_bounds__(kMergeThreads)
 
 template <typename T, bool FP8, int DP, int MT>
 cudaError_t launch_step(const AttnParams& p, int64_t grid, cudaStream_t st) {
-  constexpr int smem = StepShape<T, FP8, DP>::smem(MT);
+  using Shape = StepShape<T, FP8, DP>;
+  constexpr int smem = Shape::smem(MT);
   auto k = paged_step_kernel<T, FP8, DP, MT>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(kStepThreads), smem, st, p);
+  CUtensorMap km = {}, vm = {};
+  if (p.page_shift >= 3) {
+    constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int es = FP8 ? 1 : 2;
+    if (!make_cache_map(&km, p.k, es, bf16, Shape::kPanelBytes / es, kStepKeys, true, p, p.kp, p.ks,
+                        p.kh) ||
+        !make_cache_map(&vm, p.v, es, bf16, Shape::kPanelBytes / es, kStepKeys, true, p, p.vp, p.vs,
+                        p.vh))
+      return cudaErrorInvalidValue;
+  }
+  return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(kStepThreads + 32), smem, st, p, km,
+                    vm);
 }
 template <typename T, bool FP8, int DP>
 cudaError_t launch_step_mt(const AttnParams& p, int mt, int64_t grid, cudaStream_t st) {
@@ -654,11 +740,8 @@ AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t d, int64
   int64_t splits = tiles >= want ? 1 : ceil_div(want, tiles > 0 ? tiles : 1);
   const int64_t most = ceil_div(range, a.prefill ? 512 : 256);
   if (splits > most) splits = most;
-  const int64_t cap = a.prefill ? int64_t(1) << 30 : (int64_t(kSplitPages) - 1) << page_shift;
-  if (splits < ceil_div(range, cap)) splits = ceil_div(range, cap);
   if (splits < 1) splits = 1;
   int64_t len = ceil_div(ceil_div(range, splits), step) * step;
-  if (len > cap) len = cap;
   if (len < 1) len = 1;
   a.split_len = static_cast<int>(len);
   a.splits = static_cast<int>(range > 0 ? ceil_div(range, len) : 1);

@@ -3,6 +3,7 @@
 
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "gbnorm.h"
@@ -39,6 +40,12 @@ struct AttnParams {
   int split_len;
   float scale_log2;    // scale * log2(e)
 };
+
+// Tensor map of a cache as [pages][slots][heads][d]: boxes of `inner` elements of
+// one head in min(page, rows) slots, in the 128-byte (64-byte, where a row is no
+// longer) swizzle or plain.  False if the driver refuses it.
+bool make_cache_map(CUtensorMap* map, const void* base, int esize, bool bf16, int inner, int rows,
+                    bool swizzle, const AttnParams& p, int64_t sp, int64_t ss, int64_t sh);
 
 // The tcgen05 kernel for many rows per kv head (two-byte caches and E4M3,
 // head sizes up to 128).

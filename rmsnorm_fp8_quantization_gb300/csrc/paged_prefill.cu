@@ -202,15 +202,6 @@ __host__ __device__ constexpr uint32_t instr_desc(int type, int m, int n, int bm
          (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
-                                        int c3, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // Three-input maximum (a number wins over NaN, as fmaxf).
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -790,29 +781,6 @@ EncodeFn encoder() {
   return fn;
 }
 
-// A cache as [pages][slots][heads][d], boxes of min(page, 128) slots of one head:
-// 64 two-byte elements, or (E4M3) dp codes.
-bool make_map(CUtensorMap* map, const void* base, int esize, bool bf16, int dp, const AttnParams& p,
-              int64_t sp, int64_t ss, int64_t sh) {
-  EncodeFn enc = encoder();
-  if (!enc) return false;
-  const cuuint64_t page = cuuint64_t(1) << p.page_shift;
-  const cuuint64_t dims[4] = {cuuint64_t(p.d), cuuint64_t(p.hkv), page,
-                              cuuint64_t(p.num_pages > 0 ? p.num_pages : 1)};
-  // Dimensions of one element may have any stride: give those a valid one.
-  const cuuint64_t strides[3] = {p.hkv > 1 ? cuuint64_t(sh) * esize : 16, page > 1 ? cuuint64_t(ss) * esize : 16,
-                                 p.num_pages > 1 ? cuuint64_t(sp) * esize : 16};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(esize == 1 ? dp : 64), 1, static_cast<cuuint32_t>(page < 128 ? page : 128), 1};
-  const cuuint32_t step[4] = {1, 1, 1, 1};
-  const CUtensorMapDataType type = esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                   : bf16     ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  return enc(map, type, 4,
-             const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             esize == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <typename T, bool FP8, int DP>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm,
                    cudaStream_t st) {
@@ -828,13 +796,39 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap
 
 }  // namespace
 
+bool make_cache_map(CUtensorMap* map, const void* base, int esize, bool bf16, int inner, int rows,
+                    bool swizzle, const AttnParams& p, int64_t sp, int64_t ss, int64_t sh) {
+  EncodeFn enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t es = static_cast<cuuint64_t>(esize), page = cuuint64_t(1) << p.page_shift;
+  const cuuint64_t pages = cuuint64_t(p.num_pages > 0 ? p.num_pages : 1);
+  const cuuint64_t dims[4] = {cuuint64_t(p.d), cuuint64_t(p.hkv), page, pages};
+  // Dimensions of one element may have any stride: give those a valid one.
+  const cuuint64_t strides[3] = {p.hkv > 1 ? cuuint64_t(sh) * es : 16,
+                                 page > 1 ? cuuint64_t(ss) * es : 16,
+                                 pages > 1 ? cuuint64_t(sp) * es : 16};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(inner), 1,
+                             static_cast<cuuint32_t>(page < cuuint64_t(rows) ? page : rows), 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  const CUtensorMapDataType type = esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : bf16     ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUtensorMapSwizzle sw = !swizzle              ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                : inner * esize >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                       : CU_TENSOR_MAP_SWIZZLE_64B;
+  return enc(map, type, 4, const_cast<void*>(base), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_paged_prefill(const AttnParams& p, gbn_dtype dtype, gbn_dtype cache_dtype,
                                  cudaStream_t stream) {
   const bool fp8 = cache_dtype == GBN_E4M3, bf16 = dtype == GBN_BF16;
   CUtensorMap km = {}, vm = {};
   const int esize = fp8 ? 1 : 2, dp = p.d <= 64 ? 64 : 128;
-  if (!make_map(&km, p.k, esize, bf16, dp, p, p.kp, p.ks, p.kh) ||
-      !make_map(&vm, p.v, esize, bf16, dp, p, p.vp, p.vs, p.vh))
+  const int inner = fp8 ? dp : 64;
+  if (!make_cache_map(&km, p.k, esize, bf16, inner, kKeys, !fp8, p, p.kp, p.ks, p.kh) ||
+      !make_cache_map(&vm, p.v, esize, bf16, inner, kKeys, !fp8, p, p.vp, p.vs, p.vh))
     return cudaErrorInvalidValue;
   if (p.d <= 64) {
     if (fp8)

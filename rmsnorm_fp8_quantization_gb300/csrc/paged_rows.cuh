@@ -50,6 +50,16 @@ __device__ __forceinline__ float ex2(float a) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
   return r;
 }
+// One box of a tensor map into shared memory, reported as transactions on `bar`.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                        int c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Two E4M3 codes (low 16 bits) to a pair of f16, exact; NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
   uint32_t r;
