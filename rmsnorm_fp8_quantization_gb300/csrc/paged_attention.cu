@@ -120,6 +120,9 @@ struct StepShape {
   static constexpr int kMerge = 4 * 16 * DP * 4;  // outputs of the four warps, over the ring
   static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
   static constexpr int kQPitch = DP * 2 + 16;
+  // CTAs an SM, by shared memory and registers (E4M3 heads of 128 in three CTAs
+  // of 128 registers spill: 111 us for 262144 keys against 95 in two).
+  static constexpr int kResident = DP <= 64 ? 3 : DP <= 128 ? 2 : 1;
   static constexpr int smem(int mt) {
     return kBody + 16 * mt * kQPitch + 4 * 16 * 8 + 16 * mt * 4 + 2 * kStages * 8;
   }
@@ -127,7 +130,7 @@ struct StepShape {
 
 // T: q's type.  MT: 16-row tiles (1, 2, 4).
 template <typename T, bool FP8, int DP, int MT>
-__global__ void __launch_bounds__(kStepThreads + 32)
+__global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8, DP>::kResident : 1)
     paged_step_kernel(const __grid_constant__ AttnParams p,
                       const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
@@ -722,7 +725,9 @@ AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t d, int64
   // The tcgen05 kernel from the first size on that fills half a tile of it;
   // its boxes are at least 8 slots (one swizzle atom).
   a.prefill = r > 64 && d <= 128 && page_shift >= 3;
-  a.rows = a.prefill ? kPrefillRows : r <= 16 ? 16 : r <= 32 ? 32 : 64;
+  // 33 to 64 rows as two tiles of 32: a step is shorter (each warp has half of
+  // the keys) and the second read of the keys comes from L2.
+  a.rows = a.prefill ? kPrefillRows : r <= 16 ? 16 : r <= 64 ? 32 : 64;
   a.row_tiles = static_cast<int>(ceil_div(r, a.rows));
   // Longest key range of a row tile.
   int64_t range = max_kv;
@@ -733,13 +738,27 @@ AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t d, int64
   }
   const int64_t tiles = batches * hkv * a.row_tiles;
   const int64_t step = a.prefill ? kPrefillKeys : kStepKeys;
-  // Splits.  Few rows: enough CTAs for several rounds of two per SM, at least
-  // 256 keys each.  Prefill (one CTA per SM): two rounds where the row tiles
-  // alone do not fill one, at least 512 keys each.
-  const int64_t want = a.prefill ? (tiles < sms ? 2ll * sms : 0) : 8ll * sms;
-  int64_t splits = tiles >= want ? 1 : ceil_div(want, tiles > 0 ? tiles : 1);
-  const int64_t most = ceil_div(range, a.prefill ? 512 : 256);
-  if (splits > most) splits = most;
+  int64_t splits = 1;
+  if (a.prefill) {
+    // One CTA per SM: two rounds where the row tiles alone do not fill one, at
+    // least 512 keys each.
+    if (tiles < sms) splits = ceil_div(2ll * sms, tiles > 0 ? tiles : 1);
+    const int64_t most = ceil_div(range, 512);
+    if (splits > most) splits = most;
+  } else if (range > 320) {
+    // CTAs for so many rounds of the SMs, at the longest range.  One sequence:
+    // exactly one round (131072 keys, 8 kv heads, bf16: 82-87 us; 1.5 rounds 88 to
+    // 106).  Several may differ in length, and the long ones' CTAs are then what
+    // is left: 8 sequences of 2000-16000 keys 51 us at 1.7 rounds, 64 at 0.8;
+    // 64 sequences 350 us at 10 rounds, 377 at 3.4.  At least 192 keys each, and
+    // none up to 320 (a second kernel merges: 3-4 us).
+    const int64_t slots = sms * (d <= 64 ? 3 : d <= 128 ? 2 : 1);
+    const int64_t rounds2 = batches == 1 ? 2 : tiles * 4 < slots ? 3 : tiles < slots ? 8 : 20;
+    splits = rounds2 * slots / (2 * (tiles > 0 ? tiles : 1));
+    const int64_t most = ceil_div(range, 192);
+    if (splits > most) splits = most;
+    if (splits > kMaxSplits) splits = kMaxSplits;
+  }
   if (splits < 1) splits = 1;
   int64_t len = ceil_div(ceil_div(range, splits), step) * step;
   if (len < 1) len = 1;
