@@ -39,7 +39,7 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeUnits = 4;                       // units per thread
 constexpr int kRopeItems = kRopeThreads * kRopeUnits;
 constexpr int kRopeMaxTokens = 64;                  // tokens per CTA
-constexpr int kRopeTrig = 2048;                     // (cos, sin) entries per CTA (16 KB)
+constexpr int kRopeTrig = 2048;                     // (cos, sin) pairs per CTA (16 KB)
 
 struct Strided {  // element strides
   int64_t b, s, h;
@@ -186,7 +186,11 @@ __device__ __forceinline__ void put(void* base, int64_t at, const float* f, floa
 template <typename T, int V, bool APPEND, bool FP8>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
   pdl_begin();
-  __shared__ float2 trig[kRopeTrig];
+  // cos and sin of each token's pairs, in the order in which they are read: W
+  // consecutive pairs of a unit side by side, then the same of the next unit, so
+  // that neighbouring lanes read neighbouring vectors.
+  constexpr int W = V < 4 ? V : 4, K = V / W;
+  __shared__ __align__(16) float trig[2 * kRopeTrig];
   __shared__ int64_t s_pos[kRopeMaxTokens];   // APPEND: position, or -1: leave the token alone
   __shared__ int64_t s_page[kRopeMaxTokens];  // APPEND: page
   const int tid = threadIdx.x;
@@ -199,16 +203,30 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const int nrot = p.rot / (2 * V);  // units that turn
   const int half = p.layout == GBN_ROPE_HALF ? p.rot / 2 : 0;
 
-  // Token and head row of this thread's unit i; false past the end.
-  auto locate = [&](int i, int& tok, int& row, int& u) {
-    const uint32_t item = tid + i * kRopeThreads;
-    const uint32_t r = div_by(item, p.units_mul);
-    u = static_cast<int>(item - r * p.units);
-    tok = static_cast<int>(div_by(r, p.rows_mul));
-    row = static_cast<int>(r) - tok * p.rows_per_cta;
-    return tok < ntok && row < rows;
+  // Batch and place of the CTA's first token: one division, in 32 bits where it
+  // fits (64 bits take a hundred instructions).
+  int64_t b0 = 0, s0 = t0;
+  if (!APPEND && p.seq != p.tokens) {
+    b0 = p.tokens <= INT32_MAX
+             ? static_cast<int64_t>(static_cast<uint32_t>(t0) / static_cast<uint32_t>(p.seq))
+             : t0 / p.seq;
+    s0 = t0 - b0 * p.seq;
+  }
+  auto place_of = [&](int tok, int64_t& bi, int64_t& si) {
+    bi = b0;
+    si = s0 + tok;
+    if (!APPEND && si >= p.seq) {
+      if (p.seq >= kRopeMaxTokens) {
+        ++bi;
+        si -= p.seq;
+      } else {
+        const uint32_t n = static_cast<uint32_t>(si) / static_cast<uint32_t>(p.seq);
+        bi += n;
+        si -= static_cast<int64_t>(n) * p.seq;
+      }
+    }
   };
-  // Element offsets of the unit's two vectors within its head.
+  // Element offsets of a unit's two vectors within its head.
   auto places = [&](int u, int& a, int& b) {
     if (u < nrot) {
       a = half ? u * V : 2 * u * V;
@@ -219,25 +237,30 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     }
   };
 
+  // Token (6 bits), head row (14) and unit of this thread's items; -1: none.
+  int code[kRopeUnits];
   Raw<T, V> va[kRopeUnits], vb[kRopeUnits];
 #pragma unroll
   for (int i = 0; i < kRopeUnits; ++i) {
-    int tok, row, u, a, b;
-    if (!locate(i, tok, row, u)) continue;
-    places(u, a, b);
+    const uint32_t item = tid + i * kRopeThreads;
+    const uint32_t r = div_by(item, p.units_mul);
+    const int u = static_cast<int>(item - r * p.units);
+    const int tok = static_cast<int>(div_by(r, p.rows_mul));
+    int row = static_cast<int>(r) - tok * p.rows_per_cta;
+    code[i] = -1;
+    if (tok >= ntok || row >= rows) continue;
     row += row0;
-    const int64_t t = t0 + tok;
-    int64_t bi = 0, si = t;
-    if constexpr (!APPEND) {
-      bi = p.seq == p.tokens ? 0 : t / p.seq;
-      si = t - bi * p.seq;
-    }
-    const T* src;
-    if (row < p.hq) src = reinterpret_cast<const T*>(p.q) + bi * p.qs.b + si * p.qs.s + row * p.qs.h;
-    else if (row < p.hq + p.hk)
-      src = reinterpret_cast<const T*>(p.k) + bi * p.ks.b + si * p.ks.s + (row - p.hq) * p.ks.h;
-    else
-      src = reinterpret_cast<const T*>(p.v) + si * p.vs.s + (row - p.hq - p.hk) * p.vs.h;
+    code[i] = tok | (row << 6) | (u << 20);
+    int a, b;
+    places(u, a, b);
+    int64_t bi, si;
+    place_of(tok, bi, si);
+    const bool is_q = row < p.hq;
+    const bool is_v = APPEND && row >= p.hq + p.hk;
+    const Strided& st = is_q ? p.qs : is_v ? p.vs : p.ks;
+    const int h = is_q ? row : is_v ? row - p.hq - p.hk : row - p.hq;
+    const T* src = reinterpret_cast<const T*>(is_q ? p.q : is_v ? p.v : p.k) + si * st.s + h * st.h;
+    if (!APPEND) src += bi * st.b;
     va[i].load(src + a);
     if (b < p.d) vb[i].load(src + b);
   }
@@ -271,22 +294,25 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const int pairs = p.rot / 2;
   if (p.inv_freq != nullptr) {
     for (int i = tid; i < ntok * pairs; i += kRopeThreads) {
-      const int tok = i / pairs;
+      const int tok = static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(pairs));
       const int pr = i - tok * pairs;
       int64_t pos;
       if constexpr (APPEND) {
         pos = s_pos[tok];
       } else {
-        const int64_t t = t0 + tok;
-        const int64_t bi = p.seq == p.tokens ? 0 : t / p.seq;
-        const int64_t si = t - bi * p.seq;
+        int64_t bi, si;
+        place_of(tok, bi, si);
         if (p.positions == nullptr) pos = si;
         else if (p.pos_bytes == 8)
           pos = reinterpret_cast<const int64_t*>(p.positions)[bi * p.pos_stride + si];
         else
           pos = reinterpret_cast<const int32_t*>(p.positions)[bi * p.pos_stride + si];
       }
-      trig[i] = turn(p.inv_freq[pr], pos, p.mscale, p.sign);
+      const float2 cs = turn(p.inv_freq[pr], pos, p.mscale, p.sign);
+      const int u = pr / V, e = pr % V;
+      float* at = trig + ((tok * 2 * K + e / W) * nrot + u) * W + e % W;
+      at[0] = cs.x;
+      at[K * nrot * W] = cs.y;
     }
   }
   __syncthreads();
@@ -298,50 +324,49 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   }
 #pragma unroll
   for (int i = 0; i < kRopeUnits; ++i) {
-    int tok, row, u, a, b;
-    if (!locate(i, tok, row, u)) continue;
+    if (code[i] < 0) continue;
+    const int tok = code[i] & 63, row = (code[i] >> 6) & 0x3FFF, u = code[i] >> 20;
     if constexpr (APPEND) {
       if (s_pos[tok] < 0) continue;
     }
+    int a, b;
     places(u, a, b);
-    row += row0;
     float fa[V], fb[V];
     va[i].floats(fa);
     if (b < p.d) vb[i].floats(fb);
     if (u < nrot && row < p.hq + p.hk && p.inv_freq != nullptr) {
-      const float2* tr = trig + tok * pairs;
-      if (half) {
-        const float2* c = tr + u * V;
+      float c[V], sn[V];
+      const float* at = trig + (tok * 2 * K * nrot + u) * W;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          c[k * W + e] = at[k * nrot * W + e];
+          sn[k * W + e] = at[(K + k) * nrot * W + e];
+        }
+      if (half || V == 1) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float x = fa[e], y = fb[e];
-          fa[e] = x * c[e].x - y * c[e].y;
-          fb[e] = x * c[e].y + y * c[e].x;
+          fa[e] = x * c[e] - y * sn[e];
+          fb[e] = x * sn[e] + y * c[e];
         }
       } else {
-        const float2* c = tr + u * V;  // 2V elements from 2uV: V pairs
-        if constexpr (V == 1) {
-          const float x = fa[0], y = fb[0];
-          fa[0] = x * c[0].x - y * c[0].y;
-          fb[0] = x * c[0].y + y * c[0].x;
-        } else {
+        // 2 V elements from 2 u V: V pairs side by side.
 #pragma unroll
-          for (int e = 0; e < V / 2; ++e) {
-            const float x = fa[2 * e], y = fa[2 * e + 1];
-            fa[2 * e] = x * c[e].x - y * c[e].y;
-            fa[2 * e + 1] = x * c[e].y + y * c[e].x;
-            const float2 c2 = c[V / 2 + e];
-            const float z = fb[2 * e], w = fb[2 * e + 1];
-            fb[2 * e] = z * c2.x - w * c2.y;
-            fb[2 * e + 1] = z * c2.y + w * c2.x;
-          }
+        for (int e = 0; e < V / 2; ++e) {
+          const float x = fa[2 * e], y = fa[2 * e + 1];
+          fa[2 * e] = x * c[e] - y * sn[e];
+          fa[2 * e + 1] = x * sn[e] + y * c[e];
+          const float z = fb[2 * e], w = fb[2 * e + 1];
+          fb[2 * e] = z * c[V / 2 + e] - w * sn[V / 2 + e];
+          fb[2 * e + 1] = z * sn[V / 2 + e] + w * c[V / 2 + e];
         }
       }
     }
-    const int64_t t = t0 + tok;
     if constexpr (APPEND) {
       if (row < p.hq) {
-        const int64_t at = t * p.qo.s + row * p.qo.h;
+        const int64_t at = (t0 + tok) * p.qo.s + row * p.qo.h;
         put<T, V, false>(p.q_out, at + a, fa, 1.f);
         if (b < p.d) put<T, V, false>(p.q_out, at + b, fb, 1.f);
       } else {
@@ -356,8 +381,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
         if (b < p.d) put<T, V, FP8>(dst, at + b, fb, sc);
       }
     } else {
-      const int64_t bi = p.seq == p.tokens ? 0 : t / p.seq;
-      const int64_t si = t - bi * p.seq;
+      int64_t bi, si;
+      place_of(tok, bi, si);
       const bool is_q = row < p.hq;
       const Strided& st = is_q ? p.qo : p.ko;
       void* dst = is_q ? p.q_out : p.k_out;
