@@ -443,8 +443,10 @@ gbn_status gbn_paged_append(const gbn_paged_append_args* args, cudaStream_t stre
  * (f16 for E4M3 caches) for the product with the values.  Deterministic.
  * head_dim: a multiple of 16 up to GBN_PAGED_MAX_DIM; scale finite and
  * positive; q_heads a multiple of kv_heads; tokens * q_heads < 2^31; max_kv
- * up to 2^30 (else GBN_ERR_SHAPE).  All base pointers 16-byte aligned and all
- * strides multiples of 16 bytes (else GBN_ERR_ALIGNMENT). */
+ * up to 2^30, the caches' strides in (0, 2^40) bytes (else GBN_ERR_SHAPE).  All
+ * base pointers 16-byte aligned and all strides multiples of 16 bytes (else
+ * GBN_ERR_ALIGNMENT).  A key that a row does not keep has no part in it,
+ * whatever stands in its slot (infinities and NaN among them). */
 gbn_status gbn_paged_attention_workspace_size(int64_t tokens, int64_t batches, int64_t q_heads,
                                               int64_t kv_heads, int64_t head_dim,
                                               int64_t page_size, int64_t table_pages,

@@ -567,6 +567,15 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
     const int gr = r0 + r;
     const int token = s.q0 + gr / p.group, head = h * p.group + gr % p.group;
     const int64_t ro = static_cast<int64_t>(token) * p.hq + head;
+    bool nan = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) nan |= acc[e] != acc[e];
+    if (nan && !(mm != mm)) {
+      const int low = max(row_low(p, s, gr / p.group), k0), high = min(row_high(p, s, gr / p.group), k1);
+      if (low > k0 || high < k1)  // it dropped keys that others of its tile keep
+        row_again<T, FP8>(p, b, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
+                          FP8 ? p.scale_log2 * *p.k_scale_inv : p.scale_log2, mm, low, high, c, acc);
+    }
     if (p.splits > 1) {
       float* dst = p.part_o + (static_cast<int64_t>(split) * p.tokens * p.hq + ro) * p.d + c;
       *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -872,6 +881,14 @@ gbn_status gbn_paged_attention(const gbn_paged_attention_args* args, cudaStream_
       off(c.page_size, c.k_cache_strides[1], ce) || off(c.page_size, c.v_cache_strides[1], ce) ||
       off(c.kv_heads, c.k_cache_strides[2], ce) || off(c.kv_heads, c.v_cache_strides[2], ce))
     return GBN_ERR_ALIGNMENT;
+  // What a tensor map takes: cache strides in (0, 2^40) bytes.
+  auto far = [&](int64_t extent, int64_t stride) {
+    return extent > 1 && (stride <= 0 || stride >= (int64_t(1) << 40) / ce);
+  };
+  if (far(c.num_pages, c.k_cache_strides[0]) || far(c.num_pages, c.v_cache_strides[0]) ||
+      far(c.page_size, c.k_cache_strides[1]) || far(c.page_size, c.v_cache_strides[1]) ||
+      far(c.kv_heads, c.k_cache_strides[2]) || far(c.kv_heads, c.v_cache_strides[2]))
+    return GBN_ERR_SHAPE;
   AttnPlan a;
   st = plan_for(z, c.causal, &a);
   if (st != GBN_OK) return st;

@@ -728,6 +728,23 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
         const int col = q4 * 32;
+        if (live && n > 0 && (rlo > k0 || rhi < k1)) {
+          // It dropped keys that other rows of its tiles keep.
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            bool nan = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              nan |= __uint_as_float(o[i + e]) != __uint_as_float(o[i + e]);
+            if (nan && col + i < p.d) {
+              float acc[8];
+              row_again<T, FP8>(p, b, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
+                                FP8 ? p.scale_log2 * kscale : p.scale_log2, m, rlo, rhi, col + i, acc);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[i + e] = __float_as_uint(acc[e]);
+            }
+          }
+        }
         if (live && part) {
           float* dst = p.part_o + (static_cast<int64_t>(split) * p.tokens * p.hq + ro) * p.d;
           if (l != 0.f) {

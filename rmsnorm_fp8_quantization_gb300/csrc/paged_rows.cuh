@@ -97,6 +97,55 @@ __device__ __forceinline__ float q_to_f16(uint4& w) {
   }
 }
 
+// Eight cache elements from element offset `at`.
+template <typename T, bool FP8>
+__device__ __forceinline__ void cache_values(const void* cache, int64_t at, float* f) {
+  if constexpr (FP8) {
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) + at);
+    const uint32_t h[4] = {e4m3x2_to_f16x2(w.x & 0xFFFFu), e4m3x2_to_f16x2(w.x >> 16),
+                           e4m3x2_to_f16x2(w.y & 0xFFFFu), e4m3x2_to_f16x2(w.y >> 16)};
+    unpack<__half, 8>(h, f);
+  } else {
+    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const T*>(cache) + at);
+    const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+    unpack<T, 8>(h, f);
+  }
+}
+
+// Eight output columns of one row again, key by key: sum_j 2^(scale q.k_j - m) v_j
+// over j in [lo, hi) alone.  The products of whole tiles give a dropped key the
+// weight 0, and 0 times an infinity or NaN among its values is NaN; a row that
+// dropped keys of its tiles and came out NaN is computed here, where dropped keys
+// do not enter (a NaN that belongs there comes out again).  Rare, and slow.
+template <typename T, bool FP8>
+__device__ __noinline__ void row_again(const AttnParams& p, int b, int h, const T* q, float scale,
+                                       float m, int lo, int hi, int col, float* acc) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  const float mb = m == -INFINITY ? 0.f : m;
+  for (int j = lo; j < hi; ++j) {
+    const int pg = p.table[b * p.table_stride + (j >> p.page_shift)];
+    if (pg < 0 || pg >= p.num_pages) continue;
+    const int slot = j & ((1 << p.page_shift) - 1);
+    const int64_t ko = pg * p.kp + slot * p.ks + h * p.kh, vo = pg * p.vp + slot * p.vs + h * p.vh;
+    float s = 0.f;
+    for (int c = 0; c < p.d; c += 8) {
+      float qf[8], kf[8];
+      const uint4 w = *reinterpret_cast<const uint4*>(q + c);
+      const uint32_t qw[4] = {w.x, w.y, w.z, w.w};
+      unpack<T, 8>(qw, qf);
+      cache_values<T, FP8>(p.k, ko + c, kf);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s = fmaf(qf[e], kf[e], s);
+    }
+    const float w = ex2(s * scale - mb);
+    float vf[8];
+    cache_values<T, FP8>(p.v, vo + col, vf);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, vf[e], acc[e]);
+  }
+}
+
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kAttnLog2e = 1.4426950408889634f;
 

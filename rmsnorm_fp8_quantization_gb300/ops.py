@@ -175,6 +175,16 @@ def _call(dev, fn, *args):
         return fn(*args)
 
 
+def _on_stream(stream, device, fn, *args, **kw):
+    """fn(...) with ``stream`` current, so that what it allocates belongs to the
+    stream that uses it (a workspace allocated on another stream could be handed
+    out again there while this one still works in it)."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
+
+
 def _on_gpu(t):
     if t.device.type != "cuda":
         raise ValueError(f"expected CUDA tensors, got one on {t.device}")
@@ -280,6 +290,10 @@ def _check_rope(q, k, inv_freq, positions, q_out, k_out):
 
 
 def _rope(call, where, q, k, inv_freq, positions, layout, mscale, q_out, k_out, stream):
+    if stream is not None and (q_out is None and q is not None or k_out is None and k is not None):
+        _check_rope(q, k, inv_freq, positions, q_out, k_out)
+        return _on_stream(stream, inv_freq.device, _rope, call, where, q, k, inv_freq, positions,
+                          layout, mscale, q_out, k_out, None)
     # The usual call in one expression; anything else goes through the checks one by one.
     if not (q is not None and k is not None and q_out is None and k_out is None
             and positions is not None and q.is_contiguous() and k.is_contiguous()
@@ -414,6 +428,10 @@ def paged_append(k, v, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, q=
     and then with unwritten padding rows)."""
     cdt, hk, d = _paged_args(k, k_cache, v_cache, cu_seqlens, kv_lens, block_table)
     dev = k.device
+    if stream is not None and q is not None and q_out is None and k.is_cuda:
+        return _on_stream(stream, dev, paged_append, k, v, k_cache, v_cache, cu_seqlens, kv_lens,
+                          block_table, q=q, inv_freq=inv_freq, layout=layout, mscale=mscale,
+                          k_scale=k_scale, v_scale=v_scale)
     _same("v", v, k.dtype, dev, 3)
     if v.shape != k.shape or k.shape[1] != hk:
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)}: expected "
@@ -494,6 +512,11 @@ def paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, ma
     cdt, hk, d = _paged_args(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table)
     dev, t, hq = q.device, q.shape[0], q.shape[1]
     _inner("q", q)
+    if stream is not None and q.is_cuda:
+        return _on_stream(stream, dev, paged_attention, q, k_cache, v_cache, cu_seqlens, kv_lens,
+                          block_table, max_q=max_q, max_kv=max_kv, scale=scale, causal=causal,
+                          window=window, k_scale_inv=k_scale_inv, v_scale_inv=v_scale_inv,
+                          return_lse=return_lse, out=out, lse=lse, workspace=workspace)
     if out is None:
         out = torch.empty_like(q)
     else:

@@ -196,6 +196,58 @@ def test_bad_pages_and_lengths_are_flagged(gpu, c):
     assert device_flags() == 0
 
 
+@pytest.mark.parametrize("c", [
+    B([6, 5], [70, 300], heads=4, kv_heads=2, dim=64),
+    B([6, 5], [70, 3000], heads=8, kv_heads=1, dim=128, dtype="f16", window=60),
+    B([6, 5], [70, 300], heads=4, kv_heads=2, dim=128, fp8=True),
+    B([150, 90], [150, 700], heads=4, kv_heads=2, dim=128),
+    B([150, 90], [150, 700], heads=4, kv_heads=1, dim=64, fp8=True, window=100),
+    B([40, 50], [40, 130], heads=2, kv_heads=1, dim=256),
+], ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=["nan", "inf"])
+def test_what_stands_in_a_dropped_key_does_not_enter(gpu, c, bad):
+    """Keys and values that some rows of a tile keep and others drop, not finite:
+    the rows that drop them are as if they were not there."""
+    s = make(c)
+    if c.fp8 and bad == float("inf"):
+        bad = float("nan")  # E4M3 has no infinity
+    cpu = s["cpu"]
+    poisoned = [c.kv_lens[0] - 2, c.kv_lens[1] - 3]
+    for name in ("k_cache", "v_cache"):
+        host = s[name].float().cpu()
+        for b, t in enumerate(poisoned):
+            host[cpu["table"][b][t // c.page], t % c.page, :, 3:9] = bad
+        s[name].copy_(host.to(s[name].dtype))
+        cpu[name] = s[name].float().cpu().double().numpy()
+    out, lse = attend(gpu, c, s)
+    torch.cuda.synchronize()
+    first = []  # rows before the poisoned position, per sequence
+    for b in range(2):
+        off = c.kv_lens[b] - c.q_lens[b]
+        first += [cpu["cu"][b] + i for i in range(c.q_lens[b])
+                  if off + i < poisoned[b] or (c.window and off + i - c.window >= poisoned[b])]
+    rows = torch.tensor(first)
+    assert torch.isfinite(out[rows.cuda()].float()).all()
+    # against the oracle: only those rows (the others are not finite on both sides)
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref, rl, mag = P.paged_attend(cpu["q"], cpu["k_cache"], cpu["v_cache"], cpu["cu"],
+                                      cpu["kv_lens"], cpu["table"], c.dim ** -0.5, c.causal,
+                                      c.window, cpu["inv"], cpu["inv"])
+    clean = {**cpu, "k_cache": np.where(np.isfinite(cpu["k_cache"]), cpu["k_cache"], 0)}
+    ds = (c.dim / 16 + 6) * 2.0 ** -23 * score_size(clean, c.dim ** -0.5)
+    dt = DT[c.dtype]
+    half = torch.finfo(dt).eps / 2
+    rel = (torch.finfo(torch.float16 if c.fp8 else dt).eps / 2 + 2 * ds[..., None]
+           + (max(c.kv_lens) / 16 + 24) * 2.0 ** -23)
+    inner = mag * rel
+    lim = half * (np.abs(ref) + inner) + inner + (2.0 ** -25 if c.dtype == "f16" else 0.0)
+    err = np.abs(out.double().cpu().numpy() - ref)
+    r = rows.numpy()
+    assert (err[r] <= lim[r]).all(), (np.nanmax(err[r] / lim[r]))
+    others = [i for i in range(cpu["cu"][-1]) if i not in set(first)]
+    assert torch.isnan(out[torch.tensor(others).cuda()].float()).any(-1).all()
+
+
 def test_attention_graph_with_lengths_that_change(gpu):
     """One captured call follows the lengths and the table on the device."""
     c = B([1, 1, 1], [900, 40, 300], dim=128, heads=8, kv_heads=2)
@@ -229,6 +281,32 @@ def test_two_streams_with_their_own_workspaces(gpu):
     torch.cuda.synchronize()
     for o, r in outs:
         assert torch.equal(o, r)
+
+
+def test_stream_argument_while_the_current_stream_is_busy(gpu):
+    """A call on another stream than the current one, its workspace and outputs
+    allocated by the call, while the current stream reuses freed memory."""
+    c = B([1, 1], [9000, 7000], dim=128, heads=8, kv_heads=2)
+    s = make(c)
+    ref, rl = attend(gpu, c, s)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for handle in (side, side.cuda_stream):
+        outs = []
+        for _ in range(30):
+            outs.append(attend(gpu, c, s, stream=handle))
+            junk = [torch.full((1 << 20,), 3.0, device="cuda") for _ in range(4)]
+            del junk
+        torch.cuda.synchronize()
+        for o, l in outs:
+            assert torch.equal(o, ref) and torch.equal(l, rl)
+    q, k = torch.randn(2, 5, 4, 64, device="cuda"), torch.randn(2, 5, 2, 64, device="cuda")
+    f = gpu.rope_frequencies(64)
+    want = gpu.rope_fwd(q, k, f)
+    torch.cuda.synchronize()
+    got = gpu.rope_fwd(q, k, f, stream=side)
+    side.synchronize()
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
 
 
 # ---------------------------------------------------------------- append

@@ -112,6 +112,9 @@ def test_attention_refusals(ops):
                 dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
                 dict(scale=float("inf")), dict(tokens=1 << 30), dict(num_pages=-1)):
         assert _attend(G, **bad) == G.GBN_ERR_SHAPE, bad
+    for bad in (dict(k_cache_strides=(0, 128, 64)), dict(v_cache_strides=(2048, 128, -64)),
+                dict(k_cache_strides=(1 << 40, 128, 64))):   # not what a tensor map takes
+        assert _attend(G, **{**HAVE, **bad}) == G.GBN_ERR_SHAPE, bad
     for bad in (dict(q=FAKE + 8), dict(out=FAKE + 2), dict(k_cache=FAKE + 4),
                 dict(q_strides=(252, 64)), dict(out_strides=(256, 68)),
                 dict(k_cache_strides=(2048, 132, 64)), dict(v_cache_strides=(2050, 128, 64))):
