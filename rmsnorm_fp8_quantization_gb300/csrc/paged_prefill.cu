@@ -55,6 +55,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kZeroWarp = 11, kConvertWarp = 12;
 constexpr int kLoaders = 128;              // E4M3 caches: threads of warps 12-15
 constexpr int kStaging = 4;                // E4M3 caches: at most so many tiles of codes
+constexpr int kSortBatches = 256;          // up to so many sequences are taken by length
 constexpr float kRescale = 8.f;            // log2 growth before the reference moves
 
 struct Barriers {
@@ -63,6 +64,7 @@ struct Barriers {
   uint64_t raw_full[kStaging], raw_empty[kStaging];  // E4M3 caches
   float q_scale[2][kRowsT];  // E4M3 caches: what a q row's scores are times
   uint32_t tmem;
+  int sequence;  // of this CTA
 };
 
 template <bool FP8, int DP>
@@ -235,15 +237,32 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
 
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // Row blocks from the last one down: causal rows late in a sequence have the
-  // most keys.
+  // The longest work first, so that the last CTAs to start are short: sequences
+  // by their keys, a sequence's row blocks from the last one down (causal rows
+  // late in it have the most keys).
   uint32_t x = blockIdx.x;
   const int h = x % p.hkv;
   x /= p.hkv;
   const int split = x % p.splits;
   x /= p.splits;
-  const int b = x % p.batches;
-  const int rt = p.row_tiles - 1 - static_cast<int>(x / p.batches);
+  const int rt = p.row_tiles - 1 - static_cast<int>(x % p.row_tiles);
+  int b = x / p.row_tiles;
+  if (p.batches > 1 && p.batches <= kSortBatches) {
+    // The sequence with b longer ones.  Every CTA counts for itself: a few hundred
+    // cycles against a second launch.
+    for (int i = tid; i < p.batches; i += Shape::kThreads) {
+      const int mine = p.kv_lens[i];
+      int before = 0;
+#pragma unroll 8
+      for (int j = 0; j < p.batches; ++j) {
+        const int kv = p.kv_lens[j];
+        before += kv > mine || (kv == mine && j < i);
+      }
+      if (before == b) bars.sequence = i;
+    }
+    __syncthreads();
+    b = bars.sequence;
+  }
 
   const SeqRange s = seq_range(p, b, tid == 0 && split == 0 && rt == 0 && h == 0);
   const int r0 = rt * kPrefillRows;
