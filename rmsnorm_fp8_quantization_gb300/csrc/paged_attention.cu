@@ -680,7 +680,8 @@ cudaError_t launch_step(const AttnParams& p, int64_t grid, cudaStream_t st) {
   using Shape = StepShape<T, FP8, DP>;
   constexpr int smem = Shape::smem(MT);
   auto k = paged_step_kernel<T, FP8, DP, MT>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(k, smem, done);
   if (e != cudaSuccess) return e;
   CUtensorMap km = {}, vm = {};
   if (p.page_shift >= 3) {

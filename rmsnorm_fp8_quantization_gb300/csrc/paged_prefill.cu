@@ -822,8 +822,8 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap
                    cudaStream_t st) {
   using Shape = PrefillShape<FP8, DP>;
   auto k = paged_prefill_kernel<T, FP8, DP>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(k, Shape::kSmem, done);
   if (e != cudaSuccess) return e;
   const int64_t grid = int64_t(p.row_tiles) * p.batches * p.splits * p.hkv;
   return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(Shape::kThreads), Shape::kSmem, st, p,

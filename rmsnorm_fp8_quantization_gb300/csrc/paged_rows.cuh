@@ -8,10 +8,26 @@
 //   high = off + i + 1 (causal) or kv_len, low = off + i - window + 1 or 0.
 #pragma once
 
+#include <atomic>
+
 #include "paged.cuh"
 #include "paged_attn.h"
 
 namespace gbn {
+
+// Raises a kernel's limit of dynamic shared memory, once per kernel and device
+// (`done`: one bit per device; the setting lasts as long as the context).
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 struct SeqRange {
   int q0;    // first token

@@ -118,6 +118,13 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def current_stream(device_index):
+    """Raw handle of that device's current stream (the device being current)."""
+    if _raw_stream is not None:
+        return _raw_stream(device_index)
+    return torch.cuda.current_stream().cuda_stream
+
+
 def gbn_status_string(status: int) -> str:
     return _lib.gbn_status_string(int(status)).decode()
 
@@ -197,9 +204,9 @@ def gbn_softmax_bwd(dy, y, dx, rows, sk, dtype, scale, stream=None) -> int:
 
 # The argument structs of include/gbnorm.h, as packed bytes (native layout:
 # pointers, 64-bit sizes and strides, then 32-bit fields; no padding).
-_rope_args = struct.Struct("=6Q19q3if").pack
-_append_args = struct.Struct("=12Q24q3if").pack
-_attention_args = struct.Struct("=12Q22q3if").pack
+rope_args = struct.Struct("=6Q19q3if").pack
+append_args = struct.Struct("=12Q24q3if").pack
+attention_args = struct.Struct("=12Q22q3if").pack
 
 
 def _addr(t):
@@ -214,8 +221,8 @@ def gbn_rope_fwd(q, k, positions, inv_freq, q_out, k_out, batches, seq, q_heads,
                  position_bytes, dtype, layout, mscale, stream=None) -> int:
     """Strides: (batch, position, head) triples in elements."""
     return _lib.gbn_rope_fwd(
-        _rope_args(_addr(q), _addr(k), _addr(positions), _addr(inv_freq), _addr(q_out),
-                   _addr(k_out), batches, seq, q_heads, k_heads, head_dim, rotary_dim, *q_strides,
+        rope_args(_addr(q), _addr(k), _addr(positions), _addr(inv_freq), _addr(q_out),
+                  _addr(k_out), batches, seq, q_heads, k_heads, head_dim, rotary_dim, *q_strides,
                    *k_strides, *q_out_strides, *k_out_strides, position_stride, position_bytes,
                    dtype, layout, mscale), _stream(stream))
 
@@ -224,7 +231,7 @@ def gbn_rope_bwd(dq, dk, positions, inv_freq, dq_out, dk_out, batches, seq, q_he
                  head_dim, rotary_dim, q_strides, k_strides, q_out_strides, k_out_strides,
                  position_stride, position_bytes, dtype, layout, mscale, stream=None) -> int:
     return _lib.gbn_rope_bwd(
-        _rope_args(_addr(dq), _addr(dk), _addr(positions), _addr(inv_freq), _addr(dq_out),
+        rope_args(_addr(dq), _addr(dk), _addr(positions), _addr(inv_freq), _addr(dq_out),
                    _addr(dk_out), batches, seq, q_heads, k_heads, head_dim, rotary_dim, *q_strides,
                    *k_strides, *q_out_strides, *k_out_strides, position_stride, position_bytes,
                    dtype, layout, mscale), _stream(stream))
@@ -237,7 +244,7 @@ def gbn_paged_append(q, k, v, q_out, k_cache, v_cache, inv_freq, k_scale, v_scal
                      cache_dtype, layout, mscale, stream=None) -> int:
     """Strides in elements: (token, head) pairs, and (page, slot, head) triples of the caches."""
     return _lib.gbn_paged_append(
-        _append_args(_addr(q), _addr(k), _addr(v), _addr(q_out), _addr(k_cache), _addr(v_cache),
+        append_args(_addr(q), _addr(k), _addr(v), _addr(q_out), _addr(k_cache), _addr(v_cache),
                      _addr(inv_freq), _addr(k_scale), _addr(v_scale), _addr(cu_seqlens),
                      _addr(kv_lens), _addr(block_table), tokens, batches, q_heads, kv_heads,
                      head_dim, rotary_dim, num_pages, page_size, table_pages, table_stride,
@@ -265,7 +272,7 @@ def gbn_paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, k
                         stream=None) -> int:
     """Strides in elements: (token, head) pairs, and (page, slot, head) triples of the caches."""
     return _lib.gbn_paged_attention(
-        _attention_args(_addr(q), _addr(k_cache), _addr(v_cache), _addr(cu_seqlens),
+        attention_args(_addr(q), _addr(k_cache), _addr(v_cache), _addr(cu_seqlens),
                         _addr(kv_lens), _addr(block_table), _addr(k_scale_inv),
                         _addr(v_scale_inv), _addr(out), _addr(lse), _addr(workspace),
                         workspace_bytes, tokens, batches, q_heads, kv_heads, head_dim, num_pages,

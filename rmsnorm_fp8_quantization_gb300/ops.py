@@ -166,13 +166,16 @@ _NO_STRIDES = (0, 0, 0)
 _INT_DTYPES = (torch.int32, torch.int64)
 
 
-def _call(dev, fn, *args):
-    """fn(*args) with ``dev`` the current device (the launch and the current
-    stream go by it)."""
-    if dev.index == torch.cuda.current_device():
-        return fn(*args)
-    with torch.cuda.device(dev):
-        return fn(*args)
+def _launch(where, fn, args, device_index, stream):
+    """Calls a C entry point that takes a packed argument struct, with the
+    tensors' device current (the launch and the current stream go by it)."""
+    if device_index == torch.cuda.current_device():
+        st = fn(args, G.current_stream(device_index) if stream is None else G._stream(stream))
+    else:
+        with torch.cuda.device(device_index):
+            st = fn(args, G._stream(stream))
+    if st:
+        raise G.GbnError(st, where)
 
 
 def _on_stream(stream, device, fn, *args, **kw):
@@ -296,34 +299,35 @@ def _rope(call, where, q, k, inv_freq, positions, layout, mscale, q_out, k_out, 
                           layout, mscale, q_out, k_out, None)
     # The usual call in one expression; anything else goes through the checks one by one.
     if not (q is not None and k is not None and q_out is None and k_out is None
-            and positions is not None and q.is_contiguous() and k.is_contiguous()
-            and positions.is_contiguous() and q.dim() == 4 and q.shape[:2] == positions.shape
-            and k.shape[:2] == positions.shape and q.shape[3] == k.shape[3]
-            and q.dtype is k.dtype and q.dtype in G.TORCH_DTYPE and positions.dtype in _INT_DTYPES
-            and inv_freq.dtype is torch.float64 and inv_freq.dim() == 1
-            and inv_freq.is_contiguous() and q.is_cuda and q.get_device() == k.get_device()
-            == positions.get_device() == inv_freq.get_device()):
+            and positions is not None and q.dim() == 4 == k.dim() and q.stride(3) == 1 == k.stride(3)
+            and positions.is_contiguous() and q.shape[:2] == k.shape[:2] == positions.shape
+            and q.shape[3] == k.shape[3] and q.dtype is k.dtype and q.dtype in G.TORCH_DTYPE
+            and positions.dtype in _INT_DTYPES and inv_freq.dtype is torch.float64
+            and inv_freq.dim() == 1 and inv_freq.is_contiguous() and q.is_cuda
+            and q.get_device() == k.get_device() == positions.get_device()
+            == inv_freq.get_device()):
         _check_rope(q, k, inv_freq, positions, q_out, k_out)
-    b, s, _, d = (k if q is None else q).shape
-    hq = hk = 0
+    x = k if q is None else q
+    b, s, _, d = x.shape
+    hq = hk = qa = ka = qoa = koa = 0
     qs = ks = qo = ko = _NO_STRIDES
     if q is not None:
         q_out = torch.empty_like(q) if q_out is None else q_out
-        hq, qs, qo = q.shape[2], q.stride()[:3], q_out.stride()[:3]
+        hq, qs, qo, qa, qoa = q.shape[2], q.stride(), q_out.stride(), q.data_ptr(), q_out.data_ptr()
     if k is not None:
         k_out = torch.empty_like(k) if k_out is None else k_out
-        hk, ks, ko = k.shape[2], k.stride()[:3], k_out.stride()[:3]
-    pos_stride, pos_bytes = 0, 8
+        hk, ks, ko, ka, koa = k.shape[2], k.stride(), k_out.stride(), k.data_ptr(), k_out.data_ptr()
+    pos_stride, pos_bytes, pa = 0, 8, 0
     if positions is not None:
-        pos_bytes = positions.itemsize
+        pos_bytes, pa = positions.itemsize, positions.data_ptr()
         if positions.dim() == 2 and positions.shape[0] > 1:
             pos_stride = positions.stride(0)
-    x = k if q is None else q
-    st = _call(x.device, call, q, k, positions, inv_freq, q_out, k_out, b, s, hq, hk, d,
-               2 * inv_freq.shape[0], qs, ks, qo, ko, pos_stride, pos_bytes,
-               G.TORCH_DTYPE[x.dtype], _ROPE_LAYOUT[layout], mscale, stream)
-    if st:
-        _check(st, where)
+    _launch(where, call,
+            G.rope_args(qa, ka, pa, inv_freq.data_ptr(), qoa, koa, b, s, hq, hk, d,
+                        2 * inv_freq.shape[0], qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], qo[0],
+                        qo[1], qo[2], ko[0], ko[1], ko[2], pos_stride, pos_bytes,
+                        G.TORCH_DTYPE[x.dtype], _ROPE_LAYOUT[layout], mscale),
+            x.get_device(), stream)
     return q_out, k_out
 
 
@@ -335,14 +339,14 @@ def rope_fwd(q, k, inv_freq, positions=None, *, layout="half", mscale=1.0, q_out
     themselves may be).  ``inv_freq``: ``rope_frequencies(rotary_dim)``; of the
     head's elements the first rotary_dim = 2 * len(inv_freq) turn.  ``layout``:
     pairs (i, i + rotary_dim / 2) ("half") or (2i, 2i + 1) ("interleaved")."""
-    return _rope(G.gbn_rope_fwd, "gbn_rope_fwd", q, k, inv_freq, positions, layout, mscale, q_out,
+    return _rope(G.library().gbn_rope_fwd, "gbn_rope_fwd", q, k, inv_freq, positions, layout, mscale, q_out,
                  k_out, stream)
 
 
 def rope_bwd(dq, dk, inv_freq, positions=None, *, layout="half", mscale=1.0, dq_out=None,
              dk_out=None, stream=None):
     """Gradients of ``rope_fwd``'s inputs from those of its outputs."""
-    return _rope(G.gbn_rope_bwd, "gbn_rope_bwd", dq, dk, inv_freq, positions, layout, mscale,
+    return _rope(G.library().gbn_rope_bwd, "gbn_rope_bwd", dq, dk, inv_freq, positions, layout, mscale,
                  dq_out, dk_out, stream)
 
 
@@ -432,7 +436,9 @@ def paged_append(k, v, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, q=
         return _on_stream(stream, dev, paged_append, k, v, k_cache, v_cache, cu_seqlens, kv_lens,
                           block_table, q=q, inv_freq=inv_freq, layout=layout, mscale=mscale,
                           k_scale=k_scale, v_scale=v_scale)
-    _same("v", v, k.dtype, dev, 3)
+    dt = k.dtype
+    if v.dtype is not dt or v.dim() != 3 or v.get_device() != k.get_device():
+        _same("v", v, dt, dev, 3)
     if v.shape != k.shape or k.shape[1] != hk:
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)}: expected "
                          f"[tokens, {hk}, {d}]")
@@ -440,7 +446,8 @@ def paged_append(k, v, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, q=
     _inner("v", v)
     hq, qs, qo = 0, (0, 0), (0, 0)
     if q is not None:
-        _same("q", q, k.dtype, dev, 3)
+        if q.dtype is not dt or q.dim() != 3 or q.get_device() != k.get_device():
+            _same("q", q, dt, dev, 3)
         if q.shape[0] != k.shape[0] or q.shape[2] != d:
             raise ValueError(f"q: shape {tuple(q.shape)} does not go with k {tuple(k.shape)}")
         _inner("q", q)
@@ -451,7 +458,7 @@ def paged_append(k, v, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, q=
             if q_out.shape != q.shape:
                 raise ValueError(f"q_out: shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
             _inner("q_out", q_out)
-        hq, qs, qo = q.shape[1], q.stride()[:2], q_out.stride()[:2]
+        hq, qs, qo = q.shape[1], q.stride(), q_out.stride()
     elif q_out is not None:
         raise ValueError("q_out without q")
     rot = 0
@@ -466,14 +473,19 @@ def paged_append(k, v, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, q=
         _scalar("k_scale", k_scale, dev)
         _scalar("v_scale", v_scale, dev)
     _on_gpu(k)
-    st = _call(dev, G.gbn_paged_append, q, k, v, q_out, k_cache, v_cache, inv_freq, k_scale,
-               v_scale, cu_seqlens, kv_lens, block_table, k.shape[0], kv_lens.shape[0], hq, hk, d,
-               rot, k_cache.shape[0], k_cache.shape[1], block_table.shape[1],
-               block_table.stride(0), qs, k.stride()[:2], v.stride()[:2], qo,
-               k_cache.stride()[:3], v_cache.stride()[:3], G.TORCH_DTYPE[k.dtype], cdt,
-               _ROPE_LAYOUT[layout], mscale, stream)
-    if st:
-        _check(st, "gbn_paged_append")
+    ks, vs, kc, vc = k.stride(), v.stride(), k_cache.stride(), v_cache.stride()
+    _launch("gbn_paged_append", G.library().gbn_paged_append,
+            G.append_args(0 if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                          0 if q is None else q_out.data_ptr(), k_cache.data_ptr(),
+                          v_cache.data_ptr(), 0 if inv_freq is None else inv_freq.data_ptr(),
+                          0 if k_scale is None else k_scale.data_ptr(),
+                          0 if v_scale is None else v_scale.data_ptr(), cu_seqlens.data_ptr(),
+                          kv_lens.data_ptr(), block_table.data_ptr(), k.shape[0],
+                          kv_lens.shape[0], hq, hk, d, rot, k_cache.shape[0], k_cache.shape[1],
+                          block_table.shape[1], block_table.stride(0), qs[0], qs[1], ks[0], ks[1],
+                          vs[0], vs[1], qo[0], qo[1], kc[0], kc[1], kc[2], vc[0], vc[1], vc[2],
+                          G.TORCH_DTYPE[k.dtype], cdt, _ROPE_LAYOUT[layout], mscale),
+            k.get_device(), stream)
     return q_out
 
 
@@ -490,7 +502,7 @@ def paged_attention_workspace(q, k_cache, block_table, *, max_q, max_kv=None, ca
                               window=0):
     """A workspace for ``paged_attention`` calls of these sizes (None: they need none)."""
     cdt = _cache_dtype(k_cache, k_cache, q.dtype)
-    mkv = block_table.shape[1] * k_cache.shape[1] if max_kv is None else max_kv
+    mkv = min(block_table.shape[1] * k_cache.shape[1], 1 << 30) if max_kv is None else max_kv
     _on_gpu(q)
     n = _attention_bytes(q.get_device(), q.shape[0], block_table.shape[0], q.shape[1],
                          k_cache.shape[2], q.shape[2], k_cache.shape[1], block_table.shape[1],
@@ -536,7 +548,7 @@ def paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, ma
         _scalar("k_scale_inv", k_scale_inv, dev)
         _scalar("v_scale_inv", v_scale_inv, dev)
     page, pages = k_cache.shape[1], block_table.shape[1]
-    mkv = pages * page if max_kv is None else max_kv
+    mkv = min(pages * page, 1 << 30) if max_kv is None else max_kv
     dt = G.TORCH_DTYPE[q.dtype]
     n = kv_lens.shape[0]
     _on_gpu(q)
@@ -548,11 +560,17 @@ def paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, ma
                                 bool(causal), dt, cdt)
         if size:
             workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    st = _call(dev, G.gbn_paged_attention, q, k_cache, v_cache, cu_seqlens, kv_lens, block_table,
-               k_scale_inv, v_scale_inv, out, lse, workspace, size, t, n, hq, hk, d,
-               k_cache.shape[0], page, pages, block_table.stride(0), max_q, mkv, q.stride()[:2],
-               out.stride()[:2], k_cache.stride()[:3], v_cache.stride()[:3], dt, cdt, causal,
-               window, d ** -0.5 if scale is None else scale, stream)
-    if st:
-        _check(st, "gbn_paged_attention")
+    qs, os, kc, vc = q.stride(), out.stride(), k_cache.stride(), v_cache.stride()
+    _launch("gbn_paged_attention", G.library().gbn_paged_attention,
+            G.attention_args(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                             cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(),
+                             0 if k_scale_inv is None else k_scale_inv.data_ptr(),
+                             0 if v_scale_inv is None else v_scale_inv.data_ptr(),
+                             out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+                             0 if workspace is None else workspace.data_ptr(), size, t, n, hq, hk,
+                             d, k_cache.shape[0], page, pages, block_table.stride(0), max_q, mkv,
+                             qs[0], qs[1], os[0], os[1], kc[0], kc[1], kc[2], vc[0], vc[1], vc[2],
+                             window, dt, cdt, 1 if causal else 0,
+                             d ** -0.5 if scale is None else scale),
+            q.get_device(), stream)
     return (out, lse) if return_lse else out
