@@ -596,8 +596,8 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
 //   o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s
 // in the order of the splits within each of the CTA's split groups, the
 // groups added in order: the same bits every time.
-// 128 threads, or 512 where there are many splits to add up for few rows.
-template <typename T, int kMergeThreads>
+constexpr int kMergeThreads = 512;
+template <typename T>
 __global__ void __launch_bounds__(kMergeThreads)
     paged_merge_kernel(const __grid_constant__ AttnParams p, int fp8) {
   pdl_begin();
@@ -709,11 +709,61 @@ cudaError_t launch_step_d(const AttnParams& p, int mt, int64_t grid, cudaStream_
   return launch_step_mt<T, FP8, 256>(p, mt, grid, st);
 }
 
+// The same for up to 32 splits: a warp per row, a lane per split for the weights
+// and D / 32 columns per lane for the outputs, nothing shared (14400 rows of two
+// splits: a CTA per row took 18 us).
+constexpr int kMergeRows = 4;  // rows (warps) per CTA
+template <typename T>
+__global__ void __launch_bounds__(32 * kMergeRows)
+    paged_merge_few_kernel(const __grid_constant__ AttnParams p, int fp8) {
+  pdl_begin();
+  const int lane = threadIdx.x & 31;
+  const int64_t ro = static_cast<int64_t>(blockIdx.x) * kMergeRows + (threadIdx.x >> 5);
+  if (ro >= static_cast<int64_t>(p.tokens) * p.hq) return;
+  const int token = static_cast<int>(ro / p.hq), head = static_cast<int>(ro - static_cast<int64_t>(token) * p.hq);
+  if (token >= p.cu[p.batches] || token < p.cu[0]) return;  // padding rows
+  const float2 ml = lane < p.splits ? p.part_ml[ro * p.splits + lane] : make_float2(-INFINITY, 0.f);
+  float m = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  const float mb = m == -INFINITY ? 0.f : m;
+  const float w = ml.y == 0.f ? 0.f : ex2(ml.x - mb);
+  const float l = warp_sum(ml.y == 0.f ? 0.f : ml.y * w);
+  const int cols = p.d / 4;  // float4 columns (4 .. 64)
+  const float inv = l == 0.f ? 0.f : (fp8 ? *p.v_scale_inv : 1.f) / l;
+  const int64_t step = static_cast<int64_t>(p.tokens) * p.hq * p.d;
+  for (int c0 = 0; c0 < cols; c0 += 32) {
+    const int col = c0 + lane;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* src = p.part_o + ro * p.d + col * 4;
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+      const float ws = __shfl_sync(0xFFFFFFFFu, w, s);
+      if (ws != 0.f && col < cols) {
+        const float4 v = *reinterpret_cast<const float4*>(src + s * step);
+        acc.x = fmaf(v.x, ws, acc.x);
+        acc.y = fmaf(v.y, ws, acc.y);
+        acc.z = fmaf(v.z, ws, acc.z);
+        acc.w = fmaf(v.w, ws, acc.w);
+      }
+    }
+    if (col < cols) {
+      uint32_t o[2] = {narrow2<T>(p2(acc.x * inv, acc.y * inv)), narrow2<T>(p2(acc.z * inv, acc.w * inv))};
+      st_words<2>(reinterpret_cast<T*>(p.out) + token * p.ot + head * p.oh + col * 4, o);
+    }
+  }
+  if (lane == 0 && p.lse) p.lse[ro] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
 template <typename T>
 cudaError_t launch_merge(const AttnParams& p, bool fp8, cudaStream_t st) {
-  const dim3 g(static_cast<unsigned>(static_cast<int64_t>(p.tokens) * p.hq));
-  return p.splits > 16 ? launch_pdl(paged_merge_kernel<T, 512>, g, dim3(512), 0, st, p, int(fp8))
-                       : launch_pdl(paged_merge_kernel<T, 128>, g, dim3(128), 0, st, p, int(fp8));
+  const int64_t rows = static_cast<int64_t>(p.tokens) * p.hq;
+  if (p.splits <= 32 && (rows >= 256 || p.splits <= 8))
+    return launch_pdl(paged_merge_few_kernel<T>,
+                      dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows)),
+                      dim3(32 * kMergeRows), 0, st, p, int(fp8));
+  return launch_pdl(paged_merge_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(kMergeThreads), 0,
+                    st, p, int(fp8));
 }
 
 // How a call is carried out: a function of sizes that the host knows.
@@ -732,9 +782,14 @@ AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t d, int64
                    int64_t max_kv, int64_t window, int causal, int page_shift, int sms) {
   AttnPlan a;
   const int64_t r = max_q * group;
-  // The tcgen05 kernel from the first size on that fills half a tile of it;
-  // its boxes are at least 8 slots (one swizzle atom).
-  a.prefill = r > 64 && d <= 128 && page_shift >= 3;
+  // The tcgen05 kernel from the first size on that fills half a tile of it, and
+  // for 33 to 64 rows of wide heads where the keys are many: 35 sequences of
+  // 18000-32000 keys, 48 rows: 540 us against 680 on mma.sync (E4M3 608 against
+  // 984), but 4 of 1000-4000 keys 35 us against 20 (its CTAs take longer to
+  // start); heads of 64 gain nothing (462 against 420).  Its boxes are at least 8
+  // slots (one swizzle atom).
+  const bool many = batches * hkv * max_kv > 786432 && d > 64;
+  a.prefill = (r > 64 || (r > 32 && many)) && d <= 128 && page_shift >= 3;
   // 33 to 64 rows as two tiles of 32: a step is shorter (each warp has half of
   // the keys) and the second read of the keys comes from L2.
   a.rows = a.prefill ? kPrefillRows : r <= 16 ? 16 : r <= 64 ? 32 : 64;
@@ -750,9 +805,10 @@ AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t d, int64
   const int64_t step = a.prefill ? kPrefillKeys : kStepKeys;
   int64_t splits = 1;
   if (a.prefill) {
-    // One CTA per SM: two rounds where the row tiles alone do not fill one, at
-    // least 512 keys each.
-    if (tiles < sms) splits = ceil_div(2ll * sms, tiles > 0 ? tiles : 1);
+    // One CTA per SM: as many as fit one round, at least 512 keys each (4 sequences
+    // of 6000 keys, 50 new tokens, 8 kv heads: 43 us in one round, 59 in half of
+    // one, 60 in two).
+    splits = sms / (tiles > 0 ? tiles : 1);
     const int64_t most = ceil_div(range, 512);
     if (splits > most) splits = most;
   } else if (range > 320) {

@@ -211,6 +211,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// The lowest n bits set (none for n <= 0, all from 64 on).
+__device__ __forceinline__ uint64_t low_bits(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
 }
@@ -674,12 +679,20 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
         tc_ld32(th, sc);
         tc_ld32(th + 32, sc + 32);
         tc_wait_ld<64>(sc);
+        // Bit e: key tb + e is kept (two comparisons a key took 1000 cycles a step).
+        const uint64_t kept = low_bits(rhi - tb) & ~low_bits(rlo - tb);
+        const uint32_t kept_lo = static_cast<uint32_t>(kept), kept_hi = static_cast<uint32_t>(kept >> 32);
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int e = 0; e < 64; ++e) {
-          if (tb + e < rlo || tb + e >= rhi) sc[e] = 0xFF800000u;  // -inf
-          mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sc[e]));
+          const uint32_t bit = (e < 32 ? kept_lo : kept_hi) & (1u << (e & 31));
+          sc[e] = bit ? sc[e] : 0xFF800000u;  // -inf
         }
+#pragma unroll
+        for (int e = 0; e < 64; e += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mx[i] = max3(mx[i], __uint_as_float(sc[e + i]), __uint_as_float(sc[e + 4 + i]));
         const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
         if (__any_sync(0xFFFFFFFFu, mt - m > kRescale)) {
           const float mn = fmaxf(m, mt);
