@@ -16,6 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgbnorm.so")
+FAST = os.path.join(PKG, "_fastcall.so")   # host-side shortcut of the wrappers (csrc/fastcall.cpp)
 BUILD_DIR = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "kernels_f32.cu", "kernels_bf16.cu", "kernels_f16.cu", "finalize.cu",
@@ -41,6 +42,34 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def build_fastcall() -> None:
+    """The wrappers' host-side shortcut, a small CPython module over torch's C++
+    headers.  Without a compiler or the headers it is left out (the wrappers
+    then do the same in Python, at 10 to 15 us more host time a call)."""
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    gxx = shutil.which("g++")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = FAST + f".tmp{os.getpid()}"
+    cmd = [gxx or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(home, "include"),
+           "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "fastcall.cpp"), "-o", tmp, "-L", os.path.join(home, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True) if gxx else None
+    if r is None or r.returncode != 0:
+        sys.stderr.write("fastcall.cpp not built (the wrappers work without it)"
+                         + (f":\n{r.stderr[-2000:]}\n" if r else ": no g++\n"))
+        if os.path.exists(FAST):
+            os.remove(FAST)
+        return
+    os.replace(tmp, FAST)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and up_to_date():
         return LIB
@@ -59,8 +88,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        fast = ex.submit(build_fastcall)
         results = list(ex.map(compile_one, SOURCES))
+        fast.result()
     if verbose_ptxas:
         for _, log in results:
             sys.stderr.write(log)

@@ -7,6 +7,7 @@ allocate device memory and marshal arguments.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 import math
 
@@ -160,6 +161,22 @@ def softmax_bwd(dy, y, scale=1.0, out=None, stream=None):
 
 
 # ---- rotary positions and the paged key/value cache
+
+try:  # the shortcut of the usual calls (csrc/fastcall.cpp); they work without it
+    from . import _fastcall as _fast
+    _fast.setup(*(ctypes.cast(getattr(G.library(), n), ctypes.c_void_p).value
+                  for n in ("gbn_rope_fwd", "gbn_rope_bwd", "gbn_paged_append",
+                            "gbn_paged_attention", "gbn_paged_attention_workspace_size")))
+except ImportError:
+    _fast = None
+
+
+def _taken(r, where):
+    """What the shortcut returned: the results, or the status of a refused call."""
+    if type(r) is int:
+        raise G.GbnError(r, where)
+    return r
+
 
 _ROPE_LAYOUT = {"half": G.GBN_ROPE_HALF, "interleaved": G.GBN_ROPE_INTERLEAVED}
 _NO_STRIDES = (0, 0, 0)
@@ -339,6 +356,10 @@ def rope_fwd(q, k, inv_freq, positions=None, *, layout="half", mscale=1.0, q_out
     themselves may be).  ``inv_freq``: ``rope_frequencies(rotary_dim)``; of the
     head's elements the first rotary_dim = 2 * len(inv_freq) turn.  ``layout``:
     pairs (i, i + rotary_dim / 2) ("half") or (2i, 2i + 1) ("interleaved")."""
+    if _fast is not None and q_out is None and k_out is None and stream is None:
+        r = _fast.rope(0, q, k, inv_freq, positions, _ROPE_LAYOUT[layout], mscale)
+        if r is not None:
+            return _taken(r, "gbn_rope_fwd")
     return _rope(G.library().gbn_rope_fwd, "gbn_rope_fwd", q, k, inv_freq, positions, layout, mscale, q_out,
                  k_out, stream)
 
@@ -346,6 +367,10 @@ def rope_fwd(q, k, inv_freq, positions=None, *, layout="half", mscale=1.0, q_out
 def rope_bwd(dq, dk, inv_freq, positions=None, *, layout="half", mscale=1.0, dq_out=None,
              dk_out=None, stream=None):
     """Gradients of ``rope_fwd``'s inputs from those of its outputs."""
+    if _fast is not None and dq_out is None and dk_out is None and stream is None:
+        r = _fast.rope(1, dq, dk, inv_freq, positions, _ROPE_LAYOUT[layout], mscale)
+        if r is not None:
+            return _taken(r, "gbn_rope_bwd")
     return _rope(G.library().gbn_rope_bwd, "gbn_rope_bwd", dq, dk, inv_freq, positions, layout, mscale,
                  dq_out, dk_out, stream)
 
@@ -430,6 +455,11 @@ def paged_append(k, v, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, q=
     keys are rotated to their positions on the way, and ``q`` [tokens, heads,
     head_dim], if given, into ``q_out`` (returned; a new tensor unless given,
     and then with unwritten padding rows)."""
+    if _fast is not None and q_out is None and stream is None:
+        r = _fast.append(k, v, k_cache, v_cache, cu_seqlens, kv_lens, block_table, q, inv_freq,
+                         _ROPE_LAYOUT[layout], mscale, k_scale, v_scale)
+        if r is not None:
+            return _taken(r, "gbn_paged_append")
     cdt, hk, d = _paged_args(k, k_cache, v_cache, cu_seqlens, kv_lens, block_table)
     dev = k.device
     if stream is not None and q is not None and q_out is None and k.is_cuda:
@@ -521,6 +551,12 @@ def paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, ma
     to the token's own.  Returns out, or (out, lse) with ``return_lse``; both
     are new tensors unless given (padding rows are not written).
     ``workspace``: ``paged_attention_workspace``; allocated here when needed."""
+    if (_fast is not None and out is None and lse is None and workspace is None
+            and stream is None):
+        r = _fast.attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, max_q, max_kv,
+                            scale, causal, window, k_scale_inv, v_scale_inv, return_lse)
+        if r is not None:
+            return _taken(r, "gbn_paged_attention")
     cdt, hk, d = _paged_args(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table)
     dev, t, hq = q.device, q.shape[0], q.shape[1]
     _inner("q", q)
