@@ -283,6 +283,73 @@ def test_two_streams_with_their_own_workspaces(gpu):
         assert torch.equal(o, r)
 
 
+@pytest.mark.parametrize("c", [B([2, 1], [40, 33], heads=16, kv_heads=8, dim=128),
+                               B([100, 30], [100, 90], heads=16, kv_heads=8, dim=128),
+                               B([2, 1], [40, 33], heads=16, kv_heads=8, dim=128, fp8=True),
+                               B([100, 30], [100, 90], heads=16, kv_heads=8, dim=128, fp8=True),
+                               B([2, 1], [40, 33], heads=16, kv_heads=8, dim=128, page=2)], ids=str)
+def test_caches_beyond_two_to_the_31_elements(gpu, c):
+    """Pages whose element (and byte) offsets do not fit 32 bits, written by the
+    append and read by the attention."""
+    s = make(c)
+    used = s["k_cache"].shape[0]
+    pages = (1 << 32) // (c.page * c.kv_heads * c.dim) + used + 5  # over 2^32 elements
+    big = {}
+    for n in ("k_cache", "v_cache"):
+        big[n] = torch.empty(pages, *s[n].shape[1:], dtype=s[n].dtype, device="cuda")
+        big[n][pages - used:].view(torch.uint8).copy_(s[n].view(torch.uint8))
+    s["table"] = torch.where(s["table"] >= 0, s["table"] + (pages - used), -1).int()
+    out, lse = attend(gpu, c, {**s, **big})
+    torch.cuda.synchronize()
+    check_attention(c, s, out, lse)
+    f = gpu.rope_frequencies(c.dim)
+    before = s["k_cache"].cpu().clone(), s["v_cache"].cpu().clone()
+    qo = gpu.paged_append(s["k"], s["v"], big["k_cache"], big["v_cache"], s["cu"], s["kv_lens"],
+                          s["table"], q=s["q"], inv_freq=f, k_scale=s["scale"], v_scale=s["scale"])
+    torch.cuda.synchronize()
+    tail = {n: big[n][pages - used:].clone() for n in big}
+    del big
+    check_append(c, {**s, **tail}, before, qo, f.cpu().numpy(), "half", 1.0)
+
+
+def test_more_sequences_than_are_taken_by_length(gpu):
+    n = 300
+    c = B([9 + i % 3 for i in range(n)], [9 + i % 3 + (i * 37) % 80 for i in range(n)], heads=8,
+          kv_heads=1, dim=64)
+    s = make(c)
+    out, lse = attend(gpu, c, s)
+    torch.cuda.synchronize()
+    check_attention(c, s, out, lse)
+
+
+@pytest.mark.parametrize("q,kv", [((3, 1), (90, 700)), ((150, 70), (150, 700))])
+def test_e4m3_scales_of_any_sign_and_large_queries(gpu, q, kv):
+    """A negative k_scale_inv turns the scores' sign, 0 makes them equal; bf16
+    queries far beyond f16's range, with a scale to match, change nothing."""
+    c = B(q, kv, heads=8, kv_heads=2, dim=128, fp8=True)
+    s = make(c)
+    plus, lp = attend(gpu, c, s)
+    s["q"].neg_()
+    minus, lm = gpu.paged_attention(s["q"], s["k_cache"], s["v_cache"], s["cu"], s["kv_lens"],
+                                    s["table"], max_q=s["max_q"], k_scale_inv=-s["scale_inv"],
+                                    v_scale_inv=s["scale_inv"], return_lse=True)
+    assert torch.equal(plus, minus) and torch.equal(lp, lm)
+    s["q"].neg_()
+    for e in (90, -90):
+        big = s["q"] * 2.0 ** e
+        out = gpu.paged_attention(big, s["k_cache"], s["v_cache"], s["cu"], s["kv_lens"],
+                                  s["table"], max_q=s["max_q"], k_scale_inv=s["scale_inv"],
+                                  v_scale_inv=s["scale_inv"], scale=c.dim ** -0.5 * 2.0 ** -e)
+        # the same bits but for roundings of the (power-of-two scaled) score factor
+        assert torch.equal(out, plus)
+    zero = torch.zeros(1, device="cuda")
+    out, lse = gpu.paged_attention(s["q"], s["k_cache"], s["v_cache"], s["cu"], s["kv_lens"],
+                                   s["table"], max_q=s["max_q"], k_scale_inv=zero,
+                                   v_scale_inv=s["scale_inv"], return_lse=True)
+    s["cpu"]["q"] = s["cpu"]["q"] * 0
+    check_attention(c, s, out, lse)
+
+
 def test_stream_argument_while_the_current_stream_is_busy(gpu):
     """A call on another stream than the current one, its workspace and outputs
     allocated by the call, while the current stream reuses freed memory."""
