@@ -18,8 +18,9 @@
 // warp has its own 16 rows and all keys.  The products run on mma.sync m16n8k16:
 // the tensor work per byte is far below what tcgen05 is for, and the accumulators
 // stay in registers next to the softmax.  Long key ranges are split over CTAs
-// (fp32 partial outputs, merged by a second kernel), so that a few sequences fill
-// the GPU.
+// so that a few sequences fill the GPU: up to eight of them are a thread-block
+// cluster, whose CTAs read one another's fp32 partial outputs from shared memory
+// and write the result; more leave them in the workspace for a second kernel.
 //
 // Pages of fewer than 8 slots are smaller than the swizzle's pattern: the same
 // warp then copies them 16 bytes a lane (cp.async) into the same places.
@@ -52,6 +53,14 @@ static_assert(sizeof(gbn_paged_attention_args) == 12 * 8 + 22 * 8 + 4 * 4, "");
 constexpr int kStepThreads = 128;
 constexpr int kStepKeys = 64;          // keys per tile
 constexpr int kMaxSplits = 512;
+constexpr int kMaxCluster = 8;         // splits that merge within a cluster (the portable size)
+
+// Shared-memory address `a` of this CTA, in CTA `rank` of its cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t a, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -118,13 +127,14 @@ struct StepShape {
   static constexpr int kStages = kRowBytes >= 512 ? 2 : kRowBytes >= 256 ? 3 : 4;
   static constexpr int kRing = kStages * 2 * kTileBytes;
   static constexpr int kMerge = 4 * 16 * DP * 4;  // outputs of the four warps, over the ring
-  static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
+  // Over the ring too: this CTA's own merged rows, for its cluster.
+  static constexpr int kBody = kRing > 2 * kMerge ? kRing : 2 * kMerge;
   static constexpr int kQPitch = DP * 2 + 16;
   // CTAs an SM, by shared memory and registers (E4M3 heads of 128 in three CTAs
   // of 128 registers spill: 111 us for 262144 keys against 95 in two).
   static constexpr int kResident = DP <= 64 ? 3 : DP <= 128 ? 2 : 1;
   static constexpr int smem(int mt) {
-    return kBody + 16 * mt * kQPitch + 4 * 16 * 8 + 16 * mt * 4 + 2 * kStages * 8;
+    return kBody + 16 * mt * kQPitch + 4 * 16 * 8 + 16 * mt * (4 + 8) + 2 * kStages * 8;
   }
 };
 
@@ -146,7 +156,8 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
   uint8_t* s_q = smem + Shape::kBody;
   float2* s_ml = reinterpret_cast<float2*>(s_q + 16 * MT * Shape::kQPitch);
   float* s_qs = reinterpret_cast<float*>(s_ml + 4 * 16);  // E4M3: what a q row's scores are times
-  uint64_t* s_full = reinterpret_cast<uint64_t*>(s_qs + 16 * MT);
+  float2* s_pml = reinterpret_cast<float2*>(s_qs + 16 * MT);  // cluster: max and sum of each row
+  uint64_t* s_full = reinterpret_cast<uint64_t*>(s_pml + 16 * MT);
   uint64_t* s_empty = s_full + Shape::kStages;
 
   pdl_begin();
@@ -154,12 +165,20 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
   const int wm = warp / WN, wn = warp % WN;
   const int qr = lane >> 2, qc = lane & 3;
   uint32_t x = blockIdx.x;
+  int split = 0;
+  if (p.cluster) {  // a cluster is consecutive CTAs
+    split = x % p.splits;
+    x /= p.splits;
+  }
   const int h = x % p.hkv;
   x /= p.hkv;
   const int rt = x % p.row_tiles;
   x /= p.row_tiles;
-  const int split = x % p.splits;
-  const int b = x / p.splits;
+  if (!p.cluster) {
+    split = x % p.splits;
+    x /= p.splits;
+  }
+  const int b = x;
 
   const SeqRange s = seq_range(p, b, tid == 0 && split == 0 && rt == 0 && h == 0);
   const int r0 = rt * 16 * MT;
@@ -172,7 +191,7 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
   const int k1 = static_cast<int>(min(start + p.split_len, static_cast<int64_t>(max(hi, 0))));
   const int base = k0 & ~(kStepKeys - 1);  // first key of the tiles
   const int ntiles = k1 > k0 ? (k1 - base + kStepKeys - 1) / kStepKeys : 0;
-  if (ntiles == 0 && split > 0) {
+  if (ntiles == 0 && split > 0 && !p.cluster) {
     // Nothing here: say so (the merge reads every split's maximum and sum).
     for (int r = tid; r < rows; r += kStepThreads + 32) {
       const int gr = r0 + r;
@@ -544,6 +563,7 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
   __syncthreads();
   const float vscale = FP8 ? *p.v_scale_inv : 1.f;
   constexpr int Q4 = DP / 8;  // groups of 8 columns per row
+  float* s_part = reinterpret_cast<float*>(smem + Shape::kMerge);
   for (int i = tid; i < rows * Q4; i += kStepThreads + 32) {
     const int r = i / Q4, c = (i % Q4) * 8;
     if (c >= p.d) continue;
@@ -576,7 +596,12 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
         row_again<T, FP8>(p, b, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
                           FP8 ? p.scale_log2 * *p.k_scale_inv : p.scale_log2, mm, low, high, c, acc);
     }
-    if (p.splits > 1) {
+    if (p.cluster) {
+      float* dst = s_part + r * DP + c;
+      *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      *reinterpret_cast<float4*>(dst + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      if (c == 0) s_pml[r] = make_float2(mm, ll);
+    } else if (p.splits > 1) {
       float* dst = p.part_o + (static_cast<int64_t>(split) * p.tokens * p.hq + ro) * p.d + c;
       *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
       *reinterpret_cast<float4*>(dst + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
@@ -589,6 +614,56 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
       st_words<4>(reinterpret_cast<T*>(p.out) + token * p.ot + head * p.oh + c, w);
       if (c == 0 && p.lse) p.lse[ro] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
     }
+  }
+  if (p.cluster) {
+    // Every CTA of the cluster merges a share of the rows from all of them, in the
+    // order of the splits.
+    cluster_sync();
+    const uint32_t part = smem_u32(s_part), pml = smem_u32(s_pml);
+    for (int i = split * (kStepThreads + 32) + tid; i < rows * Q4;
+         i += p.splits * (kStepThreads + 32)) {
+      const int r = i / Q4, c = (i % Q4) * 8;
+      if (c >= p.d) continue;
+      float2 ml[kMaxCluster];
+      float m2 = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (k < p.splits) {
+          const uint32_t a = cluster_addr(pml + r * 8, k);
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(ml[k].x), "=f"(ml[k].y) : "r"(a));
+        }
+        m2 = fmaxf(m2, ml[k].x);
+      }
+      const float mb = m2 == -INFINITY ? 0.f : m2;
+      float l2 = 0.f, acc[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        if (k >= p.splits || ml[k].y == 0.f) continue;
+        const float w = ex2(ml[k].x - mb);
+        l2 += ml[k].y * w;
+        const uint32_t a = cluster_addr(part + (r * DP + c) * 4, k);
+        float v[8];
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(a));
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "r"(a + 16));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(v[e], w, acc[e]);
+      }
+      const int gr = r0 + r;
+      const int token = s.q0 + gr / p.group, head = h * p.group + gr % p.group;
+      const float inv = l2 == 0.f ? 0.f : vscale / l2;
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = narrow2<T>(p2(acc[2 * e] * inv, acc[2 * e + 1] * inv));
+      st_words<4>(reinterpret_cast<T*>(p.out) + token * p.ot + head * p.oh + c, w);
+      if (c == 0 && p.lse)
+        p.lse[static_cast<int64_t>(token) * p.hq + head] = l2 == 0.f ? -INFINITY : (m2 + log2f(l2)) * kLn2;
+    }
+    cluster_sync();  // nobody leaves while its shared memory is read
   }
 }
 
@@ -693,8 +768,21 @@ cudaError_t launch_step(const AttnParams& p, int64_t grid, cudaStream_t st) {
                         p.vh))
       return cudaErrorInvalidValue;
   }
-  return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(kStepThreads + 32), smem, st, p, km,
-                    vm);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.splits);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kStepThreads + 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster ? 2 : 1;
+  const cudaError_t le = cudaLaunchKernelEx(&cfg, k, p, km, vm);
+  return le != cudaSuccess ? le : cudaGetLastError();
 }
 template <typename T, bool FP8, int DP>
 cudaError_t launch_step_mt(const AttnParams& p, int mt, int64_t grid, cudaStream_t st) {
@@ -773,6 +861,7 @@ struct AttnPlan {
   int row_tiles;
   int splits;
   int split_len;
+  bool cluster;   // the splits merge within a cluster: no workspace, no second kernel
   int64_t ctas;
 };
 
@@ -803,6 +892,7 @@ AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t d, int64
   }
   const int64_t tiles = batches * hkv * a.row_tiles;
   const int64_t step = a.prefill ? kPrefillKeys : kStepKeys;
+  const int64_t slots = sms * (d <= 64 ? 3 : d <= 128 ? 2 : 1);  // CTAs of the step kernel at once
   int64_t splits = 1;
   if (a.prefill) {
     // One CTA per SM: as many as fit one round, at least 512 keys each (4 sequences
@@ -816,20 +906,26 @@ AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t d, int64
     // exactly one round (131072 keys, 8 kv heads, bf16: 82-87 us; 1.5 rounds 88 to
     // 106).  Several may differ in length, and the long ones' CTAs are then what
     // is left: 8 sequences of 2000-16000 keys 51 us at 1.7 rounds, 64 at 0.8;
-    // 64 sequences 350 us at 10 rounds, 377 at 3.4.  At least 192 keys each, and
-    // none up to 320 (a second kernel merges: 3-4 us).
-    const int64_t slots = sms * (d <= 64 ? 3 : d <= 128 ? 2 : 1);
+    // 64 sequences 350 us at 10 rounds, 377 at 3.4.  Each has so many keys that it
+    // pays its start: 64 sequences of 100-1000 keys 35 us whole, 66 in fives.
     const int64_t rounds2 = batches == 1 ? 2 : tiles * 4 < slots ? 3 : tiles < slots ? 8 : 20;
     splits = rounds2 * slots / (2 * (tiles > 0 ? tiles : 1));
-    const int64_t most = ceil_div(range, 192);
+    const int64_t most = ceil_div(range, tiles >= slots ? 1536 : tiles * 4 >= slots ? 512 : 192);
     if (splits > most) splits = most;
     if (splits > kMaxSplits) splits = kMaxSplits;
+    // What a cluster can merge, where that leaves no more than 512 keys each.
+    if (splits > kMaxCluster && range <= kMaxCluster * 512 && tiles * kMaxCluster <= slots)
+      splits = kMaxCluster;
   }
   if (splits < 1) splits = 1;
   int64_t len = ceil_div(ceil_div(range, splits), step) * step;
   if (len < 1) len = 1;
   a.split_len = static_cast<int>(len);
   a.splits = static_cast<int>(range > 0 ? ceil_div(range, len) : 1);
+  // Clusters where all of them are resident at once: 4 sequences of up to 700 keys
+  // 6.4 us against 7.3 with a second kernel; beyond that, clusters wait for room
+  // for all their CTAs (64 sequences of 2000-16000 keys in sixes 510 us against 348).
+  a.cluster = !a.prefill && a.splits > 1 && a.splits <= kMaxCluster && tiles * a.splits <= slots;
   a.ctas = tiles * a.splits;
   return a;
 }
@@ -874,7 +970,7 @@ gbn_status plan_for(const AttnSizes& z, int causal, AttnPlan* a) {
 }
 
 size_t plan_bytes(const AttnSizes& z, const AttnPlan& a) {
-  if (a.splits <= 1) return 0;
+  if (a.splits <= 1 || a.cluster) return 0;
   const int64_t rows = z.tokens * z.hq;
   return static_cast<size_t>(align256(rows * a.splits * 8) + rows * a.splits * z.d * 4);
 }
@@ -994,6 +1090,7 @@ gbn_status gbn_paged_attention(const gbn_paged_attention_args* args, cudaStream_
   p.row_tiles = a.row_tiles;
   p.splits = a.splits;
   p.split_len = a.split_len;
+  p.cluster = a.cluster;
   p.scale_log2 = c.scale * kAttnLog2e;
 
   const int mt = a.rows / 16;
@@ -1007,7 +1104,7 @@ gbn_status gbn_paged_attention(const gbn_paged_attention_args* args, cudaStream_
     e = fp8 ? launch_step_d<__half, true>(p, mt, a.ctas, stream)
             : launch_step_d<__half, false>(p, mt, a.ctas, stream);
   if (e != cudaSuccess) return GBN_ERR_CUDA;
-  if (a.splits > 1) {
+  if (a.splits > 1 && !a.cluster) {
     e = dtype == GBN_BF16 ? launch_merge<__nv_bfloat16>(p, fp8, stream)
                           : launch_merge<__half>(p, fp8, stream);
     if (e != cudaSuccess) return GBN_ERR_CUDA;

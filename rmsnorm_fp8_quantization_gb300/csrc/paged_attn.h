@@ -38,6 +38,7 @@ struct AttnParams {
   int row_tiles;       // row tiles per (sequence, kv head)
   int splits;
   int split_len;
+  int cluster;         // the splits of a row tile are a thread-block cluster and merge themselves
   float scale_log2;    // scale * log2(e)
 };
 
