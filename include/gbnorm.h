@@ -428,7 +428,7 @@ gbn_status gbn_paged_append(const gbn_paged_append_args* args, cudaStream_t stre
  * lse = -inf.  Query head n reads kv head n / (q_heads / kv_heads).
  *
  *   q, out     [tokens, q_heads, head_dim] dtype (BF16 or F16), element
- *              strides for token and head
+ *              strides for token and head; out must not overlap q
  *   lse        fp32 [tokens, q_heads] contiguous, or NULL
  *   k_scale_inv, v_scale_inv  fp32 [1], device, E4M3 caches only: what the
  *              codes are multiplied by

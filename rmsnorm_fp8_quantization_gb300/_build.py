@@ -72,6 +72,8 @@ def build_fastcall() -> None:
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and up_to_date():
+        if not os.path.exists(FAST):
+            build_fastcall()
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)

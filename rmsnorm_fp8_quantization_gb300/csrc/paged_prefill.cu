@@ -760,8 +760,9 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
         const int col = q4 * 32;
-        if (live && n > 0 && (rlo > k0 || rhi < k1)) {
-          // It dropped keys that other rows of its tiles keep.
+        if (live && n > 0 && l == l && (rlo > k0 || rhi < k1)) {
+          // It dropped keys that other rows of its tiles keep (a NaN sum: a kept
+          // score is NaN, and so is the row).
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
             bool nan = false;

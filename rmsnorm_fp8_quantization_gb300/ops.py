@@ -199,8 +199,9 @@ def _on_stream(stream, device, fn, *args, **kw):
     """fn(...) with ``stream`` current, so that what it allocates belongs to the
     stream that uses it (a workspace allocated on another stream could be handed
     out again there while this one still works in it)."""
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # a raw handle, or an object that holds one
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        stream = torch.cuda.ExternalStream(handle, device=device)
     with torch.cuda.stream(stream):
         return fn(*args, **kw)
 
@@ -572,6 +573,8 @@ def paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, ma
         if out.shape != q.shape:
             raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(q.shape)}")
         _inner("out", out)
+        if out.data_ptr() == q.data_ptr() and q.numel():
+            raise ValueError("out must not be q")
     if return_lse and lse is None:
         lse = torch.empty(t, hq, dtype=torch.float32, device=dev)
     elif lse is not None:
@@ -590,7 +593,9 @@ def paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, ma
     _on_gpu(q)
     size = 0
     if workspace is not None:
-        size = workspace.numel()
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: contiguous, on {dev}")
+        size = workspace.numel() * workspace.element_size()
     else:
         size = _attention_bytes(q.get_device(), t, n, hq, hk, d, page, pages, max_q, mkv, window,
                                 bool(causal), dt, cdt)

@@ -312,6 +312,37 @@ def test_caches_beyond_two_to_the_31_elements(gpu, c):
     check_append(c, {**s, **tail}, before, qo, f.cpu().numpy(), "half", 1.0)
 
 
+@pytest.mark.parametrize("c", [B([1, 2], [300, 77], dim=128), B([100, 40], [300, 77], dim=64),
+                               B([100, 1], [300, 77], dim=128, fp8=True)], ids=str)
+def test_keys_and_values_in_one_tensor_and_strided_queries(gpu, c):
+    """[pages, 2, page, heads, dim] caches, q as a view of a packed projection, the
+    table as a view of a wider one, other values around all of them."""
+    s = make(c)
+    one = torch.stack([s["k_cache"], s["v_cache"]], 1)
+    kc, vc = one[:, 0], one[:, 1]
+    wide = torch.randn(s["q"].shape[0], c.heads + 3, c.dim, device="cuda").to(s["q"].dtype)
+    wide[:, 1:1 + c.heads] = s["q"]
+    table = torch.full((s["table"].shape[0], s["table"].shape[1] + 4), 10 ** 9, dtype=torch.int32,
+                       device="cuda")
+    table[:, :-4] = s["table"]
+    v = {**s, "k_cache": kc, "v_cache": vc, "q": wide[:, 1:1 + c.heads], "table": table[:, :-4]}
+    out, lse = attend(gpu, c, v)
+    ref, rl = attend(gpu, c, s)
+    assert torch.equal(out, ref) and torch.equal(lse, rl)
+    f = gpu.rope_frequencies(c.dim)
+    before = s["k_cache"].cpu().clone(), s["v_cache"].cpu().clone()
+    qo = gpu.paged_append(s["k"], s["v"], kc, vc, s["cu"], s["kv_lens"], table[:, :-4], q=v["q"],
+                          inv_freq=f, k_scale=s["scale"], v_scale=s["scale"])
+    check_append(c, {**s, "k_cache": kc, "v_cache": vc}, before, qo, f.cpu().numpy(), "half", 1.0)
+
+
+def test_attention_refuses_q_as_its_output(gpu):
+    c = B([1], [20])
+    s = make(c)
+    with pytest.raises(ValueError):
+        attend(gpu, c, s, out=s["q"])
+
+
 def test_more_sequences_than_are_taken_by_length(gpu):
     n = 300
     c = B([9 + i % 3 for i in range(n)], [9 + i % 3 + (i * 37) % 80 for i in range(n)], heads=8,
