@@ -588,22 +588,31 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
     const bool live = t * kRowsT + r < rows;
     const int token_i = live ? gr / p.group : i_last;
     const int head = h * p.group + (live ? gr % p.group : 0);
-    // q's rows, by whole warps: a row's 16-byte chunks by neighbouring lanes.
+    // q's rows, by whole warps: a row's 16-byte chunks by neighbouring lanes.  All
+    // loads first: one at a time they took most of the 21000 cycles that a CTA
+    // needed up to its first scores.
     {
       constexpr int C = DP / 8;
       const T* q = reinterpret_cast<const T*>(p.q);
       // A negative factor of the keys turns q's sign, a factor of 0 clears it:
       // what is left multiplies the scores by something positive.
       const uint32_t flip = kscale < 0.f ? 0x80008000u : 0u, keep = kscale == 0.f ? 0u : ~0u;
-      for (int i = lane; i < 32 * C; i += 32) {
-        const int rr = quad * 32 + i / C, c = i % C;
-        const int row = t * kRowsT + rr;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      const int c = lane % C;
+      uint4 ws[C];
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const int row = t * kRowsT + quad * 32 + i * (32 / C) + lane / C;
+        ws[i] = make_uint4(0u, 0u, 0u, 0u);
         if (row < rows && c * 8 < p.d) {
           const int g = r0 + row;
-          w = *reinterpret_cast<const uint4*>(q + (s.q0 + g / p.group) * p.qt +
-                                              (h * p.group + g % p.group) * p.qh + c * 8);
+          ws[i] = *reinterpret_cast<const uint4*>(q + (s.q0 + g / p.group) * p.qt +
+                                                  (h * p.group + g % p.group) * p.qh + c * 8);
         }
+      }
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const int rr = quad * 32 + i * (32 / C) + lane / C;
+        uint4& w = ws[i];
         if constexpr (FP8) {
           const float back = q_to_f16<T, C>(w);
           if (c == 0) bars.q_scale[t][rr] = back;
