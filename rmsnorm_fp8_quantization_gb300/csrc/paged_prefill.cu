@@ -587,10 +587,10 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
     const int gr = r0 + t * kRowsT + r;          // row of the (sequence, kv head)
     const bool live = t * kRowsT + r < rows;
     const int token_i = live ? gr / p.group : i_last;
-    const int head = h * p.group + (live ? gr % p.group : 0);
-    // q's rows, by whole warps: a row's 16-byte chunks by neighbouring lanes.  All
-    // loads first: one at a time they took most of the 21000 cycles that a CTA
-    // needed up to its first scores.
+    const int head = h * p.group + (live ? gr - token_i * p.group : 0);
+    // q's rows, by whole warps: a row's 16-byte chunks by neighbouring lanes, its
+    // place from the lane that has divided for it.  All loads first: one at a time
+    // they took most of the 21000 cycles that a CTA needed up to its first scores.
     {
       constexpr int C = DP / 8;
       const T* q = reinterpret_cast<const T*>(p.q);
@@ -598,16 +598,15 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
       // what is left multiplies the scores by something positive.
       const uint32_t flip = kscale < 0.f ? 0x80008000u : 0u, keep = kscale == 0.f ? 0u : ~0u;
       const int c = lane % C;
+      const int64_t q_at = (s.q0 + token_i) * p.qt + head * p.qh;
       uint4 ws[C];
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        const int row = t * kRowsT + quad * 32 + i * (32 / C) + lane / C;
+        const int rr = i * (32 / C) + lane / C;
+        const int64_t from = __shfl_sync(0xFFFFFFFFu, q_at, rr);
         ws[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (row < rows && c * 8 < p.d) {
-          const int g = r0 + row;
-          ws[i] = *reinterpret_cast<const uint4*>(q + (s.q0 + g / p.group) * p.qt +
-                                                  (h * p.group + g % p.group) * p.qh + c * 8);
-        }
+        if (t * kRowsT + quad * 32 + rr < rows && c * 8 < p.d)
+          ws[i] = *reinterpret_cast<const uint4*>(q + from + c * 8);
       }
 #pragma unroll
       for (int i = 0; i < C; ++i) {
@@ -753,61 +752,91 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
       const int64_t token = s.q0 + token_i;
       const int64_t ro = token * p.hq + head;
       const bool part = p.splits > 1;
+      // Through shared memory (q's rows of this warp are used up), 128 bytes a row at
+      // a time, so that a store writes whole lines: a lane to a row took 5400 cycles
+      // a CTA.
+      uint8_t* const stage = gen0 + t * Shape::kSlot + quad * 32 * 128;
+      const bool mine = live && (!part || l != 0.f);
+      uint8_t* const dst = part ? reinterpret_cast<uint8_t*>(p.part_o) : static_cast<uint8_t*>(p.out);
+      const int64_t at = part ? (static_cast<int64_t>(split) * p.tokens * p.hq + ro) * p.d * 4
+                              : (token * p.ot + head * p.oh) * 2;
+      auto put = [&](int c, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+            make_uint4(w0, w1, w2, w3);
+      };
+      auto flush = [&](int from, int chunks) {  // byte of the row, 16-byte chunks
+        __syncwarp();
+        const int c = lane & 7;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = i * 4 + (lane >> 3);
+          const int64_t row = __shfl_sync(0xFFFFFFFFu, at, rr);
+          const bool on = __shfl_sync(0xFFFFFFFFu, static_cast<int>(mine), rr);
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
+          if (on && c < chunks) *reinterpret_cast<uint4*>(dst + row + from + c * 16) = w;
+        }
+        __syncwarp();
+      };
       const float inv = part ? 1.f : l == 0.f ? 0.f : vscale / l;
       if (live) {
         if (part) p.part_ml[ro * p.splits + split] = make_float2(m, l);
         else if (p.lse) p.lse[ro] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
-#pragma unroll
+      // (one copy of the code: a CTA runs it once, and fetching it is what it costs)
+#pragma unroll 1
       for (int q4 = 0; q4 < DP / 32; ++q4) {
+        const int col = q4 * 32;
         uint32_t o[32];
+        uint32_t bad = 0;  // bit i: a NaN in columns col + 8 i .. + 7
         if (n > 0) {
-          tc_ld32(to + q4 * 32, o);
+          tc_ld32(to + col, o);
           tc_wait_ld<32>(o);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
-        const int col = q4 * 32;
-        if (live && n > 0 && l == l && (rlo > k0 || rhi < k1)) {
-          // It dropped keys that other rows of its tiles keep (a NaN sum: a kept
-          // score is NaN, and so is the row).
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            bool nan = false;
+        for (int i = 0; i < 32; ++i)
+          bad |= __uint_as_float(o[i]) != __uint_as_float(o[i]) ? 1u << (i / 8) : 0u;
+        auto narrow = [&](float x, float y) {
+          return narrow2<T>(p2(l == 0.f ? 0.f : x * inv, l == 0.f ? 0.f : y * inv));
+        };
+        if (part) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              nan |= __uint_as_float(o[i + e]) != __uint_as_float(o[i + e]);
-            if (nan && col + i < p.d) {
-              float acc[8];
-              row_again<T, FP8>(p, b, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
-                                FP8 ? p.scale_log2 * kscale : p.scale_log2, m, rlo, rhi, col + i, acc);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) o[i + e] = __float_as_uint(acc[e]);
-            }
-          }
-        }
-        if (live && part) {
-          float* dst = p.part_o + (static_cast<int64_t>(split) * p.tokens * p.hq + ro) * p.d;
-          if (l != 0.f) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              if (col + i < p.d)
-                *reinterpret_cast<uint4*>(dst + col + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-          }
-        } else if (live) {
-          T* dst = reinterpret_cast<T*>(p.out) + token * p.ot + head * p.oh;
+          for (int i = 0; i < 8; ++i) put(i, o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else {
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              w[e] = narrow2<T>(p2(l == 0.f ? 0.f : __uint_as_float(o[i + 2 * e]) * inv,
-                                   l == 0.f ? 0.f : __uint_as_float(o[i + 2 * e + 1]) * inv));
-            if (col + i < p.d) st_words<4>(dst + col + i, w);
+              w[e] = narrow(__uint_as_float(o[i + 2 * e]), __uint_as_float(o[i + 2 * e + 1]));
+            put((q4 & 1) * 4 + i / 8, w[0], w[1], w[2], w[3]);
           }
         }
-        __syncwarp();  // the loads of tensor memory take the whole warp
+        if (bad && live && n > 0 && l == l && (rlo > k0 || rhi < k1)) {
+          // It dropped keys that other rows of its tiles keep (a NaN sum: a kept
+          // score is NaN, and so is the row).
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            if (!(bad & (1u << i)) || col + 8 * i >= p.d) continue;
+            float f[8];
+            row_again<T, FP8>(p, b, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
+                              FP8 ? p.scale_log2 * kscale : p.scale_log2, m, rlo, rhi, col + 8 * i, f);
+            if (part) {
+#pragma unroll
+              for (int e = 0; e < 8; e += 4)
+                put(2 * i + e / 4, __float_as_uint(f[e]), __float_as_uint(f[e + 1]),
+                    __float_as_uint(f[e + 2]), __float_as_uint(f[e + 3]));
+            } else {
+              put((q4 & 1) * 4 + i, narrow(f[0], f[1]), narrow(f[2], f[3]), narrow(f[4], f[5]),
+                  narrow(f[6], f[7]));
+            }
+          }
+        }
+        if (part) flush(col * 4, (p.d - col) / 4);
+        else if (q4 & 1) flush((col - 32) * 2, (p.d - (col - 32)) / 8);
+        else __syncwarp();  // the loads of tensor memory take the whole warp
       }
     }
   }
