@@ -751,12 +751,56 @@ __global__ void __launch_bounds__(kMergeThreads)
 // ---- host side
 
 template <typename T, bool FP8, int DP, int MT>
+cudaError_t allow_step() {
+  static std::atomic<uint64_t> done{0};
+  return allow_smem(paged_step_kernel<T, FP8, DP, MT>, StepShape<T, FP8, DP>::smem(MT), done);
+}
+
+// Clusters of c CTAs of this kernel that device `dev` holds at once (they do not
+// cross the SM groups of the chip, so fewer than its CTA slots / c); 0: unknown.
+// Asked of the runtime once per device and size.
+template <bool FP8, int DP, int MT>
+int step_room(int c, int dev) {
+  using T = __nv_bfloat16;  // the same footprint as __half
+  static std::atomic<int> known[16][kMaxCluster + 1];
+  if (dev < 16 && known[dev][c].load(std::memory_order_relaxed) > 0)
+    return known[dev][c].load(std::memory_order_relaxed) - 1;
+  int n = 0;
+  if (allow_step<T, FP8, DP, MT>() != cudaSuccess) return 0;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(c);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(c));
+  cfg.blockDim = dim3(kStepThreads + 32);
+  cfg.dynamicSmemBytes = StepShape<T, FP8, DP>::smem(MT);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, paged_step_kernel<T, FP8, DP, MT>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (dev < 16) known[dev][c].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+template <bool FP8, int DP>
+int step_room_mt(int mt, int c, int dev) {
+  return mt == 1 ? step_room<FP8, DP, 1>(c, dev)
+                 : mt == 2 ? step_room<FP8, DP, 2>(c, dev) : step_room<FP8, DP, 4>(c, dev);
+}
+template <bool FP8>
+int step_room_d(int64_t d, int mt, int c, int dev) {
+  return d <= 64 ? step_room_mt<FP8, 64>(mt, c, dev)
+                 : d <= 128 ? step_room_mt<FP8, 128>(mt, c, dev) : step_room_mt<FP8, 256>(mt, c, dev);
+}
+
+template <typename T, bool FP8, int DP, int MT>
 cudaError_t launch_step(const AttnParams& p, int64_t grid, cudaStream_t st) {
   using Shape = StepShape<T, FP8, DP>;
   constexpr int smem = Shape::smem(MT);
   auto k = paged_step_kernel<T, FP8, DP, MT>;
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(k, smem, done);
+  const cudaError_t e = allow_step<T, FP8, DP, MT>();
   if (e != cudaSuccess) return e;
   CUtensorMap km = {}, vm = {};
   if (p.page_shift >= 3) {
@@ -868,17 +912,19 @@ struct AttnPlan {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t d, int64_t max_q,
-                   int64_t max_kv, int64_t window, int causal, int page_shift, int sms) {
+                   int64_t max_kv, int64_t window, int causal, int page_shift, bool fp8, int sms,
+                   int dev) {
   AttnPlan a;
   const int64_t r = max_q * group;
+  const int64_t keys = window > 0 && causal && window + max_q < max_kv ? window + max_q : max_kv;
   // The tcgen05 kernel from the first size on that fills half a tile of it, and
-  // for 33 to 64 rows of wide heads where the keys are many: 35 sequences of
-  // 18000-32000 keys, 48 rows: 540 us against 680 on mma.sync (E4M3 608 against
-  // 984), but 4 of 1000-4000 keys 35 us against 20 (its CTAs take longer to
-  // start); heads of 64 gain nothing (462 against 420).  Its boxes are at least 8
-  // slots (one swizzle atom).
-  const bool many = batches * hkv * max_kv > 786432 && d > 64;
-  a.prefill = (r > 64 || (r > 32 && many)) && d <= 128 && page_shift >= 3;
+  // for 33 to 64 rows of wide heads but for short sequences (48 rows, heads of 128:
+  // 4 sequences of 3000-4000 keys 21 us against 34 on mma.sync, 35 of 18000-25000 470
+  // against 680, E4M3 550 against 900; one of 2000 the same; 4 of 300 11.0 against
+  // 10.1).  Heads of 64 gain 15 % at most and lose 40 % where sequences bring fewer
+  // tokens than the longest (24 of 8 to 48 rows, 24 us against 19).  Its boxes are
+  // at least 8 slots (one swizzle atom).
+  a.prefill = (r > 64 || (r > 32 && d > 64 && keys > 512)) && d <= 128 && page_shift >= 3;
   // 33 to 64 rows as two tiles of 32: a step is shorter (each warp has half of
   // the keys) and the second read of the keys comes from L2.
   a.rows = a.prefill ? kPrefillRows : r <= 16 ? 16 : r <= 64 ? 32 : 64;
@@ -893,29 +939,56 @@ AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t d, int64
   const int64_t tiles = batches * hkv * a.row_tiles;
   const int64_t step = a.prefill ? kPrefillKeys : kStepKeys;
   const int64_t slots = sms * (d <= 64 ? 3 : d <= 128 ? 2 : 1);  // CTAs of the step kernel at once
+  auto room = [&](int c) {  // clusters of c CTAs at once
+    return fp8 ? step_room_d<true>(d, a.rows / 16, c, dev) : step_room_d<false>(d, a.rows / 16, c, dev);
+  };
   int64_t splits = 1;
   if (a.prefill) {
-    // One CTA per SM: as many as fit one round, at least 512 keys each (4 sequences
-    // of 6000 keys, 50 new tokens, 8 kv heads: 43 us in one round, 59 in half of
-    // one, 60 in two).
+    // One CTA per SM: as many as fit one round, at least 256 keys each (one sequence
+    // of 2000 keys, 48 rows, 8 kv heads: 12.1 us in eights, 13.8 in fours, 26 whole; 4
+    // of 4000 keys: 21 us in one round, 30 in half of one, 28 in 1.5).
     splits = sms / (tiles > 0 ? tiles : 1);
-    const int64_t most = ceil_div(range, 512);
+    const int64_t most = ceil_div(range, 256);
     if (splits > most) splits = most;
   } else if (range > 320) {
-    // CTAs for so many rounds of the SMs, at the longest range.  One sequence:
-    // exactly one round (131072 keys, 8 kv heads, bf16: 82-87 us; 1.5 rounds 88 to
-    // 106).  Several may differ in length, and the long ones' CTAs are then what
-    // is left: 8 sequences of 2000-16000 keys 51 us at 1.7 rounds, 64 at 0.8;
-    // 64 sequences 350 us at 10 rounds, 377 at 3.4.  Each has so many keys that it
-    // pays its start: 64 sequences of 100-1000 keys 35 us whole, 66 in fives.
-    const int64_t rounds2 = batches == 1 ? 2 : tiles * 4 < slots ? 3 : tiles < slots ? 8 : 20;
-    splits = rounds2 * slots / (2 * (tiles > 0 ? tiles : 1));
-    const int64_t most = ceil_div(range, tiles >= slots ? 1536 : tiles * 4 >= slots ? 512 : 192);
-    if (splits > most) splits = most;
+    // One round of CTAs: the largest clusters of which there is room for all.  Up to
+    // 16 sequences of 6000-8000 keys, heads of 128, one token each: 73 us against 82
+    // in shares of 512 keys and a second kernel; 1000-8000 keys 54 against 59.
+    // Beyond what eight CTAs do in 512 keys each, as many as fill the GPU (2 sequences
+    // of 12000-16000: 26 us against 30 in one and a half rounds).  Each CTA's
+    // share is limited: where sequences differ in length, the longest alone decides
+    // (4 E4M3 sequences of 5000-40000 keys: 69 us in clusters, 47 in more and smaller
+    // shares; two-byte caches share what the short ones leave of HBM).
+    int64_t one = 0;
+    if (a.row_tiles == 1 && tiles <= slots) {
+      if (range > kMaxCluster * 512 && (batches == 1 || tiles * 12 <= slots)) {
+        one = slots / tiles;
+      } else {
+        for (const int c : {8, 6, 4, 3, 2, 1}) {
+          one = c;
+          if (c == 1 || room(c) >= tiles) break;
+        }
+      }
+      if (batches > 1 && range > one * (fp8 ? 1024 : 8192)) one = 0;
+    }
+    if (one > 0) {
+      splits = one;
+      const int64_t most = ceil_div(range, 192);
+      if (splits > most) splits = most;
+    } else {
+      // Several rounds.  Sequences may differ in length, and the long ones' CTAs are
+      // then what is left: 64 sequences of 2000-16000 keys 350 us at 10 rounds, 377
+      // at 3.4.  Each CTA has so many keys that it pays its start: 64 sequences
+      // of 100-1000 keys 35 us whole, 66 in fives.
+      const int64_t rounds2 = tiles * 4 < slots ? 3 : tiles < slots ? 8 : 20;
+      splits = rounds2 * slots / (2 * (tiles > 0 ? tiles : 1));
+      const int64_t most = ceil_div(range, tiles >= slots ? 1536 : tiles * 4 >= slots ? 512 : 192);
+      if (splits > most) splits = most;
+      // What a cluster can merge, where that leaves no more than 512 keys each.
+      if (splits > kMaxCluster && range <= kMaxCluster * 512 && tiles * kMaxCluster <= slots)
+        splits = kMaxCluster;
+    }
     if (splits > kMaxSplits) splits = kMaxSplits;
-    // What a cluster can merge, where that leaves no more than 512 keys each.
-    if (splits > kMaxCluster && range <= kMaxCluster * 512 && tiles * kMaxCluster <= slots)
-      splits = kMaxCluster;
   }
   if (splits < 1) splits = 1;
   int64_t len = ceil_div(ceil_div(range, splits), step) * step;
@@ -924,8 +997,10 @@ AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t d, int64
   a.splits = static_cast<int>(range > 0 ? ceil_div(range, len) : 1);
   // Clusters where all of them are resident at once: 4 sequences of up to 700 keys
   // 6.4 us against 7.3 with a second kernel; beyond that, clusters wait for room
-  // for all their CTAs (64 sequences of 2000-16000 keys in sixes 510 us against 348).
-  a.cluster = !a.prefill && a.splits > 1 && a.splits <= kMaxCluster && tiles * a.splits <= slots;
+  // for all their CTAs (64 sequences of 2000-16000 keys in sixes 510 us against 348;
+  // 6 sequences of 4000 keys, 48 clusters of six where 46 fit, 24 us, of four 17).
+  a.cluster = !a.prefill && a.splits > 1 && a.splits <= kMaxCluster && tiles * a.splits <= slots &&
+              room(a.splits) >= tiles;
   a.ctas = tiles * a.splits;
   return a;
 }
@@ -955,7 +1030,7 @@ int log2_of(int64_t v) {
   return s;
 }
 
-gbn_status plan_for(const AttnSizes& z, int causal, AttnPlan* a) {
+gbn_status plan_for(const AttnSizes& z, int causal, bool fp8, AttnPlan* a) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -964,7 +1039,7 @@ gbn_status plan_for(const AttnSizes& z, int causal, AttnPlan* a) {
   const int64_t kv = z.max_kv < room ? z.max_kv : room;
   const int64_t mq = z.max_q < z.tokens ? z.max_q : z.tokens;
   *a = attn_plan(z.batches, z.hkv, z.hq / z.hkv, z.d, mq, kv, z.window, causal, log2_of(z.page),
-                 sms);
+                 fp8, sms, dev);
   if (a->splits > kMaxSplits || a->ctas > 0x7FFFFFFF) return GBN_ERR_SHAPE;
   return GBN_OK;
 }
@@ -999,7 +1074,7 @@ gbn_status gbn_paged_attention_workspace_size(int64_t tokens, int64_t batches, i
   *bytes = 0;
   if (tokens == 0 || batches == 0 || max_q == 0) return GBN_OK;
   AttnPlan a;
-  st = plan_for(z, causal, &a);
+  st = plan_for(z, causal, cache_dtype == GBN_E4M3, &a);
   if (st != GBN_OK) return st;
   *bytes = plan_bytes(z, a);
   return GBN_OK;
@@ -1043,7 +1118,7 @@ gbn_status gbn_paged_attention(const gbn_paged_attention_args* args, cudaStream_
       far(c.kv_heads, c.k_cache_strides[2]) || far(c.kv_heads, c.v_cache_strides[2]))
     return GBN_ERR_SHAPE;
   AttnPlan a;
-  st = plan_for(z, c.causal, &a);
+  st = plan_for(z, c.causal, fp8, &a);
   if (st != GBN_OK) return st;
   if (plan_bytes(z, a) > 0 &&
       (!c.workspace || c.workspace_bytes < plan_bytes(z, a) || !aligned(c.workspace)))
