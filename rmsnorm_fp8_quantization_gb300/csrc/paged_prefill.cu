@@ -211,6 +211,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// The same, NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // The lowest n bits set (none for n <= 0, all from 64 on).
 __device__ __forceinline__ uint64_t low_bits(int n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
@@ -754,9 +761,9 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
       const bool part = p.splits > 1;
       // Through shared memory (q's rows of this warp are used up), 128 bytes a row at
       // a time, so that a store writes whole lines: a lane to a row took 5400 cycles
-      // a CTA.
+      // a CTA, this 3900.
       uint8_t* const stage = gen0 + t * Shape::kSlot + quad * 32 * 128;
-      const bool mine = live && (!part || l != 0.f);
+      const uint32_t some = __ballot_sync(0xFFFFFFFFu, live && (!part || l != 0.f));
       uint8_t* const dst = part ? reinterpret_cast<uint8_t*>(p.part_o) : static_cast<uint8_t*>(p.out);
       const int64_t at = part ? (static_cast<int64_t>(split) * p.tokens * p.hq + ro) * p.d * 4
                               : (token * p.ot + head * p.oh) * 2;
@@ -771,7 +778,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
         for (int i = 0; i < 8; ++i) {
           const int rr = i * 4 + (lane >> 3);
           const int64_t row = __shfl_sync(0xFFFFFFFFu, at, rr);
-          const bool on = __shfl_sync(0xFFFFFFFFu, static_cast<int>(mine), rr);
+          const bool on = (some >> rr) & 1;
           const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
           if (on && c < chunks) *reinterpret_cast<uint4*>(dst + row + from + c * 16) = w;
         }
@@ -796,11 +803,15 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          bad |= __uint_as_float(o[i]) != __uint_as_float(o[i]) ? 1u << (i / 8) : 0u;
-        auto narrow = [&](float x, float y) {
-          return narrow2<T>(p2(l == 0.f ? 0.f : x * inv, l == 0.f ? 0.f : y * inv));
-        };
+        for (int i = 0; i < 32; i += 8) {
+          float x = __uint_as_float(o[i]);
+#pragma unroll
+          for (int e = 1; e < 7; e += 2)
+            x = max3_nan(x, __uint_as_float(o[i + e]), __uint_as_float(o[i + e + 1]));
+          x = max3_nan(x, x, __uint_as_float(o[i + 7]));
+          bad |= x != x ? 1u << (i / 8) : 0u;
+        }
+        auto narrow = [&](float x, float y) { return narrow2<T>(mul2(p2(x, y), p2(inv, inv))); };
         if (part) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) put(i, o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -814,15 +825,17 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
             put((q4 & 1) * 4 + i / 8, w[0], w[1], w[2], w[3]);
           }
         }
-        if (bad && live && n > 0 && l == l && (rlo > k0 || rhi < k1)) {
+        if (bad && live && l == l && (l == 0.f || rlo > k0 || rhi < k1)) {
           // It dropped keys that other rows of its tiles keep (a NaN sum: a kept
-          // score is NaN, and so is the row).
+          // score is NaN, and so is the row).  A sum of 0: nothing has a weight.
 #pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             if (!(bad & (1u << i)) || col + 8 * i >= p.d) continue;
-            float f[8];
-            row_again<T, FP8>(p, b, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
-                              FP8 ? p.scale_log2 * kscale : p.scale_log2, m, rlo, rhi, col + 8 * i, f);
+            float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (l != 0.f)
+              row_again<T, FP8>(p, b, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
+                                FP8 ? p.scale_log2 * kscale : p.scale_log2, m, rlo, rhi, col + 8 * i,
+                                f);
             if (part) {
 #pragma unroll
               for (int e = 0; e < 8; e += 4)
