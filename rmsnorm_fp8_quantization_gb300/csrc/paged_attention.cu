@@ -90,6 +90,10 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
   return r;
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   if constexpr (std::is_same<T, __half>::value)
@@ -160,8 +164,19 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
   uint64_t* s_full = reinterpret_cast<uint64_t*>(s_pml + 16 * MT);
   uint64_t* s_empty = s_full + Shape::kStages;
 
-  pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool by_tma = p.page_shift >= 3;
+  if (tid == 0) {
+#pragma unroll
+    for (int i = 0; i < Shape::kStages; ++i) {
+      mbar_init(&s_full[i], by_tma ? 1 : 32);
+      mbar_init(&s_empty[i], 4);
+    }
+    fence_mbar_init();
+  }
+  if (by_tma && warp == 4 && lane < 2) prefetch_map(lane ? &vmap : &kmap);
+  __syncthreads();
+  pdl_begin();
   const int wm = warp / WN, wn = warp % WN;
   const int qr = lane >> 2, qc = lane & 3;
   uint32_t x = blockIdx.x;
@@ -201,20 +216,12 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
     return;
   }
 
-  const bool by_tma = p.page_shift >= 3;
-  if (tid == 0) {
-#pragma unroll
-    for (int i = 0; i < Shape::kStages; ++i) {
-      mbar_init(&s_full[i], by_tma ? 1 : 32);
-      mbar_init(&s_empty[i], 4);
-    }
-    fence_mbar_init();
-  }
-  // q's rows into shared memory (rows past the end and columns past d: zero).
-  {
+  // q's rows into shared memory (rows past the end and columns past d: zero), by
+  // the computing warps alone: the fetch of keys does not wait for them.
+  if (warp < 4) {
     constexpr int C = DP / 8;
     const T* q = reinterpret_cast<const T*>(p.q);
-    for (int i = tid; warp < 4 && i < 16 * MT * C; i += kStepThreads) {
+    for (int i = tid; i < 16 * MT * C; i += kStepThreads) {
       const int r = i / C, c = i % C;
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
       if (r < rows && c * 8 < p.d) {
@@ -229,8 +236,8 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
       }
       *reinterpret_cast<uint4*>(s_q + r * Shape::kQPitch + c * 16) = w;
     }
+    asm volatile("bar.sync 1, %0;" ::"n"(kStepThreads) : "memory");
   }
-  __syncthreads();
 
   const uint32_t ring = smem_u32(smem);
   bool ok = true;
@@ -639,19 +646,30 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
       float l2 = 0.f, acc[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+      // Four splits' outputs are requested together (one at a time, with a latency
+      // each, took 3500 cycles of a call's 11000).
 #pragma unroll
-      for (int k = 0; k < kMaxCluster; ++k) {
-        if (k >= p.splits || ml[k].y == 0.f) continue;
-        const float w = ex2(ml[k].x - mb);
-        l2 += ml[k].y * w;
-        const uint32_t a = cluster_addr(part + (r * DP + c) * 4, k);
-        float v[8];
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(a));
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "r"(a + 16));
+      for (int k = 0; k < kMaxCluster; k += 4) {
+        if (k >= p.splits) break;
+        float v[4][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = fmaf(v[e], w, acc[e]);
+        for (int i4 = 0; i4 < 4; ++i4) {
+          const uint32_t a = cluster_addr(part + (r * DP + c) * 4, min(k + i4, p.splits - 1));
+#pragma unroll
+          for (int e = 0; e < 8; e += 4)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v[i4][e]), "=f"(v[i4][e + 1]), "=f"(v[i4][e + 2]), "=f"(v[i4][e + 3])
+                         : "r"(a + e * 4));
+        }
+#pragma unroll
+        for (int i4 = 0; i4 < 4; ++i4) {
+          const float2 x = ml[k + i4];
+          if (x.y == 0.f) continue;  // nothing kept there (also: no such split)
+          const float w = ex2(x.x - mb);
+          l2 += x.y * w;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = fmaf(v[i4][e], w, acc[e]);
+        }
       }
       const int gr = r0 + r;
       const int token = s.q0 + gr / p.group, head = h * p.group + gr % p.group;
