@@ -663,12 +663,13 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
         }
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4) {
+          // (nothing kept there, or no such split: a weight of 0 and no value; each
+          // load is waited for all the same)
           const float2 x = ml[k + i4];
-          if (x.y == 0.f) continue;  // nothing kept there (also: no such split)
-          const float w = ex2(x.x - mb);
+          const float w = x.y == 0.f ? 0.f : ex2(x.x - mb);
           l2 += x.y * w;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] = fmaf(v[i4][e], w, acc[e]);
+          for (int e = 0; e < 8; ++e) acc[e] = fmaf(x.y == 0.f ? 0.f : v[i4][e], w, acc[e]);
         }
       }
       const int gr = r0 + r;
@@ -681,7 +682,10 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
       if (c == 0 && p.lse)
         p.lse[static_cast<int64_t>(token) * p.hq + head] = l2 == 0.f ? -INFINITY : (m2 + log2f(l2)) * kLn2;
     }
-    cluster_sync();  // nobody leaves while its shared memory is read
+    // Nobody leaves while its shared memory is read.  What was read has been used, and
+    // nothing is handed over: no ordering, which would wait for the outputs to land.
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
   }
 }
 
