@@ -972,7 +972,7 @@ AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t d, int64
     splits = sms / (tiles > 0 ? tiles : 1);
     const int64_t most = ceil_div(range, 256);
     if (splits > most) splits = most;
-  } else if (range > 320) {
+  } else if (range > 256) {
     // One round of CTAs: the largest clusters of which there is room for all.  Up to
     // 16 sequences of 6000-8000 keys, heads of 128, one token each: 73 us against 82
     // in shares of 512 keys and a second kernel; 1000-8000 keys 54 against 59.
@@ -994,8 +994,9 @@ AttnPlan attn_plan(int64_t batches, int64_t hkv, int64_t group, int64_t d, int64
       if (batches > 1 && range > one * (fp8 ? 1024 : 8192)) one = 0;
     }
     if (one > 0) {
+      // At least 128 keys each (one sequence of 300 keys: 5.8 us in threes, 7.3 whole).
       splits = one;
-      const int64_t most = ceil_div(range, 192);
+      const int64_t most = ceil_div(range, 128);
       if (splits > most) splits = most;
     } else {
       // Several rounds.  Sequences may differ in length, and the long ones' CTAs are
