@@ -596,39 +596,53 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
     const int token_i = live ? gr / p.group : i_last;
     const int head = h * p.group + (live ? gr - token_i * p.group : 0);
     // q's rows, by whole warps: a row's 16-byte chunks by neighbouring lanes, its
-    // place from the lane that has divided for it.  All loads first: one at a time
-    // they took most of the 21000 cycles that a CTA needed up to its first scores.
+    // place from the lane that has divided for it.  Nothing waits before all of them
+    // are under way: one load at a time took most of the 21000 cycles that a CTA
+    // needed up to its first scores.
     {
       constexpr int C = DP / 8;
       const T* q = reinterpret_cast<const T*>(p.q);
-      // A negative factor of the keys turns q's sign, a factor of 0 clears it:
-      // what is left multiplies the scores by something positive.
-      const uint32_t flip = kscale < 0.f ? 0x80008000u : 0u, keep = kscale == 0.f ? 0u : ~0u;
       const int c = lane % C;
       const int64_t q_at = (s.q0 + token_i) * p.qt + head * p.qh;
-      uint4 ws[C];
+      const bool in_d = c * 8 < p.d;
+      auto place = [&](int rr) {  // of this lane's chunk of the warp's row rr, in bytes
+        const int row = quad * 32 + rr;
+        return t * Shape::kSlot + (c / 8) * kPanel + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+      };
+      const int left = rows - t * kRowsT - quad * 32;  // rows of this warp that there are
+      if constexpr (!FP8) {
+#pragma unroll 1
+        for (int i = 0; i < C; ++i) {
+          const int rr = i * (32 / C) + lane / C;
+          const int64_t from = __shfl_sync(0xFFFFFFFFu, q_at, rr);
+          const bool on = rr < left && in_d;
+          cp_async16(qs + place(rr), q + (on ? from + c * 8 : 0), on);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      } else {
+        // A negative factor of the keys turns q's sign, a factor of 0 clears it:
+        // what is left multiplies the scores by something positive.
+        const uint32_t flip = kscale < 0.f ? 0x80008000u : 0u, keep = kscale == 0.f ? 0u : ~0u;
+        uint4 ws[C];
 #pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int rr = i * (32 / C) + lane / C;
-        const int64_t from = __shfl_sync(0xFFFFFFFFu, q_at, rr);
-        ws[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (t * kRowsT + quad * 32 + rr < rows && c * 8 < p.d)
-          ws[i] = *reinterpret_cast<const uint4*>(q + from + c * 8);
-      }
+        for (int i = 0; i < C; ++i) {
+          const int rr = i * (32 / C) + lane / C;
+          const int64_t from = __shfl_sync(0xFFFFFFFFu, q_at, rr);
+          ws[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (rr < left && in_d) ws[i] = *reinterpret_cast<const uint4*>(q + from + c * 8);
+        }
 #pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int rr = quad * 32 + i * (32 / C) + lane / C;
-        uint4& w = ws[i];
-        if constexpr (FP8) {
+        for (int i = 0; i < C; ++i) {
+          const int rr = i * (32 / C) + lane / C;
+          uint4& w = ws[i];
           const float back = q_to_f16<T, C>(w);
-          if (c == 0) bars.q_scale[t][rr] = back;
+          if (c == 0) bars.q_scale[t][quad * 32 + rr] = back;
           w.x = (w.x ^ flip) & keep;
           w.y = (w.y ^ flip) & keep;
           w.z = (w.z ^ flip) & keep;
           w.w = (w.w ^ flip) & keep;
+          *reinterpret_cast<uint4*>(gen0 + place(rr)) = w;
         }
-        *reinterpret_cast<uint4*>(gen0 + t * Shape::kSlot + (c / 8) * kPanel + rr * 128 +
-                                  (((c & 7) ^ (rr & 7)) << 4)) = w;
       }
       fence_async_smem();
       __syncwarp();
