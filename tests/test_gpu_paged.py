@@ -137,6 +137,89 @@ def test_attention(gpu, c):
     check_attention(c, s, out, lse)
 
 
+def spread(n, longest, **kw):
+    """n sequences of one new token, from ``longest`` keys down to one."""
+    return B([1] * n, [max(1, longest - i * longest // n) for i in range(n)], **kw)
+
+
+# Key ranges split over as many CTAs as there is room for at once: eights, sixes, fours, threes,
+# twos, one; a second kernel beyond; around the sizes where the split begins and where 33 rows
+# and more change kernels.
+ROUND = [
+    spread(4, 1030, heads=16, kv_heads=8, dim=128),
+    spread(5, 900, heads=8, kv_heads=8, dim=128, dtype="f16"),
+    spread(9, 700, heads=16, kv_heads=8, dim=128, fp8=True),
+    spread(12, 641, heads=8, kv_heads=8, dim=112, page=8),
+    spread(16, 300, heads=8, kv_heads=8, dim=128),
+    spread(24, 280, heads=16, kv_heads=8, dim=128, fp8=True, page=4),
+    spread(14, 520, heads=8, kv_heads=8, dim=64),
+    spread(7, 1200, heads=8, kv_heads=8, dim=64, fp8=True, dtype="f16", page=1),
+    spread(2, 5000, heads=8, kv_heads=8, dim=32),
+    spread(2, 1100, heads=8, kv_heads=4, dim=256),
+    B([1, 1, 1], [256, 257, 255], heads=4, kv_heads=2, dim=128),
+    B([1, 0, 1, 1], [257, 70, 0, 384], heads=4, kv_heads=2, dim=64, pad=2),
+    B([4, 4, 1], [700, 4, 260], heads=8, kv_heads=2, dim=128, window=300),
+    B([9, 1], [512, 300], heads=8, kv_heads=2, dim=128),
+    B([9, 1, 9], [513, 300, 3], heads=8, kv_heads=2, dim=128, pad=1),
+    B([9, 5], [600, 513], heads=8, kv_heads=2, dim=80, fp8=True),
+    B([9, 5], [600, 513], heads=8, kv_heads=2, dim=64),
+    B([16, 2], [700, 900], heads=8, kv_heads=2, dim=96, window=500, page=64),
+    B([33, 33], [1500, 40], heads=2, kv_heads=2, dim=128, dtype="f16", causal=False),
+]
+
+
+@pytest.mark.parametrize("c", ROUND, ids=str)
+def test_attention_in_one_round_and_around_the_choices(gpu, c):
+    s = make(c)
+    device_flags()
+    out, lse = attend(gpu, c, s)
+    again, _ = attend(gpu, c, s)
+    torch.cuda.synchronize()
+    assert device_flags() == 0
+    n = s["cpu"]["cu"][-1]
+    assert torch.equal(out[:n], again[:n])
+    check_attention(c, s, out, lse)
+
+
+@pytest.mark.parametrize("c", [B([9, 12], [700, 600], heads=8, kv_heads=2, dim=128, window=400),
+                               B([40, 70], [300, 70], heads=4, kv_heads=1, dim=80)], ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=["nan", "inf"])
+def test_a_bad_value_that_some_rows_drop(gpu, c, bad):
+    """One value element of one key of the first sequence is bad: rows that keep it get a bad
+    element there, rows that drop it (and every other column) are as they were."""
+    s = make(c)
+    clean, lse0 = attend(gpu, c, s)
+    # Half of the rows come before the key; the window leaves it to half of the rows.
+    key, col = 280 if c.window == 0 else 295, 5
+    page = s["table"][0, key // c.page].item()
+    s["v_cache"][page, key % c.page, 0, col] = bad
+    out, lse = attend(gpu, c, s)
+    torch.cuda.synchronize()
+    assert torch.equal(lse, lse0)
+    q0, off = c.q_lens[0], c.kv_lens[0] - c.q_lens[0]
+    kept = torch.tensor([key <= off + i and (c.window == 0 or key > off + i - c.window)
+                         for i in range(q0)])
+    heads = c.heads // c.kv_heads
+    hit = torch.zeros(out.shape, dtype=torch.bool)
+    hit[:q0, :heads, col] = kept[:, None]
+    assert not torch.isfinite(out.cpu()[hit]).any()
+    same = torch.ones(out.shape, dtype=torch.bool)
+    same[:q0, :heads, :] = False
+    assert torch.equal(out.cpu()[same], clean.cpu()[same])
+    # Rows that drop it: recomputed where the products of whole tiles met it.
+    rest = ~hit & ~same
+    a, b = out.cpu()[rest].double(), clean.cpu()[rest].double()
+    assert torch.isfinite(a).all()
+    # Both are within the tolerance of the header of the exact value, A and the result at most
+    # the largest value.
+    ds = ((c.dim / 16 + 6) * 2.0 ** -23 * score_size(s["cpu"], c.dim ** -0.5)).max()
+    top = np.nan_to_num(np.abs(s["cpu"]["v_cache"])).max()
+    half = torch.finfo(DT[c.dtype]).eps / 2
+    rel = half + 2 * ds + (max(c.kv_lens) / 16 + 24) * 2.0 ** -23
+    assert kept.any() and not kept.all()
+    assert ((a - b).abs() <= 2 * (half * (1 + rel) + rel) * top).all()
+
+
 @pytest.mark.parametrize("c", [STEP[2], FEW[0], CHUNK[1], CHUNK[7]], ids=str)
 def test_attention_repeats_bit_for_bit_and_without_lse(gpu, c):
     s = make(c)
