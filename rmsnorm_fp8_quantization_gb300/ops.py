@@ -258,7 +258,8 @@ def rope_frequencies(rotary_dim, base=10000.0, *, scaling="none", factor=1.0,
                     / (2 * math.log(base)))
 
         lo = max(0.0, math.floor(index_of(fast_turns)))
-        hi = min(rotary_dim // 2 - 1.0, math.ceil(index_of(slow_turns)))
+        # Beyond the last pair where even that one turns oftener than slow_turns.
+        hi = min(rotary_dim - 1.0, math.ceil(index_of(slow_turns)))
         ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
         f = f * (1 - ramp) + f / factor * ramp
     elif scaling not in ("none", "ntk"):
