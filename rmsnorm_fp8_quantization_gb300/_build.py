@@ -10,14 +10,18 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgbnorm.so")
-FAST = os.path.join(PKG, "_fastcall.so")   # host-side shortcut of the wrappers (csrc/fastcall.cpp)
 BUILD_DIR = os.path.join(PKG, "_build")
+# The wrappers' host-side shortcut (csrc/fastcall.cpp), named for this interpreter, and what
+# torch it was compiled against.
+FAST = os.path.join(PKG, "_fastcall" + sysconfig.get_config_var("EXT_SUFFIX"))
+FAST_STAMP = os.path.join(BUILD_DIR, "fastcall.txt")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "kernels_f32.cu", "kernels_bf16.cu", "kernels_f16.cu", "finalize.cu",
            "noalloc.cu", "softmax.cu", "rope.cu", "paged_attention.cu",
@@ -42,37 +46,59 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
-def build_fastcall() -> None:
-    """The wrappers' host-side shortcut, a small CPython module over torch's C++
-    headers.  Without a compiler or the headers it is left out (the wrappers
-    then do the same in Python, at 10 to 15 us more host time a call)."""
-    import sysconfig
-
+def torch_tag() -> str:
+    """The torch whose object layouts the shortcut has compiled in; another one must not load it."""
     import torch
-    home = os.path.dirname(torch.__file__)
+    return f"{torch.__version__} {torch.version.git_version}"
+
+
+def fastcall_up_to_date() -> bool:
+    try:
+        with open(FAST_STAMP) as f:
+            return os.path.exists(FAST) and f.read() == torch_tag()
+    except OSError:
+        return False
+
+
+def _compile_fastcall() -> str:
+    """Compiles FAST; returns why it could not, or an empty string."""
+    import torch
     gxx = shutil.which("g++")
+    if gxx is None:
+        return "no g++"
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    home = os.path.dirname(torch.__file__)
     tmp = FAST + f".tmp{os.getpid()}"
-    cmd = [gxx or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+    cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DGBN_BUILT_FOR="{torch_tag()}"', "-I", INCLUDE,
            "-I", os.path.join(home, "include"),
            "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
            "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
            os.path.join(CSRC, "fastcall.cpp"), "-o", tmp, "-L", os.path.join(home, "lib"),
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True) if gxx else None
-    if r is None or r.returncode != 0:
-        sys.stderr.write("fastcall.cpp not built (the wrappers work without it)"
-                         + (f":\n{r.stderr[-2000:]}\n" if r else ": no g++\n"))
-        if os.path.exists(FAST):
-            os.remove(FAST)
-        return
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        return r.stderr[-2000:]
     os.replace(tmp, FAST)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(FAST_STAMP, "w") as f:
+        f.write(torch_tag())
+    return ""
+
+
+def build_fastcall() -> None:
+    """The wrappers' host-side shortcut, a small CPython module over torch's C++
+    headers.  Without a compiler, the toolkit's headers or torch's it is left out (the
+    wrappers then do the same in Python, at 10 to 15 us more host time a call)."""
+    why = _compile_fastcall()
+    if why:
+        sys.stderr.write(f"fastcall.cpp not built (the wrappers work without it): {why}\n")
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and up_to_date():
-        if not os.path.exists(FAST):
+        if not fastcall_up_to_date():
             build_fastcall()
         return LIB
     nvcc = _nvcc()

@@ -332,4 +332,9 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, kMethods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fastcall() { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__fastcall() {
+  PyObject* m = PyModule_Create(&kModule);
+  // The torch whose headers this was compiled with: the wrappers use it with no other.
+  if (m && PyModule_AddStringConstant(m, "built_for", GBN_BUILT_FOR) < 0) Py_CLEAR(m);
+  return m;
+}

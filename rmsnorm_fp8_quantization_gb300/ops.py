@@ -14,6 +14,7 @@ import math
 import torch
 
 from . import gbnorm as G
+from ._build import torch_tag
 
 _NORM = {"layernorm": G.GBN_LAYERNORM, "rmsnorm": G.GBN_RMSNORM}
 _SCALING = {"none": G.GBN_SCALING_NONE, "delayed": G.GBN_SCALING_DELAYED_TENSOR,
@@ -162,13 +163,22 @@ def softmax_bwd(dy, y, scale=1.0, out=None, stream=None):
 
 # ---- rotary positions and the paged key/value cache
 
-try:  # the shortcut of the usual calls (csrc/fastcall.cpp); they work without it
-    from . import _fastcall as _fast
-    _fast.setup(*(ctypes.cast(getattr(G.library(), n), ctypes.c_void_p).value
-                  for n in ("gbn_rope_fwd", "gbn_rope_bwd", "gbn_paged_append",
-                            "gbn_paged_attention", "gbn_paged_attention_workspace_size")))
-except ImportError:
-    _fast = None
+def _shortcut():
+    """The shortcut of the usual calls (csrc/fastcall.cpp), or None: they work without it, and one
+    compiled against another torch would read its objects wrongly."""
+    try:
+        from . import _fastcall as fast
+    except ImportError:
+        return None
+    if getattr(fast, "built_for", None) != torch_tag():
+        return None
+    fast.setup(*(ctypes.cast(getattr(G.library(), n), ctypes.c_void_p).value
+                 for n in ("gbn_rope_fwd", "gbn_rope_bwd", "gbn_paged_append",
+                           "gbn_paged_attention", "gbn_paged_attention_workspace_size")))
+    return fast
+
+
+_fast = _shortcut()
 
 
 def _taken(r, where):

@@ -1,0 +1,52 @@
+"""The wrappers' host-side shortcut without a GPU: it is used with the torch it was
+compiled against alone."""
+import importlib
+import os
+import sys
+import types
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from rmsnorm_fp8_quantization_gb300 import _build
+    _build.build()
+    from rmsnorm_fp8_quantization_gb300 import ops as o
+    return o
+
+
+def test_it_says_what_it_was_compiled_against(ops):
+    from rmsnorm_fp8_quantization_gb300 import _build
+    assert ops._fast is not None and ops._fast.built_for == _build.torch_tag()
+    assert torch.__version__ in _build.torch_tag() and _build.fastcall_up_to_date()
+
+
+@pytest.mark.parametrize("built_for", [None, "2.0.0 0123"])
+def test_one_compiled_against_another_torch_is_not_used(ops, monkeypatch, built_for):
+    def never(*a):
+        raise AssertionError("used")
+    other = types.ModuleType("rmsnorm_fp8_quantization_gb300._fastcall")
+    other.setup = never
+    if built_for is not None:
+        other.built_for = built_for
+    import rmsnorm_fp8_quantization_gb300 as package
+    monkeypatch.setitem(sys.modules, other.__name__, other)
+    monkeypatch.setattr(package, "_fastcall", other, raising=False)
+    assert ops._shortcut() is None
+
+
+def test_it_is_compiled_again_for_another_torch(ops, monkeypatch, tmp_path):
+    from rmsnorm_fp8_quantization_gb300 import _build
+    calls = []
+    monkeypatch.setattr(_build, "build_fastcall", lambda: calls.append(1))
+    monkeypatch.setattr(_build, "up_to_date", lambda: True)
+    assert _build.build() == _build.LIB and calls == []
+    stamp = tmp_path / "stamp"
+    stamp.write_text("2.0.0 0123")
+    monkeypatch.setattr(_build, "FAST_STAMP", str(stamp))
+    assert _build.build() == _build.LIB and calls == [1]
+    monkeypatch.setattr(_build, "FAST_STAMP", str(tmp_path / "none"))
+    assert _build.build() == _build.LIB and calls == [1, 1]
+    assert importlib.machinery.EXTENSION_SUFFIXES[0] in os.path.basename(_build.FAST)
