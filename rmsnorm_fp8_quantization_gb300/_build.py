@@ -66,7 +66,10 @@ def _compile_fastcall() -> str:
     gxx = shutil.which("g++")
     if gxx is None:
         return "no g++"
-    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    try:
+        cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    except RuntimeError as e:
+        return str(e)
     home = os.path.dirname(torch.__file__)
     tmp = FAST + f".tmp{os.getpid()}"
     cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG",
@@ -91,7 +94,10 @@ def build_fastcall() -> None:
     """The wrappers' host-side shortcut, a small CPython module over torch's C++
     headers.  Without a compiler, the toolkit's headers or torch's it is left out (the
     wrappers then do the same in Python, at 10 to 15 us more host time a call)."""
-    why = _compile_fastcall()
+    try:
+        why = _compile_fastcall()
+    except OSError as e:
+        why = str(e)
     if why:
         sys.stderr.write(f"fastcall.cpp not built (the wrappers work without it): {why}\n")
 

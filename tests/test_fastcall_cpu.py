@@ -50,3 +50,23 @@ def test_it_is_compiled_again_for_another_torch(ops, monkeypatch, tmp_path):
     monkeypatch.setattr(_build, "FAST_STAMP", str(tmp_path / "none"))
     assert _build.build() == _build.LIB and calls == [1, 1]
     assert importlib.machinery.EXTENSION_SUFFIXES[0] in os.path.basename(_build.FAST)
+
+
+@pytest.mark.parametrize("missing", ["toolkit", "compiler", "room"])
+def test_a_build_without_it_goes_on(ops, monkeypatch, tmp_path, capsys, missing):
+    """The library is there, the shortcut is not, and nothing can compile it."""
+    from rmsnorm_fp8_quantization_gb300 import _build
+
+    def refuse(*a, **k):
+        raise OSError("read-only") if missing == "room" else RuntimeError("nvcc not found")
+    monkeypatch.setattr(_build, "up_to_date", lambda: True)
+    monkeypatch.setattr(_build, "FAST", str(tmp_path / "_fastcall.so"))
+    monkeypatch.setattr(_build, "FAST_STAMP", str(tmp_path / "stamp"))
+    if missing == "toolkit":
+        monkeypatch.setattr(_build, "_nvcc", refuse)
+    elif missing == "compiler":
+        monkeypatch.setattr(_build.shutil, "which", lambda n: None)
+    else:
+        monkeypatch.setattr(_build.subprocess, "run", refuse)
+    assert _build.build() == _build.LIB
+    assert "not built" in capsys.readouterr().err and not list(tmp_path.iterdir())
