@@ -10,6 +10,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include <ATen/core/Tensor.h>
@@ -74,11 +75,16 @@ PyObject* setup(PyObject*, PyObject* args) {
   Py_RETURN_NONE;
 }
 
+// A number that fp32 has room for (the wrapper's own way says so where it has not).
 bool number(PyObject* o, double* v) {
   if (PyFloat_CheckExact(o)) *v = PyFloat_AS_DOUBLE(o);
   else if (PyLong_CheckExact(o)) *v = PyLong_AsDouble(o);
   else return false;
-  return !(*v == -1.0 && PyErr_Occurred());
+  if (*v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    return false;
+  }
+  return !(std::fabs(*v) > FLT_MAX) || std::isinf(*v);
 }
 bool whole(PyObject* o, int64_t* v) {
   if (!PyLong_CheckExact(o)) return false;

@@ -70,3 +70,16 @@ def test_a_build_without_it_goes_on(ops, monkeypatch, tmp_path, capsys, missing)
         monkeypatch.setattr(_build.subprocess, "run", refuse)
     assert _build.build() == _build.LIB
     assert "not built" in capsys.readouterr().err and not list(tmp_path.iterdir())
+
+
+def test_numbers_beyond_a_float_are_left_to_the_wrapper(ops):
+    """The shortcut says that it is not its call, with no exception set; the wrapper raises."""
+    fast = ops._fast
+    q, k = torch.zeros(2, 3, 4, 64), torch.zeros(2, 3, 2, 64)
+    f, pos = torch.zeros(32, dtype=torch.float64), torch.zeros(2, 3, dtype=torch.int64)
+    for mscale in (10 ** 400, -10 ** 400, 1e300):
+        assert fast.rope(0, q, k, f, pos, 0, mscale) is None
+    b = torch.zeros(2, 4, 64)
+    cache = torch.zeros(2, 16, 4, 64)
+    i = torch.zeros(2, dtype=torch.int32)
+    assert fast.append(b, b, cache, cache, i, i, i, b, f, 0, 10 ** 400, None, None) is None
