@@ -117,5 +117,8 @@ class _Rope(torch.autograd.Function):
 
 def rope(q, k, inv_freq, positions=None, layout="half", mscale=1.0):
     """Rotary positions of q and k [batch, seq, heads, head_dim] (k may be
-    None): ``ops.rope_fwd`` with its gradient."""
+    None): ``ops.rope_fwd`` with its gradient, for q and k alone (inv_freq is refused
+    where it requires one)."""
+    if inv_freq.requires_grad and torch.is_grad_enabled():
+        raise ValueError("inv_freq requires a gradient, and rope has none for it")
     return _Rope.apply(q, k, inv_freq, positions, layout, mscale)
