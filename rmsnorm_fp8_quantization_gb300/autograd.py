@@ -106,6 +106,7 @@ class _Rope(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dq, dk):
         inv_freq, positions = ctx.saved_tensors
+        dq, dk = (t if need else None for t, need in zip((dq, dk), ctx.needs_input_grad))
         # A gradient whose head elements are not contiguous (an expanded or
         # transposed view) is copied; other strides are taken as they are.
         dq, dk = (t if t is None or t.stride(-1) == 1 else t.contiguous() for t in (dq, dk))

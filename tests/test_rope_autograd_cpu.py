@@ -34,3 +34,14 @@ def test_frequencies_that_require_a_gradient_are_refused(rope):
     with torch.no_grad():   # nothing is asked of them
         rope[0](q, k, f.clone().requires_grad_())
     assert rope[0](q, k, f)[0].requires_grad
+
+
+@pytest.mark.parametrize("need", [(True, False), (False, True), (True, True)])
+def test_only_the_gradients_that_are_needed_are_rotated(rope, need):
+    f = torch.ones(4, dtype=torch.float64)
+    q = torch.randn(1, 2, 3, 8).requires_grad_(need[0])
+    k = torch.randn(1, 2, 1, 8).requires_grad_(need[1])
+    a, b = rope[0](q, k, f)
+    (a.sum() + b.sum()).backward()
+    assert rope[1] == [(False, True, True), (True, *need)]
+    assert (q.grad is not None, k.grad is not None) == need
