@@ -54,6 +54,7 @@ constexpr int kStepThreads = 128;
 constexpr int kStepKeys = 64;          // keys per tile
 constexpr int kMaxSplits = 512;
 constexpr int kMaxCluster = 8;         // splits that merge within a cluster (the portable size)
+constexpr int kHeadroom = 15;          // the row's largest probability is 2^15 in f16 (at most 65504)
 
 // Shared-memory address `a` of this CTA, in CTA `rank` of its cluster.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t a, int rank) {
@@ -153,9 +154,11 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
   using TP = typename std::conditional<FP8, __half, T>::type;  // type of both products
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* s_q = smem + Shape::kBody;
+  // Of each warp's rows (and in the workspace of each split's): the reference of its sums
+  // (below the maximum next to f16 values) and the sum.
   float2* s_ml = reinterpret_cast<float2*>(s_q + 16 * MT * Shape::kQPitch);
   float* s_qs = reinterpret_cast<float*>(s_ml + 4 * 16);  // E4M3: what a q row's scores are times
-  float2* s_pml = reinterpret_cast<float2*>(s_qs + 16 * MT);  // cluster: max and sum of each row
+  float2* s_pml = reinterpret_cast<float2*>(s_qs + 16 * MT);  // cluster: the same of each row
   uint64_t* s_full = reinterpret_cast<uint64_t*>(s_pml + 16 * MT);
   uint64_t* s_empty = s_full + Shape::kStages;
 
@@ -451,15 +454,15 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
           mx[e >> 1] = fmaxf(mx[e >> 1], sc[n][e]);
         }
     }
-    float base[2];
+    float base[2];  // what the scores are taken against
     bool grew = false;
     float al[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));
       mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 2));
-      base[e] = mx[e] == -INFINITY ? 0.f : mx[e];
-      al[e] = ex2(m[e] - base[e]);  // m = -inf: 0, and the sums are still 0
+      base[e] = mx[e] == -INFINITY ? 0.f : reference<TP, kHeadroom>(mx[e]);
+      al[e] = ex2(reference<TP, kHeadroom>(m[e]) - base[e]);  // m = -inf: 0, and the sums are still 0
       grew |= mx[e] != m[e];
       m[e] = mx[e];
     }
@@ -478,8 +481,9 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
         sc[n][e] = ex2(sc[n][e] - base[e >> 1]);
         l[e >> 1] += sc[n][e];
       }
-    // P V.  P is rounded to the values' type (at most half a step relative:
-    // the sums l keep it unrounded).
+    // P V.  P is rounded to the values' type, the sums l keep it unrounded: at most
+    // half a step relative, in f16 for weights down to 2^-29 of the row's largest so
+    // far, and 2^-40 of that largest below.
 #pragma unroll
     for (int kk = 0; kk < NT / 2; ++kk) {
       uint32_t a[4];
@@ -559,8 +563,8 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
       s_o[r * DP + col] = o[d][e];
     }
   if (warp < 4 && qc == 0) {
-    s_ml[warp * 16 + qr] = make_float2(m[0], l[0]);
-    s_ml[warp * 16 + qr + 8] = make_float2(m[1], l[1]);
+    s_ml[warp * 16 + qr] = make_float2(reference<TP, kHeadroom>(m[0]), l[0]);
+    s_ml[warp * 16 + qr + 8] = make_float2(reference<TP, kHeadroom>(m[1]), l[1]);
   }
   __syncthreads();
   const float vscale = FP8 ? *p.v_scale_inv : 1.f;

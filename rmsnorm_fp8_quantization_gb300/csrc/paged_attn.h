@@ -22,7 +22,7 @@ struct AttnParams {
   const float* k_scale_inv;  // E4M3 caches
   const float* v_scale_inv;
   float* part_o;       // [splits][tokens * hq][d] fp32
-  float2* part_ml;     // [tokens * hq][splits]: (max in log2 units, sum)
+  float2* part_ml;     // [tokens * hq][splits]: (reference in log2 units, sum)
   int64_t qt, qh;      // element strides of q
   int64_t ot, oh;      // of out
   int64_t kp, ks, kh;  // of the caches: page, slot, head

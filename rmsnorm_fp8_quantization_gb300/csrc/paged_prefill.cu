@@ -23,10 +23,12 @@
 //
 // The outputs stay in tensor memory for the whole key range.  A row's
 // reference maximum moves only when the running maximum has grown by more
-// than 2^8 over it: until then the probabilities, at most 256, lose nothing in
+// than 2^8 over it (bf16; f16: 2^4): until then the probabilities lose nothing in
 // fp32 sums or 16-bit mantissas, and O is not touched; when it moves the
 // row's own thread rescales O (a few times per row, mostly in the first
-// tiles).
+// tiles).  f16 holds probabilities from 2^-14 on with all its bits: they are taken
+// 2^11 larger there, so those down to 2^-25 of the row's largest so far keep
+// 2^-11 relative and smaller ones lose at most 2^-36 of that largest.
 //
 // K and V tiles: [128 keys][64 elements] panels with 128-byte rows in the
 // 128-byte swizzle, written by TMA boxes of one page (or 128 slots of a larger
@@ -56,7 +58,11 @@ constexpr int kMmaWarp = 8, kLoadWarp = 10, kZeroWarp = 11, kConvertWarp = 12;
 constexpr int kLoaders = 128;              // E4M3 caches: threads of warps 12-15
 constexpr int kStaging = 4;                // E4M3 caches: at most so many tiles of codes
 constexpr int kSortBatches = 256;          // up to so many sequences are taken by length
-constexpr float kRescale = 8.f;            // log2 growth before the reference moves
+// log2 growth of a row's maximum before its reference moves, and how far below the
+// first maximum the reference stands (f16 values): 2^(4 + 11) fits f16.
+template <typename TP>
+constexpr float kRescale = std::is_same<TP, __half>::value ? 4.f : 8.f;
+constexpr int kHeadroom = 11;
 
 struct Barriers {
   // p_full, o_full: [row tile][half of the keys]
@@ -679,7 +685,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
         tc_ld32(th, sc);
         tc_ld32(th + 32, sc + 32);
         tc_wait_ld<64>(sc);
-        const float mb = m == -INFINITY ? 0.f : m;
+        const float mb = m == -INFINITY ? 0.f : reference<TP, kHeadroom>(m);
         const uint64_t sc2 = p2(scale, scale), mb2 = p2(-mb, -mb);
         uint64_t l2[2] = {p2(l, 0.f), 0ull};
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -694,7 +700,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
         }
         const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
         // -inf - -inf is not a number: no growth.
-        if (!__any_sync(0xFFFFFFFFu, mt - m > kRescale)) {
+        if (!__any_sync(0xFFFFFFFFu, mt - m > kRescale<TP>)) {
           tc_st32(th, pk);
           const float2 la = u2(add2(l2[0], l2[1]));
           l = la.x + la.y;
@@ -723,9 +729,10 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
           for (int i = 0; i < 4; ++i)
             mx[i] = max3(mx[i], __uint_as_float(sc[e + i]), __uint_as_float(sc[e + 4 + i]));
         const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
-        if (__any_sync(0xFFFFFFFFu, mt - m > kRescale)) {
+        if (__any_sync(0xFFFFFFFFu, mt - m > kRescale<TP>)) {
           const float mn = fmaxf(m, mt);
-          const float al = mn == -INFINITY ? 1.f : ex2(m - mn);
+          const float al = mn == -INFINITY ? 1.f
+                                           : ex2(reference<TP, kHeadroom>(m) - reference<TP, kHeadroom>(mn));
           l *= al;
           m = mn;
           if (i > 0) {
@@ -744,7 +751,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
             }
           }
         }
-        const float mb = m == -INFINITY ? 0.f : m;
+        const float mb = m == -INFINITY ? 0.f : reference<TP, kHeadroom>(m);
         const uint64_t sc2 = p2(scale, scale), mb2 = p2(-mb, -mb);
         uint64_t l2[2] = {p2(l, 0.f), 0ull};
 #pragma unroll
@@ -799,9 +806,10 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
         __syncwarp();
       };
       const float inv = part ? 1.f : l == 0.f ? 0.f : vscale / l;
+      const float ref = reference<TP, kHeadroom>(m);
       if (live) {
-        if (part) p.part_ml[ro * p.splits + split] = make_float2(m, l);
-        else if (p.lse) p.lse[ro] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (part) p.part_ml[ro * p.splits + split] = make_float2(ref, l);
+        else if (p.lse) p.lse[ro] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
       }
       // (one copy of the code: a CTA runs it once, and fetching it is what it costs)
 #pragma unroll 1
@@ -848,7 +856,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
             float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (l != 0.f)
               row_again<T, FP8>(p, b, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
-                                FP8 ? p.scale_log2 * kscale : p.scale_log2, m, rlo, rhi, col + 8 * i,
+                                FP8 ? p.scale_log2 * kscale : p.scale_log2, ref, rlo, rhi, col + 8 * i,
                                 f);
             if (part) {
 #pragma unroll

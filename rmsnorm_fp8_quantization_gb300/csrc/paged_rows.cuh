@@ -66,6 +66,17 @@ __device__ __forceinline__ float ex2(float a) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
   return r;
 }
+// The reference that a row's probabilities 2^(s - reference) are taken against, from
+// its maximum m (log2 units; -inf stays).  bf16: m itself.  f16 ends at 2^-14 (2^-24
+// with fewer bits) where fp32 and bf16 go on: against m, 262144 keys 18 nats below one
+// that dominates would all vanish from the product with the values and stay in the
+// sum.  So f16 takes a reference 2^H lower, which the division by the sum takes out
+// again; not for maxima whose own spacing (2^-3 from 2^20 on) would blur it.
+template <typename T, int H>
+__device__ __forceinline__ float reference(float m) {
+  if constexpr (Elem<T>::kDt == DT_F16) return fabsf(m) < 1048576.f ? m - H : m;
+  else return m;
+}
 // 16 bytes into shared memory, zeros where not `live` (nothing is read then).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
