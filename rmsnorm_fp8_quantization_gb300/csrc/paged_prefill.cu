@@ -63,6 +63,7 @@ constexpr int kSortBatches = 256;          // up to so many sequences are taken 
 template <typename TP>
 constexpr float kRescale = std::is_same<TP, __half>::value ? 4.f : 8.f;
 constexpr int kHeadroom = 11;
+constexpr float kLargeScore = 268435456.f;  // 2^28: see large_factor
 
 struct Barriers {
   // p_full, o_full: [row tile][half of the keys]
@@ -222,6 +223,15 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// The factor of a row whose largest score is beyond 2^28 (log2 units) in magnitude: the power
+// of two at or below the row's own, with which products are exact.  Any other rounds them by up
+// to 8 and more there, and taken against the rounded maximum the largest key's probability
+// would be 0 or infinite.  Scores so large are 16 powers of two apart or equal: with a
+// factor up to half as large the largest still has the weight.
+__device__ __forceinline__ float large_factor(float scale) {
+  return __uint_as_float(__float_as_uint(scale) & 0xFF800000u);
 }
 
 // The lowest n bits set (none for n <= 0, all from 64 on).
@@ -655,8 +665,12 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
       if (lane == 0) mbar_arrive(&bars.q_full);
     }
     const int rlo = max(row_low(p, s, token_i), k0), rhi = min(row_high(p, s, token_i), k1);
-    float scale = p.scale_log2 * (kscale == 0.f ? 1.f : fabsf(kscale));
-    if constexpr (FP8) scale *= bars.q_scale[t][r];  // written by this warp
+    auto factor = [&]() {  // of the row's scores
+      float f = p.scale_log2 * (kscale == 0.f ? 1.f : fabsf(kscale));
+      if constexpr (FP8) f *= bars.q_scale[t][r];  // written by this warp
+      return f == 0.f ? 1.4e-45f : f;  // (a product that vanished: -inf times it has to stay -inf)
+    };
+    float scale = factor();
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128;             // S, and P over it
     const uint32_t to = tmem + lanes + 256 + t * 128;
@@ -728,11 +742,19 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             mx[i] = max3(mx[i], __uint_as_float(sc[e + i]), __uint_as_float(sc[e + 4 + i]));
-        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
+        const float raw = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), mt = raw * scale;
         if (__any_sync(0xFFFFFFFFu, mt - m > kRescale<TP>)) {
-          const float mn = fmaxf(m, mt);
-          const float al = mn == -INFINITY ? 1.f
-                                           : ex2(reference<TP, kHeadroom>(m) - reference<TP, kHeadroom>(mn));
+          float mn = fmaxf(m, mt);
+          float al = mn == -INFINITY ? 1.f
+                                     : ex2(reference<TP, kHeadroom>(m) - reference<TP, kHeadroom>(mn));
+          if ((fabsf(mn) >= kLargeScore || (fabsf(m) >= kLargeScore && m != -INFINITY)) && mn != -INFINITY) {
+            // Large scores, now or so far: both maxima by the row's own factor.
+            const float f = factor(), was = m / scale, m0 = scale == f ? m : was * f;
+            const float n0 = fmaxf(m0, raw * f);
+            al = fminf(ex2(m0 - n0), 1.f);
+            scale = fabsf(n0) >= kLargeScore ? large_factor(f) : f;
+            mn = n0 == m0 && scale == f ? m0 : fmaxf(was, raw) * scale;
+          }
           l *= al;
           m = mn;
           if (i > 0) {
@@ -806,7 +828,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
         __syncwarp();
       };
       const float inv = part ? 1.f : l == 0.f ? 0.f : vscale / l;
-      const float ref = reference<TP, kHeadroom>(m);
+      const float ref = reference<TP, kHeadroom>(scale == factor() ? m : m / scale * factor());
       if (live) {
         if (part) p.part_ml[ro * p.splits + split] = make_float2(ref, l);
         else if (p.lse) p.lse[ro] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
