@@ -441,7 +441,7 @@ gbn_status gbn_paged_append(const gbn_paged_append_args* args, cudaStream_t stre
  *              GPU need one each.
  * fp32 scores, sums and outputs, probabilities rounded to the values' type
  * (f16 for E4M3 caches) for the product with the values: half a step relative;
- * f16 ones below 2^-25 of the row's largest by up to 2^-36 of that largest.
+ * f16 ones below 2^-23 of the row's largest by up to 2^-34 of that largest.
  * Deterministic.
  * head_dim: a multiple of 16 up to GBN_PAGED_MAX_DIM; scale finite and
  * positive; q_heads a multiple of kv_heads; tokens * q_heads < 2^31; max_kv

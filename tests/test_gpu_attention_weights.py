@@ -4,7 +4,7 @@ largest score, whose share of the result is small but not nothing.
 Tolerance: that of test_gpu_paged's header.  It counts the rounding of a
 probability to f16 as 2^-11 of it, which holds while what is rounded is normal:
 at most 29 powers of two (20 nats) below the row's largest in the kernel for few
-rows, 25 (17 nats) in the one for many, whose gaps below are chosen within."""
+rows, 23 (15.9 nats) in the one for many, whose gaps below are chosen within."""
 import numpy as np
 import pytest
 import torch
@@ -51,14 +51,14 @@ SHAPES = {
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["two-byte", "e4m3"])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("gap", [8, 13, 17])
-@pytest.mark.parametrize("shape", list(SHAPES))
+@pytest.mark.parametrize("shape,gap", [(n, g) for n in SHAPES
+                                       for g in (8, 13, 15 if n in ("many", "prompt") else 17)])
 def test_keys_far_below_the_largest_keep_their_share(gpu, shape, gap, dtype, fp8):
     c, s = sink(*SHAPES[shape], gap, heads=4, kv_heads=1, dim=64, dtype=dtype, fp8=fp8)
     out, lse = attend(gpu, c, s, scale=1.0)
     check_attention(c, s, out, lse, 1.0)
     n = s["cpu"]["cu"][-1]
-    if gap == 17 and shape != "prompt":
+    if gap >= 15 and shape != "prompt":
         assert (out[:n].float() > 0).all()
 
 
