@@ -360,7 +360,7 @@ gbn_status gbn_rope_bwd(const gbn_rope_args* args, cudaStream_t stream);
  * A batch of sequences, each with some new tokens, packed: sequence b owns
  * the token rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (int32, batches + 1
  * entries, ascending; rows before the first and behind the last sequence are
- * padding, neither read nor written).  kv_lens[b] (int32) counts the
+ * padding: not written, and what they hold does not matter).  kv_lens[b] (int32) counts the
  * sequence's keys INCLUDING its new tokens, so new token i of q_len stands at
  * key position kv_lens[b] - q_len + i.  Position t lives in slot
  * t % page_size of page block_table[b][t / page_size] (int32, table_pages

@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
         kv = p.kv_lens[i];
       }
       int64_t pos = -1, page = -1;
-      if (b < p.batches) {  // else a padding row behind the last sequence
+      // Rows before the first and behind the last sequence are padding.
+      if (b < p.batches && !(b == 0 && t < c0)) {
         pos = kv - (c1 - c0) + (t - c0);
         const int64_t e = pos >> p.page_shift;
         if (t < c0 || pos < 0 || e >= p.table_pages) {
