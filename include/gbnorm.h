@@ -302,10 +302,10 @@ gbn_status gbn_softmax_bwd(const void* dy, const void* y, void* dx, int64_t rows
  *     a' = mscale * (a cos - b sin),   b' = mscale * (a sin + b cos),
  * (a, b) = elements (i, i + rotary_dim / 2) (HALF) or (2i, 2i + 1)
  * (INTERLEAVED).  Scaled contexts are a matter of inv_freq and mscale.
- * inv_freq is fp64 [rotary_dim / 2], radians per position, finite and below
- * 2^50 in magnitude; the angle is reduced exactly (fixed point, modulo one
- * turn), so far positions lose nothing.  fp32 arithmetic, one rounding to the
- * tensors' type. */
+ * inv_freq is fp64 [rotary_dim / 2], radians per position, below 2^50 in
+ * magnitude (a pair whose frequency is not finite comes out as NaN); the angle
+ * is reduced exactly (fixed point, modulo one turn), so far positions lose
+ * nothing.  fp32 arithmetic, one rounding to the tensors' type. */
 typedef enum { GBN_ROPE_HALF = 0, GBN_ROPE_INTERLEAVED = 1 } gbn_rope_layout;
 
 #define GBN_ROPE_MAX_DIM 1024 /* largest head_dim */

@@ -95,7 +95,7 @@ __device__ __forceinline__ uint64_t turn_fraction(double x) {
   constexpr uint64_t kC = 0xA2F9836E4E441529ull;  // floor(2^66 / (2 pi)) = floor(2^64 * 2 / pi)
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x));
   const int ex = static_cast<int>((u >> 52) & 0x7FFu);
-  if (ex == 0 || ex == 0x7FF) return 0ull;  // zero and subnormal: no turn; not finite: refused by contract
+  if (ex == 0) return 0ull;  // zero and subnormal: no turn
   const uint64_t m = (u & 0xFFFFFFFFFFFFFull) | 0x10000000000000ull;
   const int s = 2 - (ex - 1075);  // right shift of m * C
   const uint64_t hi = __umul64hi(m, kC), lo = m * kC;
@@ -106,11 +106,15 @@ __device__ __forceinline__ uint64_t turn_fraction(double x) {
   return (u >> 63) ? 0ull - f : f;
 }
 
-// mscale * (cos, sign * sin) of pos * inv_freq.
+// mscale * (cos, sign * sin) of pos * inv_freq; NaN where inv_freq is not finite.
 __device__ __forceinline__ float2 turn(double inv_freq, int64_t pos, float mscale, float sign) {
   const uint64_t t = turn_fraction(inv_freq) * static_cast<uint64_t>(pos);
   const uint32_t quarter = static_cast<uint32_t>((t + (1ull << 61)) >> 62);
   const int64_t rest = static_cast<int64_t>(t - (static_cast<uint64_t>(quarter) << 62));
+  // The high word of an infinite or NaN double is a NaN as a float, that of any below 2^1017
+  // a finite one: 0 times it is NaN, or 0.  (A comparison and a selection took the fp32
+  // backward from 11.8 to 12.7 us.)
+  mscale = fmaf(__int_as_float(__double2hiint(inv_freq)), 0.f, mscale);
   float s, c;
   sincospif(static_cast<float>(rest) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
   const float c2 = quarter & 1 ? -s : c, s2 = quarter & 1 ? c : s;
