@@ -304,8 +304,9 @@ gbn_status gbn_softmax_bwd(const void* dy, const void* y, void* dx, int64_t rows
  * (INTERLEAVED).  Scaled contexts are a matter of inv_freq and mscale.
  * inv_freq is fp64 [rotary_dim / 2], radians per position, below 2^50 in
  * magnitude (a pair whose frequency is not finite comes out as NaN); the angle
- * is reduced exactly (fixed point, modulo one turn), so far positions lose
- * nothing.  fp32 arithmetic, one rounding to the tensors' type. */
+ * is reduced in fixed point, to 2^-64 (1 + |inv_freq| / 4) of a turn for each
+ * position: with frequencies up to 1 below fp32's own rounding up to position
+ * 2^36.  fp32 arithmetic, one rounding to the tensors' type. */
 typedef enum { GBN_ROPE_HALF = 0, GBN_ROPE_INTERLEAVED = 1 } gbn_rope_layout;
 
 #define GBN_ROPE_MAX_DIM 1024 /* largest head_dim */

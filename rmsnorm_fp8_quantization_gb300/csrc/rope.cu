@@ -8,8 +8,11 @@
 // Angles.  A position's angle matters modulo one turn only, so it is kept as
 // a 64-bit fixed-point fraction of a turn: inv_freq / (2 pi) * 2^64 times the
 // position in wrapping integer arithmetic is exact modulo one turn up to the
-// fraction's own rounding (2^-64 of a turn per position), where the product
-// in fp32 would have no fraction left at far positions.  What is left after
+// fraction's own error for each position (2^-64 of a turn, and 2^-66 of the frequency
+// from 64 bits of 2 / pi: another word of it, for frequencies beyond 4, cost registers
+// and 15 % of the fp32 kernel's time), where the product in fp32 would have no
+// fraction left at far positions.  (The leading bits of 2 / pi: after Payne and
+// Hanek's reduction.)  What is left after
 // taking off the nearest quarter turn converts to fp32 with a relative error
 // of 2^-24, and cos and sin of it come from sincospif.  No 64-bit
 // floating-point arithmetic: its rate on this chip is about 1/64 of fp32's.
