@@ -82,6 +82,7 @@ struct RopeParams {
   int table_pages;        // entries per row
   int64_t num_pages;
   int page_shift;
+  bool each;              // a lane for each sequence
   const float* k_scale;
   const float* v_scale;
 };
@@ -189,8 +190,9 @@ __device__ __forceinline__ void put(void* base, int64_t at, const float* f, floa
 }
 
 // V: elements per vector.  APPEND: k and v go to the paged cache, tokens are
-// rows of a packed batch.  FP8 (append): the cache holds E4M3 codes.
-template <typename T, int V, bool APPEND, bool FP8>
+// rows of a packed batch.  FP8 (append): the cache holds E4M3 codes.  EACH (append):
+// up to 31 sequences, which the lanes of a warp hold to look a token up.
+template <typename T, int V, bool APPEND, bool FP8, bool EACH>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
   pdl_begin();
   // cos and sin of each token's pairs, in the order in which they are read: W
@@ -279,20 +281,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   }
 
   if constexpr (APPEND) {
-    // Sequence, position and page of each token, one warp per token.  E4M3 caches, up
-    // to 31 sequences: a lane for each, so that the search costs one read (5000
-    // tokens of heads of 64: 8.5 us against 9.7; two-byte caches lose by it, 44.2
-    // against 42.6 for 9000 tokens of heads of 128).
+    // Sequence, position and page of each token, one warp per token.
     const int lane = tid & 31;
-    const bool few = FP8 && p.batches < 32;
-    const int cl = few && lane <= p.batches ? p.cu[lane] : INT32_MAX;
-    const int kl = few && lane < p.batches ? p.kv_lens[lane] : 0;
+    const int cl = EACH && lane <= p.batches ? p.cu[lane] : INT32_MAX;
+    const int kl = EACH && lane < p.batches ? p.kv_lens[lane] : 0;
     for (int tok = tid >> 5; tok < ntok; tok += kRopeThreads / 32) {
       const int64_t t = t0 + tok;
-      const int b = few ? __popc(__ballot_sync(0xFFFFFFFFu, lane > 0 && lane <= p.batches && cl <= t))
+      const int b = EACH ? __popc(__ballot_sync(0xFFFFFFFFu, lane > 0 && lane <= p.batches && cl <= t))
                         : warp_find_sequence(p.cu, p.batches, t);
       int64_t c0, c1, kv;
-      if (few) {  // (past the last sequence: unused)
+      if (EACH) {  // (past the last sequence: unused)
         c0 = __shfl_sync(0xFFFFFFFFu, cl, b);
         c1 = __shfl_sync(0xFFFFFFFFu, cl, b + 1);
         kv = __shfl_sync(0xFFFFFFFFu, kl, b);
@@ -443,9 +441,8 @@ bool rope_geometry(RopeParams& p, int v, int sms, int64_t* grid) {
   const int fit = kRopeItems / p.units;  // head rows per CTA
   // Small calls: a CTA per token and head range of one unit a thread, so
   // that the latency of one round of loads is all there is.
-  const int want = p.tokens * rows * p.units <= int64_t(kRopeItems) * sms
-                       ? (kRopeThreads / p.units > 0 ? kRopeThreads / p.units : 1)
-                       : fit;
+  const bool small = p.tokens * rows * p.units <= int64_t(kRopeItems) * sms;
+  const int want = small ? (kRopeThreads / p.units > 0 ? kRopeThreads / p.units : 1) : fit;
   if (rows > want) {
     p.row_chunks = (rows + want - 1) / want;
     p.rows_per_cta = (rows + p.row_chunks - 1) / p.row_chunks;
@@ -460,6 +457,13 @@ bool rope_geometry(RopeParams& p, int v, int sms, int64_t* grid) {
     if (t < 1) t = 1;
     p.tokens_per_cta = t;
   }
+  // Append: up to 31 sequences are looked up with a lane for each, one read instead of a
+  // search, where a CTA waits for the look-up: in small calls (31 tokens 2.6 us against
+  // 2.9) and where it has many tokens (10 of them, 5200 in all: 12.2 us against 13.0; 5:
+  // 17.2 against 17.5).  Where it has few it waits for their loads, and the search is ahead
+  // (one, 9300 in all: 72.4 us against 77.0; two: 43.5 against 44.9; four: 30.7 against
+  // 31.3).  Two-byte and E4M3 caches alike.
+  p.each = p.batches < 32 && (small || p.tokens_per_cta > 4);
   p.units_mul = div_mul(p.units);
   p.rows_mul = div_mul(p.rows_per_cta);
   const int64_t blocks = (p.tokens + p.tokens_per_cta - 1) / p.tokens_per_cta;
@@ -492,6 +496,18 @@ int rope_vector(const RopeParams& p, bool append, bool fp8) {
   return 1;
 }
 
+template <typename T, bool APPEND, bool FP8, bool EACH>
+cudaError_t rope_launch_v(const RopeParams& p, int v, int64_t grid, cudaStream_t stream) {
+  const dim3 g(static_cast<unsigned>(grid)), b(kRopeThreads);
+  constexpr int kV16 = 16 / (int)sizeof(T), kV8 = 8 / (int)sizeof(T);
+  if (v == kV16) return launch_pdl(rope_kernel<T, kV16, APPEND, FP8, EACH>, g, b, 0, stream, p);
+  if (v == kV8) {
+    if constexpr (FP8 && kV8 < 4) return cudaErrorInvalidValue;
+    else return launch_pdl(rope_kernel<T, kV8, APPEND, FP8, EACH>, g, b, 0, stream, p);
+  }
+  return launch_pdl(rope_kernel<T, 1, APPEND, FP8, EACH>, g, b, 0, stream, p);
+}
+
 template <typename T, bool APPEND, bool FP8>
 gbn_status rope_launch(RopeParams& p, cudaStream_t stream) {
   int dev = 0, sms = 0;
@@ -501,17 +517,12 @@ gbn_status rope_launch(RopeParams& p, cudaStream_t stream) {
   const int v = rope_vector<T>(p, APPEND, FP8);
   int64_t grid = 0;
   if (!rope_geometry(p, v, sms, &grid)) return GBN_ERR_SHAPE;
-  const dim3 g(static_cast<unsigned>(grid)), b(kRopeThreads);
   cudaError_t e;
-  constexpr int kV16 = 16 / (int)sizeof(T), kV8 = 8 / (int)sizeof(T);
-  if (v == kV16) {
-    e = launch_pdl(rope_kernel<T, kV16, APPEND, FP8>, g, b, 0, stream, p);
-  } else if (v == kV8) {
-    if constexpr (FP8 && kV8 < 4) e = cudaErrorInvalidValue;
-    else e = launch_pdl(rope_kernel<T, kV8, APPEND, FP8>, g, b, 0, stream, p);
-  } else {
-    e = launch_pdl(rope_kernel<T, 1, APPEND, FP8>, g, b, 0, stream, p);
-  }
+  if constexpr (APPEND)
+    e = p.each ? rope_launch_v<T, true, FP8, true>(p, v, grid, stream)
+               : rope_launch_v<T, true, FP8, false>(p, v, grid, stream);
+  else
+    e = rope_launch_v<T, false, false, false>(p, v, grid, stream);
   return e == cudaSuccess ? GBN_OK : GBN_ERR_CUDA;
 }
 
