@@ -49,6 +49,13 @@ int gbn_type(at::ScalarType t) {
   }
 }
 bool inner_ok(const at::Tensor& t) { return t.stride(-1) == 1; }
+// An output like t, the elements of a head side by side.  (Where t's elements share
+// memory, empty_like orders the dimensions by their strides, and the last may not be
+// the innermost.)
+at::Tensor output_like(const at::Tensor& t) {
+  at::Tensor o = at::empty_like(t);
+  return inner_ok(o) ? o : at::empty(t.sizes(), t.options());
+}
 
 // Keeps the interpreter's rules: a C++ exception becomes "not the usual call".
 template <typename F>
@@ -113,7 +120,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !f->is_cuda() || !pos->is_cuda() || k->get_device() != dev || f->get_device() != dev ||
         pos->get_device() != dev || c10::cuda::current_device() != dev)
       Py_RETURN_NONE;
-    at::Tensor qo = at::empty_like(*q), ko = at::empty_like(*k);
+    at::Tensor qo = output_like(*q), ko = output_like(*k);
     gbn_rope_args g;
     g.q = q->data_ptr();
     g.k = k->data_ptr();
@@ -209,7 +216,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         f->get_device() != dev || !scalar_ok(a[11], fp8, dev, &g.k_scale) ||
         !scalar_ok(a[12], fp8, dev, &g.v_scale))
       Py_RETURN_NONE;
-    at::Tensor qo = at::empty_like(*q);
+    at::Tensor qo = output_like(*q);
     g.q = q->data_ptr();
     g.k = k->data_ptr();
     g.v = v->data_ptr();
@@ -294,7 +301,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                             static_cast<gbn_dtype>(g.dtype), static_cast<gbn_dtype>(g.cache_dtype),
                             &bytes);
     if (st != GBN_OK) return status(st);
-    at::Tensor out = at::empty_like(*q), lse, work;
+    at::Tensor out = output_like(*q), lse, work;
     if (a[13] == Py_True) lse = at::empty({g.tokens, g.q_heads}, q->options().dtype(at::kFloat));
     if (bytes) work = at::empty({static_cast<int64_t>(bytes)}, q->options().dtype(at::kByte));
     g.q = q->data_ptr();

@@ -282,6 +282,13 @@ def rope_mscale(factor):
     return 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
 
 
+def _output_like(t):
+    """An output like t, the elements of a head side by side.  (Where t's elements share memory,
+    empty_like orders the dimensions by their strides, and the last may not be the innermost.)"""
+    o = torch.empty_like(t)
+    return o if o.stride(-1) == 1 else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _rope_tensor(name, t, o, x):
     """Checks q or k against x (whichever of them is given first), and its output."""
     if t.dim() != 4:
@@ -341,10 +348,10 @@ def _rope(call, where, q, k, inv_freq, positions, layout, mscale, q_out, k_out, 
     hq = hk = qa = ka = qoa = koa = 0
     qs = ks = qo = ko = _NO_STRIDES
     if q is not None:
-        q_out = torch.empty_like(q) if q_out is None else q_out
+        q_out = _output_like(q) if q_out is None else q_out
         hq, qs, qo, qa, qoa = q.shape[2], q.stride(), q_out.stride(), q.data_ptr(), q_out.data_ptr()
     if k is not None:
-        k_out = torch.empty_like(k) if k_out is None else k_out
+        k_out = _output_like(k) if k_out is None else k_out
         hk, ks, ko, ka, koa = k.shape[2], k.stride(), k_out.stride(), k.data_ptr(), k_out.data_ptr()
     pos_stride, pos_bytes, pa = 0, 8, 0
     if positions is not None:
@@ -494,7 +501,7 @@ def paged_append(k, v, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, q=
             raise ValueError(f"q: shape {tuple(q.shape)} does not go with k {tuple(k.shape)}")
         _inner("q", q)
         if q_out is None:
-            q_out = torch.empty_like(q)
+            q_out = _output_like(q)
         else:
             _same("q_out", q_out, k.dtype, dev, 3)
             if q_out.shape != q.shape:
@@ -578,7 +585,7 @@ def paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, ma
                           window=window, k_scale_inv=k_scale_inv, v_scale_inv=v_scale_inv,
                           return_lse=return_lse, out=out, lse=lse, workspace=workspace)
     if out is None:
-        out = torch.empty_like(q)
+        out = _output_like(q)
     else:
         _same("out", out, q.dtype, dev, 3)
         if out.shape != q.shape:
