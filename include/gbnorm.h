@@ -444,8 +444,8 @@ gbn_status gbn_paged_append(const gbn_paged_append_args* args, cudaStream_t stre
  * (f16 for E4M3 caches) for the product with the values: half a step relative;
  * f16 ones below 2^-23 of the row's largest by up to 2^-34 of that largest.
  * Deterministic.
- * head_dim: a multiple of 16 up to GBN_PAGED_MAX_DIM; scale finite and
- * positive; q_heads a multiple of kv_heads; tokens * q_heads < 2^31; max_kv
+ * head_dim: a multiple of 16 up to GBN_PAGED_MAX_DIM; scale positive,
+ * scale * log2 e finite in fp32; q_heads a multiple of kv_heads; tokens * q_heads < 2^31; max_kv
  * up to 2^30, the caches' strides in (0, 2^40) bytes (else GBN_ERR_SHAPE).  All
  * base pointers 16-byte aligned and all strides multiples of 16 bytes (else
  * GBN_ERR_ALIGNMENT).  A key that a row does not keep has no part in it,

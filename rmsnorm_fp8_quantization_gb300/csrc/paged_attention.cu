@@ -35,6 +35,7 @@
 // elements 2^-22 below that and smaller lose bits, 2^-33 of the row's largest.
 // (Keys in bf16 took four instructions a pair, and the kernel 133 us instead of
 // 79 us of HBM time for 262144 keys.)
+#include <cmath>
 #include <type_traits>
 
 #include <cuda.h>
@@ -1111,8 +1112,9 @@ gbn_status gbn_paged_attention(const gbn_paged_attention_args* args, cudaStream_
                     c.page_size, c.table_pages, c.max_q,   c.max_kv,   c.window};
   gbn_status st = check_sizes(z, dtype, cache_dtype);
   if (st != GBN_OK) return st;
+  // The kernels work with scale * log2 e, which has to be finite too.
   if (c.num_pages < 0 || c.num_pages > INT32_MAX || c.table_stride < 0 || !(c.scale > 0.f) ||
-      c.scale > 3.0e38f)
+      !std::isfinite(c.scale * kAttnLog2e))
     return GBN_ERR_SHAPE;
   if (c.tokens == 0 || c.batches == 0 || c.max_q == 0) return GBN_OK;
   if (!c.q || !c.k_cache || !c.v_cache || !c.cu_seqlens || !c.kv_lens || !c.block_table || !c.out)
