@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          sc[n][e] *= scale[e >> 1];
+          sc[n][e] = __fmul_rn(sc[n][e], scale[e >> 1]);  // (never one with the subtraction below)
           mx[e >> 1] = fmaxf(mx[e >> 1], sc[n][e]);
         }
     } else {
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
         for (int e = 0; e < 4; ++e) {
           const int j = jbase + n * 8 + qc * 2 + (e & 1);
           const bool keep = j >= rlo[e >> 1] && j < rhi[e >> 1];
-          sc[n][e] = keep ? sc[n][e] * scale[e >> 1] : -INFINITY;
+          sc[n][e] = keep ? __fmul_rn(sc[n][e], scale[e >> 1]) : -INFINITY;
           mx[e >> 1] = fmaxf(mx[e >> 1], sc[n][e]);
         }
     }
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
       const int low = max(row_low(p, s, gr / p.group), k0), high = min(row_high(p, s, gr / p.group), k1);
       if (low > k0 || high < k1)  // it dropped keys that others of its tile keep
         row_again<T, FP8>(p, b, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
-                          FP8 ? p.scale_log2 * *p.k_scale_inv : p.scale_log2, mm, low, high, c, acc);
+                          FP8 ? p.scale_log2 * *p.k_scale_inv : p.scale_log2, ll, low, high, c, acc);
     }
     if (p.cluster) {
       float* dst = s_part + r * DP + c;

@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
             float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (l != 0.f)
               row_again<T, FP8>(p, b, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
-                                FP8 ? p.scale_log2 * kscale : p.scale_log2, ref, rlo, rhi, col + 8 * i,
+                                FP8 ? p.scale_log2 * kscale : p.scale_log2, l, rlo, rhi, col + 8 * i,
                                 f);
             if (part) {
 #pragma unroll

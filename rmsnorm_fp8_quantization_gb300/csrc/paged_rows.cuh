@@ -145,38 +145,51 @@ __device__ __forceinline__ void cache_values(const void* cache, int64_t at, floa
   }
 }
 
-// Eight output columns of one row again, key by key: sum_j 2^(scale q.k_j - m) v_j
-// over j in [lo, hi) alone.  The products of whole tiles give a dropped key the
-// weight 0, and 0 times an infinity or NaN among its values is NaN; a row that
-// dropped keys of its tiles and came out NaN is computed here, where dropped keys
-// do not enter (a NaN that belongs there comes out again).  Rare, and slow.
+// Eight output columns of one row again, key by key, over j in [lo, hi) alone:
+// l times the mean of v_j with the weights 2^(scale q.k_j), l the row's sum.  The
+// products of whole tiles give a dropped key the weight 0, and 0 times an infinity
+// or NaN among its values is NaN; a row that dropped keys of its tiles and came out
+// NaN is computed here, where dropped keys do not enter (a NaN that belongs there
+// comes out again).  Against its own maximum and sum: of large scores the rounding,
+// which goes by the order of summation, exceeds one.  Rare, and slow.
 template <typename T, bool FP8>
 __device__ __noinline__ void row_again(const AttnParams& p, int b, int h, const T* q, float scale,
-                                       float m, int lo, int hi, int col, float* acc) {
+                                       float l, int lo, int hi, int col, float* acc) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  const float mb = m == -INFINITY ? 0.f : m;
-  for (int j = lo; j < hi; ++j) {
-    const int pg = p.table[b * p.table_stride + (j >> p.page_shift)];
-    if (pg < 0 || pg >= p.num_pages) continue;
-    const int slot = j & ((1 << p.page_shift) - 1);
-    const int64_t ko = pg * p.kp + slot * p.ks + h * p.kh, vo = pg * p.vp + slot * p.vs + h * p.vh;
-    float s = 0.f;
-    for (int c = 0; c < p.d; c += 8) {
-      float qf[8], kf[8];
-      const uint4 w = *reinterpret_cast<const uint4*>(q + c);
-      const uint32_t qw[4] = {w.x, w.y, w.z, w.w};
-      unpack<T, 8>(qw, qf);
-      cache_values<T, FP8>(p.k, ko + c, kf);
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass)
+    for (int j = lo; j < hi; ++j) {
+      const int pg = p.table[b * p.table_stride + (j >> p.page_shift)];
+      if (pg < 0 || pg >= p.num_pages) continue;
+      const int slot = j & ((1 << p.page_shift) - 1);
+      const int64_t ko = pg * p.kp + slot * p.ks + h * p.kh, vo = pg * p.vp + slot * p.vs + h * p.vh;
+      float s = 0.f;
+      for (int c = 0; c < p.d; c += 8) {
+        float qf[8], kf[8];
+        const uint4 w = *reinterpret_cast<const uint4*>(q + c);
+        const uint32_t qw[4] = {w.x, w.y, w.z, w.w};
+        unpack<T, 8>(qw, qf);
+        cache_values<T, FP8>(p.k, ko + c, kf);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(qf[e], kf[e], s);
+        for (int e = 0; e < 8; ++e) s = fmaf(qf[e], kf[e], s);
+      }
+      s = __fmul_rn(s, scale);  // (not into the subtraction below: its rounding is the maximum's)
+      if (pass == 0) {
+        top = fmaxf(top, s);
+        continue;
+      }
+      const float w = ex2(s - (top == -INFINITY ? 0.f : top));
+      sum += w;
+      float vf[8];
+      cache_values<T, FP8>(p.v, vo + col, vf);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, vf[e], acc[e]);
     }
-    const float w = ex2(s * scale - mb);
-    float vf[8];
-    cache_values<T, FP8>(p.v, vo + col, vf);
+  const float back = sum == 0.f ? 0.f : l / sum;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, vf[e], acc[e]);
-  }
+  for (int e = 0; e < 8; ++e) acc[e] *= back;
 }
 
 constexpr float kLn2 = 0.6931471805599453f;

@@ -82,3 +82,31 @@ def test_the_largest_score_takes_all(gpu, order, q_lens, kv_lens, fp8, dtype):
                 assert ((o[row, h].double() - mean).abs() <= lim).all(), (b, i, h)
             row += 1
     assert seen > 0 and np.isfinite(lse.cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["two-byte", "e4m3"])
+@pytest.mark.parametrize("q_lens,kv_lens", [([4, 3], [90, 100]), ([16], [300]), ([80, 100], [90, 100]),
+                                            ([200], [700])], ids=["few", "more", "many", "chunk"])
+def test_next_to_a_bad_value_that_the_row_drops(gpu, q_lens, kv_lens, fp8, dtype):
+    """The last key's values are NaN: rows before it are what they were."""
+    c, s, kw, best = batch("mixed", q_lens, kv_lens, fp8, dtype)
+    cpu = s["cpu"]
+    clean, _ = attend(gpu, c, s, scale=1.0, **kw)
+    v = s["v_cache"].float().cpu()
+    for b, kv in enumerate(c.kv_lens):
+        v[cpu["table"][b][(kv - 1) // c.page], (kv - 1) % c.page] = float("nan")
+    s["v_cache"].copy_(v.to(s["v_cache"].dtype))
+    out, _ = attend(gpu, c, s, scale=1.0, **kw)
+    eps = torch.finfo(DT[dtype]).eps
+    row, seen = 0, 0
+    for b, (n, kv) in enumerate(zip(c.q_lens, c.kv_lens)):
+        for i in range(n - 1):
+            if best[b][kv - n + i][1] == 1:
+                seen += 1
+                # (both within the first test's distance of the exact value)
+                a, e = out[row + i, ::2].double(), clean[row + i, ::2].double()
+                assert ((a - e).abs() <= 2 * (e.abs() * 2.1 * eps + 2.0 ** -25)).all(), (b, i)
+            assert torch.isfinite(out[row + i]).all()
+        row += n
+    assert seen > 0
