@@ -443,6 +443,9 @@ gbn_status gbn_paged_append(const gbn_paged_append_args* args, cudaStream_t stre
  * fp32 scores, sums and outputs, probabilities rounded to the values' type
  * (f16 for E4M3 caches) for the product with the values: half a step relative;
  * f16 ones below 2^-23 of the row's largest by up to 2^-34 of that largest.
+ * Next to an E4M3 cache a bf16 q row is taken in f16, scaled by a power of two:
+ * its elements below 2^-22 of the row's largest lose up to 2^-33 of that largest.
+ * Scores beyond 2^28 in magnitude (times log2 e) count as far apart or equal.
  * Deterministic.
  * head_dim: a multiple of 16 up to GBN_PAGED_MAX_DIM; scale positive,
  * scale * log2 e finite in fp32; q_heads a multiple of kv_heads; tokens * q_heads < 2^31; max_kv
