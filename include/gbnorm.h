@@ -485,6 +485,124 @@ typedef struct {
 } gbn_paged_attention_args;
 gbn_status gbn_paged_attention(const gbn_paged_attention_args* args, cudaStream_t stream);
 
+/* ---- Attention over whole sequences, with its backward pass (training).
+ *
+ * `batches` sequences, each with its queries and its keys, packed: sequence b
+ * owns the rows cu_q[b] .. cu_q[b+1] - 1 of q, out, lse, dout and dq, and the
+ * rows cu_k[b] .. cu_k[b+1] - 1 of k, v, dk and dv (int32, device, batches + 1
+ * entries, ascending; the same array for both where queries and keys are the
+ * same tokens).  cu_q = NULL: every sequence has max_q queries (tokens =
+ * batches * max_q, else GBN_ERR_SHAPE); cu_k = NULL: max_k keys, likewise.
+ * Rows before the first and behind the last sequence are padding: neither read
+ * into a result nor written.  Masks, scale and lse are the paged attention's:
+ * query i of n stands at key position keys - n + i (bottom-right aligned) and
+ * keeps, if causal, the keys up to it; with window > 0 only the last `window`
+ * of them.  A query that keeps nothing: out = 0, lse = -inf, dq = 0.  A pair
+ * that is not kept has no part in any result, whatever stands there.
+ *
+ * Tensors are [tokens, heads, head_dim] in dtype (BF16 or F16), the elements
+ * of a head contiguous, element strides for token and head; query head n goes
+ * with kv head n / (q_heads / kv_heads).  head_dim: a multiple of 8 up to
+ * GBN_ATTENTION_MAX_DIM; tokens * q_heads < 2^31; scale positive, scale *
+ * log2 e finite in fp32; strides of q (backward), k, v and dout in (0, 2^40)
+ * bytes (else GBN_ERR_SHAPE).  Base pointers on 16 bytes, strides multiples of
+ * 16 bytes (else GBN_ERR_ALIGNMENT).  max_q and max_k bound the lengths (any
+ * bounds work, tight ones are faster); lengths that do not fit them or the
+ * tensors set GBN_DEVICE_ERR_BAD_INDEX, and the rows concerned are unspecified.
+ * Deterministic.  Outputs must not overlap inputs or each other. */
+#define GBN_ATTENTION_MAX_DIM 128
+
+/* Forward: out, and lse (fp32 [tokens, q_heads] contiguous, or NULL), rounded
+ * as in gbn_paged_attention; head_dim 128 and 64 waste no work. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  void* out;
+  float* lse;
+  int64_t tokens, keys, batches, q_heads, kv_heads, head_dim, max_q, max_k, window;
+  int64_t q_strides[2]; /* token, head */
+  int64_t k_strides[2];
+  int64_t v_strides[2];
+  int64_t out_strides[2];
+  int32_t dtype; /* gbn_dtype */
+  int32_t causal;
+  float scale;
+  int32_t reserved;
+} gbn_attention_fwd_args;
+gbn_status gbn_attention_fwd(const gbn_attention_fwd_args* args, cudaStream_t stream);
+
+/* Backward: dq, dk, dv from dout and the forward's inputs and results.  The
+ * probabilities are computed again:
+ *     p_ij = exp(scale * q_i . k_j - lse_i),
+ *     ds_ij = p_ij * (dout_i . v_j - dout_i . out_i),
+ *     dq_i = scale * sum_j ds_ij k_j,  dk_j = scale * sum_i ds_ij q_i,
+ *     dv_j = sum_i p_ij dout_i
+ * (over the queries of every head that shares the key).  fp32 scores, sums and
+ * results; p and ds are rounded to dtype for their products: half a step
+ * relative.  f16: probabilities below 2^-26 by up to 2^-37, ds below 2^-29 of
+ * the largest |dout_i| |v_j| of the sequence and kv head by up to 2^-40 of it.
+ *   workspace  gbn_attention_bwd_workspace_size() bytes, 16-byte aligned (else
+ *              GBN_ERR_WORKSPACE); needs no initialization; calls that may
+ *              overlap on the GPU need one each. */
+gbn_status gbn_attention_bwd_workspace_size(int64_t tokens, int64_t batches, int64_t q_heads,
+                                            int64_t kv_heads, gbn_dtype dtype, size_t* bytes);
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* out;
+  const void* dout;
+  const float* lse;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  void* dq;
+  void* dk;
+  void* dv;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t tokens, keys, batches, q_heads, kv_heads, head_dim, max_q, max_k, window;
+  int64_t q_strides[2]; /* token, head */
+  int64_t k_strides[2];
+  int64_t v_strides[2];
+  int64_t out_strides[2];
+  int64_t dout_strides[2];
+  int64_t dq_strides[2];
+  int64_t dk_strides[2];
+  int64_t dv_strides[2];
+  int32_t dtype; /* gbn_dtype */
+  int32_t causal;
+  float scale;
+  int32_t reserved;
+} gbn_attention_bwd_args;
+gbn_status gbn_attention_bwd(const gbn_attention_bwd_args* args, cudaStream_t stream);
+
+/* ---- Dropout, its mask never stored, with the residual's addition.
+ *
+ *     out = (kept ? x / (1 - p) : 0) + residual
+ *
+ * over n contiguous elements (dtype F32, BF16 or F16; residual NULL: 0), in
+ * fp32, one rounding.  Element e is dropped where w(e) < p * 2^32, w(e) being
+ * word e % 4 of Philox 4x32-10 with the counter words (low and high half of
+ * e / 4, low and high half of rng[1]) and the key words (low and high half of
+ * rng[0]).  rng: int64 [2], device: seed and offset, read on the GPU (a
+ * captured graph draws anew when its rng is changed between replays); calls
+ * that are to be independent differ in either.  A dropped element of x has no
+ * part in out, whatever it is.  out may be x or residual.  Pointers that are
+ * not on 16 bytes take a scalar path; not on the element's own size:
+ * GBN_ERR_ALIGNMENT.  GBN_ERR_SHAPE: n outside [0, GBN_DROPOUT_MAX_ELEMENTS],
+ * p outside [0, 1]. */
+#define GBN_DROPOUT_MAX_ELEMENTS (INT64_C(1) << 40)
+gbn_status gbn_dropout_fwd(const void* x, const void* residual, void* out, const int64_t* rng,
+                           int64_t n, double p, gbn_dtype dtype, cudaStream_t stream);
+
+/* Backward: dx = kept ? dout / (1 - p) : 0 with the forward's rng and p (the
+ * residual's gradient is dout itself).  dx may be dout. */
+gbn_status gbn_dropout_bwd(const void* dout, void* dx, const int64_t* rng, int64_t n, double p,
+                           gbn_dtype dtype, cudaStream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* gbn_status_string(gbn_status status);
 

@@ -25,7 +25,7 @@ FAST_STAMP = os.path.join(BUILD_DIR, "fastcall.txt")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "kernels_f32.cu", "kernels_bf16.cu", "kernels_f16.cu", "finalize.cu",
            "noalloc.cu", "softmax.cu", "rope.cu", "paged_attention.cu",
-           "paged_prefill.cu"]
+           "paged_prefill.cu", "attention_bwd.cu", "dropout.cu"]
 
 
 def _nvcc() -> str:

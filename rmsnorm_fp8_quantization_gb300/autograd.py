@@ -13,6 +13,11 @@ residual gradient, plus grad_weight).
 the transposed rotation of both gradients in one launch, and saves nothing but
 the positions and frequencies.
 
+``attention`` runs the attention over whole sequences and saves its output and the
+rows' logarithms of their sums; its backward computes the probabilities again.
+``dropout`` (with the residual's addition) saves two numbers; its backward draws
+the mask again.
+
 Shapes (norms): x is [..., hidden], contiguous, on a CUDA device; gamma (and beta)
 [hidden].  The outputs have x's dtype; weight gradients have the weights'
 dtype.  Every step runs in the library's kernels; this module only reshapes
@@ -25,7 +30,8 @@ from torch.autograd.function import once_differentiable
 
 from . import ops
 
-__all__ = ["layer_norm", "rms_norm", "layer_norm_with_residual", "rms_norm_with_residual", "rope"]
+__all__ = ["layer_norm", "rms_norm", "layer_norm_with_residual", "rms_norm_with_residual", "rope",
+           "attention", "dropout"]
 
 
 def _rows(x: torch.Tensor, hidden: int) -> torch.Tensor:
@@ -123,3 +129,71 @@ def rope(q, k, inv_freq, positions=None, layout="half", mscale=1.0):
     if inv_freq.requires_grad and torch.is_grad_enabled():
         raise ValueError("inv_freq requires a gradient, and rope has none for it")
     return _Rope.apply(q, k, inv_freq, positions, layout, mscale)
+
+
+def _whole_rows(t):
+    """t, or a copy where its strides are not what the attention takes."""
+    ok = t.stride(-1) == 1 and t.data_ptr() % 16 == 0
+    for n, st in zip(t.shape[:-1], t.stride()):
+        ok = ok and (n <= 1 or st > 0 and st * t.element_size() % 16 == 0)
+    if ok and t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1:
+        ok = t.stride(0) == t.shape[1] * t.stride(1)
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, cu_seqlens_k, kw):
+        q, k, v = (_whole_rows(t) for t in (q, k, v))
+        # Padding rows are not written: zeros there, and in their gradients.
+        out = None if cu_seqlens is None else torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        out, lse = ops.attention_fwd(q, k, v, cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k,
+                                     out=out, **kw)
+        ctx.save_for_backward(q, k, v, out, lse, cu_seqlens, cu_seqlens_k)
+        ctx.kw = kw
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        q, k, v, out, lse, cu, cu_k = ctx.saved_tensors
+        d = (None,) * 3
+        if cu is not None:
+            d = tuple(torch.zeros(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+        dq, dk, dv = ops.attention_bwd(_whole_rows(dout), q, k, v, out, lse, cu_seqlens=cu,
+                                       cu_seqlens_k=cu_k, dq=d[0], dk=d[1], dv=d[2], **ctx.kw)
+        return dq, dk, dv, None, None, None
+
+
+def attention(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, max_q=None, max_k=None, scale=None,
+              causal=True, window=0):
+    """``ops.attention_fwd`` with its gradient, for q, k and v; returns its output.  Padding rows
+    of packed tensors get 0, in the output and in the gradients.  Tensors whose strides the
+    kernels do not take are copied."""
+    kw = dict(max_q=max_q, max_k=max_k, scale=scale, causal=causal, window=window)
+    return _Attention.apply(q, k, v, cu_seqlens, cu_seqlens_k, kw)
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, rng, residual):
+        # The caller's is advanced in place before the backward runs.
+        rng = rng.clone()
+        ctx.save_for_backward(rng)
+        ctx.p = p
+        return ops.dropout_fwd(x, p, rng, residual=residual)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        dx = None
+        if ctx.needs_input_grad[0]:
+            rng, = ctx.saved_tensors
+            dx = ops.dropout_bwd(dout.contiguous(), ctx.p, rng)
+        return dx, None, None, dout if ctx.needs_input_grad[3] else None
+
+
+def dropout(x, p, rng, residual=None):
+    """``ops.dropout_fwd`` with its gradient, for x and residual.  rng (seed, offset) is copied:
+    the caller may advance it in place."""
+    return _Dropout.apply(x, p, rng, residual)

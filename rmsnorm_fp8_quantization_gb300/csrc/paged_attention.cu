@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
     if (nan && ll == ll) {  // (a NaN sum: a kept score is NaN, and so is the row)
       const int low = max(row_low(p, s, gr / p.group), k0), high = min(row_high(p, s, gr / p.group), k1);
       if (low > k0 || high < k1)  // it dropped keys that others of its tile keep
-        row_again<T, FP8>(p, b, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
+        row_again<T, FP8>(p, b, 0, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
                           FP8 ? p.scale_log2 * *p.k_scale_inv : p.scale_log2, ll, low, high, c, acc);
     }
     if (p.cluster) {

@@ -19,17 +19,19 @@ struct AttnParams {
   const int32_t* cu;       // [batches + 1]
   const int32_t* kv_lens;  // [batches]
   const int32_t* table;
+  const int32_t* cu_k;       // contiguous keys: [batches + 1]; null (cu too): max_q, max_kv each
   const float* k_scale_inv;  // E4M3 caches
   const float* v_scale_inv;
   float* part_o;       // [splits][tokens * hq][d] fp32
   float2* part_ml;     // [tokens * hq][splits]: (reference in log2 units, sum)
   int64_t qt, qh;      // element strides of q
   int64_t ot, oh;      // of out
-  int64_t kp, ks, kh;  // of the caches: page, slot, head
+  int64_t kp, ks, kh;  // of the caches: page, slot, head (contiguous keys: ks is the token's)
   int64_t vp, vs, vh;
   int64_t table_stride;
   int64_t num_pages;
   int tokens, batches;
+  int keys;            // contiguous keys: their tokens
   int hq, hkv, group;  // group = hq / hkv
   int d;
   int page_shift, table_pages;
@@ -52,7 +54,10 @@ bool make_cache_map(CUtensorMap* map, const void* base, int esize, bool bf16, in
 // head sizes up to 128).
 cudaError_t launch_paged_prefill(const AttnParams& p, gbn_dtype dtype, gbn_dtype cache_dtype,
                                  cudaStream_t stream);
+// The same kernel over contiguous keys and values (two-byte types).
+cudaError_t launch_attention_fwd(const AttnParams& p, gbn_dtype dtype, cudaStream_t stream);
 cudaError_t read_prefill_error(unsigned int* v, bool clear);
+cudaError_t read_attention_bwd_error(unsigned int* v, bool clear);
 cudaError_t read_attention_error(unsigned int* v, bool clear);
 cudaError_t read_rope_error(unsigned int* v, bool clear);
 

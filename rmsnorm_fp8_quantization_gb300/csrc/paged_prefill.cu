@@ -45,6 +45,7 @@
 #include <cuda_fp16.h>
 
 #include "paged_rows.cuh"
+#include "tensor_core.cuh"
 
 namespace gbn {
 namespace {
@@ -53,7 +54,6 @@ constexpr int kRowsT = 128;                // rows per tile
 constexpr int kKeys = kPrefillKeys;        // keys per tile
 constexpr int kHalf = kKeys / 2;           // keys per step of the tensor core and the softmax
 constexpr int kPanel = kKeys * 128;        // bytes of [128][64] 16-bit elements
-constexpr uint32_t kTmemCols = 512;
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kZeroWarp = 11, kConvertWarp = 12;
 constexpr int kLoaders = 128;              // E4M3 caches: threads of warps 12-15
 constexpr int kStaging = 4;                // E4M3 caches: at most so many tiles of codes
@@ -100,133 +100,6 @@ struct PrefillShape {
   static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther == kThreads * kRegsLaunch, "");
 };
 
-// ---- tcgen05
-
-__device__ __forceinline__ void tc_alloc(uint32_t* dst) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                   smem_u32(dst)),
-               "r"(kTmemCols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tc_dealloc(uint32_t t) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(kTmemCols)
-               : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
-}
-// D[tmem] (+)= A[smem] B[smem].  Descriptors as (low, high) words: the high one
-// is a constant and the low one the address, so a step costs one addition --
-// the issuing thread has to stay ahead of the tensor core (64 cycles a step).
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
-                                          uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
-                                          uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-      "mov.b64 db, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// 32 columns of this warp's 32 lanes.
-__device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(a)
-      : "memory");
-}
-__device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-// The loaded registers pass through, so that nothing uses them earlier.
-__device__ __forceinline__ void tc_loaded(uint32_t* r) {
-  asm volatile(""
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
-                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
-                 "+r"(r[31])::"memory");
-}
-template <int N>
-__device__ __forceinline__ void tc_wait_ld(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < N; i += 32) tc_loaded(r + i);
-}
-__device__ __forceinline__ void tc_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// Shared-memory operand descriptor, 128-byte swizzle, 8-row groups 1024 bytes
-// apart (high word); low word: the address and, MN-major only, the distance
-// `panel` of the next 64 elements.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t panel) {
-  return ((addr & 0x3FFFFu) >> 4) | ((panel >> 4) << 16);
-}
-// Instruction descriptor: fp32 accumulator, A and B f16 (0) or bf16 (1), M x N;
-// bmn: B is MN-major.
-__host__ __device__ constexpr uint32_t instr_desc(int type, int m, int n, int bmn) {
-  return (1u << 4) | (static_cast<uint32_t>(type) << 7) | (static_cast<uint32_t>(type) << 10) |
-         (static_cast<uint32_t>(bmn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
-         (static_cast<uint32_t>(m >> 4) << 24);
-}
-
-// Three-input maximum (a number wins over NaN, as fmaxf).
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// The same, NaN if one of them is.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // The factor of a row whose largest score is beyond 2^28 (log2 units) in magnitude: the power
 // of two at or below the row's own, with which products are exact.  Any other rounds them by up
 // to 8 and more there, and taken against the rounded maximum the largest key's probability
@@ -236,25 +109,7 @@ __device__ __forceinline__ float large_factor(float scale) {
   return __uint_as_float(__float_as_uint(scale) & 0xFF800000u);
 }
 
-// The lowest n bits set (none for n <= 0, all from 64 on).
-__device__ __forceinline__ uint64_t low_bits(int n) {
-  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
-}
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
-}
-
-template <int N>
-__device__ __forceinline__ void set_regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void set_regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-template <typename T, bool FP8, int DP>
+template <typename T, bool FP8, int DP, bool PACKED>
 __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ AttnParams p,
                          const __grid_constant__ CUtensorMap kmap,
@@ -277,15 +132,16 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
   x /= p.splits;
   const int rt = p.row_tiles - 1 - static_cast<int>(x % p.row_tiles);
   int b = x / p.row_tiles;
-  if (p.batches > 1 && p.batches <= kSortBatches) {
+  if (p.batches > 1 && p.batches <= kSortBatches && (!PACKED || p.cu_k)) {
+    auto keys_of = [&](int i) { return PACKED ? p.cu_k[i + 1] - p.cu_k[i] : p.kv_lens[i]; };
     // The sequence with b longer ones.  Every CTA counts for itself: a few hundred
     // cycles against a second launch.
     for (int i = tid; i < p.batches; i += Shape::kThreads) {
-      const int mine = p.kv_lens[i];
+      const int mine = keys_of(i);
       int before = 0;
 #pragma unroll 8
       for (int j = 0; j < p.batches; ++j) {
-        const int kv = p.kv_lens[j];
+        const int kv = keys_of(j);
         before += kv > mine || (kv == mine && j < i);
       }
       if (before == b) bars.sequence = i;
@@ -294,7 +150,9 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
     b = bars.sequence;
   }
 
-  const SeqRange s = seq_range(p, b, tid == 0 && split == 0 && rt == 0 && h == 0);
+  const bool flag = tid == 0 && split == 0 && rt == 0 && h == 0;
+  const SeqRange s = PACKED ? packed_range(p.cu, p.cu_k, b, p.tokens, p.keys, p.max_q, p.max_kv, flag)
+                            : seq_range(p, b, flag);
   const int r0 = rt * kPrefillRows;
   const int rows = min(kPrefillRows, s.qlen * p.group - r0);
   if (rows <= 0) return;
@@ -500,7 +358,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
       }
     } else if (warp == kLoadWarp) {
       // ------------------------------------------------ TMA loads
-      const int page = 1 << p.page_shift;
+      const int page = PACKED ? kKeys : 1 << p.page_shift;
       const int box = min(page, kKeys);           // keys per box
       const int boxes = kKeys / box;              // per panel, at most 16
       const int32_t* tab = p.table + b * p.table_stride;
@@ -513,6 +371,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
         return lane < boxes && key < k1 && key + box > k0;
       };
       auto entry = [&](int j) {
+        if constexpr (PACKED) return 0;
         const int key = base + j * kKeys + lane * box;
         return wanted(j) ? tab[min(key >> p.page_shift, e_last)] : 0;
       };
@@ -528,7 +387,9 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
       for (int j = 0; ok && j < nmax; ++j) {
         const int next = j + 1 < nmax ? entry(j + 1) : 0;
         int pg = zero_page;
-        if (wanted(j)) {
+        if constexpr (PACKED) {
+          pg = 0;  // (rows behind the sequence are the next one's, behind the last zeros)
+        } else if (wanted(j)) {
           if (cur >= 0 && cur < p.num_pages) pg = cur;
           else flag_bad_index();
         }
@@ -543,7 +404,8 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
 #pragma unroll
             for (int pn = 0; pn < (FP8 ? 1 : Shape::kPanels); ++pn)
               tma_box(dst0 + slot * kBytes + pn * kPanel + lane * box * (FP8 ? DP : 128),
-                      kv ? &vmap : &kmap, pn * 64, h, key & (page - 1), pg, &full[slot]);
+                      kv ? &vmap : &kmap, pn * 64, h,
+                      PACKED ? s.k0 + key : key & (page - 1), pg, &full[slot]);
           }
           issued = it + 1;
         }
@@ -879,7 +741,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
             if (!(bad & (1u << i)) || col + 8 * i >= p.d) continue;
             float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (l != 0.f)
-              row_again<T, FP8>(p, b, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
+              row_again<T, FP8, PACKED>(p, b, s.k0, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
                                 FP8 ? p.scale_log2 * kscale : p.scale_log2, l, rlo, rhi, col + 8 * i,
                                 f);
             if (part) {
@@ -909,30 +771,11 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
 
 // ---- host side
 
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor map encoder (looked up once; no link against libcuda).
-EncodeFn encoder() {
-  static const EncodeFn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult st;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &st) != cudaSuccess ||
-        st != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeFn>(f);
-  }();
-  return fn;
-}
-
-template <typename T, bool FP8, int DP>
+template <typename T, bool FP8, int DP, bool PACKED = false>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm,
                    cudaStream_t st) {
   using Shape = PrefillShape<FP8, DP>;
-  auto k = paged_prefill_kernel<T, FP8, DP>;
+  auto k = paged_prefill_kernel<T, FP8, DP, PACKED>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(k, Shape::kSmem, done);
   if (e != cudaSuccess) return e;
@@ -989,6 +832,19 @@ cudaError_t launch_paged_prefill(const AttnParams& p, gbn_dtype dtype, gbn_dtype
                 : launch<__half, true, 128>(p, km, vm, stream);
   return bf16 ? launch<__nv_bfloat16, false, 128>(p, km, vm, stream)
               : launch<__half, false, 128>(p, km, vm, stream);
+}
+
+cudaError_t launch_attention_fwd(const AttnParams& p, gbn_dtype dtype, cudaStream_t stream) {
+  const bool bf16 = dtype == GBN_BF16;
+  CUtensorMap km = {}, vm = {};
+  if (!make_packed_map(&km, p.k, bf16, p.d, p.hkv, p.keys, p.ks, p.kh, kKeys) ||
+      !make_packed_map(&vm, p.v, bf16, p.d, p.hkv, p.keys, p.vs, p.vh, kKeys))
+    return cudaErrorInvalidValue;
+  if (p.d <= 64)
+    return bf16 ? launch<__nv_bfloat16, false, 64, true>(p, km, vm, stream)
+                : launch<__half, false, 64, true>(p, km, vm, stream);
+  return bf16 ? launch<__nv_bfloat16, false, 128, true>(p, km, vm, stream)
+              : launch<__half, false, 128, true>(p, km, vm, stream);
 }
 
 cudaError_t read_prefill_error(unsigned int* v, bool clear) { return read_paged_error(v, clear); }

@@ -34,6 +34,7 @@ struct SeqRange {
   int qlen;  // new tokens
   int kv;    // keys with them
   int off;   // kv - qlen (negative: the first tokens keep nothing)
+  int k0;    // first key's row (contiguous keys only)
 };
 
 // Sequence b's lengths, bounded by the buffers whatever the values are; what
@@ -46,8 +47,38 @@ __device__ __forceinline__ SeqRange seq_range(const AttnParams& p, int b, bool f
   const int64_t room = static_cast<int64_t>(p.table_pages) << p.page_shift;
   s.kv = static_cast<int>(min(static_cast<int64_t>(min(max(kv, 0), p.max_kv)), room));
   s.off = s.kv - s.qlen;
+  s.k0 = 0;
   if (flag && (s.q0 != c0 || s.q0 + s.qlen != c1 || s.kv != kv || s.qlen > p.max_q))
     flag_bad_index();
+  return s;
+}
+
+// Rows [cu[b], cu[b + 1]) of a packed tensor (null: b-th run of `most` rows), bounded by
+// its `rows` rows whatever the values are; *bad if they did not fit.
+__device__ __forceinline__ int2 packed_rows(const int32_t* cu, int b, int rows, int most, bool* bad) {
+  const int64_t c0 = cu ? cu[b] : static_cast<int64_t>(b) * most;
+  const int64_t c1 = cu ? cu[b + 1] : c0 + most;
+  const int first = static_cast<int>(min(max(c0, int64_t(0)), static_cast<int64_t>(rows)));
+  const int end = static_cast<int>(min(max(c1, static_cast<int64_t>(first)), static_cast<int64_t>(rows)));
+  const int n = min(end - first, most);
+  *bad = *bad || first != c0 || first + n != c1;
+  return make_int2(first, n);
+}
+
+// The same of a sequence whose keys and values are contiguous.
+__device__ __forceinline__ SeqRange packed_range(const int32_t* cu_q, const int32_t* cu_k, int b,
+                                                 int tokens, int keys, int max_q, int max_k,
+                                                 bool flag) {
+  bool bad = false;
+  const int2 q = packed_rows(cu_q, b, tokens, max_q, &bad);
+  const int2 k = packed_rows(cu_k, b, keys, max_k, &bad);
+  if (flag && bad) flag_bad_index();
+  SeqRange s;
+  s.q0 = q.x;
+  s.qlen = q.y;
+  s.kv = k.y;
+  s.off = s.kv - s.qlen;
+  s.k0 = k.x;
   return s;
 }
 
@@ -152,18 +183,21 @@ __device__ __forceinline__ void cache_values(const void* cache, int64_t at, floa
 // NaN is computed here, where dropped keys do not enter (a NaN that belongs there
 // comes out again).  Against its own maximum and sum: of large scores the rounding,
 // which goes by the order of summation, exceeds one.  Rare, and slow.
-template <typename T, bool FP8>
-__device__ __noinline__ void row_again(const AttnParams& p, int b, int h, const T* q, float scale,
-                                       float l, int lo, int hi, int col, float* acc) {
+template <typename T, bool FP8, bool PACKED = false>
+__device__ __noinline__ void row_again(const AttnParams& p, int b, int first, int h, const T* q,
+                                       float scale, float l, int lo, int hi, int col, float* acc) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
   float top = -INFINITY, sum = 0.f;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass)
     for (int j = lo; j < hi; ++j) {
-      const int pg = p.table[b * p.table_stride + (j >> p.page_shift)];
-      if (pg < 0 || pg >= p.num_pages) continue;
-      const int slot = j & ((1 << p.page_shift) - 1);
+      int64_t pg = 0, slot = first + j;
+      if constexpr (!PACKED) {
+        pg = p.table[b * p.table_stride + (j >> p.page_shift)];
+        if (pg < 0 || pg >= p.num_pages) continue;
+        slot = j & ((1 << p.page_shift) - 1);
+      }
       const int64_t ko = pg * p.kp + slot * p.ks + h * p.kh, vo = pg * p.vp + slot * p.vs + h * p.vh;
       float s = 0.f;
       for (int c = 0; c < p.d; c += 8) {

@@ -32,13 +32,16 @@ FUNCTIONS = ("gbn_norm_fwd_workspace_size", "gbn_norm_fwd", "gbn_norm_bwd_worksp
              "gbn_norm_bwd", "gbn_norm_bwd_noalloc", "gbn_device_error", "gbn_status_string",
              "gbn_softmax_fwd", "gbn_softmax_bwd", "gbn_selftest_copy_timeout", "gbn_rope_fwd",
              "gbn_rope_bwd", "gbn_paged_append", "gbn_paged_attention_workspace_size",
-             "gbn_paged_attention")
+             "gbn_paged_attention", "gbn_attention_fwd", "gbn_attention_bwd_workspace_size",
+             "gbn_attention_bwd", "gbn_dropout_fwd", "gbn_dropout_bwd")
 (GBN_SOFTMAX_NO_MASK, GBN_SOFTMAX_PADDING, GBN_SOFTMAX_CAUSAL_UPPER,
  GBN_SOFTMAX_CAUSAL_ALIGNED) = range(4)
 GBN_SOFTMAX_MAX_KEYS = 16384
 GBN_DEVICE_ERR_COPY_TIMEOUT, GBN_DEVICE_ERR_BAD_INDEX = 1, 2
 GBN_ROPE_HALF, GBN_ROPE_INTERLEAVED = 0, 1
 GBN_ROPE_MAX_DIM = 1024
+GBN_ATTENTION_MAX_DIM = 128
+GBN_DROPOUT_MAX_ELEMENTS = 1 << 40
 GBN_PAGED_MAX_BATCHES, GBN_PAGED_MAX_PAGE, GBN_PAGED_MAX_DIM = 1 << 20, 65536, 256
 
 
@@ -74,11 +77,18 @@ def _load():
     lib.gbn_softmax_fwd.restype = I
     lib.gbn_softmax_bwd.argtypes = [P, P, P, I64, I64, I, F, P]
     lib.gbn_softmax_bwd.restype = I
-    for f in (lib.gbn_rope_fwd, lib.gbn_rope_bwd, lib.gbn_paged_append, lib.gbn_paged_attention):
+    for f in (lib.gbn_rope_fwd, lib.gbn_rope_bwd, lib.gbn_paged_append, lib.gbn_paged_attention,
+              lib.gbn_attention_fwd, lib.gbn_attention_bwd):
         f.argtypes = [P, P]  # the argument struct (packed bytes), the stream
         f.restype = I
     lib.gbn_paged_attention_workspace_size.argtypes = [I64] * 10 + [I, I, I, ctypes.POINTER(SZ)]
     lib.gbn_paged_attention_workspace_size.restype = I
+    lib.gbn_attention_bwd_workspace_size.argtypes = [I64] * 4 + [I, ctypes.POINTER(SZ)]
+    lib.gbn_attention_bwd_workspace_size.restype = I
+    lib.gbn_dropout_fwd.argtypes = [P, P, P, P, I64, ctypes.c_double, I, P]
+    lib.gbn_dropout_fwd.restype = I
+    lib.gbn_dropout_bwd.argtypes = [P, P, P, I64, ctypes.c_double, I, P]
+    lib.gbn_dropout_bwd.restype = I
     lib.gbn_selftest_copy_timeout.argtypes = [ctypes.c_uint, P]
     lib.gbn_selftest_copy_timeout.restype = I
     lib.gbn_status_string.argtypes = [I]
@@ -207,6 +217,8 @@ def gbn_softmax_bwd(dy, y, dx, rows, sk, dtype, scale, stream=None) -> int:
 rope_args = struct.Struct("=6Q19q3if").pack
 append_args = struct.Struct("=12Q24q3if").pack
 attention_args = struct.Struct("=12Q22q3if").pack
+attention_fwd_args = struct.Struct("=7Q17q2if4x").pack
+attention_bwd_args = struct.Struct("=13Q25q2if4x").pack
 
 
 def _addr(t):
@@ -279,6 +291,48 @@ def gbn_paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, k
                         page_size, table_pages, table_stride, max_q, max_kv, *q_strides,
                         *out_strides, *k_cache_strides, *v_cache_strides, window, dtype,
                         cache_dtype, 1 if causal else 0, scale), _stream(stream))
+
+
+def gbn_attention_fwd(q, k, v, cu_q, cu_k, out, lse, tokens, keys, batches, q_heads, kv_heads,
+                      head_dim, max_q, max_k, window, q_strides, k_strides, v_strides, out_strides,
+                      dtype, causal, scale, stream=None) -> int:
+    """Strides: (token, head) pairs in elements."""
+    return _lib.gbn_attention_fwd(
+        attention_fwd_args(_addr(q), _addr(k), _addr(v), _addr(cu_q), _addr(cu_k), _addr(out),
+                           _addr(lse), tokens, keys, batches, q_heads, kv_heads, head_dim, max_q,
+                           max_k, window, *q_strides, *k_strides, *v_strides, *out_strides, dtype,
+                           1 if causal else 0, scale), _stream(stream))
+
+
+def gbn_attention_bwd_workspace_size(tokens, batches, q_heads, kv_heads, dtype):
+    """Returns (status, bytes)."""
+    n = ctypes.c_size_t(0)
+    st = _lib.gbn_attention_bwd_workspace_size(tokens, batches, q_heads, kv_heads, dtype,
+                                               ctypes.byref(n))
+    return st, n.value
+
+
+def gbn_attention_bwd(q, k, v, out, dout, lse, cu_q, cu_k, dq, dk, dv, workspace, workspace_bytes,
+                      tokens, keys, batches, q_heads, kv_heads, head_dim, max_q, max_k, window,
+                      q_strides, k_strides, v_strides, out_strides, dout_strides, dq_strides,
+                      dk_strides, dv_strides, dtype, causal, scale, stream=None) -> int:
+    """Strides: (token, head) pairs in elements."""
+    return _lib.gbn_attention_bwd(
+        attention_bwd_args(_addr(q), _addr(k), _addr(v), _addr(out), _addr(dout), _addr(lse),
+                           _addr(cu_q), _addr(cu_k), _addr(dq), _addr(dk), _addr(dv),
+                           _addr(workspace), workspace_bytes, tokens, keys, batches, q_heads,
+                           kv_heads, head_dim, max_q, max_k, window, *q_strides, *k_strides,
+                           *v_strides, *out_strides, *dout_strides, *dq_strides, *dk_strides,
+                           *dv_strides, dtype, 1 if causal else 0, scale), _stream(stream))
+
+
+def gbn_dropout_fwd(x, residual, out, rng, n, p, dtype, stream=None) -> int:
+    return _lib.gbn_dropout_fwd(_ptr(x), _ptr(residual), _ptr(out), _ptr(rng), n, float(p), dtype,
+                                _stream(stream))
+
+
+def gbn_dropout_bwd(dout, dx, rng, n, p, dtype, stream=None) -> int:
+    return _lib.gbn_dropout_bwd(_ptr(dout), _ptr(dx), _ptr(rng), n, float(p), dtype, _stream(stream))
 
 
 def gbn_selftest_copy_timeout(timeout_us, stream=None) -> int:

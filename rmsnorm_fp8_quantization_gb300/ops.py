@@ -633,3 +633,218 @@ def paged_attention(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, *, ma
                              d ** -0.5 if scale is None else scale),
             q.get_device(), stream)
     return (out, lse) if return_lse else out
+
+
+# ---- attention over whole sequences, and dropout
+
+def _tokens(name, t, like):
+    """t as [tokens, heads, head_dim]: it is one, or (``like`` four-dimensional) a batch of
+    sequences of one length, whose tokens have to be one run of rows."""
+    _same(name, t, like.dtype, like.device, like.dim())
+    _inner(name, t)
+    if t.dim() == 3:
+        return t
+    try:
+        return t.view(t.shape[0] * t.shape[1], t.shape[2], t.shape[3])
+    except RuntimeError:
+        raise ValueError(f"{name}: batch and sequence must be one run of tokens (strides "
+                         f"{tuple(t.stride())} of {tuple(t.shape)})") from None
+
+
+def _attention_tensors(q, k, v, cu_seqlens, cu_seqlens_k, max_q, max_k):
+    """Checks what both passes share; ((q, k, v) as tokens, cu_q, cu_k, sizes)."""
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"unsupported dtype {q.dtype}: bfloat16 or float16")
+    if q.dim() not in (3, 4):
+        raise ValueError("q: expected [batch, seq, heads, head_dim], or [tokens, heads, head_dim] "
+                         f"with cu_seqlens; got {tuple(q.shape)}")
+    if (q.dim() == 4) != (cu_seqlens is None):
+        raise ValueError("cu_seqlens goes with [tokens, heads, head_dim], and only with it")
+    x = tuple(_tokens(n, t, q) for n, t in (("q", q), ("k", k), ("v", v)))
+    if k.shape != v.shape:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} differ")
+    if k.shape[-1] != q.shape[-1]:
+        raise ValueError(f"k: head_dim {k.shape[-1]}, expected {q.shape[-1]}")
+    if q.dim() == 4:
+        if cu_seqlens_k is not None or max_q is not None or max_k is not None:
+            raise ValueError("cu_seqlens_k, max_q and max_k go with cu_seqlens")
+        if k.shape[0] != q.shape[0]:
+            raise ValueError(f"k: {k.shape[0]} sequences, expected {q.shape[0]}")
+        batches, mq, mk, cu_k = q.shape[0], q.shape[1], k.shape[1], None
+    else:
+        if max_q is None:
+            raise ValueError("cu_seqlens needs max_q")
+        _same("cu_seqlens", cu_seqlens, torch.int32, q.device, 1)
+        cu_k = cu_seqlens
+        mq = mk = max_q
+        if cu_seqlens_k is not None:
+            if max_k is None:
+                raise ValueError("cu_seqlens_k needs max_k")
+            _same("cu_seqlens_k", cu_seqlens_k, torch.int32, q.device, 1)
+            if cu_seqlens_k.shape != cu_seqlens.shape:
+                raise ValueError(f"cu_seqlens_k: {cu_seqlens_k.shape[0]} entries, expected "
+                                 f"{cu_seqlens.shape[0]}")
+            cu_k, mk = cu_seqlens_k, max_k
+        elif max_k is not None:
+            raise ValueError("max_k goes with cu_seqlens_k")
+        elif k.shape[0] != q.shape[0]:
+            raise ValueError(f"k: {k.shape[0]} tokens, expected {q.shape[0]}")
+        if not (cu_seqlens.is_contiguous() and cu_k.is_contiguous()):
+            raise ValueError("cu_seqlens must be contiguous")
+        batches = cu_seqlens.shape[0] - 1
+        if batches < 0:
+            raise ValueError("cu_seqlens: at least one entry expected")
+    _on_gpu(q)
+    return x, cu_seqlens, cu_k, (x[0].shape[0], x[1].shape[0], batches, q.shape[-2], k.shape[-2],
+                                 q.shape[-1], mq, mk)
+
+
+def _given(name, t, like, inputs):
+    """An output like ``like`` that was given, checked; or a new one."""
+    if t is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if t.shape != like.shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    if t.numel() and any(t.data_ptr() == i.data_ptr() for i in inputs):
+        raise ValueError(f"{name} must not be an input")
+    return t
+
+
+def _lse(lse, q, new):
+    if lse is None and new:
+        return torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    _same("lse", lse, torch.float32, q.device)
+    if lse.shape != q.shape[:-1] or not lse.is_contiguous():
+        raise ValueError(f"lse: contiguous {tuple(q.shape[:-1])} expected")
+    return lse
+
+
+def attention_fwd(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, max_q=None, max_k=None,
+                  scale=None, causal=True, window=0, out=None, lse=None, stream=None):
+    """Attention over whole sequences; returns (out, lse), what ``attention_bwd`` needs.
+
+    q [batch, seq, heads, head_dim] with k, v [batch, keys, kv_heads, head_dim]; or packed: q
+    [tokens, heads, head_dim] whose rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (int32) are
+    sequence b's, at most max_q each, with k and v of the same tokens or, with ``cu_seqlens_k``
+    and ``max_k``, of their own.  Views of a packed projection need no copy.  ``scale``: 1 /
+    sqrt(head_dim) by default.  ``causal``: bottom-right aligned; ``window`` > 0: only the last
+    ``window`` positions up to the query's own.  lse is fp32 [batch, seq, heads] or [tokens,
+    heads].  Both are new tensors unless given; padding rows are not written."""
+    x, cu_q, cu_k, sizes = _attention_tensors(q, k, v, cu_seqlens, cu_seqlens_k, max_q, max_k)
+    if stream is not None:
+        return _on_stream(stream, q.device, attention_fwd, q, k, v, cu_seqlens=cu_seqlens,
+                          cu_seqlens_k=cu_seqlens_k, max_q=max_q, max_k=max_k, scale=scale,
+                          causal=causal, window=window, out=out, lse=lse)
+    out = _given("out", out, q, x)
+    lse = _lse(lse, q, True)
+    o = _tokens("out", out, q)
+    qs, ks, vs, os = (t.stride() for t in (*x, o))
+    _launch("gbn_attention_fwd", G.library().gbn_attention_fwd,
+            G.attention_fwd_args(x[0].data_ptr(), x[1].data_ptr(), x[2].data_ptr(), G._addr(cu_q),
+                                 G._addr(cu_k), out.data_ptr(), lse.data_ptr(), *sizes, window,
+                                 qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1],
+                                 G.TORCH_DTYPE[q.dtype], 1 if causal else 0,
+                                 q.shape[-1] ** -0.5 if scale is None else scale),
+            q.get_device(), None)
+    return out, lse
+
+
+def attention_bwd_workspace(q, k, cu_seqlens=None):
+    """A workspace for ``attention_bwd`` calls with these q, k and cu_seqlens."""
+    _on_gpu(q)
+    tokens = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
+    batches = q.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    return torch.empty(_attention_bwd_bytes(tokens, batches, q.shape[-2], k.shape[-2],
+                                            G.TORCH_DTYPE[q.dtype]), dtype=torch.uint8,
+                       device=q.device)
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_bwd_bytes(*sizes):
+    st, n = G.gbn_attention_bwd_workspace_size(*sizes)
+    _check(st, "gbn_attention_bwd_workspace_size")
+    return n
+
+
+def attention_bwd(dout, q, k, v, out, lse, *, cu_seqlens=None, cu_seqlens_k=None, max_q=None,
+                  max_k=None, scale=None, causal=True, window=0, dq=None, dk=None, dv=None,
+                  workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of ``attention_fwd``'s inputs from ``dout``, that of its first
+    output; out and lse are its results, the other arguments its own.  The probabilities are
+    computed again.  The gradients are new tensors unless given; padding rows are not written.
+    ``workspace``: ``attention_bwd_workspace``; allocated here when needed."""
+    x, cu_q, cu_k, sizes = _attention_tensors(q, k, v, cu_seqlens, cu_seqlens_k, max_q, max_k)
+    if stream is not None:
+        return _on_stream(stream, q.device, attention_bwd, dout, q, k, v, out, lse,
+                          cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k, max_q=max_q,
+                          max_k=max_k, scale=scale, causal=causal, window=window, dq=dq, dk=dk,
+                          dv=dv, workspace=workspace)
+    for name, t in (("out", out), ("dout", dout)):
+        if t.shape != q.shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(q.shape)}")
+    x += _tokens("out", out, q), _tokens("dout", dout, q)
+    lse = _lse(lse, q, False)
+    dq, dk, dv = (_given(n, t, like, x) for n, t, like in (("dq", dq, q), ("dk", dk, k),
+                                                           ("dv", dv, v)))
+    y = tuple(_tokens(n, t, q) for n, t in (("dq", dq), ("dk", dk), ("dv", dv)))
+    dt = G.TORCH_DTYPE[q.dtype]
+    if workspace is None:
+        size = _attention_bwd_bytes(sizes[0], sizes[2], sizes[3], sizes[4], dt)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    else:
+        if workspace.device != q.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace: contiguous, on {q.device}")
+        size = workspace.numel() * workspace.element_size()
+    strides = [n for t in x + y for n in t.stride()[:2]]
+    _launch("gbn_attention_bwd", G.library().gbn_attention_bwd,
+            G.attention_bwd_args(*(t.data_ptr() for t in x), lse.data_ptr(), G._addr(cu_q),
+                                 G._addr(cu_k), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                 workspace.data_ptr(), size, *sizes, window, *strides, dt,
+                                 1 if causal else 0,
+                                 q.shape[-1] ** -0.5 if scale is None else scale),
+            q.get_device(), None)
+    return dq, dk, dv
+
+
+def _dropout_check(x, rng, out, residual=None):
+    if x.dtype not in G.TORCH_DTYPE:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    for name, t in (("x", x), ("residual", residual), ("out", out)):
+        if t is None:
+            continue
+        _same(name, t, x.dtype, x.device)
+        if t.shape != x.shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(x.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    _same("rng", rng, torch.int64, x.device, 1)
+    if rng.shape[0] != 2 or not rng.is_contiguous():
+        raise ValueError("rng: int64 [2] (seed, offset) expected")
+    _on_gpu(x)
+
+
+def _dropout(where, x, p, rng, residual, out, stream):
+    _dropout_check(x, rng, out, residual)
+    if stream is not None and out is None:
+        return _on_stream(stream, x.device, _dropout, where, x, p, rng, residual, out, None)
+    out = torch.empty_like(x) if out is None else out
+    args = (x.data_ptr(), residual.data_ptr() if residual is not None else None, out.data_ptr())
+    if where == "gbn_dropout_bwd":
+        args = args[::2]
+    fn, dt, n = getattr(G.library(), where), G.TORCH_DTYPE[x.dtype], x.numel()
+    _launch(where, lambda a, s: fn(*a, rng.data_ptr(), n, p, dt, s), args, x.get_device(), stream)
+    return out
+
+
+def dropout_fwd(x, p, rng, *, residual=None, out=None, stream=None):
+    """(kept ? x / (1 - p) : 0) + residual, the mask a function of rng = (seed, offset), an
+    int64 tensor [2] on x's device, and an element's place in x alone: it is never stored.
+    Calls that are to be independent differ in seed or offset (add 1 to the offset).  x and
+    residual are contiguous; out, a new tensor unless given, may be either."""
+    return _dropout("gbn_dropout_fwd", x, p, rng, residual, out, stream)
+
+
+def dropout_bwd(dout, p, rng, *, out=None, stream=None):
+    """Gradient of ``dropout_fwd``'s x, with the forward's p and rng (that of the residual is
+    dout itself).  out, a new tensor unless given, may be dout."""
+    return _dropout("gbn_dropout_bwd", dout, p, rng, None, out, stream)
