@@ -1,7 +1,9 @@
 // Attention over whole sequences, forward (host side; the kernel is the prompts' of
 // paged_prefill.cu) and backward.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -15,35 +17,62 @@ namespace {
 // ---- row statistics
 //
 // delta_i = dout_i.out_i for every query and head, and lse beside it in the form and order
-// that the kernels of the backward read: by head, then query.  A CTA takes 16 tokens and 32
-// heads; a row of 8 elements a lane is C lanes.  Bound by reading out and dout once.
+// that the kernels below read: by head, then query.  f16 besides: the largest squared norms of
+// dout's and v's rows (a maximum: the order does not matter).  A CTA takes 16 tokens and 32
+// heads; a row is C lanes of 8 elements.  Bound by reading out and dout once.
 constexpr int kStatTokens = 16, kStatHeads = 32, kStatThreads = 256;
 
 template <typename T, int C>
 __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const AttnBwdParams p) {
-  __shared__ float tile[kStatHeads][kStatTokens + 1];
+  constexpr bool kNorms = Elem<T>::kDt == DT_F16;
+  __shared__ float deltas[kStatHeads][kStatTokens + 1];
+  __shared__ float norms[kNorms ? 2 : 1][kStatHeads][kStatTokens + 1];  // of dout, of v
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int blocks = (p.max_q + kStatTokens - 1) / kStatTokens;  // of a sequence
+  const int longest = kNorms ? max(p.max_q, p.max_k) : p.max_q;
+  const int blocks = (longest + kStatTokens - 1) / kStatTokens;  // of a sequence
   const int b = blockIdx.x / blocks, i0 = blockIdx.x % blocks * kStatTokens, h0 = blockIdx.y * kStatHeads;
   const SeqRange s = bwd_range(p, b, tid == 0 && i0 == 0 && h0 == 0);
-  if (i0 >= s.qlen) return;
-  constexpr int kRows = 32 / C;  // rows a warp reads at once
+  const bool keys = kNorms && i0 < s.kv && h0 < p.hkv;
+  if (i0 >= s.qlen && !keys) return;
   const int c = lane % C;
-  for (int r = warp * kRows + lane / C; r < kStatTokens * kStatHeads; r += kStatThreads / 32 * kRows) {
+  auto row_sum = [&](float v) {
+#pragma unroll
+    for (int o = C / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+  };
+  constexpr int kStep = kStatThreads / C;  // rows the CTA reads at once
+#pragma unroll 4
+  for (int r = warp * (32 / C) + lane / C; r < kStatTokens * kStatHeads; r += kStep) {
     const int t = r / kStatHeads, hh = r % kStatHeads;
-    float sum = 0.f;
+    float sum = 0.f, square = 0.f, vsquare = 0.f;
     if (i0 + t < s.qlen && h0 + hh < p.hq && c * 8 < p.d) {
       const int64_t at = s.q0 + i0 + t, head = h0 + hh;
       float x[8], y[8];
       eight<T>(p.out, at * p.ot + head * p.oh + c * 8, x);
       eight<T>(p.dout, at * p.gt + head * p.gh + c * 8, y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
+      for (int e = 0; e < 8; ++e) {
+        sum = fmaf(x[e], y[e], sum);
+        square = fmaf(y[e], y[e], square);
+      }
     }
+    sum = row_sum(sum);
+    if (c == 0) deltas[hh][t] = -sum;
+    if constexpr (kNorms) {
+      if (keys && i0 + t < s.kv && h0 + hh < p.hkv && c * 8 < p.d) {
+        float y[8];
+        eight<T>(p.v, (static_cast<int64_t>(s.k0) + i0 + t) * p.vt + (h0 + hh) * p.vh + c * 8, y);
 #pragma unroll
-    for (int o = C / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (c == 0) tile[hh][t] = -sum;
+        for (int e = 0; e < 8; ++e) vsquare = fmaf(y[e], y[e], vsquare);
+      }
+      square = row_sum(square);
+      vsquare = row_sum(vsquare);
+      if (c == 0) {
+        norms[0][hh][t] = square;
+        norms[kNorms][hh][t] = vsquare;
+      }
+    }
   }
   __syncthreads();
   const int64_t base = stat_base(s.q0, b) + i0;
@@ -51,52 +80,603 @@ __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const Att
     const int t = r % kStatTokens, hh = r / kStatTokens;
     if (i0 + t >= s.qlen || h0 + hh >= p.hq) continue;
     const int64_t at = (h0 + hh) * p.stat_stride + base + t;
-    p.ndelta[at] = tile[hh][t];
+    p.ndelta[at] = deltas[hh][t];
     p.nlse[at] = fmaf(p.lse[(s.q0 + static_cast<int64_t>(i0) + t) * p.hq + h0 + hh], -kAttnLog2e,
                       static_cast<float>(kWeightLog2<T>));
   }
+  if constexpr (kNorms) {
+    if (tid < 2 * kStatHeads) {
+      const int w = tid / kStatHeads, hh = tid % kStatHeads;
+      float most = 0.f;
+#pragma unroll
+      for (int t = 0; t < kStatTokens; ++t) most = fmax_nan(most, norms[w * kNorms][hh][t]);
+      const int head = w ? h0 + hh : (h0 + hh) / p.group;
+      // (bits of numbers that are not negative order as they do, NaN above all)
+      if (head < p.hkv && most != 0.f)
+        atomicMax(p.norms + 2 * (static_cast<int64_t>(b) * p.hkv + head) + w, __float_as_uint(most) & 0x7FFFFFFFu);
+    }
+  }
 }
 
-// ---- the simplest form: a thread computes eight columns of one row
+// ---- the gradients on the tensor cores
+//
+// Both kernels hold one tile of 128 rows (x: keys for dk and dv, queries for dq) and stream
+// tiles of 128 rows of the other side (y) past it; with x1, x2 = k, v and y1, y2 = q, dout
+// (or the other way round) a step is
+//     S = x1 y1^T,  dP = x2 y2^T                    both operands in shared memory
+//     P = 2^(S scale log2(e) - lse log2(e)),  dS = P (dP - delta)
+//     acc1 += dS y1 (dk, or dq),  acc2 += P y2 (dv)   first operand in tensor memory
+// P and dS are transposed for dk and dv as they come, so neither passes through shared
+// memory: they go back into the columns of S and dP as 16-bit pairs.  One kernel for all
+// three gradients would need five products a step instead of the seven of both, but its dq
+// is a sum over CTAs: in memory, by additions in an order that changes from run to run, and
+// of as many bytes as the products read.  Two kernels add everything up in registers of the
+// tensor core, in a fixed order.
+//
+// Roles (as in the forward): warps 0-3 and 4-7 take the columns 0-63 and 64-127 of a step, a
+// thread per row; warp 8 issues the tcgen05.mma, warp 9 the TMA loads, warp 10 zeroes rows of
+// y behind the sequence.  Order of the products, so that the threads' work on one is hidden
+// behind three others (dk and dv: P beside dk and dP, dS beside dv and S) -- and with dP in
+// two buffers for dq, where tensor memory has room for it:
+//     dk, dv:  dv(i)  S(i+1)  dk(i)  dP(i+1)
+//     dq:      S(i+1)  dP(i+1)  dq(i)
+// Bound by the tensor core: 2048 (dk, dv) and 1536 (dq) cycles a step of 128 x 128 at
+// head_dim 128, shared memory busy for as long (S and dP read 128 bytes a cycle).
 
-template <typename T, int WHICH>
-__global__ void __launch_bounds__(128) attention_bwd_plain_kernel(const AttnBwdParams p) {
+struct BwdBarriers {
+  uint64_t full[8], empty[8], s_full, p_full, dp_full[2], ds_full[2], x_full, acc_full;
+  uint64_t stat_full[2], stat_empty[2], cut, zeroed;
+  uint32_t tmem;
+  int sequence;  // of this CTA
+};
+
+constexpr int kSortBatches = 256;  // up to so many sequences are taken by length
+
+template <int DP>
+struct BwdShape {
+  static constexpr int kPanel = kBwdTile * 128;  // bytes of [128][64] 16-bit elements
+  static constexpr int kPanels = DP / 64;
+  static constexpr int kSlot = kPanels * kPanel;
+  static constexpr int kSlots = DP == 128 ? 5 : 8;  // y1 and y2 alternate
+  static constexpr int kStats = 2 * kSlot + kSlots * kSlot;  // then -lse and -delta, two stages
+  static constexpr int kStat = kBwdTile * 4;
+  static constexpr int kBody = kStats + 4 * kStat;
+  static constexpr int kSmem = kBody + (int)sizeof(BwdBarriers);
+  static_assert(kSmem <= 232448 && kSlots <= 8, "");
+  static constexpr int kThreads = 384;
+  // 256 x softmax + 128 x other = threads x launch, exactly.
+  static constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
+  static_assert(256 * kRegsSoftmax + 128 * kRegsOther == kThreads * kRegsLaunch, "");
+};
+constexpr int kBwdMmaWarp = 8, kBwdLoadWarp = 9, kBwdZeroWarp = 10;
+
+// What f16 ds is taken larger by: a power of two u with u |dout_i| |v_j| 2 < 2^15 for every
+// pair of the sequence and kv head (|ds| <= |dp| + |delta|, and |delta| is a mean of dp).  ds
+// falls with the number of keys and f16 ends early: without it, gradients of long
+// sequences would be sums of numbers without bits.
+template <typename T>
+__device__ __forceinline__ float ds_factor(const AttnBwdParams& p, int b, int h) {
+  if constexpr (Elem<T>::kDt != DT_F16) return 1.f;
+  const uint32_t* m = p.norms + 2 * (static_cast<int64_t>(b) * p.hkv + h);
+  const float most = 2.f * sqrtf(__uint_as_float(m[0])) * sqrtf(__uint_as_float(m[1]));
+  if (!(most > 0.f) || !(most < INFINITY)) return 1.f;
+  const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 100);
+  return __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+}
+
+template <typename T, int DP, bool KV>
+__global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
+    attention_bwd_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ CUtensorMap x1map,
+                         const __grid_constant__ CUtensorMap x2map,
+                         const __grid_constant__ CUtensorMap y1map,
+                         const __grid_constant__ CUtensorMap y2map) {
+  using Shape = BwdShape<DP>;
+  constexpr int kType = std::is_same<T, __half>::value ? 0 : 1;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  BwdBarriers& bars = *reinterpret_cast<BwdBarriers*>(raw + Shape::kBody);
+
   pdl_begin();
-  const int b = blockIdx.z, head = blockIdx.y, h = WHICH ? head : head / p.group;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // The longest work first: sequences by their pairs, causal keys from the first on (the most
+  // queries see those), queries from the last.
+  uint32_t bx = blockIdx.x;
+  const int heads = KV ? p.hkv : p.hq, x_tiles = KV ? p.k_tiles : p.q_tiles;
+  const int xh = bx % heads;
+  bx /= heads;
+  const int xt = KV ? bx % x_tiles : x_tiles - 1 - static_cast<int>(bx % x_tiles);
+  int b = bx / x_tiles;
+  if (p.batches > 1 && p.batches <= kSortBatches && (p.cu || p.cu_k)) {
+    auto pairs_of = [&](int i) {
+      return static_cast<float>(p.cu ? p.cu[i + 1] - p.cu[i] : p.max_q) *
+             static_cast<float>(p.cu_k ? p.cu_k[i + 1] - p.cu_k[i] : p.max_k);
+    };
+    for (int i = tid; i < p.batches; i += Shape::kThreads) {
+      const float mine = pairs_of(i);
+      int before = 0;
+#pragma unroll 8
+      for (int j = 0; j < p.batches; ++j) {
+        const float other = pairs_of(j);
+        before += other > mine || (other == mine && j < i);
+      }
+      if (before == b) bars.sequence = i;
+    }
+    __syncthreads();
+    b = bars.sequence;
+  }
   const SeqRange s = bwd_range(p, b, false);
-  const int n = WHICH ? s.kv : s.qlen, chunks = p.d / 8;
-  const int64_t x = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
-  const int row = static_cast<int>(x / chunks), col = static_cast<int>(x % chunks) * 8;
-  if (row >= n) return;
-  float f[8];
-  grad_again<T, WHICH>(p, s, b, head, h, row, col, f);
-  T* dst = static_cast<T*>(WHICH == 0 ? p.dq : WHICH == 1 ? p.dk : p.dv);
-  const int64_t at = WHICH == 0   ? (s.q0 + static_cast<int64_t>(row)) * p.dqt + head * p.dqh
-                     : WHICH == 1 ? (s.k0 + static_cast<int64_t>(row)) * p.dkt + h * p.dkh
-                                  : (s.k0 + static_cast<int64_t>(row)) * p.dvt + h * p.dvh;
-  uint32_t w[4];
+  const int nx = KV ? s.kv : s.qlen, ny = KV ? s.qlen : s.kv, x0 = xt * kBwdTile;
+  const int rows = min(kBwdTile, nx - x0);
+  if (rows <= 0) return;
+  const int h = KV ? xh : xh / p.group;  // kv head
+
+  // Rows of y that some row of x goes with, [y_lo, y_hi), in tiles from `base` on; for dk
+  // and dv once for every head of the group.
+  const int y_lo = KV ? query_first(p, s, x0) : key_first(p, s, x0);
+  const int y_hi = KV ? query_end(p, s, x0 + rows - 1) : key_end(p, s, x0 + rows - 1);
+  const int base = y_lo & ~(kBwdTile - 1);
+  const int nt = y_hi > y_lo ? (y_hi - base + kBwdTile - 1) / kBwdTile : 0;
+  const int n = nt * (KV ? p.group : 1);
+  // The last tile reaches beyond the sequence.
+  const bool cut_last = base + nt * kBwdTile > ny;
+
+  const uint32_t xs = smem_u32(raw), ring = xs + 2 * Shape::kSlot;
+  if (xs & 1023u) {  // the swizzle goes by address bits; the compiler's alignment holds
+    if (tid == 0) flag_wait_timeout();
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < Shape::kSlots; ++i) {
+      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.empty[i], 1);
+    }
+    mbar_init(&bars.s_full, 1);
+    mbar_init(&bars.p_full, 8);  // one arrival per warp
+    mbar_init(&bars.x_full, 1);
+    mbar_init(&bars.acc_full, 1);
+    mbar_init(&bars.cut, 1);
+    mbar_init(&bars.zeroed, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.dp_full[i], 1);
+      mbar_init(&bars.ds_full[i], 8);
+      mbar_init(&bars.stat_full[i], 1);
+      mbar_init(&bars.stat_empty[i], 8);
+    }
+    fence_mbar_init();
+  }
+  if (warp == kBwdMmaWarp) tc_alloc(&bars.tmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  constexpr uint32_t kDp = 128, kAcc1 = KV ? 256 + DP : 384, kAcc2 = 256;  // columns (S: 0)
+  bool ok = true;
+
+  if (warp >= kBwdMmaWarp) {
+    set_regs_dec<Shape::kRegsOther>();
+    if (warp == kBwdMmaWarp) {
+      // ------------------------------------------------ tensor core issue
+      constexpr uint32_t kIdXY = instr_desc(kType, kBwdTile, kBwdTile, 0);
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      const uint32_t x_lo = __shfl_sync(0xFFFFFFFFu, desc_lo(xs, 16), 0);
+      const uint32_t k_lo = __shfl_sync(0xFFFFFFFFu, desc_lo(ring, 16), 0);
+      const uint32_t mn_lo = __shfl_sync(0xFFFFFFFFu, desc_lo(ring, Shape::kPanel), 0);
+      const int steps = __shfl_sync(0xFFFFFFFFu, (p.d + 15) / 16, 0);  // of 16 elements of a head
+      const uint32_t id_acc = instr_desc(kType, kBwdTile, 16 * steps, 1);
+      if (lane == 0 && n > 0) {
+        // D = x_i y^T
+        auto product = [&](int which, int slot, uint32_t to) {
+          const uint32_t xt_lo = x_lo + which * (Shape::kSlot >> 4);
+          const uint32_t y_lo2 = k_lo + slot * (Shape::kSlot >> 4);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = narrow2<T>(p2(f[2 * e], f[2 * e + 1]));
-  *reinterpret_cast<uint4*>(dst + at + col) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int kk = 0; kk < DP / 16; ++kk) {
+            if (kk >= steps) break;
+            const uint32_t at = ((kk / 4) * Shape::kPanel + (kk % 4) * 32) >> 4;
+            tc_mma_ss(to, xt_lo + at, y_lo2 + at, kDescHi, kIdXY, kk > 0);
+          }
+        };
+        // D += (16-bit pairs in tensor memory) y
+        auto add = [&](uint32_t from, int slot, uint32_t to, bool more) {
+          const uint32_t y = mn_lo + slot * (Shape::kSlot >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kBwdTile / 16; ++kk)
+            tc_mma_ts(to, from + (kk >> 2) * 64 + (kk & 3) * 8, y + kk * (2048 >> 4), kDescHi, id_acc,
+                      kk > 0 ? 1u : static_cast<uint32_t>(more));
+        };
+        // The next tile of the ring: waits until it is there, rows behind the sequence zeroed
+        // (a weight of 0 times what stands there must be 0; v is never weighed for dq).
+        int slot = 0, left = nt;  // tiles up to the end of the sequence
+        uint32_t phase = 0, zeros = 0;
+        auto next = [&](int which) {
+          const int at = slot;
+          ok = ok && mbar_wait(&bars.full[at], phase);
+          if (which == 0) --left;
+          if (ok && cut_last && left == 0 && (KV || which == 0)) {
+            mbar_arrive(&bars.cut);
+            ok = mbar_wait(&bars.zeroed, zeros++ & 1);
+          }
+          if (which == 1 && left == 0) left = nt;
+          if (++slot == Shape::kSlots) slot = 0, phase ^= 1;
+          return at;
+        };
+        ok = mbar_wait(&bars.x_full, 0);
+        int y1 = next(0), y2 = y1;
+        if (ok) {
+          tc_fence_after();
+          product(0, y1, tm);
+          tc_commit(&bars.s_full);
+          y2 = next(1);
+        }
+        if (ok) {
+          tc_fence_after();
+          product(1, y2, tm + kDp);
+          tc_commit(&bars.dp_full[0]);
+          if (!KV) tc_commit(&bars.empty[y2]);
+        }
+        for (int i = 0; ok && i < n; ++i) {
+          const bool more = i + 1 < n;
+          int z1 = y1, z2 = y2;
+          if constexpr (KV) {
+            ok = mbar_wait(&bars.p_full, i & 1);
+            if (!ok) break;
+            tc_fence_after();
+            add(tm, y2, tm + kAcc2, i > 0);
+            tc_commit(&bars.empty[y2]);
+            if (more) {
+              z1 = next(0);
+              if (!ok) break;
+              tc_fence_after();
+              product(0, z1, tm);
+              tc_commit(&bars.s_full);
+            }
+            ok = mbar_wait(&bars.ds_full[0], i & 1);
+            if (!ok) break;
+            tc_fence_after();
+            add(tm + kDp, y1, tm + kAcc1, i > 0);
+            tc_commit(&bars.empty[y1]);
+            if (more) {
+              z2 = next(1);
+              if (!ok) break;
+              tc_fence_after();
+              product(1, z2, tm + kDp);
+              tc_commit(&bars.dp_full[0]);
+            }
+          } else {
+            if (more) {
+              ok = mbar_wait(&bars.p_full, i & 1);
+              z1 = next(0);
+              if (!ok) break;
+              tc_fence_after();
+              product(0, z1, tm);
+              tc_commit(&bars.s_full);
+              z2 = next(1);
+              if (!ok) break;
+              tc_fence_after();
+              product(1, z2, tm + kDp + ((i + 1) & 1) * 128);
+              tc_commit(&bars.dp_full[(i + 1) & 1]);
+              tc_commit(&bars.empty[z2]);
+            }
+            ok = mbar_wait(&bars.ds_full[i & 1], (i >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            add(tm + kDp + (i & 1) * 128, y1, tm + kAcc1, i > 0);
+            tc_commit(&bars.empty[y1]);
+          }
+          y1 = z1;
+          y2 = z2;
+        }
+        if (ok) {
+          tc_commit(&bars.acc_full);
+          // The last arrivals have landed before the CTA ends.
+          ok = mbar_wait(&bars.empty[y1], ((2 * n - 2) / Shape::kSlots) & 1) &&
+               mbar_wait(&bars.empty[y2], ((2 * n - 1) / Shape::kSlots) & 1);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kBwdLoadWarp) {
+      // ------------------------------------------------ TMA loads
+      if (lane == 0 && n > 0) {
+        auto tile = [&](uint32_t dst, const CUtensorMap* map, int head, int row, uint64_t* bar) {
+#pragma unroll
+          for (int pn = 0; pn < Shape::kPanels; ++pn)
+            tma_box(dst + pn * Shape::kPanel, map, pn * 64, head, row, 0, bar);
+        };
+        mbar_arrive_expect_tx(&bars.x_full, 2 * Shape::kSlot);
+        const int xr = (KV ? s.k0 : s.q0) + x0;
+        tile(xs, &x1map, xh, xr, &bars.x_full);
+        tile(xs + Shape::kSlot, &x2map, xh, xr, &bars.x_full);
+        const int64_t stat = stat_base(s.q0, b) + base;
+        int slot = 0, issued = 0, t = 0, g = 0, i = 0;
+        uint32_t phase = 0;
+        for (; ok && i < n; ++i) {
+          const int yr = (KV ? s.q0 : s.k0) + base + t * kBwdTile;
+          const int yh = KV ? h * p.group + g : h;
+          for (int w = 0; ok && w < 2; ++w) {
+            if (issued >= Shape::kSlots) ok = mbar_wait(&bars.empty[slot], phase ^ 1);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&bars.full[slot], Shape::kSlot);
+            tile(ring + slot * Shape::kSlot, w ? &y2map : &y1map, yh, yr, &bars.full[slot]);
+            ++issued;
+            if (++slot == Shape::kSlots) slot = 0, phase ^= 1;
+            if (KV && w == 0) {
+              const int st = i & 1;
+              if (i >= 2) ok = mbar_wait(&bars.stat_empty[st], ((i >> 1) - 1) & 1);
+              if (!ok) break;
+              mbar_arrive_expect_tx(&bars.stat_full[st], 2 * Shape::kStat);
+              uint8_t* dst = raw + Shape::kStats + st * 2 * Shape::kStat;
+              const int64_t from = yh * p.stat_stride + stat + t * kBwdTile;
+              bulk_g2s(dst, p.nlse + from, Shape::kStat, &bars.stat_full[st]);
+              bulk_g2s(dst + Shape::kStat, p.ndelta + from, Shape::kStat, &bars.stat_full[st]);
+            }
+          }
+          if (++t == nt) t = 0, ++g;
+        }
+        if (!ok) {
+          // Leave no copy in flight behind.
+          mbar_wait(&bars.x_full, 0);
+          for (int j = max(0, issued - Shape::kSlots); j < issued; ++j)
+            mbar_wait(&bars.full[j % Shape::kSlots], (j / Shape::kSlots) & 1);
+          if (KV)
+            for (int j = max(0, i - 2); j < i; ++j) mbar_wait(&bars.stat_full[j & 1], (j >> 1) & 1);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kBwdZeroWarp && cut_last) {
+      // ------------------------------------------------ rows of y behind the sequence
+      const int events = KV ? 2 * p.group : 1;
+      const int from = ny - (base + (nt - 1) * kBwdTile);  // first row to zero of the last tile
+      for (int e = 0; ok && e < events; ++e) {
+        // (a whole range may lie before the last tile's turn: a longer limit)
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(&bars.cut, e & 1, 30 * kWaitLimitNs));
+        if (!ok) break;
+        const int64_t tile = KV ? 2 * (static_cast<int64_t>(e >> 1) * nt + nt - 1) + (e & 1)
+                                : 2 * static_cast<int64_t>(nt - 1);
+        uint8_t* at = raw + (2 + static_cast<int>(tile % Shape::kSlots)) * Shape::kSlot;
+        for (int j = lane; j < (kBwdTile - from) * 8 * Shape::kPanels; j += 32)
+          *reinterpret_cast<uint4*>(at + (j >> 3) % Shape::kPanels * Shape::kPanel +
+                                    (from + (j >> 3) / Shape::kPanels) * 128 + (j & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.zeroed);
+      }
+    }
+  } else {
+    // -------------------------------------------------- probabilities and their gradients
+    set_regs_inc<Shape::kRegsSoftmax>();
+    const int w = warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane, x = x0 + r;
+    const bool live = r < rows;
+    // The rows of y that this thread's row goes with.
+    const int lo = !live ? 0 : KV ? query_first(p, s, x) : key_first(p, s, x);
+    const int hi = !live ? 0 : KV ? query_end(p, s, x) : key_end(p, s, x);
+    const float up = ds_factor<T>(p, b, h);
+    const uint64_t sc2 = p2(p.scale_log2, p.scale_log2);
+    const float back = ex2(-static_cast<float>(kWeightLog2<T>));  // P is 2^kWeightLog2 larger
+    const uint64_t up2 = p2(up * back, up * back);
+    uint64_t nl2 = 0, nd2 = 0;  // dq: the row's own
+    if (!KV && live) {
+      const int64_t at = xh * p.stat_stride + stat_base(s.q0, b) + x;
+      nl2 = p2(p.nlse[at], p.nlse[at]);
+      nd2 = p2(p.ndelta[at], p.ndelta[at]);
+    }
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t ts = tmem + lanes + w * 64;  // this warp's half of S
+    int t = 0;
+    for (int i = 0; i < n; ++i) {
+      const ulonglong2* stat =
+          reinterpret_cast<const ulonglong2*>(raw + Shape::kStats + (i & 1) * 2 * Shape::kStat + w * 256);
+      ok = warp_wait(&bars.s_full, i & 1);
+      if (KV) ok = ok && warp_wait(&bars.stat_full[i & 1], (i >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sc[64];
+      tc_ld32(ts, sc);
+      tc_ld32(ts + 32, sc + 32);
+      tc_wait_ld<64>(sc);
+      if constexpr (!KV) {  // S is free again
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full);
+      }
+      const int tb = base + t * kBwdTile + w * 64;
+      if (++t == nt) t = 0;
+      const bool cut = __any_sync(0xFFFFFFFFu, tb < lo || tb + 64 > hi);
+      // Bit e: row tb + e of y is kept.
+      const uint64_t kept = low_bits(hi - tb) & ~low_bits(lo - tb);
+      const uint32_t kept_lo = static_cast<uint32_t>(kept), kept_hi = static_cast<uint32_t>(kept >> 32);
+      uint64_t pr[32];
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        ulonglong2 nl = make_ulonglong2(nl2, nl2);
+        if (KV) nl = stat[e / 2];
+        const float2 a = u2(fma2(p2(__uint_as_float(sc[2 * e]), __uint_as_float(sc[2 * e + 1])), sc2, nl.x));
+        const float2 c = u2(fma2(p2(__uint_as_float(sc[2 * e + 2]), __uint_as_float(sc[2 * e + 3])), sc2, nl.y));
+        pr[e] = p2(ex2(a.x), ex2(a.y));
+        pr[e + 1] = p2(ex2(c.x), ex2(c.y));
+      }
+      if (cut) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const uint32_t bits = e < 16 ? kept_lo >> (2 * e) : kept_hi >> (2 * e - 32);
+          const float2 a = u2(pr[e]);
+          pr[e] = p2(bits & 1u ? a.x : 0.f, bits & 2u ? a.y : 0.f);
+        }
+      }
+      uint32_t pk[32];
+      if constexpr (KV) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) pk[e] = narrow2<T>(pr[e]);
+        tc_st32(ts, pk);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full);
+      }
+      const int buf = KV ? 0 : i & 1;
+      ok = warp_wait(&bars.dp_full[buf], KV ? i & 1 : (i >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t td = ts + kDp + buf * 128;
+      tc_ld32(td, sc);
+      tc_ld32(td + 32, sc + 32);
+      tc_wait_ld<64>(sc);
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        ulonglong2 nd = make_ulonglong2(nd2, nd2);
+        if (KV) nd = stat[Shape::kStat / 16 + e / 2];
+        uint64_t a = add2(p2(__uint_as_float(sc[2 * e]), __uint_as_float(sc[2 * e + 1])), nd.x);
+        uint64_t c = add2(p2(__uint_as_float(sc[2 * e + 2]), __uint_as_float(sc[2 * e + 3])), nd.y);
+        if constexpr (kType == 0) {
+          a = mul2(a, up2);
+          c = mul2(c, up2);
+        }
+        pk[e] = narrow2<T>(mul2(a, pr[e]));
+        pk[e + 1] = narrow2<T>(mul2(c, pr[e + 1]));
+      }
+      if (cut) {
+        // (0 times an infinity or NaN of a pair that is not kept)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const uint32_t bits = e < 16 ? kept_lo >> (2 * e) : kept_hi >> (2 * e - 32);
+          pk[e] &= (bits & 1u ? 0xFFFFu : 0u) | (bits & 2u ? 0xFFFF0000u : 0u);
+        }
+      }
+      tc_st32(td, pk);
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bars.ds_full[buf]);
+        if (KV) mbar_arrive(&bars.stat_empty[i & 1]);
+      }
+    }
+    // Output: dv by the warps 0-3, dk by 4-7; or half of dq's columns by each.
+    if (ok && n > 0) {
+      ok = warp_wait(&bars.acc_full, 0);
+      tc_fence_after();
+    }
+    if (ok) {
+      constexpr int kCols = KV ? DP : DP / 2;
+      const int col0 = KV ? 0 : w * kCols;
+      const uint32_t from = tmem + lanes + (KV && w == 0 ? kAcc2 : kAcc1 + col0);
+      const float factor = KV && w == 0 ? back : p.scale / up;
+      T* const dst = static_cast<T*>(KV ? (w == 0 ? p.dv : p.dk) : p.dq);
+      const int64_t row = (KV ? s.k0 : s.q0) + static_cast<int64_t>(x);
+      const int64_t at = KV ? (w == 0 ? row * p.dvt + xh * p.dvh : row * p.dkt + xh * p.dkh)
+                            : row * p.dqt + xh * p.dqh;
+      const uint32_t some = __ballot_sync(0xFFFFFFFFu, live);
+      // Next to pairs of its tiles that it dropped.
+      const bool dropped = live && n > 0 && (lo > base || hi < min(base + nt * kBwdTile, ny));
+      // Through shared memory (x is used up), so that a store writes whole sectors.
+      uint8_t* const stage = raw + warp * 32 * 64;
+#pragma unroll 1
+      for (int c = 0; c < kCols && col0 + c < p.d; c += 32) {
+        uint32_t o[32];
+        if (n > 0) {
+          tc_ld32(from + c, o);
+          tc_wait_ld<32>(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        uint32_t bad = 0;  // bit e: a NaN in columns 8 e .. 8 e + 7
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          float f = __uint_as_float(o[e]);
+#pragma unroll
+          for (int q = 1; q < 7; q += 2)
+            f = max3_nan(f, __uint_as_float(o[e + q]), __uint_as_float(o[e + q + 1]));
+          f = max3_nan(f, f, __uint_as_float(o[e + 7]));
+          bad |= f != f ? 1u << (e / 8) : 0u;
+        }
+        auto put = [&](int e, const uint32_t* v) {
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(v[0], v[1], v[2], v[3]);
+        };
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            v[q] = narrow2<T>(mul2(p2(__uint_as_float(o[8 * e + 2 * q]), __uint_as_float(o[8 * e + 2 * q + 1])),
+                                   p2(factor, factor)));
+          put(e, v);
+        }
+        if (bad && dropped) {
+#pragma unroll 1
+          for (int e = 0; e < 4; ++e) {
+            if (!(bad & (1u << e)) || col0 + c + 8 * e >= p.d) continue;
+            float f[8];
+            if (!KV) grad_again<T, 0>(p, s, b, xh, h, x, col0 + c + 8 * e, f);
+            else if (w == 0) grad_again<T, 2>(p, s, b, 0, h, x, c + 8 * e, f);
+            else grad_again<T, 1>(p, s, b, 0, h, x, c + 8 * e, f);
+            uint32_t v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = narrow2<T>(p2(f[2 * q], f[2 * q + 1]));
+            put(e, v);
+          }
+        }
+        __syncwarp();
+        const int e = lane & 3;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int rr = q * 8 + (lane >> 2);
+          const int64_t to = __shfl_sync(0xFFFFFFFFu, at, rr);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((e ^ ((rr >> 1) & 3)) << 4));
+          if (((some >> rr) & 1) && col0 + c + 8 * e < p.d)
+            *reinterpret_cast<uint4*>(dst + to + col0 + c + 8 * e) = v;
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  if (!ok && lane == 0) flag_wait_timeout();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kBwdMmaWarp) tc_dealloc(tmem);
+}
+
+template <typename T, int DP, bool KV>
+cudaError_t launch_tiles(const AttnBwdParams& p, const CUtensorMap* m, cudaStream_t st) {
+  auto k = attention_bwd_kernel<T, DP, KV>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(k, BwdShape<DP>::kSmem, done);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = KV ? int64_t(p.k_tiles) * p.batches * p.hkv : int64_t(p.q_tiles) * p.batches * p.hq;
+  if (grid == 0) return cudaSuccess;
+  const dim3 g(static_cast<unsigned>(grid)), t(BwdShape<DP>::kThreads);
+  // m: q, k, v, dout
+  return KV ? launch_pdl(k, g, t, BwdShape<DP>::kSmem, st, p, m[1], m[2], m[0], m[3])
+            : launch_pdl(k, g, t, BwdShape<DP>::kSmem, st, p, m[0], m[3], m[1], m[2]);
 }
 
 template <typename T>
 cudaError_t launch_bwd(const AttnBwdParams& p, cudaStream_t st) {
-  const dim3 sg((p.max_q + kStatTokens - 1) / kStatTokens * p.batches, (p.hq + kStatHeads - 1) / kStatHeads);
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   cudaError_t e = cudaSuccess;
-  if (p.max_q > 0) {
-    e = p.d <= 64 ? launch_pdl(attention_stats_kernel<T, 8>, sg, dim3(kStatThreads), 0, st, p)
-                  : launch_pdl(attention_stats_kernel<T, 16>, sg, dim3(kStatThreads), 0, st, p);
-    if (e != cudaSuccess) return e;
-    const unsigned nq = (p.max_q * (p.d / 8) + 127) / 128;
-    e = launch_pdl(attention_bwd_plain_kernel<T, 0>, dim3(nq, p.hq, p.batches), dim3(128), 0, st, p);
+  if (!kBf16) {
+    e = cudaMemsetAsync(p.norms, 0, static_cast<size_t>(p.batches) * p.hkv * 8, st);
     if (e != cudaSuccess) return e;
   }
-  if (p.max_k == 0) return e;
-  const unsigned nk = (p.max_k * (p.d / 8) + 127) / 128;
-  e = launch_pdl(attention_bwd_plain_kernel<T, 1>, dim3(nk, p.hkv, p.batches), dim3(128), 0, st, p);
+  const int longest = kBf16 || p.max_q > p.max_k ? p.max_q : p.max_k;
+  if (longest > 0) {
+    const dim3 g(static_cast<unsigned>((longest + kStatTokens - 1) / kStatTokens) * p.batches,
+                 (p.hq + kStatHeads - 1) / kStatHeads);
+    e = p.d <= 64 ? launch_pdl(attention_stats_kernel<T, 8>, g, dim3(kStatThreads), 0, st, p)
+                  : launch_pdl(attention_stats_kernel<T, 16>, g, dim3(kStatThreads), 0, st, p);
+    if (e != cudaSuccess) return e;
+  }
+  CUtensorMap m[4] = {};
+  if (!make_packed_map(&m[0], p.q, kBf16, p.d, p.hq, p.tokens, p.qt, p.qh, kBwdTile) ||
+      !make_packed_map(&m[1], p.k, kBf16, p.d, p.hkv, p.keys, p.kt, p.kh, kBwdTile) ||
+      !make_packed_map(&m[2], p.v, kBf16, p.d, p.hkv, p.keys, p.vt, p.vh, kBwdTile) ||
+      !make_packed_map(&m[3], p.dout, kBf16, p.d, p.hq, p.tokens, p.gt, p.gh, kBwdTile))
+    return cudaErrorInvalidValue;
+  e = p.d <= 64 ? launch_tiles<T, 64, true>(p, m, st) : launch_tiles<T, 128, true>(p, m, st);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attention_bwd_plain_kernel<T, 2>, dim3(nk, p.hkv, p.batches), dim3(128), 0, st, p);
+  return p.d <= 64 ? launch_tiles<T, 64, false>(p, m, st) : launch_tiles<T, 128, false>(p, m, st);
 }
 
 // ---- host side
@@ -250,11 +830,12 @@ gbn_status gbn_attention_bwd(const gbn_attention_bwd_args* args, cudaStream_t st
     return GBN_ERR_WORKSPACE;
 
   AttnBwdParams p = {};
-  p.q = c.q;
-  p.k = c.k;
-  p.v = c.v;
+  // (no queries or no keys: nothing of them is read, but the maps need an address)
+  p.q = z.tokens > 0 ? c.q : c.k;
+  p.k = z.keys > 0 ? c.k : c.q;
+  p.v = z.keys > 0 ? c.v : c.q;
   p.out = c.out;
-  p.dout = c.dout;
+  p.dout = z.tokens > 0 ? c.dout : c.k;
   p.lse = c.lse;
   p.cu = c.cu_q;
   p.cu_k = c.cu_k;
@@ -292,6 +873,11 @@ gbn_status gbn_attention_bwd(const gbn_attention_bwd_args* args, cudaStream_t st
   p.max_k = static_cast<int>(z.max_k < z.keys ? z.max_k : z.keys);
   p.causal = c.causal != 0;
   p.window = static_cast<int>(z.window);
+  p.q_tiles = static_cast<int>(tiles(p.max_q, kBwdTile));
+  p.k_tiles = static_cast<int>(tiles(p.max_k, kBwdTile));
+  if (p.q_tiles * z.batches * z.q_heads > INT32_MAX || p.k_tiles * z.batches * z.kv_heads > INT32_MAX ||
+      tiles(p.max_q > p.max_k ? p.max_q : p.max_k, kStatTokens) * z.batches > INT32_MAX)
+    return GBN_ERR_SHAPE;
   p.scale = c.scale;
   p.scale_log2 = c.scale * kAttnLog2e;
   const cudaError_t e = dtype == GBN_BF16 ? launch_bwd<__nv_bfloat16>(p, stream)

@@ -183,7 +183,8 @@ inline bool make_packed_map(CUtensorMap* map, const void* base, bool bf16, int d
                             int64_t token_stride, int64_t head_stride, int rows) {
   EncodeFn enc = encoder();
   if (!enc) return false;
-  const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(tokens), 1};
+  const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(heads),
+                              cuuint64_t(tokens > 0 ? tokens : 1), 1};
   // Dimensions of one element may have any stride: give those a valid one.
   const cuuint64_t strides[3] = {heads > 1 ? cuuint64_t(head_stride) * 2 : 16,
                                  tokens > 1 ? cuuint64_t(token_stride) * 2 : 16, 16};
