@@ -114,18 +114,19 @@ __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const Att
 // tensor core, in a fixed order.
 //
 // Roles (as in the forward): warps 0-3 and 4-7 take the columns 0-63 and 64-127 of a step, a
-// thread per row; warp 8 issues the tcgen05.mma, warp 9 the TMA loads, warp 10 zeroes rows of
-// y behind the sequence.  Order of the products, so that the threads' work on one is hidden
-// behind three others (dk and dv: P beside dk and dP, dS beside dv and S) -- and with dP in
-// two buffers for dq, where tensor memory has room for it:
-//     dk, dv:  dv(i)  S(i+1)  dk(i)  dP(i+1)
-//     dq:      S(i+1)  dP(i+1)  dq(i)
+// thread per row; warps 8 and 9 issue the tcgen05.mma (one thread each), warp 10 the TMA
+// loads, warp 11 zeroes rows of y behind the sequence.  Order of the products, so that the
+// threads' work on one is hidden behind the next ones:
+//     dk, dv:  dv(i)  S(i+1)  |  dk(i)  dP(i+1)
+//     dq:      S(i+1)  |  dq(i)  dP(i+1)
+// x goes to tensor memory too where there is room (for dq, and at head_dim 64): a product
+// reads 64 bytes of shared memory a cycle then instead of 128, all there are.
 // Bound by the tensor core: 2048 (dk, dv) and 1536 (dq) cycles a step of 128 x 128 at
-// head_dim 128, shared memory busy for as long (S and dP read 128 bytes a cycle).
+// head_dim 128.
 
 struct BwdBarriers {
-  uint64_t full[8], empty[8], s_full, p_full, dp_full[2], ds_full[2], x_full, acc_full;
-  uint64_t stat_full[2], stat_empty[2], cut, zeroed;
+  uint64_t full[8], empty[8], s_full, p_full, dp_full, ds_full, x_full, x_ready, acc_full;
+  uint64_t turn[2], stat_full[2], stat_empty[2], cut[2], zeroed[2];
   uint32_t tmem;
   int sequence;  // of this CTA
 };
@@ -148,7 +149,7 @@ struct BwdShape {
   static constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
   static_assert(256 * kRegsSoftmax + 128 * kRegsOther == kThreads * kRegsLaunch, "");
 };
-constexpr int kBwdMmaWarp = 8, kBwdLoadWarp = 9, kBwdZeroWarp = 10;
+constexpr int kBwdMmaWarp = 8, kBwdMmaWarp2 = 9, kBwdLoadWarp = 10, kBwdZeroWarp = 11;
 
 // What f16 ds is taken larger by: a power of two u with u |dout_i| |v_j| 2 < 2^15 for every
 // pair of the sequence and kv head (|ds| <= |dp| + |delta|, and |delta| is a mean of dp).  ds
@@ -227,17 +228,19 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < Shape::kSlots; ++i) {
       mbar_init(&bars.full[i], 1);
-      mbar_init(&bars.empty[i], 1);
+      mbar_init(&bars.empty[i], 2);  // one arrival for each of the threads that issue
     }
     mbar_init(&bars.s_full, 1);
     mbar_init(&bars.p_full, 8);  // one arrival per warp
     mbar_init(&bars.x_full, 1);
-    mbar_init(&bars.acc_full, 1);
-    mbar_init(&bars.cut, 1);
-    mbar_init(&bars.zeroed, 1);
+    mbar_init(&bars.x_ready, 8);
+    mbar_init(&bars.dp_full, 1);
+    mbar_init(&bars.ds_full, 8);
+    mbar_init(&bars.acc_full, 2);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.dp_full[i], 1);
-      mbar_init(&bars.ds_full[i], 8);
+      mbar_init(&bars.turn[i], 1);
+      mbar_init(&bars.cut[i], 1);
+      mbar_init(&bars.zeroed[i], 1);
       mbar_init(&bars.stat_full[i], 1);
       mbar_init(&bars.stat_empty[i], 8);
     }
@@ -248,127 +251,116 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
-  constexpr uint32_t kDp = 128, kAcc1 = KV ? 256 + DP : 384, kAcc2 = 256;  // columns (S: 0)
+  // Columns (S: 0).  x as the products' first operand, 16-bit pairs: not for dk and dv at 128.
+  constexpr uint32_t kDp = 128, kAcc2 = 256, kAcc1 = KV ? 256 + DP : 256, kX = 384;
+  constexpr bool kXInTmem = !KV || DP == 64;
+  static_assert(kAcc1 + DP <= (kXInTmem ? kX : kTmemCols), "");
   bool ok = true;
 
   if (warp >= kBwdMmaWarp) {
     set_regs_dec<Shape::kRegsOther>();
-    if (warp == kBwdMmaWarp) {
+    if (warp == kBwdMmaWarp || warp == kBwdMmaWarp2) {
       // ------------------------------------------------ tensor core issue
       constexpr uint32_t kIdXY = instr_desc(kType, kBwdTile, kBwdTile, 0);
+      const bool first = warp == kBwdMmaWarp;  // the one of S (and dv), else of dP and acc1
       const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-      const uint32_t x_lo = __shfl_sync(0xFFFFFFFFu, desc_lo(xs, 16), 0);
+      const uint32_t x_lo = __shfl_sync(0xFFFFFFFFu, desc_lo(xs + (first ? 0 : Shape::kSlot), 16), 0);
       const uint32_t k_lo = __shfl_sync(0xFFFFFFFFu, desc_lo(ring, 16), 0);
       const uint32_t mn_lo = __shfl_sync(0xFFFFFFFFu, desc_lo(ring, Shape::kPanel), 0);
       const int steps = __shfl_sync(0xFFFFFFFFu, (p.d + 15) / 16, 0);  // of 16 elements of a head
       const uint32_t id_acc = instr_desc(kType, kBwdTile, 16 * steps, 1);
-      if (lane == 0 && n > 0) {
-        // D = x_i y^T
-        auto product = [&](int which, int slot, uint32_t to) {
-          const uint32_t xt_lo = x_lo + which * (Shape::kSlot >> 4);
-          const uint32_t y_lo2 = k_lo + slot * (Shape::kSlot >> 4);
+      // The tensor core's queue is short: a thread that waits on a barrier between two
+      // products, also on a complete one (100 cycles), leaves it idle.  So two threads issue,
+      // and each waits while the other's products run.  They take turns: turn i of the
+      // first one is dv(i - 1), S(i), of the second dk or dq(i - 1), dP(i); a turn passes two
+      // instructions before its end, so that it arrives in time.
+      if (n > 0 && elect_one()) {
+        uint64_t* const mine = &bars.turn[first ? 0 : 1];
+        uint64_t* const other = &bars.turn[first ? 1 : 0];
+        // D = x y^T, x from tensor memory where it has room for it
+        auto product = [&](int slot, uint32_t to) {
+          const uint32_t y = k_lo + slot * (Shape::kSlot >> 4);
 #pragma unroll
           for (int kk = 0; kk < DP / 16; ++kk) {
             if (kk >= steps) break;
+            if (kk == max(steps - 2, 0)) mbar_arrive(other);
             const uint32_t at = ((kk / 4) * Shape::kPanel + (kk % 4) * 32) >> 4;
-            tc_mma_ss(to, xt_lo + at, y_lo2 + at, kDescHi, kIdXY, kk > 0);
+            if constexpr (kXInTmem)
+              tc_mma_ts(to, tm + kX + (first ? 0 : DP / 2) + kk * 8, y + at, kDescHi, kIdXY, kk > 0);
+            else
+              tc_mma_ss(to, x_lo + at, y + at, kDescHi, kIdXY, kk > 0);
           }
         };
         // D += (16-bit pairs in tensor memory) y
-        auto add = [&](uint32_t from, int slot, uint32_t to, bool more) {
+        auto add = [&](uint32_t from, int slot, uint32_t to, bool more, bool pass) {
           const uint32_t y = mn_lo + slot * (Shape::kSlot >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kBwdTile / 16; ++kk)
+          for (int kk = 0; kk < kBwdTile / 16; ++kk) {
+            if (kk == kBwdTile / 16 - 2 && pass) mbar_arrive(other);
             tc_mma_ts(to, from + (kk >> 2) * 64 + (kk & 3) * 8, y + kk * (2048 >> 4), kDescHi, id_acc,
                       kk > 0 ? 1u : static_cast<uint32_t>(more));
-        };
-        // The next tile of the ring: waits until it is there, rows behind the sequence zeroed
-        // (a weight of 0 times what stands there must be 0; v is never weighed for dq).
-        int slot = 0, left = nt;  // tiles up to the end of the sequence
-        uint32_t phase = 0, zeros = 0;
-        auto next = [&](int which) {
-          const int at = slot;
-          ok = ok && mbar_wait(&bars.full[at], phase);
-          if (which == 0) --left;
-          if (ok && cut_last && left == 0 && (KV || which == 0)) {
-            mbar_arrive(&bars.cut);
-            ok = mbar_wait(&bars.zeroed, zeros++ & 1);
           }
-          if (which == 1 && left == 0) left = nt;
+        };
+        ok = mbar_wait(kXInTmem ? &bars.x_ready : &bars.x_full, 0);
+        const int own = first ? 0 : 1;  // y1 or y2: what this thread's product reads
+        int y1 = 0, y2 = 0, left = nt;  // slots of the step before; tiles up to the sequence's end
+        uint32_t zeros = 0;
+        int slot = 0;
+        uint32_t phase = 0;
+        for (int i = 0; ok && i <= n; ++i) {
+          // Everything this turn needs, then the turn.
+          int z1 = slot, z2 = slot;
+          uint32_t ph1 = phase, ph2 = phase;
           if (++slot == Shape::kSlots) slot = 0, phase ^= 1;
-          return at;
-        };
-        ok = mbar_wait(&bars.x_full, 0);
-        int y1 = next(0), y2 = y1;
-        if (ok) {
-          tc_fence_after();
-          product(0, y1, tm);
-          tc_commit(&bars.s_full);
-          y2 = next(1);
-        }
-        if (ok) {
-          tc_fence_after();
-          product(1, y2, tm + kDp);
-          tc_commit(&bars.dp_full[0]);
-          if (!KV) tc_commit(&bars.empty[y2]);
-        }
-        for (int i = 0; ok && i < n; ++i) {
-          const bool more = i + 1 < n;
-          int z1 = y1, z2 = y2;
-          if constexpr (KV) {
-            ok = mbar_wait(&bars.p_full, i & 1);
-            if (!ok) break;
-            tc_fence_after();
-            add(tm, y2, tm + kAcc2, i > 0);
-            tc_commit(&bars.empty[y2]);
-            if (more) {
-              z1 = next(0);
-              if (!ok) break;
-              tc_fence_after();
-              product(0, z1, tm);
-              tc_commit(&bars.s_full);
+          z2 = slot, ph2 = phase;
+          if (++slot == Shape::kSlots) slot = 0, phase ^= 1;
+          if (i < n) {
+            ok = mbar_wait(&bars.full[own ? z2 : z1], own ? ph2 : ph1);
+            // Rows behind the sequence zeroed (a weight of 0 times what stands there must be
+            // 0; v is never weighed for dq).
+            if (--left == 0) {
+              left = nt;
+              if (ok && cut_last && (KV || first)) {
+                mbar_arrive(&bars.cut[own]);
+                ok = mbar_wait(&bars.zeroed[own], zeros++ & 1);
+              }
             }
-            ok = mbar_wait(&bars.ds_full[0], i & 1);
-            if (!ok) break;
-            tc_fence_after();
-            add(tm + kDp, y1, tm + kAcc1, i > 0);
-            tc_commit(&bars.empty[y1]);
-            if (more) {
-              z2 = next(1);
-              if (!ok) break;
-              tc_fence_after();
-              product(1, z2, tm + kDp);
-              tc_commit(&bars.dp_full[0]);
-            }
-          } else {
-            if (more) {
-              ok = mbar_wait(&bars.p_full, i & 1);
-              z1 = next(0);
-              if (!ok) break;
-              tc_fence_after();
-              product(0, z1, tm);
-              tc_commit(&bars.s_full);
-              z2 = next(1);
-              if (!ok) break;
-              tc_fence_after();
-              product(1, z2, tm + kDp + ((i + 1) & 1) * 128);
-              tc_commit(&bars.dp_full[(i + 1) & 1]);
-              tc_commit(&bars.empty[z2]);
-            }
-            ok = mbar_wait(&bars.ds_full[i & 1], (i >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            add(tm + kDp + (i & 1) * 128, y1, tm + kAcc1, i > 0);
-            tc_commit(&bars.empty[y1]);
           }
-          y1 = z1;
-          y2 = z2;
+          if (i > 0) {
+            if (first) ok = ok && mbar_wait(&bars.p_full, (i - 1) & 1);
+            else ok = ok && mbar_wait(&bars.ds_full, (i - 1) & 1);
+          }
+          // (the second thread's turn i follows the first one's)
+          if (first ? i > 0 : true) ok = ok && mbar_wait(mine, (first ? i - 1 : i) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (i > 0) {
+            if (first) {
+              if constexpr (KV) {
+                add(tm, y2, tm + kAcc2, i > 1, i == n);
+                tc_commit(&bars.empty[y2]);
+              } else if (i == n) {
+                mbar_arrive(other);
+              }
+            } else {
+              add(tm + kDp, y1, tm + kAcc1, i > 1, i == n);
+              tc_commit(&bars.empty[y1]);
+            }
+          }
+          if (i < n) {
+            product(first ? z1 : z2, tm + (first ? 0 : kDp));
+            tc_commit(first ? &bars.s_full : &bars.dp_full);
+            tc_commit(&bars.empty[first ? z1 : z2]);
+            if (!KV && !first) tc_commit(&bars.empty[z2]);  // (two arrivals a use of a slot)
+            y1 = z1, y2 = z2;
+          }
         }
         if (ok) {
           tc_commit(&bars.acc_full);
           // The last arrivals have landed before the CTA ends.
           ok = mbar_wait(&bars.empty[y1], ((2 * n - 2) / Shape::kSlots) & 1) &&
                mbar_wait(&bars.empty[y2], ((2 * n - 1) / Shape::kSlots) & 1);
+          if (first) ok = ok && mbar_wait(mine, n & 1);
         }
       }
       __syncwarp();
@@ -426,7 +418,8 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
       const int from = ny - (base + (nt - 1) * kBwdTile);  // first row to zero of the last tile
       for (int e = 0; ok && e < events; ++e) {
         // (a whole range may lie before the last tile's turn: a longer limit)
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(&bars.cut, e & 1, 30 * kWaitLimitNs));
+        const int own = e & 1, use = e >> 1;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(&bars.cut[own], use & 1, 30 * kWaitLimitNs));
         if (!ok) break;
         const int64_t tile = KV ? 2 * (static_cast<int64_t>(e >> 1) * nt + nt - 1) + (e & 1)
                                 : 2 * static_cast<int64_t>(nt - 1);
@@ -437,7 +430,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
               make_uint4(0u, 0u, 0u, 0u);
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.zeroed);
+        if (lane == 0) mbar_arrive(&bars.zeroed[own]);
       }
     }
   } else {
@@ -461,8 +454,27 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
     }
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t ts = tmem + lanes + w * 64;  // this warp's half of S
+    if (kXInTmem && n > 0) {
+      // x1 and x2 into tensor memory, a row by a thread.
+      ok = warp_wait(&bars.x_full, 0);
+      const uint8_t* from = raw + w * Shape::kSlot + r * 128;
+#pragma unroll
+      for (int pn = 0; pn < Shape::kPanels; ++pn) {
+        uint32_t v[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 q = *reinterpret_cast<const uint4*>(from + pn * Shape::kPanel + ((c ^ (r & 7)) << 4));
+          v[4 * c] = q.x, v[4 * c + 1] = q.y, v[4 * c + 2] = q.z, v[4 * c + 3] = q.w;
+        }
+        tc_st32(tmem + lanes + kX + w * (DP / 2) + pn * 32, v);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.x_ready);
+    }
     int t = 0;
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0; ok && i < n; ++i) {
       const ulonglong2* stat =
           reinterpret_cast<const ulonglong2*>(raw + Shape::kStats + (i & 1) * 2 * Shape::kStat + w * 256);
       ok = warp_wait(&bars.s_full, i & 1);
@@ -512,11 +524,10 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full);
       }
-      const int buf = KV ? 0 : i & 1;
-      ok = warp_wait(&bars.dp_full[buf], KV ? i & 1 : (i >> 1) & 1);
+      ok = warp_wait(&bars.dp_full, i & 1);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t td = ts + kDp + buf * 128;
+      const uint32_t td = ts + kDp;
       tc_ld32(td, sc);
       tc_ld32(td + 32, sc + 32);
       tc_wait_ld<64>(sc);
@@ -546,7 +557,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&bars.ds_full[buf]);
+        mbar_arrive(&bars.ds_full);
         if (KV) mbar_arrive(&bars.stat_empty[i & 1]);
       }
     }
@@ -631,7 +642,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
     }
   }
 
-  if (!ok && lane == 0) flag_wait_timeout();
+  if (!ok) flag_wait_timeout();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
       // tensor core waits (600 us for a prompt of 8192 tokens instead of the 500
       // of one thread for both).  The turn passes two steps before its end, so
       // that it arrives in time.
-      if (lane == 0 && nmax > 0) {
+      if (nmax > 0 && elect_one()) {
         const int t = warp - kMmaWarp, n = nt[t];
         const uint32_t ts = tm + t * 128, to = tm + 256 + t * 128;
         const uint32_t qt = q_lo + t * (Shape::kSlot >> 4);
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
     }
   }
 
-  if (!ok && lane == 0) flag_wait_timeout();
+  if (!ok) flag_wait_timeout();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
