@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const Att
 // head_dim 128.
 
 struct BwdBarriers {
-  uint64_t full[8], empty[8], s_full, p_full, dp_full, ds_full, x_full, x_ready, acc_full;
+  uint64_t full[8], empty[8], s_full, p_full[2], dp_full, ds_full[2], x_full, x_ready, acc_full;
   uint64_t turn[2], stat_full[2], stat_empty[2], cut[2], zeroed[2];
   uint32_t tmem;
   int sequence;  // of this CTA
@@ -149,6 +149,7 @@ struct BwdShape {
   static constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
   static_assert(256 * kRegsSoftmax + 128 * kRegsOther == kThreads * kRegsLaunch, "");
 };
+constexpr int kPass = 4;  // instructions before its end that a turn passes (2 and 8: 1 % slower)
 constexpr int kBwdMmaWarp = 8, kBwdMmaWarp2 = 9, kBwdLoadWarp = 10, kBwdZeroWarp = 11;
 
 // What f16 ds is taken larger by: a power of two u with u |dout_i| |v_j| 2 < 2^15 for every
@@ -231,14 +232,14 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
       mbar_init(&bars.empty[i], 2);  // one arrival for each of the threads that issue
     }
     mbar_init(&bars.s_full, 1);
-    mbar_init(&bars.p_full, 8);  // one arrival per warp
     mbar_init(&bars.x_full, 1);
     mbar_init(&bars.x_ready, 8);
     mbar_init(&bars.dp_full, 1);
-    mbar_init(&bars.ds_full, 8);
     mbar_init(&bars.acc_full, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.turn[i], 1);
+      mbar_init(&bars.p_full[i], 8);  // one arrival per warp
+      mbar_init(&bars.ds_full[i], 8);
       mbar_init(&bars.cut[i], 1);
       mbar_init(&bars.zeroed[i], 1);
       mbar_init(&bars.stat_full[i], 1);
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
       // The tensor core's queue is short: a thread that waits on a barrier between two
       // products, also on a complete one (100 cycles), leaves it idle.  So two threads issue,
       // and each waits while the other's products run.  They take turns: turn i of the
-      // first one is dv(i - 1), S(i), of the second dk or dq(i - 1), dP(i); a turn passes two
+      // first one is dv(i - 1), S(i), of the second dk or dq(i - 1), dP(i); a turn passes four
       // instructions before its end, so that it arrives in time.
       if (n > 0 && elect_one()) {
         uint64_t* const mine = &bars.turn[first ? 0 : 1];
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < DP / 16; ++kk) {
             if (kk >= steps) break;
-            if (kk == max(steps - 2, 0)) mbar_arrive(other);
+            if (kk == max(steps - kPass, 0)) mbar_arrive(other);
             const uint32_t at = ((kk / 4) * Shape::kPanel + (kk % 4) * 32) >> 4;
             if constexpr (kXInTmem)
               tc_mma_ts(to, tm + kX + (first ? 0 : DP / 2) + kk * 8, y + at, kDescHi, kIdXY, kk > 0);
@@ -291,14 +292,22 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
               tc_mma_ss(to, x_lo + at, y + at, kDescHi, kIdXY, kk > 0);
           }
         };
-        // D += (16-bit pairs in tensor memory) y
-        auto add = [&](uint32_t from, int slot, uint32_t to, bool more, bool pass) {
+        // D += (16-bit pairs in tensor memory) y, in the halves that they come in
+        auto add = [&](uint32_t from, int slot, uint32_t to, bool more, bool pass, uint64_t* halves,
+                       uint32_t parity) {
           const uint32_t y = mn_lo + slot * (Shape::kSlot >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kBwdTile / 16; ++kk) {
-            if (kk == kBwdTile / 16 - 2 && pass) mbar_arrive(other);
-            tc_mma_ts(to, from + (kk >> 2) * 64 + (kk & 3) * 8, y + kk * (2048 >> 4), kDescHi, id_acc,
-                      kk > 0 ? 1u : static_cast<uint32_t>(more));
+          for (int hf = 0; hf < 2; ++hf) {
+            ok = ok && mbar_wait(&halves[hf], parity);
+            if (!ok) return;
+            tc_fence_after();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int kk = (e >> 1) * 4 + hf * 2 + (e & 1);
+              if (hf == 1 && e == 2 && pass) mbar_arrive(other);
+              tc_mma_ts(to, from + (kk >> 2) * 64 + (kk & 3) * 8, y + kk * (2048 >> 4), kDescHi, id_acc,
+                        hf + e > 0 ? 1u : static_cast<uint32_t>(more));
+            }
           }
         };
         ok = mbar_wait(kXInTmem ? &bars.x_ready : &bars.x_full, 0);
@@ -326,10 +335,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
               }
             }
           }
-          if (i > 0) {
-            if (first) ok = ok && mbar_wait(&bars.p_full, (i - 1) & 1);
-            else ok = ok && mbar_wait(&bars.ds_full, (i - 1) & 1);
-          }
+          if (!KV && first && i > 0) ok = ok && mbar_wait(&bars.p_full[0], (i - 1) & 1);  // S has been read
           // (the second thread's turn i follows the first one's)
           if (first ? i > 0 : true) ok = ok && mbar_wait(mine, (first ? i - 1 : i) & 1);
           if (!ok) break;
@@ -337,13 +343,15 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
           if (i > 0) {
             if (first) {
               if constexpr (KV) {
-                add(tm, y2, tm + kAcc2, i > 1, i == n);
+                add(tm, y2, tm + kAcc2, i > 1, i == n, bars.p_full, (i - 1) & 1);
+                if (!ok) break;
                 tc_commit(&bars.empty[y2]);
               } else if (i == n) {
                 mbar_arrive(other);
               }
             } else {
-              add(tm + kDp, y1, tm + kAcc1, i > 1, i == n);
+              add(tm + kDp, y1, tm + kAcc1, i > 1, i == n, bars.ds_full, (i - 1) & 1);
+              if (!ok) break;
               tc_commit(&bars.empty[y1]);
             }
           }
@@ -477,8 +485,8 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
     for (int i = 0; ok && i < n; ++i) {
       const ulonglong2* stat =
           reinterpret_cast<const ulonglong2*>(raw + Shape::kStats + (i & 1) * 2 * Shape::kStat + w * 256);
-      ok = warp_wait(&bars.s_full, i & 1);
-      if (KV) ok = ok && warp_wait(&bars.stat_full[i & 1], (i >> 1) & 1);
+      if (KV) ok = warp_wait(&bars.stat_full[i & 1], (i >> 1) & 1);
+      ok = ok && warp_wait(&bars.s_full, i & 1);
       if (!ok) break;
       tc_fence_after();
       uint32_t sc[64];
@@ -488,41 +496,47 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
       if constexpr (!KV) {  // S is free again
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full);
+        if (lane == 0) mbar_arrive(&bars.p_full[0]);
       }
       const int tb = base + t * kBwdTile + w * 64;
       if (++t == nt) t = 0;
       const bool cut = __any_sync(0xFFFFFFFFu, tb < lo || tb + 64 > hi);
       // Bit e: row tb + e of y is kept.
       const uint64_t kept = low_bits(hi - tb) & ~low_bits(lo - tb);
-      const uint32_t kept_lo = static_cast<uint32_t>(kept), kept_hi = static_cast<uint32_t>(kept >> 32);
+      const uint32_t half_kept[2] = {static_cast<uint32_t>(kept), static_cast<uint32_t>(kept >> 32)};
       uint64_t pr[32];
+      // In halves of 32 columns: the tensor core begins with the first one.
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        ulonglong2 nl = make_ulonglong2(nl2, nl2);
-        if (KV) nl = stat[e / 2];
-        const float2 a = u2(fma2(p2(__uint_as_float(sc[2 * e]), __uint_as_float(sc[2 * e + 1])), sc2, nl.x));
-        const float2 c = u2(fma2(p2(__uint_as_float(sc[2 * e + 2]), __uint_as_float(sc[2 * e + 3])), sc2, nl.y));
-        pr[e] = p2(ex2(a.x), ex2(a.y));
-        pr[e + 1] = p2(ex2(c.x), ex2(c.y));
-      }
-      if (cut) {
+      for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const uint32_t bits = e < 16 ? kept_lo >> (2 * e) : kept_hi >> (2 * e - 32);
-          const float2 a = u2(pr[e]);
-          pr[e] = p2(bits & 1u ? a.x : 0.f, bits & 2u ? a.y : 0.f);
+        for (int e = hf * 16; e < hf * 16 + 16; e += 2) {
+          ulonglong2 nl = make_ulonglong2(nl2, nl2);
+          if (KV) nl = stat[e / 2];
+          const float2 a =
+              u2(fma2(p2(__uint_as_float(sc[2 * e]), __uint_as_float(sc[2 * e + 1])), sc2, nl.x));
+          const float2 c =
+              u2(fma2(p2(__uint_as_float(sc[2 * e + 2]), __uint_as_float(sc[2 * e + 3])), sc2, nl.y));
+          pr[e] = p2(ex2(a.x), ex2(a.y));
+          pr[e + 1] = p2(ex2(c.x), ex2(c.y));
         }
-      }
-      uint32_t pk[32];
-      if constexpr (KV) {
+        if (cut) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) pk[e] = narrow2<T>(pr[e]);
-        tc_st32(ts, pk);
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full);
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t bits = half_kept[hf] >> (2 * e);
+            const float2 a = u2(pr[hf * 16 + e]);
+            pr[hf * 16 + e] = p2(bits & 1u ? a.x : 0.f, bits & 2u ? a.y : 0.f);
+          }
+        }
+        if constexpr (KV) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = narrow2<T>(pr[hf * 16 + e]);
+          tc_st16(ts + hf * 16, pk);
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.p_full[hf]);
+        }
       }
       ok = warp_wait(&bars.dp_full, i & 1);
       if (!ok) break;
@@ -532,33 +546,37 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
       tc_ld32(td + 32, sc + 32);
       tc_wait_ld<64>(sc);
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        ulonglong2 nd = make_ulonglong2(nd2, nd2);
-        if (KV) nd = stat[Shape::kStat / 16 + e / 2];
-        uint64_t a = add2(p2(__uint_as_float(sc[2 * e]), __uint_as_float(sc[2 * e + 1])), nd.x);
-        uint64_t c = add2(p2(__uint_as_float(sc[2 * e + 2]), __uint_as_float(sc[2 * e + 3])), nd.y);
-        if constexpr (kType == 0) {
-          a = mul2(a, up2);
-          c = mul2(c, up2);
-        }
-        pk[e] = narrow2<T>(mul2(a, pr[e]));
-        pk[e + 1] = narrow2<T>(mul2(c, pr[e + 1]));
-      }
-      if (cut) {
-        // (0 times an infinity or NaN of a pair that is not kept)
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const uint32_t bits = e < 16 ? kept_lo >> (2 * e) : kept_hi >> (2 * e - 32);
-          pk[e] &= (bits & 1u ? 0xFFFFu : 0u) | (bits & 2u ? 0xFFFF0000u : 0u);
+        for (int e = hf * 16; e < hf * 16 + 16; e += 2) {
+          ulonglong2 nd = make_ulonglong2(nd2, nd2);
+          if (KV) nd = stat[Shape::kStat / 16 + e / 2];
+          uint64_t a = add2(p2(__uint_as_float(sc[2 * e]), __uint_as_float(sc[2 * e + 1])), nd.x);
+          uint64_t c = add2(p2(__uint_as_float(sc[2 * e + 2]), __uint_as_float(sc[2 * e + 3])), nd.y);
+          if constexpr (kType == 0) {
+            a = mul2(a, up2);
+            c = mul2(c, up2);
+          }
+          pk[e - hf * 16] = narrow2<T>(mul2(a, pr[e]));
+          pk[e - hf * 16 + 1] = narrow2<T>(mul2(c, pr[e + 1]));
         }
-      }
-      tc_st32(td, pk);
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bars.ds_full);
-        if (KV) mbar_arrive(&bars.stat_empty[i & 1]);
+        if (cut) {
+          // (0 times an infinity or NaN of a pair that is not kept)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t bits = half_kept[hf] >> (2 * e);
+            pk[e] &= (bits & 1u ? 0xFFFFu : 0u) | (bits & 2u ? 0xFFFF0000u : 0u);
+          }
+        }
+        tc_st16(td + hf * 16, pk);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars.ds_full[hf]);
+          if (KV && hf == 1) mbar_arrive(&bars.stat_empty[i & 1]);
+        }
       }
     }
     // Output: dv by the warps 0-3, dk by 4-7; or half of dq's columns by each.
