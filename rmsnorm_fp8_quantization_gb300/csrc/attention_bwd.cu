@@ -133,13 +133,18 @@ struct BwdBarriers {
 
 constexpr int kSortBatches = 256;  // up to so many sequences are taken by length
 
-template <int DP>
+template <int DP, bool KV>
 struct BwdShape {
   static constexpr int kPanel = kBwdTile * 128;  // bytes of [128][64] 16-bit elements
   static constexpr int kPanels = DP / 64;
   static constexpr int kSlot = kPanels * kPanel;
-  static constexpr int kSlots = DP == 128 ? 5 : 8;  // y1 and y2 alternate
-  static constexpr int kStats = 2 * kSlot + kSlots * kSlot;  // then -lse and -delta, two stages
+  // x goes to tensor memory where it has room (columns: S, dP 256, results 128 or 256).
+  static constexpr bool kXInTmem = !KV || DP == 64;
+  // y1 and y2 alternate in a ring of slots; behind it x1 and x2, which become slots of it too
+  // once they are in tensor memory (at 128; dq's loads were late with 5 slots).
+  static constexpr int kFirst = DP == 128 ? 5 : 8;
+  static constexpr int kSlots = DP == 128 && kXInTmem ? kFirst + 2 : kFirst;
+  static constexpr int kStats = (kFirst + 2) * kSlot;  // then -lse and -delta, two stages
   static constexpr int kStat = kBwdTile * 4;
   static constexpr int kBody = kStats + 4 * kStat;
   static constexpr int kSmem = kBody + (int)sizeof(BwdBarriers);
@@ -167,12 +172,12 @@ __device__ __forceinline__ float ds_factor(const AttnBwdParams& p, int b, int h)
 }
 
 template <typename T, int DP, bool KV>
-__global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
+__global__ void __launch_bounds__(BwdShape<DP, KV>::kThreads, 1)
     attention_bwd_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ CUtensorMap x1map,
                          const __grid_constant__ CUtensorMap x2map,
                          const __grid_constant__ CUtensorMap y1map,
                          const __grid_constant__ CUtensorMap y2map) {
-  using Shape = BwdShape<DP>;
+  using Shape = BwdShape<DP, KV>;
   constexpr int kType = std::is_same<T, __half>::value ? 0 : 1;
   extern __shared__ __align__(1024) uint8_t raw[];
   BwdBarriers& bars = *reinterpret_cast<BwdBarriers*>(raw + Shape::kBody);
@@ -221,8 +226,8 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
   // The last tile reaches beyond the sequence.
   const bool cut_last = base + nt * kBwdTile > ny;
 
-  const uint32_t xs = smem_u32(raw), ring = xs + 2 * Shape::kSlot;
-  if (xs & 1023u) {  // the swizzle goes by address bits; the compiler's alignment holds
+  const uint32_t ring = smem_u32(raw), xs = ring + Shape::kFirst * Shape::kSlot;
+  if (ring & 1023u) {  // the swizzle goes by address bits; the compiler's alignment holds
     if (tid == 0) flag_wait_timeout();
     return;
   }
@@ -252,9 +257,9 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
-  // Columns (S: 0).  x as the products' first operand, 16-bit pairs: not for dk and dv at 128.
+  // Columns (S: 0); kX: x as the products' first operand, 16-bit pairs.
   constexpr uint32_t kDp = 128, kAcc2 = 256, kAcc1 = KV ? 256 + DP : 256, kX = 384;
-  constexpr bool kXInTmem = !KV || DP == 64;
+  constexpr bool kXInTmem = Shape::kXInTmem;
   static_assert(kAcc1 + DP <= (kXInTmem ? kX : kTmemCols), "");
   bool ok = true;
 
@@ -392,6 +397,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
           const int yh = KV ? h * p.group + g : h;
           for (int w = 0; ok && w < 2; ++w) {
             if (issued >= Shape::kSlots) ok = mbar_wait(&bars.empty[slot], phase ^ 1);
+            else if (issued == Shape::kFirst) ok = mbar_wait(&bars.x_ready, 0);  // (only where x's room is used)
             if (!ok) break;
             mbar_arrive_expect_tx(&bars.full[slot], Shape::kSlot);
             tile(ring + slot * Shape::kSlot, w ? &y2map : &y1map, yh, yr, &bars.full[slot]);
@@ -431,7 +437,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
         if (!ok) break;
         const int64_t tile = KV ? 2 * (static_cast<int64_t>(e >> 1) * nt + nt - 1) + (e & 1)
                                 : 2 * static_cast<int64_t>(nt - 1);
-        uint8_t* at = raw + (2 + static_cast<int>(tile % Shape::kSlots)) * Shape::kSlot;
+        uint8_t* at = raw + static_cast<int>(tile % Shape::kSlots) * Shape::kSlot;
         for (int j = lane; j < (kBwdTile - from) * 8 * Shape::kPanels; j += 32)
           *reinterpret_cast<uint4*>(at + (j >> 3) % Shape::kPanels * Shape::kPanel +
                                     (from + (j >> 3) / Shape::kPanels) * 128 + (j & 7) * 16) =
@@ -465,7 +471,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
     if (kXInTmem && n > 0) {
       // x1 and x2 into tensor memory, a row by a thread.
       ok = warp_wait(&bars.x_full, 0);
-      const uint8_t* from = raw + w * Shape::kSlot + r * 128;
+      const uint8_t* from = raw + (Shape::kFirst + w) * Shape::kSlot + r * 128;
 #pragma unroll
       for (int pn = 0; pn < Shape::kPanels; ++pn) {
         uint32_t v[32];
@@ -596,7 +602,7 @@ __global__ void __launch_bounds__(BwdShape<DP>::kThreads, 1)
       const uint32_t some = __ballot_sync(0xFFFFFFFFu, live);
       // Next to pairs of its tiles that it dropped.
       const bool dropped = live && n > 0 && (lo > base || hi < min(base + nt * kBwdTile, ny));
-      // Through shared memory (x is used up), so that a store writes whole sectors.
+      // Through shared memory (the ring is used up), so that a store writes whole sectors.
       uint8_t* const stage = raw + warp * 32 * 64;
 #pragma unroll 1
       for (int c = 0; c < kCols && col0 + c < p.d; c += 32) {
@@ -671,14 +677,14 @@ template <typename T, int DP, bool KV>
 cudaError_t launch_tiles(const AttnBwdParams& p, const CUtensorMap* m, cudaStream_t st) {
   auto k = attention_bwd_kernel<T, DP, KV>;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(k, BwdShape<DP>::kSmem, done);
+  const cudaError_t e = allow_smem(k, BwdShape<DP, KV>::kSmem, done);
   if (e != cudaSuccess) return e;
   const int64_t grid = KV ? int64_t(p.k_tiles) * p.batches * p.hkv : int64_t(p.q_tiles) * p.batches * p.hq;
   if (grid == 0) return cudaSuccess;
-  const dim3 g(static_cast<unsigned>(grid)), t(BwdShape<DP>::kThreads);
+  const dim3 g(static_cast<unsigned>(grid)), t(BwdShape<DP, KV>::kThreads);
   // m: q, k, v, dout
-  return KV ? launch_pdl(k, g, t, BwdShape<DP>::kSmem, st, p, m[1], m[2], m[0], m[3])
-            : launch_pdl(k, g, t, BwdShape<DP>::kSmem, st, p, m[0], m[3], m[1], m[2]);
+  return KV ? launch_pdl(k, g, t, BwdShape<DP, KV>::kSmem, st, p, m[1], m[2], m[0], m[3])
+            : launch_pdl(k, g, t, BwdShape<DP, KV>::kSmem, st, p, m[0], m[3], m[1], m[2]);
 }
 
 template <typename T>
