@@ -1,4 +1,4 @@
-// Host-side shortcut of the rotary and paged wrappers (ops.py).
+// Host-side shortcut of the rotary, paged, attention and dropout wrappers (ops.py).
 //
 // A step of a serving loop launches kernels of 2 to 10 us; the wrappers' checks,
 // allocations and argument packing in Python cost 16 to 27 us of host time a
@@ -29,10 +29,22 @@ using AppendFn = gbn_status (*)(const gbn_paged_append_args*, cudaStream_t);
 using AttendFn = gbn_status (*)(const gbn_paged_attention_args*, cudaStream_t);
 using BytesFn = gbn_status (*)(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
                                int64_t, int64_t, int64_t, int, gbn_dtype, gbn_dtype, size_t*);
+using AttnFwdFn = gbn_status (*)(const gbn_attention_fwd_args*, cudaStream_t);
+using AttnBwdFn = gbn_status (*)(const gbn_attention_bwd_args*, cudaStream_t);
+using AttnBwdBytesFn = gbn_status (*)(int64_t, int64_t, int64_t, int64_t, gbn_dtype, size_t*);
+using DropFwdFn = gbn_status (*)(const void*, const void*, void*, const int64_t*, int64_t, double,
+                                 gbn_dtype, cudaStream_t);
+using DropBwdFn = gbn_status (*)(const void*, void*, const int64_t*, int64_t, double, gbn_dtype,
+                                 cudaStream_t);
 RopeFn g_rope[2];
 AppendFn g_append;
 AttendFn g_attend;
 BytesFn g_bytes;
+AttnFwdFn g_attn_fwd;
+AttnBwdFn g_attn_bwd;
+AttnBwdBytesFn g_attn_bwd_bytes;
+DropFwdFn g_drop_fwd;
+DropBwdFn g_drop_bwd;
 
 // A plain tensor (no subclass), or null.
 const at::Tensor* plain(PyObject* o) {
@@ -72,13 +84,18 @@ PyObject* guarded(F f) {
 PyObject* status(gbn_status st) { return PyLong_FromLong(static_cast<long>(st)); }
 
 PyObject* setup(PyObject*, PyObject* args) {
-  unsigned long long a, b, c, d, e;
-  if (!PyArg_ParseTuple(args, "KKKKK", &a, &b, &c, &d, &e)) return nullptr;
+  unsigned long long a, b, c, d, e, f, g, h, i, j;
+  if (!PyArg_ParseTuple(args, "KKKKKKKKKK", &a, &b, &c, &d, &e, &f, &g, &h, &i, &j)) return nullptr;
   g_rope[0] = reinterpret_cast<RopeFn>(a);
   g_rope[1] = reinterpret_cast<RopeFn>(b);
   g_append = reinterpret_cast<AppendFn>(c);
   g_attend = reinterpret_cast<AttendFn>(d);
   g_bytes = reinterpret_cast<BytesFn>(e);
+  g_attn_fwd = reinterpret_cast<AttnFwdFn>(f);
+  g_attn_bwd = reinterpret_cast<AttnBwdFn>(g);
+  g_attn_bwd_bytes = reinterpret_cast<AttnBwdBytesFn>(h);
+  g_drop_fwd = reinterpret_cast<DropFwdFn>(i);
+  g_drop_bwd = reinterpret_cast<DropBwdFn>(j);
   Py_RETURN_NONE;
 }
 
@@ -333,12 +350,230 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (token, head) strides of [tokens, heads, dim], or of a batch of sequences of one length whose
+// tokens are one run of rows.
+bool token_strides(const at::Tensor& t, int64_t* st) {
+  if (!inner_ok(t) && t.size(-1) > 1) return false;
+  const int d = static_cast<int>(t.dim());
+  st[1] = t.stride(d - 2);
+  st[0] = t.stride(d - 3);
+  if (d == 3) return true;
+  if (t.size(0) > 1) {
+    if (t.size(1) == 1) st[0] = t.stride(0);
+    else if (t.stride(0) != t.size(1) * t.stride(1)) return false;
+  }
+  return true;
+}
+struct Sequences {
+  const at::Tensor *q, *k, *v;
+  const int32_t *cu_q, *cu_k;
+  int64_t sizes[9];  // tokens, keys, batches, q_heads, kv_heads, head_dim, max_q, max_k, window
+  int64_t strides[6];
+  int type, causal, dev;
+  float scale;
+};
+// What both passes share; a: q, k, v; r: cu, cu_k, max_q, max_k, scale, causal, window.
+bool sequences_ok(PyObject* const* a, PyObject* const* r, Sequences* s) {
+  if (!(s->q = plain(a[0])) || !(s->k = plain(a[1])) || !(s->v = plain(a[2])) || !s->q->is_cuda())
+    return false;
+  const at::Tensor &q = *s->q, &k = *s->k, &v = *s->v;
+  s->dev = q.get_device();
+  s->type = gbn_type(q.scalar_type());
+  const int64_t d = q.dim();
+  if (c10::cuda::current_device() != s->dev || (s->type != GBN_BF16 && s->type != GBN_F16) ||
+      (d != 3 && d != 4) || k.dim() != d || v.dim() != d || k.sizes() != v.sizes() ||
+      k.scalar_type() != q.scalar_type() || v.scalar_type() != q.scalar_type() || !k.is_cuda() ||
+      !v.is_cuda() || k.get_device() != s->dev || v.get_device() != s->dev ||
+      k.size(-1) != q.size(-1) || !token_strides(q, s->strides) || !token_strides(k, s->strides + 2) ||
+      !token_strides(v, s->strides + 4))
+    return false;
+  int64_t* z = s->sizes;
+  s->cu_q = s->cu_k = nullptr;
+  if (d == 4) {
+    if (r[0] != Py_None || r[1] != Py_None || r[2] != Py_None || r[3] != Py_None || k.size(0) != q.size(0))
+      return false;
+    z[0] = q.size(0) * q.size(1);
+    z[1] = k.size(0) * k.size(1);
+    z[2] = q.size(0);
+    z[6] = q.size(1);
+    z[7] = k.size(1);
+  } else {
+    auto offsets = [&](PyObject* o, const int32_t** p) -> const at::Tensor* {
+      const at::Tensor* t = plain(o);
+      if (!t || t->scalar_type() != at::kInt || t->dim() != 1 || t->size(0) < 1 || !t->is_contiguous() ||
+          !t->is_cuda() || t->get_device() != s->dev)
+        return nullptr;
+      *p = static_cast<const int32_t*>(t->data_ptr());
+      return t;
+    };
+    const at::Tensor* cu = offsets(r[0], &s->cu_q);
+    if (!cu || !whole(r[2], &z[6])) return false;
+    z[0] = q.size(0);
+    z[1] = k.size(0);
+    z[2] = cu->size(0) - 1;
+    s->cu_k = s->cu_q;
+    z[7] = z[6];
+    if (r[1] != Py_None) {
+      const at::Tensor* ck = offsets(r[1], &s->cu_k);
+      if (!ck || ck->size(0) != cu->size(0) || !whole(r[3], &z[7])) return false;
+    } else if (r[3] != Py_None || z[0] != z[1]) {
+      return false;
+    }
+  }
+  z[3] = q.size(-2);
+  z[4] = k.size(-2);
+  z[5] = q.size(-1);
+  double scale = 0.0;
+  if (r[4] == Py_None) scale = 1.0 / std::sqrt(static_cast<double>(z[5]));
+  else if (!number(r[4], &scale)) return false;
+  s->scale = static_cast<float>(scale);
+  if ((r[5] != Py_True && r[5] != Py_False) || !whole(r[6], &z[8])) return false;
+  s->causal = r[5] == Py_True;
+  return true;
+}
+template <typename A>
+void fill(const Sequences& s, A* g) {
+  g->q = s.q->data_ptr();
+  g->k = s.k->data_ptr();
+  g->v = s.v->data_ptr();
+  g->cu_q = s.cu_q;
+  g->cu_k = s.cu_k;
+  g->tokens = s.sizes[0];
+  g->keys = s.sizes[1];
+  g->batches = s.sizes[2];
+  g->q_heads = s.sizes[3];
+  g->kv_heads = s.sizes[4];
+  g->head_dim = s.sizes[5];
+  g->max_q = s.sizes[6];
+  g->max_k = s.sizes[7];
+  g->window = s.sizes[8];
+  for (int i = 0; i < 2; ++i) {
+    g->q_strides[i] = s.strides[i];
+    g->k_strides[i] = s.strides[2 + i];
+    g->v_strides[i] = s.strides[4 + i];
+  }
+  g->dtype = s.type;
+  g->causal = s.causal;
+  g->scale = s.scale;
+  g->reserved = 0;
+}
+// Strides of a new contiguous tensor [.., heads, dim].
+void plain_strides(int64_t heads, int64_t dim, int64_t* st) {
+  st[0] = heads * dim;
+  st[1] = dim;
+}
+
+// attention_fwd(q, k, v, cu, cu_k, max_q, max_k, scale, causal, window)
+PyObject* attention_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Sequences s;
+    if (n != 10 || !sequences_ok(a, a + 3, &s)) Py_RETURN_NONE;
+    gbn_attention_fwd_args g;
+    fill(s, &g);
+    at::Tensor out = at::empty(s.q->sizes(), s.q->options());
+    at::Tensor lse = at::empty(s.q->sizes().slice(0, s.q->dim() - 1), s.q->options().dtype(at::kFloat));
+    g.out = out.data_ptr();
+    g.lse = static_cast<float*>(lse.data_ptr());
+    plain_strides(g.q_heads, g.head_dim, g.out_strides);
+    const gbn_status st = g_attn_fwd(&g, c10::cuda::getCurrentCUDAStream(s.dev).stream());
+    if (st != GBN_OK) return status(st);
+    PyObject* r = PyTuple_New(2);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(out)));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(lse)));
+    return r;
+  });
+}
+
+// attention_bwd(dout, out, lse, q, k, v, cu, cu_k, max_q, max_k, scale, causal, window)
+PyObject* attention_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Sequences s;
+    const at::Tensor *dout, *out, *lse;
+    if (n != 13 || !sequences_ok(a + 3, a + 6, &s) || !(dout = plain(a[0])) || !(out = plain(a[1])) ||
+        !(lse = plain(a[2])))
+      Py_RETURN_NONE;
+    gbn_attention_bwd_args g;
+    for (const at::Tensor* t : {dout, out})
+      if (t->scalar_type() != s.q->scalar_type() || t->sizes() != s.q->sizes() || !t->is_cuda() ||
+          t->get_device() != s.dev)
+        Py_RETURN_NONE;
+    if (!token_strides(*dout, g.dout_strides) || !token_strides(*out, g.out_strides) ||
+        lse->scalar_type() != at::kFloat || lse->sizes() != s.q->sizes().slice(0, s.q->dim() - 1) ||
+        !lse->is_contiguous() || !lse->is_cuda() || lse->get_device() != s.dev)
+      Py_RETURN_NONE;
+    fill(s, &g);
+    size_t bytes = 0;
+    gbn_status st = g_attn_bwd_bytes(g.tokens, g.batches, g.q_heads, g.kv_heads,
+                                     static_cast<gbn_dtype>(g.dtype), &bytes);
+    if (st != GBN_OK) return status(st);
+    at::Tensor dq = at::empty(s.q->sizes(), s.q->options()), dk = at::empty(s.k->sizes(), s.k->options());
+    at::Tensor dv = at::empty(s.v->sizes(), s.v->options());
+    at::Tensor work = at::empty({static_cast<int64_t>(bytes)}, s.q->options().dtype(at::kByte));
+    g.out = out->data_ptr();
+    g.dout = dout->data_ptr();
+    g.lse = static_cast<const float*>(lse->data_ptr());
+    g.dq = dq.data_ptr();
+    g.dk = dk.data_ptr();
+    g.dv = dv.data_ptr();
+    g.workspace = work.data_ptr();
+    g.workspace_bytes = bytes;
+    plain_strides(g.q_heads, g.head_dim, g.dq_strides);
+    plain_strides(g.kv_heads, g.head_dim, g.dk_strides);
+    plain_strides(g.kv_heads, g.head_dim, g.dv_strides);
+    st = g_attn_bwd(&g, c10::cuda::getCurrentCUDAStream(s.dev).stream());
+    if (st != GBN_OK) return status(st);
+    PyObject* r = PyTuple_New(3);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(dq)));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(dk)));
+    PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(std::move(dv)));
+    return r;
+  });
+}
+
+// dropout(backward, x, p, rng, residual | None)
+PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    int64_t backward;
+    double p;
+    const at::Tensor *x, *rng, *res = nullptr;
+    if (n != 5 || !whole(a[0], &backward) || !(x = plain(a[1])) || !PyFloat_CheckExact(a[2]) ||
+        !(rng = plain(a[3])) || (a[4] != Py_None && !(res = plain(a[4]))))
+      Py_RETURN_NONE;
+    p = PyFloat_AS_DOUBLE(a[2]);
+    const int type = gbn_type(x->scalar_type());
+    const int dev = x->is_cuda() ? x->get_device() : -1;
+    if (dev < 0 || c10::cuda::current_device() != dev || type < 0 || type == GBN_E4M3 ||
+        !x->is_contiguous() || rng->scalar_type() != at::kLong || rng->dim() != 1 || rng->size(0) != 2 ||
+        !rng->is_contiguous() || !rng->is_cuda() || rng->get_device() != dev ||
+        (res && (res->scalar_type() != x->scalar_type() || res->sizes() != x->sizes() ||
+                 !res->is_contiguous() || !res->is_cuda() || res->get_device() != dev)))
+      Py_RETURN_NONE;
+    at::Tensor out = at::empty(x->sizes(), x->options());
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev).stream();
+    const int64_t* key = static_cast<const int64_t*>(rng->data_ptr());
+    const gbn_dtype dt = static_cast<gbn_dtype>(type);
+    const gbn_status st =
+        backward ? g_drop_bwd(x->data_ptr(), out.data_ptr(), key, x->numel(), p, dt, stream)
+                 : g_drop_fwd(x->data_ptr(), res ? res->data_ptr() : nullptr, out.data_ptr(), key,
+                              x->numel(), p, dt, stream);
+    if (st != GBN_OK) return status(st);
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
 PyMethodDef kMethods[] = {
     {"setup", setup, METH_VARARGS, "Addresses of the C entry points."},
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope)), METH_FASTCALL, ""},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append)), METH_FASTCALL, ""},
     {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention)),
      METH_FASTCALL, ""},
+    {"attention_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention_fwd)),
+     METH_FASTCALL, ""},
+    {"attention_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention_bwd)),
+     METH_FASTCALL, ""},
+    {"dropout", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(dropout)), METH_FASTCALL, ""},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

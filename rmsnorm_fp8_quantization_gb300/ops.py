@@ -174,7 +174,10 @@ def _shortcut():
         return None
     fast.setup(*(ctypes.cast(getattr(G.library(), n), ctypes.c_void_p).value
                  for n in ("gbn_rope_fwd", "gbn_rope_bwd", "gbn_paged_append",
-                           "gbn_paged_attention", "gbn_paged_attention_workspace_size")))
+                           "gbn_paged_attention", "gbn_paged_attention_workspace_size",
+                           "gbn_attention_fwd", "gbn_attention_bwd",
+                           "gbn_attention_bwd_workspace_size", "gbn_dropout_fwd",
+                           "gbn_dropout_bwd")))
     return fast
 
 
@@ -730,6 +733,11 @@ def attention_fwd(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, max_q=None, ma
     sqrt(head_dim) by default.  ``causal``: bottom-right aligned; ``window`` > 0: only the last
     ``window`` positions up to the query's own.  lse is fp32 [batch, seq, heads] or [tokens,
     heads].  Both are new tensors unless given; padding rows are not written."""
+    if _fast is not None and out is None and lse is None and stream is None:
+        r = _fast.attention_fwd(q, k, v, cu_seqlens, cu_seqlens_k, max_q, max_k, scale, causal,
+                                window)
+        if r is not None:
+            return _taken(r, "gbn_attention_fwd")
     x, cu_q, cu_k, sizes = _attention_tensors(q, k, v, cu_seqlens, cu_seqlens_k, max_q, max_k)
     if stream is not None:
         return _on_stream(stream, q.device, attention_fwd, q, k, v, cu_seqlens=cu_seqlens,
@@ -773,6 +781,12 @@ def attention_bwd(dout, q, k, v, out, lse, *, cu_seqlens=None, cu_seqlens_k=None
     output; out and lse are its results, the other arguments its own.  The probabilities are
     computed again.  The gradients are new tensors unless given; padding rows are not written.
     ``workspace``: ``attention_bwd_workspace``; allocated here when needed."""
+    if (_fast is not None and dq is None and dk is None and dv is None and workspace is None
+            and stream is None):
+        r = _fast.attention_bwd(dout, out, lse, q, k, v, cu_seqlens, cu_seqlens_k, max_q, max_k,
+                                scale, causal, window)
+        if r is not None:
+            return _taken(r, "gbn_attention_bwd")
     x, cu_q, cu_k, sizes = _attention_tensors(q, k, v, cu_seqlens, cu_seqlens_k, max_q, max_k)
     if stream is not None:
         return _on_stream(stream, q.device, attention_bwd, dout, q, k, v, out, lse,
@@ -841,10 +855,18 @@ def dropout_fwd(x, p, rng, *, residual=None, out=None, stream=None):
     int64 tensor [2] on x's device, and an element's place in x alone: it is never stored.
     Calls that are to be independent differ in seed or offset (add 1 to the offset).  x and
     residual are contiguous; out, a new tensor unless given, may be either."""
+    if _fast is not None and out is None and stream is None:
+        r = _fast.dropout(0, x, p, rng, residual)
+        if r is not None:
+            return _taken(r, "gbn_dropout_fwd")
     return _dropout("gbn_dropout_fwd", x, p, rng, residual, out, stream)
 
 
 def dropout_bwd(dout, p, rng, *, out=None, stream=None):
     """Gradient of ``dropout_fwd``'s x, with the forward's p and rng (that of the residual is
     dout itself).  out, a new tensor unless given, may be dout."""
+    if _fast is not None and out is None and stream is None:
+        r = _fast.dropout(1, dout, p, rng, None)
+        if r is not None:
+            return _taken(r, "gbn_dropout_bwd")
     return _dropout("gbn_dropout_bwd", dout, p, rng, None, out, stream)
