@@ -547,8 +547,9 @@ gbn_status gbn_attention_fwd(const gbn_attention_fwd_args* args, cudaStream_t st
  *   workspace  gbn_attention_bwd_workspace_size() bytes, 16-byte aligned (else
  *              GBN_ERR_WORKSPACE); needs no initialization; calls that may
  *              overlap on the GPU need one each. */
-gbn_status gbn_attention_bwd_workspace_size(int64_t tokens, int64_t batches, int64_t q_heads,
-                                            int64_t kv_heads, gbn_dtype dtype, size_t* bytes);
+gbn_status gbn_attention_bwd_workspace_size(int64_t tokens, int64_t keys, int64_t batches,
+                                            int64_t q_heads, int64_t kv_heads, gbn_dtype dtype,
+                                            size_t* bytes);
 typedef struct {
   const void* q;
   const void* k;

@@ -9,6 +9,7 @@
 #include <cuda_fp16.h>
 
 #include "attention_rows.cuh"
+#include "packed_tiles.cuh"
 #include "tensor_core.cuh"
 
 namespace gbn {
@@ -17,24 +18,32 @@ namespace {
 // ---- row statistics
 //
 // delta_i = dout_i.out_i for every query and head, and lse beside it in the form and order
-// that the kernels below read: by head, then query.  f16 besides: the largest squared norms of
-// dout's and v's rows (a maximum: the order does not matter).  A CTA takes 16 tokens and 32
-// heads; a row is C lanes of 8 elements.  Bound by reading out and dout once.
-constexpr int kStatTokens = 16, kStatHeads = 32, kStatThreads = 256;
+// that the kernel below reads: by head, then query.  f16 besides: the largest squared norms of
+// 16 rows of dout and v.  A CTA takes 16 tokens and 32 heads; a row is C lanes of 8
+// elements.  Bound by reading out and dout once.
+constexpr int kStatHeads = 32, kStatThreads = 256;
 
 template <typename T, int C>
 __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const AttnBwdParams p) {
   constexpr bool kNorms = Elem<T>::kDt == DT_F16;
   __shared__ float deltas[kStatHeads][kStatTokens + 1];
-  __shared__ float norms[kNorms ? 2 : 1][kStatHeads][kStatTokens + 1];  // of dout, of v
+  __shared__ float norms[kStatHeads][kStatTokens + 1];
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int longest = kNorms ? max(p.max_q, p.max_k) : p.max_q;
-  const int blocks = (longest + kStatTokens - 1) / kStatTokens;  // of a sequence
-  const int b = blockIdx.x / blocks, i0 = blockIdx.x % blocks * kStatTokens, h0 = blockIdx.y * kStatHeads;
-  const SeqRange s = bwd_range(p, b, tid == 0 && i0 == 0 && h0 == 0);
-  const bool keys = kNorms && i0 < s.kv && h0 < p.hkv;
-  if (i0 >= s.qlen && !keys) return;
+  const int h0 = blockIdx.y * kStatHeads;
+  // Lengths that do not fit are flagged here, a sequence by a thread.
+  const int64_t mine = static_cast<int64_t>(blockIdx.x) * kStatThreads + tid;
+  if ((p.cu || p.cu_k) && h0 == 0 && mine < p.batches) bwd_range(p, static_cast<int>(mine), true);
+  const bool values = static_cast<int>(blockIdx.x) >= p.q_stat_blocks;  // f16: v's rows
+  const TilePlace place =
+      values ? find_tile<kStatThreads, false>(p.cu_k, nullptr, p.batches, p.max_k, 0, 1, kStatTokens,
+                                              blockIdx.x - p.q_stat_blocks, nullptr)
+             : find_tile<kStatThreads, false>(p.cu, nullptr, p.batches, p.max_q, 0, 1, kStatTokens, blockIdx.x,
+                                              nullptr);
+  if (place.tile < 0 || (values && h0 >= p.hkv)) return;
+  const int b = place.sequence, i0 = place.tile * kStatTokens;
+  const SeqRange s = bwd_range(p, b, false);
+  const int n = values ? s.kv : s.qlen, heads = values ? p.hkv : p.hq;
   const int c = lane % C;
   auto row_sum = [&](float v) {
 #pragma unroll
@@ -45,56 +54,47 @@ __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const Att
 #pragma unroll 4
   for (int r = warp * (32 / C) + lane / C; r < kStatTokens * kStatHeads; r += kStep) {
     const int t = r / kStatHeads, hh = r % kStatHeads;
-    float sum = 0.f, square = 0.f, vsquare = 0.f;
-    if (i0 + t < s.qlen && h0 + hh < p.hq && c * 8 < p.d) {
-      const int64_t at = s.q0 + i0 + t, head = h0 + hh;
+    float sum = 0.f, square = 0.f;
+    if (i0 + t < n && h0 + hh < heads && c * 8 < p.d) {
+      const int64_t at = (values ? s.k0 : s.q0) + static_cast<int64_t>(i0) + t, head = h0 + hh;
       float x[8], y[8];
-      eight<T>(p.out, at * p.ot + head * p.oh + c * 8, x);
-      eight<T>(p.dout, at * p.gt + head * p.gh + c * 8, y);
+      if (!values) {
+        eight<T>(p.out, at * p.ot + head * p.oh + c * 8, x);
+        eight<T>(p.dout, at * p.gt + head * p.gh + c * 8, y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sum = fmaf(x[e], y[e], sum);
-        square = fmaf(y[e], y[e], square);
+        for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
+      } else {
+        eight<T>(p.v, at * p.vt + head * p.vh + c * 8, y);
+      }
+      if (kNorms) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) square = fmaf(y[e], y[e], square);
       }
     }
     sum = row_sum(sum);
-    if (c == 0) deltas[hh][t] = -sum;
-    if constexpr (kNorms) {
-      if (keys && i0 + t < s.kv && h0 + hh < p.hkv && c * 8 < p.d) {
-        float y[8];
-        eight<T>(p.v, (static_cast<int64_t>(s.k0) + i0 + t) * p.vt + (h0 + hh) * p.vh + c * 8, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) vsquare = fmaf(y[e], y[e], vsquare);
-      }
-      square = row_sum(square);
-      vsquare = row_sum(vsquare);
-      if (c == 0) {
-        norms[0][hh][t] = square;
-        norms[kNorms][hh][t] = vsquare;
-      }
+    if (kNorms) square = row_sum(square);
+    if (c == 0) {
+      deltas[hh][t] = -sum;
+      if (kNorms) norms[hh][t] = square;
     }
   }
   __syncthreads();
   const int64_t base = stat_base(s.q0, b) + i0;
-  for (int r = tid; r < kStatTokens * kStatHeads; r += kStatThreads) {
+  for (int r = tid; !values && r < kStatTokens * kStatHeads; r += kStatThreads) {
     const int t = r % kStatTokens, hh = r / kStatTokens;
-    if (i0 + t >= s.qlen || h0 + hh >= p.hq) continue;
+    if (i0 + t >= n || h0 + hh >= heads) continue;
     const int64_t at = (h0 + hh) * p.stat_stride + base + t;
     p.ndelta[at] = deltas[hh][t];
     p.nlse[at] = fmaf(p.lse[(s.q0 + static_cast<int64_t>(i0) + t) * p.hq + h0 + hh], -kAttnLog2e,
                       static_cast<float>(kWeightLog2<T>));
   }
-  if constexpr (kNorms) {
-    if (tid < 2 * kStatHeads) {
-      const int w = tid / kStatHeads, hh = tid % kStatHeads;
-      float most = 0.f;
+  if (kNorms && tid < kStatHeads && h0 + tid < heads) {
+    float most = 0.f;
 #pragma unroll
-      for (int t = 0; t < kStatTokens; ++t) most = fmax_nan(most, norms[w * kNorms][hh][t]);
-      const int head = w ? h0 + hh : (h0 + hh) / p.group;
-      // (bits of numbers that are not negative order as they do, NaN above all)
-      if (head < p.hkv && most != 0.f)
-        atomicMax(p.norms + 2 * (static_cast<int64_t>(b) * p.hkv + head) + w, __float_as_uint(most) & 0x7FFFFFFFu);
-    }
+    for (int t = 0; t < kStatTokens; ++t) most = fmax_nan(most, norms[tid][t]);
+    const int64_t head = h0 + tid;
+    if (values) p.v_norms[head * p.v_norm_stride + norm_base(s.k0, b) + place.tile] = most;
+    else p.q_norms[head * p.q_norm_stride + norm_base(s.q0, b) + place.tile] = most;
   }
 }
 
@@ -128,10 +128,7 @@ struct BwdBarriers {
   uint64_t full[8], empty[8], s_full, p_full[2], dp_full, ds_full[2], x_full, x_ready, acc_full;
   uint64_t turn[2], stat_full[2], stat_empty[2], cut[2], zeroed[2];
   uint32_t tmem;
-  int sequence;  // of this CTA
 };
-
-constexpr int kSortBatches = 256;  // up to so many sequences are taken by length
 
 template <int DP, bool KV>
 struct BwdShape {
@@ -146,70 +143,69 @@ struct BwdShape {
   static constexpr int kSlots = DP == 128 && kXInTmem ? kFirst + 2 : kFirst;
   static constexpr int kStats = (kFirst + 2) * kSlot;  // then -lse and -delta, two stages
   static constexpr int kStat = kBwdTile * 4;
-  static constexpr int kBody = kStats + 4 * kStat;
-  static constexpr int kSmem = kBody + (int)sizeof(BwdBarriers);
-  static_assert(kSmem <= 232448 && kSlots <= 8, "");
+  static_assert(kSlots <= 8, "");
   static constexpr int kThreads = 384;
   // 256 x softmax + 128 x other = threads x launch, exactly.
   static constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
   static_assert(256 * kRegsSoftmax + 128 * kRegsOther == kThreads * kRegsLaunch, "");
 };
 constexpr int kPass = 4;  // instructions before its end that a turn passes (2 and 8: 1 % slower)
+template <int DP>
+struct BwdShared {
+  static constexpr int kBody = BwdShape<DP, true>::kStats + 4 * BwdShape<DP, true>::kStat;
+  static constexpr int kSmem = kBody + (int)sizeof(BwdBarriers);
+  static_assert(kSmem <= 232448, "");
+};
 constexpr int kBwdMmaWarp = 8, kBwdMmaWarp2 = 9, kBwdLoadWarp = 10, kBwdZeroWarp = 11;
 
+// The largest of `n` numbers from `at` on, in `rows` rows `stride` apart (by a whole warp).
+__device__ __forceinline__ float warp_largest(const float* at, int64_t stride, int rows, int n) {
+  float most = 0.f;
+  for (int r = 0; r < rows; ++r)
+#pragma unroll 4
+    for (int i = threadIdx.x & 31; i < n; i += 32) most = fmax_nan(most, at[r * stride + i]);
+  return warp_max_nan(most);
+}
+
 // What f16 ds is taken larger by: a power of two u with u |dout_i| |v_j| 2 < 2^15 for every
-// pair of the sequence and kv head (|ds| <= |dp| + |delta|, and |delta| is a mean of dp).  ds
-// falls with the number of keys and f16 ends early: without it, gradients of long
-// sequences would be sums of numbers without bits.
-template <typename T>
-__device__ __forceinline__ float ds_factor(const AttnBwdParams& p, int b, int h) {
+// pair of this CTA (|ds| <= |dp| + |delta|, and |delta| is a mean of dp).  ds falls with the
+// number of keys and f16 ends early: without it, gradients of long sequences would be sums
+// of numbers without bits.
+template <typename T, bool KV>
+__device__ __forceinline__ float ds_factor(const AttnBwdParams& p, const SeqRange& s, int b, int xh, int h,
+                                           int x0, int rows) {
   if constexpr (Elem<T>::kDt != DT_F16) return 1.f;
-  const uint32_t* m = p.norms + 2 * (static_cast<int64_t>(b) * p.hkv + h);
-  const float most = 2.f * sqrtf(__uint_as_float(m[0])) * sqrtf(__uint_as_float(m[1]));
+  auto runs = [](int n) { return (n + kStatTokens - 1) / kStatTokens; };
+  const float* q = p.q_norms + (KV ? h * p.group : xh) * p.q_norm_stride + norm_base(s.q0, b);
+  const float* v = p.v_norms + h * p.v_norm_stride + norm_base(s.k0, b);
+  const float mq = KV ? warp_largest(q, p.q_norm_stride, p.group, runs(s.qlen))
+                      : warp_largest(q + x0 / kStatTokens, 0, 1, runs(rows));
+  const float mv = KV ? warp_largest(v + x0 / kStatTokens, 0, 1, runs(rows)) : warp_largest(v, 0, 1, runs(s.kv));
+  const float most = 2.f * sqrtf(mq) * sqrtf(mv);
   if (!(most > 0.f) || !(most < INFINITY)) return 1.f;
   const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 100);
   return __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
 }
 
 template <typename T, int DP, bool KV>
-__global__ void __launch_bounds__(BwdShape<DP, KV>::kThreads, 1)
-    attention_bwd_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ CUtensorMap x1map,
-                         const __grid_constant__ CUtensorMap x2map,
-                         const __grid_constant__ CUtensorMap y1map,
-                         const __grid_constant__ CUtensorMap y2map) {
+__device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const CUtensorMap& x1map,
+                                                   const CUtensorMap& x2map, const CUtensorMap& y1map,
+                                                   const CUtensorMap& y2map, int block, uint8_t* raw) {
   using Shape = BwdShape<DP, KV>;
   constexpr int kType = std::is_same<T, __half>::value ? 0 : 1;
-  extern __shared__ __align__(1024) uint8_t raw[];
-  BwdBarriers& bars = *reinterpret_cast<BwdBarriers*>(raw + Shape::kBody);
+  BwdBarriers& bars = *reinterpret_cast<BwdBarriers*>(raw + BwdShared<DP>::kBody);
 
-  pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // The longest work first: sequences by their pairs, causal keys from the first on (the most
   // queries see those), queries from the last.
-  uint32_t bx = blockIdx.x;
-  const int heads = KV ? p.hkv : p.hq, x_tiles = KV ? p.k_tiles : p.q_tiles;
-  const int xh = bx % heads;
-  bx /= heads;
-  const int xt = KV ? bx % x_tiles : x_tiles - 1 - static_cast<int>(bx % x_tiles);
-  int b = bx / x_tiles;
-  if (p.batches > 1 && p.batches <= kSortBatches && (p.cu || p.cu_k)) {
-    auto pairs_of = [&](int i) {
-      return static_cast<float>(p.cu ? p.cu[i + 1] - p.cu[i] : p.max_q) *
-             static_cast<float>(p.cu_k ? p.cu_k[i + 1] - p.cu_k[i] : p.max_k);
-    };
-    for (int i = tid; i < p.batches; i += Shape::kThreads) {
-      const float mine = pairs_of(i);
-      int before = 0;
-#pragma unroll 8
-      for (int j = 0; j < p.batches; ++j) {
-        const float other = pairs_of(j);
-        before += other > mine || (other == mine && j < i);
-      }
-      if (before == b) bars.sequence = i;
-    }
-    __syncthreads();
-    b = bars.sequence;
-  }
+  const int heads = KV ? p.hkv : p.hq;
+  const int xh = block % heads;
+  const TilePlace place = KV ? find_tile<Shape::kThreads>(p.cu_k, p.cu, p.batches, p.max_k, p.max_q, 1, kBwdTile,
+                                                         block / heads, raw)
+                             : find_tile<Shape::kThreads>(p.cu, p.cu_k, p.batches, p.max_q, p.max_k, 1, kBwdTile,
+                                                         block / heads, raw);
+  if (place.tile < 0) return;
+  const int b = place.sequence, xt = KV ? place.tile : place.tiles - 1 - place.tile;
   const SeqRange s = bwd_range(p, b, false);
   const int nx = KV ? s.kv : s.qlen, ny = KV ? s.qlen : s.kv, x0 = xt * kBwdTile;
   const int rows = min(kBwdTile, nx - x0);
@@ -456,7 +452,7 @@ __global__ void __launch_bounds__(BwdShape<DP, KV>::kThreads, 1)
     // The rows of y that this thread's row goes with.
     const int lo = !live ? 0 : KV ? query_first(p, s, x) : key_first(p, s, x);
     const int hi = !live ? 0 : KV ? query_end(p, s, x) : key_end(p, s, x);
-    const float up = ds_factor<T>(p, b, h);
+    const float up = ds_factor<T, KV>(p, s, b, xh, h, x0, rows);
     const uint64_t sc2 = p2(p.scale_log2, p.scale_log2);
     const float back = ex2(-static_cast<float>(kWeightLog2<T>));  // P is 2^kWeightLog2 larger
     const uint64_t up2 = p2(up * back, up * back);
@@ -673,32 +669,35 @@ __global__ void __launch_bounds__(BwdShape<DP, KV>::kThreads, 1)
   if (warp == kBwdMmaWarp) tc_dealloc(tmem);
 }
 
-template <typename T, int DP, bool KV>
-cudaError_t launch_tiles(const AttnBwdParams& p, const CUtensorMap* m, cudaStream_t st) {
-  auto k = attention_bwd_kernel<T, DP, KV>;
+// One launch for all gradients: dk and dv's CTAs first, dq's into the room that they leave.
+template <typename T, int DP>
+__global__ void __launch_bounds__(BwdShape<DP, true>::kThreads, 1)
+    attention_bwd_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ CUtensorMap q,
+                         const __grid_constant__ CUtensorMap k, const __grid_constant__ CUtensorMap v,
+                         const __grid_constant__ CUtensorMap dout) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  pdl_begin();
+  const int block = blockIdx.x;
+  if (block < p.kv_blocks) attention_bwd_tile<T, DP, true>(p, k, v, q, dout, block, raw);
+  else attention_bwd_tile<T, DP, false>(p, q, dout, k, v, block - p.kv_blocks, raw);
+}
+
+template <typename T, int DP>
+cudaError_t launch_tiles(const AttnBwdParams& p, const CUtensorMap* m, int64_t grid, cudaStream_t st) {
+  auto k = attention_bwd_kernel<T, DP>;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(k, BwdShape<DP, KV>::kSmem, done);
+  const cudaError_t e = allow_smem(k, BwdShared<DP>::kSmem, done);
   if (e != cudaSuccess) return e;
-  const int64_t grid = KV ? int64_t(p.k_tiles) * p.batches * p.hkv : int64_t(p.q_tiles) * p.batches * p.hq;
-  if (grid == 0) return cudaSuccess;
-  const dim3 g(static_cast<unsigned>(grid)), t(BwdShape<DP, KV>::kThreads);
-  // m: q, k, v, dout
-  return KV ? launch_pdl(k, g, t, BwdShape<DP, KV>::kSmem, st, p, m[1], m[2], m[0], m[3])
-            : launch_pdl(k, g, t, BwdShape<DP, KV>::kSmem, st, p, m[0], m[3], m[1], m[2]);
+  return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(BwdShape<DP, true>::kThreads),
+                    BwdShared<DP>::kSmem, st, p, m[0], m[1], m[2], m[3]);
 }
 
 template <typename T>
 cudaError_t launch_bwd(const AttnBwdParams& p, cudaStream_t st) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   cudaError_t e = cudaSuccess;
-  if (!kBf16) {
-    e = cudaMemsetAsync(p.norms, 0, static_cast<size_t>(p.batches) * p.hkv * 8, st);
-    if (e != cudaSuccess) return e;
-  }
-  const int longest = kBf16 || p.max_q > p.max_k ? p.max_q : p.max_k;
-  if (longest > 0) {
-    const dim3 g(static_cast<unsigned>((longest + kStatTokens - 1) / kStatTokens) * p.batches,
-                 (p.hq + kStatHeads - 1) / kStatHeads);
+  if (p.stat_blocks > 0) {
+    const dim3 g(static_cast<unsigned>(p.stat_blocks), (p.hq + kStatHeads - 1) / kStatHeads);
     e = p.d <= 64 ? launch_pdl(attention_stats_kernel<T, 8>, g, dim3(kStatThreads), 0, st, p)
                   : launch_pdl(attention_stats_kernel<T, 16>, g, dim3(kStatThreads), 0, st, p);
     if (e != cudaSuccess) return e;
@@ -709,9 +708,9 @@ cudaError_t launch_bwd(const AttnBwdParams& p, cudaStream_t st) {
       !make_packed_map(&m[2], p.v, kBf16, p.d, p.hkv, p.keys, p.vt, p.vh, kBwdTile) ||
       !make_packed_map(&m[3], p.dout, kBf16, p.d, p.hq, p.tokens, p.gt, p.gh, kBwdTile))
     return cudaErrorInvalidValue;
-  e = p.d <= 64 ? launch_tiles<T, 64, true>(p, m, st) : launch_tiles<T, 128, true>(p, m, st);
-  if (e != cudaSuccess) return e;
-  return p.d <= 64 ? launch_tiles<T, 64, false>(p, m, st) : launch_tiles<T, 128, false>(p, m, st);
+  const int64_t grid = p.kv_blocks + p.q_blocks;
+  if (grid == 0) return cudaSuccess;
+  return p.d <= 64 ? launch_tiles<T, 64>(p, m, grid, st) : launch_tiles<T, 128>(p, m, grid, st);
 }
 
 // ---- host side
@@ -738,7 +737,6 @@ gbn_status check_sizes(const AttnSizes& z, gbn_dtype dtype) {
   return GBN_OK;
 }
 
-int64_t tiles(int64_t n, int64_t of) { return (n + of - 1) / of; }
 
 // (token, head) strides of a tensor of `rows` tokens: multiples of 16 bytes; `map`: read
 // through a tensor map, which takes strides in (0, 2^40) bytes.
@@ -754,6 +752,9 @@ gbn_status check_tensor(const void* ptr, const int64_t* st, int64_t rows, int64_
 }
 
 int64_t align_up(int64_t n, int64_t a) { return (n + a - 1) / a * a; }
+
+// Elements of one head's norms of `rows` rows: every sequence's runs behind the last one's.
+int64_t norm_elements(int64_t rows, int64_t batches) { return rows / kStatTokens + batches + 1; }
 
 // Elements of one head's statistics: every sequence on a multiple of 4, and a whole tile
 // behind the last.
@@ -817,23 +818,27 @@ gbn_status gbn_attention_fwd(const gbn_attention_fwd_args* args, cudaStream_t st
   p.max_kv = static_cast<int>(z.max_k);
   p.causal = c.causal != 0;
   p.window = static_cast<int>(z.window);
-  const int64_t longest = z.max_q < z.tokens ? z.max_q : z.tokens;
-  p.row_tiles = static_cast<int>(tiles(longest * p.group, kPrefillRows));
+  const int64_t blocks = tile_blocks(p.cu, z.tokens, z.batches, z.max_q < z.tokens ? z.max_q : z.tokens,
+                                     kPrefillRows, p.group);
+  if (blocks * z.kv_heads > INT32_MAX) return GBN_ERR_SHAPE;
+  p.row_tiles = static_cast<int>(blocks);  // of all sequences
   p.splits = 1;
   p.split_len = INT32_MAX;
   p.scale_log2 = c.scale * kAttnLog2e;
-  if (int64_t(p.row_tiles) * z.batches * z.kv_heads > INT32_MAX) return GBN_ERR_SHAPE;
   return launch_attention_fwd(p, dtype, stream) == cudaSuccess ? GBN_OK : GBN_ERR_CUDA;
 }
 
-gbn_status gbn_attention_bwd_workspace_size(int64_t tokens, int64_t batches, int64_t q_heads,
-                                            int64_t kv_heads, gbn_dtype dtype, size_t* bytes) {
+gbn_status gbn_attention_bwd_workspace_size(int64_t tokens, int64_t keys, int64_t batches,
+                                            int64_t q_heads, int64_t kv_heads, gbn_dtype dtype,
+                                            size_t* bytes) {
   if (!bytes) return GBN_ERR_NULL;
-  AttnSizes z{tokens, 0, batches, q_heads, kv_heads, 8, 0, 0, 0, true, true};
+  AttnSizes z{tokens, keys, batches, q_heads, kv_heads, 8, 0, 0, 0, true, true};
   const gbn_status st = check_sizes(z, dtype);
   if (st != GBN_OK) return st;
-  *bytes = static_cast<size_t>(2 * q_heads * stat_elements(z) * 4 +
-                               align_up(dtype == GBN_F16 ? batches * kv_heads * 8 : 0, 256));
+  const int64_t norms = dtype == GBN_F16 ? q_heads * norm_elements(tokens, batches) +
+                                               kv_heads * norm_elements(keys, batches)
+                                         : 0;
+  *bytes = static_cast<size_t>((2 * q_heads * stat_elements(z) + norms) * 4);
   return GBN_OK;
 }
 
@@ -859,7 +864,7 @@ gbn_status gbn_attention_bwd(const gbn_attention_bwd_args* args, cudaStream_t st
       (st = check_tensor(c.dv, c.dv_strides, z.keys, z.kv_heads, false)) != GBN_OK)
     return st;
   size_t need = 0;
-  st = gbn_attention_bwd_workspace_size(z.tokens, z.batches, z.q_heads, z.kv_heads, dtype, &need);
+  st = gbn_attention_bwd_workspace_size(z.tokens, z.keys, z.batches, z.q_heads, z.kv_heads, dtype, &need);
   if (st != GBN_OK) return st;
   if (!c.workspace || c.workspace_bytes < need || (reinterpret_cast<uintptr_t>(c.workspace) & 15u))
     return GBN_ERR_WORKSPACE;
@@ -880,7 +885,10 @@ gbn_status gbn_attention_bwd(const gbn_attention_bwd_args* args, cudaStream_t st
   p.stat_stride = stat_elements(z);
   p.nlse = static_cast<float*>(c.workspace);
   p.ndelta = p.nlse + z.q_heads * p.stat_stride;
-  p.norms = dtype == GBN_F16 ? reinterpret_cast<uint32_t*>(p.ndelta + z.q_heads * p.stat_stride) : nullptr;
+  p.q_norm_stride = norm_elements(z.tokens, z.batches);
+  p.v_norm_stride = norm_elements(z.keys, z.batches);
+  p.q_norms = p.ndelta + z.q_heads * p.stat_stride;  // (f16 only)
+  p.v_norms = p.q_norms + z.q_heads * p.q_norm_stride;
   p.qt = c.q_strides[0];
   p.qh = c.q_strides[1];
   p.kt = c.k_strides[0];
@@ -908,11 +916,16 @@ gbn_status gbn_attention_bwd(const gbn_attention_bwd_args* args, cudaStream_t st
   p.max_k = static_cast<int>(z.max_k < z.keys ? z.max_k : z.keys);
   p.causal = c.causal != 0;
   p.window = static_cast<int>(z.window);
-  p.q_tiles = static_cast<int>(tiles(p.max_q, kBwdTile));
-  p.k_tiles = static_cast<int>(tiles(p.max_k, kBwdTile));
-  if (p.q_tiles * z.batches * z.q_heads > INT32_MAX || p.k_tiles * z.batches * z.kv_heads > INT32_MAX ||
-      tiles(p.max_q > p.max_k ? p.max_q : p.max_k, kStatTokens) * z.batches > INT32_MAX)
-    return GBN_ERR_SHAPE;
+  const int64_t kv_blocks = tile_blocks(p.cu_k, z.keys, z.batches, p.max_k, kBwdTile) * z.kv_heads;
+  const int64_t q_blocks = tile_blocks(p.cu, z.tokens, z.batches, p.max_q, kBwdTile) * z.q_heads;
+  const int64_t q_stats = tile_blocks(p.cu, z.tokens, z.batches, p.max_q, kStatTokens, 1, false);
+  const int64_t v_stats =
+      dtype == GBN_F16 ? tile_blocks(p.cu_k, z.keys, z.batches, p.max_k, kStatTokens, 1, false) : 0;
+  if (kv_blocks + q_blocks > INT32_MAX || q_stats + v_stats > INT32_MAX) return GBN_ERR_SHAPE;
+  p.q_stat_blocks = static_cast<int>(q_stats);
+  p.stat_blocks = static_cast<int>(q_stats + v_stats);
+  p.kv_blocks = static_cast<int>(kv_blocks);
+  p.q_blocks = static_cast<int>(q_blocks);
   p.scale = c.scale;
   p.scale_log2 = c.scale * kAttnLog2e;
   const cudaError_t e = dtype == GBN_BF16 ? launch_bwd<__nv_bfloat16>(p, stream)

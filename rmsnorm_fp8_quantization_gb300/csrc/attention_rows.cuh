@@ -18,17 +18,20 @@ struct AttnBwdParams {
   void *dq, *dk, *dv;
   float* nlse;    // [hq][stat_stride]: -lse log2(e) (+ kWeightLog2), sequences 16-byte aligned
   float* ndelta;  // [hq][stat_stride]: -delta
-  uint32_t* norms;  // f16: [batches][hkv][2]: largest squared norms of dout's and v's rows
+  float* q_norms;  // f16: [hq][q_norm_stride], largest squared norms of kStatTokens rows of dout
+  float* v_norms;  // and [hkv][v_norm_stride] of v
   int64_t qt, qh, kt, kh, vt, vh, ot, oh, gt, gh;  // element strides: token, head (g: dout)
   int64_t dqt, dqh, dkt, dkh, dvt, dvh;
-  int64_t stat_stride;
+  int64_t stat_stride, q_norm_stride, v_norm_stride;
   int tokens, keys, batches, hq, hkv, group, d, max_q, max_k;
   int causal, window;
-  int q_tiles, k_tiles;  // of 128 rows, of the longest sequence
+  int kv_blocks, q_blocks;         // CTAs for dk and dv, and for dq
+  int q_stat_blocks, stat_blocks;  // of the row statistics: for q's rows, and with v's
   float scale, scale_log2;
 };
 
-constexpr int kBwdTile = 128;  // queries and keys of a tile
+constexpr int kBwdTile = 128;   // queries and keys of a tile
+constexpr int kStatTokens = 16;  // rows that share a norm
 
 // f16 ends at 2^-14 (2^-24 with fewer bits) where fp32 and bf16 go on, and probabilities
 // reach that with a few thousand keys: f16 ones are taken 2^12 larger (at most 2^12 then,
@@ -41,6 +44,9 @@ constexpr int kWeightLog2 = Elem<T>::kDt == DT_F16 ? 12 : 0;
 __device__ __forceinline__ int64_t stat_base(int q0, int b) {
   return (static_cast<int64_t>(q0) + 3 * static_cast<int64_t>(b) + 3) & ~int64_t(3);
 }
+
+// Where the norms of sequence b's rows begin (its first row: `first`).
+__device__ __forceinline__ int64_t norm_base(int first, int b) { return first / kStatTokens + b; }
 
 __device__ __forceinline__ SeqRange bwd_range(const AttnBwdParams& p, int b, bool flag) {
   return packed_range(p.cu, p.cu_k, b, p.tokens, p.keys, p.max_q, p.max_k, flag);

@@ -44,6 +44,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "packed_tiles.cuh"
 #include "paged_rows.cuh"
 #include "tensor_core.cuh"
 
@@ -128,31 +129,44 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
   uint32_t x = blockIdx.x;
   const int h = x % p.hkv;
   x /= p.hkv;
-  const int split = x % p.splits;
-  x /= p.splits;
-  const int rt = p.row_tiles - 1 - static_cast<int>(x % p.row_tiles);
-  int b = x / p.row_tiles;
-  if (p.batches > 1 && p.batches <= kSortBatches && (!PACKED || p.cu_k)) {
-    auto keys_of = [&](int i) { return PACKED ? p.cu_k[i + 1] - p.cu_k[i] : p.kv_lens[i]; };
-    // The sequence with b longer ones.  Every CTA counts for itself: a few hundred
-    // cycles against a second launch.
-    for (int i = tid; i < p.batches; i += Shape::kThreads) {
-      const int mine = keys_of(i);
-      int before = 0;
+  int split = 0, rt, b;
+  SeqRange s;
+  if constexpr (PACKED) {
+    // Lengths that do not fit are flagged a sequence by a thread.
+    auto range = [&](int i, bool flag) {
+      return packed_range(p.cu, p.cu_k, i, p.tokens, p.keys, p.max_q, p.max_kv, flag);
+    };
+    const int64_t mine = static_cast<int64_t>(blockIdx.x) * Shape::kThreads + tid;
+    if ((p.cu || p.cu_k) && mine < p.batches) range(static_cast<int>(mine), true);
+    const TilePlace place = find_tile<Shape::kThreads>(p.cu, p.cu_k, p.batches, p.max_q, p.max_kv, p.group,
+                                                       kPrefillRows, static_cast<int>(x), raw);
+    if (place.tile < 0) return;
+    b = place.sequence;
+    rt = place.tiles - 1 - place.tile;
+    s = range(b, false);
+  } else {
+    split = x % p.splits;
+    x /= p.splits;
+    rt = p.row_tiles - 1 - static_cast<int>(x % p.row_tiles);
+    b = x / p.row_tiles;
+    if (p.batches > 1 && p.batches <= kSortBatches) {
+      // The sequence with b longer ones.  Every CTA counts for itself: a few hundred
+      // cycles against a second launch.
+      for (int i = tid; i < p.batches; i += Shape::kThreads) {
+        const int mine = p.kv_lens[i];
+        int before = 0;
 #pragma unroll 8
-      for (int j = 0; j < p.batches; ++j) {
-        const int kv = keys_of(j);
-        before += kv > mine || (kv == mine && j < i);
+        for (int j = 0; j < p.batches; ++j) {
+          const int kv = p.kv_lens[j];
+          before += kv > mine || (kv == mine && j < i);
+        }
+        if (before == b) bars.sequence = i;
       }
-      if (before == b) bars.sequence = i;
+      __syncthreads();
+      b = bars.sequence;
     }
-    __syncthreads();
-    b = bars.sequence;
+    s = seq_range(p, b, tid == 0 && split == 0 && rt == 0 && h == 0);
   }
-
-  const bool flag = tid == 0 && split == 0 && rt == 0 && h == 0;
-  const SeqRange s = PACKED ? packed_range(p.cu, p.cu_k, b, p.tokens, p.keys, p.max_q, p.max_kv, flag)
-                            : seq_range(p, b, flag);
   const int r0 = rt * kPrefillRows;
   const int rows = min(kPrefillRows, s.qlen * p.group - r0);
   if (rows <= 0) return;
@@ -779,7 +793,8 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(k, Shape::kSmem, done);
   if (e != cudaSuccess) return e;
-  const int64_t grid = int64_t(p.row_tiles) * p.batches * p.splits * p.hkv;
+  // (contiguous keys: row_tiles counts those of all sequences)
+  const int64_t grid = int64_t(p.row_tiles) * (PACKED ? 1 : p.batches) * p.splits * p.hkv;
   return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(Shape::kThreads), Shape::kSmem, st, p,
                     km, vm);
 }

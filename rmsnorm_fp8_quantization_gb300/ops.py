@@ -760,9 +760,9 @@ def attention_fwd(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, max_q=None, ma
 def attention_bwd_workspace(q, k, cu_seqlens=None):
     """A workspace for ``attention_bwd`` calls with these q, k and cu_seqlens."""
     _on_gpu(q)
-    tokens = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
+    tokens, keys = (t.shape[0] if t.dim() == 3 else t.shape[0] * t.shape[1] for t in (q, k))
     batches = q.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    return torch.empty(_attention_bwd_bytes(tokens, batches, q.shape[-2], k.shape[-2],
+    return torch.empty(_attention_bwd_bytes(tokens, keys, batches, q.shape[-2], k.shape[-2],
                                             G.TORCH_DTYPE[q.dtype]), dtype=torch.uint8,
                        device=q.device)
 
@@ -803,7 +803,7 @@ def attention_bwd(dout, q, k, v, out, lse, *, cu_seqlens=None, cu_seqlens_k=None
     y = tuple(_tokens(n, t, q) for n, t in (("dq", dq), ("dk", dk), ("dv", dv)))
     dt = G.TORCH_DTYPE[q.dtype]
     if workspace is None:
-        size = _attention_bwd_bytes(sizes[0], sizes[2], sizes[3], sizes[4], dt)
+        size = _attention_bwd_bytes(*sizes[:5], dt)
         workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
     else:
         if workspace.device != q.device or not workspace.is_contiguous():
