@@ -35,15 +35,22 @@ enum Mode { kDraw, kKeep, kDrop };
 constexpr int kThreads = 256;
 constexpr int kBytes = 32;  // of x a thread takes (two 16-byte vectors)
 
+__device__ __forceinline__ void wide(uint32_t a, uint32_t b, uint32_t* lo, uint32_t* hi) {
+  asm("{\n\t.reg .b64 t;\n\tmul.wide.u32 t, %2, %3;\n\tmov.b64 {%0, %1}, t;\n\t}"
+      : "=r"(*lo), "=r"(*hi)
+      : "r"(a), "r"(b));
+}
 __device__ __forceinline__ uint4 philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0,
                                         uint32_t k1) {
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
-    const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u, b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
-    c1 = static_cast<uint32_t>(b);
-    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
-    c3 = static_cast<uint32_t>(a);
+    uint32_t alo, ahi, blo, bhi;
+    wide(c0, 0xD2511F53u, &alo, &ahi);
+    wide(c2, 0xCD9E8D57u, &blo, &bhi);
+    c0 = bhi ^ c1 ^ k0;
+    c1 = blo;
+    c2 = ahi ^ c3 ^ k1;
+    c3 = alo;
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
@@ -104,14 +111,15 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p
         keep[d * 4 + e] = MODE == kKeep || (MODE == kDraw && words[e] >= p.least);
     }
     if (VEC && e0 + kElems <= p.n) {
-      float f[kElems], r[kElems];
+      float f[kElems] = {}, r[kElems];
       if (MODE != kDrop) unpack<T, kElems>(xw[u], f);
       if (ADD) unpack<T, kElems>(rw[u], r);
       uint64_t o[kElems / 2];
 #pragma unroll
       for (int e = 0; e < kElems; e += 2) {
-        const float a = keep[e] ? f[e] * p.scale : 0.f, b = keep[e + 1] ? f[e + 1] * p.scale : 0.f;
-        o[e / 2] = ADD ? add2(p2(a, b), p2(r[e], r[e + 1])) : p2(a, b);
+        const float2 y = u2(mul2(p2(f[e], f[e + 1]), p2(p.scale, p.scale)));
+        o[e / 2] = p2(keep[e] ? y.x : 0.f, keep[e + 1] ? y.y : 0.f);
+        if (ADD) o[e / 2] = add2(o[e / 2], p2(r[e], r[e + 1]));
       }
       uint32_t w[4];
       narrow_pairs<T, kElems>(o, w);
