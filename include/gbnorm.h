@@ -544,12 +544,13 @@ gbn_status gbn_attention_fwd(const gbn_attention_fwd_args* args, cudaStream_t st
  * results; p and ds are rounded to dtype for their products: half a step
  * relative.  f16: probabilities below 2^-26 by up to 2^-37, ds below 2^-29 of
  * the largest |dout_i| |v_j| of the sequence and kv head by up to 2^-40 of it.
- *   workspace  gbn_attention_bwd_workspace_size() bytes, 16-byte aligned (else
- *              GBN_ERR_WORKSPACE); needs no initialization; calls that may
+ *   workspace  gbn_attention_bwd_workspace_size() bytes (same arguments), 16-byte
+ *              aligned (else GBN_ERR_WORKSPACE); needs no initialization; calls that may
  *              overlap on the GPU need one each. */
 gbn_status gbn_attention_bwd_workspace_size(int64_t tokens, int64_t keys, int64_t batches,
-                                            int64_t q_heads, int64_t kv_heads, gbn_dtype dtype,
-                                            size_t* bytes);
+                                            int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                            int64_t max_q, int64_t max_k, int64_t window, int causal,
+                                            gbn_dtype dtype, size_t* bytes);
 typedef struct {
   const void* q;
   const void* k;

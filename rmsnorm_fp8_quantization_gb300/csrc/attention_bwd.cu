@@ -1,5 +1,6 @@
 // Attention over whole sequences, forward (host side; the kernel is the prompts' of
 // paged_prefill.cu) and backward.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -200,10 +201,13 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
   // queries see those), queries from the last.
   const int heads = KV ? p.hkv : p.hq;
   const int xh = block % heads;
+  block /= heads;
+  const int splits = KV ? p.kv_splits : p.q_splits, split = block % splits;
+  block /= splits;
   const TilePlace place = KV ? find_tile<Shape::kThreads>(p.cu_k, p.cu, p.batches, p.max_k, p.max_q, 1, kBwdTile,
-                                                         block / heads, raw)
+                                                         block, raw)
                              : find_tile<Shape::kThreads>(p.cu, p.cu_k, p.batches, p.max_q, p.max_k, 1, kBwdTile,
-                                                         block / heads, raw);
+                                                         block, raw);
   if (place.tile < 0) return;
   const int b = place.sequence, xt = KV ? place.tile : place.tiles - 1 - place.tile;
   const SeqRange s = bwd_range(p, b, false);
@@ -218,7 +222,10 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
   const int y_hi = KV ? query_end(p, s, x0 + rows - 1) : key_end(p, s, x0 + rows - 1);
   const int base = y_lo & ~(kBwdTile - 1);
   const int nt = y_hi > y_lo ? (y_hi - base + kBwdTile - 1) / kBwdTile : 0;
-  const int n = nt * (KV ? p.group : 1);
+  // Of these steps (heads of the group times tiles) this CTA takes n from step0 on.
+  const int steps_all = nt * (KV ? p.group : 1), share = (steps_all + splits - 1) / splits;
+  const int step0 = min(split * share, steps_all), n = min(share, steps_all - step0);
+  const int t0 = nt > 0 ? step0 % nt : 0, g0 = nt > 0 ? step0 / nt : 0;
   // The last tile reaches beyond the sequence.
   const bool cut_last = base + nt * kBwdTile > ny;
 
@@ -313,7 +320,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
         };
         ok = mbar_wait(kXInTmem ? &bars.x_ready : &bars.x_full, 0);
         const int own = first ? 0 : 1;  // y1 or y2: what this thread's product reads
-        int y1 = 0, y2 = 0, left = nt;  // slots of the step before; tiles up to the sequence's end
+        int y1 = 0, y2 = 0, left = nt - t0;  // slots of the step before; tiles up to the sequence's end
         uint32_t zeros = 0;
         int slot = 0;
         uint32_t phase = 0;
@@ -386,7 +393,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
         tile(xs, &x1map, xh, xr, &bars.x_full);
         tile(xs + Shape::kSlot, &x2map, xh, xr, &bars.x_full);
         const int64_t stat = stat_base(s.q0, b) + base;
-        int slot = 0, issued = 0, t = 0, g = 0, i = 0;
+        int slot = 0, issued = 0, t = t0, g = g0, i = 0;
         uint32_t phase = 0;
         for (; ok && i < n; ++i) {
           const int yr = (KV ? s.q0 : s.k0) + base + t * kBwdTile;
@@ -424,15 +431,16 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
       __syncwarp();
     } else if (warp == kBwdZeroWarp && cut_last) {
       // ------------------------------------------------ rows of y behind the sequence
-      const int events = KV ? 2 * p.group : 1;
+      const int ends = nt > 0 ? (step0 + n) / nt - g0 : 0;  // of the sequence among the steps
+      const int events = KV ? 2 * ends : ends;
       const int from = ny - (base + (nt - 1) * kBwdTile);  // first row to zero of the last tile
       for (int e = 0; ok && e < events; ++e) {
         // (a whole range may lie before the last tile's turn: a longer limit)
-        const int own = e & 1, use = e >> 1;
+        const int own = KV ? e & 1 : 0, use = KV ? e >> 1 : e;
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(&bars.cut[own], use & 1, 30 * kWaitLimitNs));
         if (!ok) break;
-        const int64_t tile = KV ? 2 * (static_cast<int64_t>(e >> 1) * nt + nt - 1) + (e & 1)
-                                : 2 * static_cast<int64_t>(nt - 1);
+        const int head = KV ? e >> 1 : e;
+        const int64_t tile = 2 * (static_cast<int64_t>(g0 + head + 1) * nt - 1 - step0) + (KV ? e & 1 : 0);
         uint8_t* at = raw + static_cast<int>(tile % Shape::kSlots) * Shape::kSlot;
         for (int j = lane; j < (kBwdTile - from) * 8 * Shape::kPanels; j += 32)
           *reinterpret_cast<uint4*>(at + (j >> 3) % Shape::kPanels * Shape::kPanel +
@@ -483,7 +491,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.x_ready);
     }
-    int t = 0;
+    int t = t0;
     for (int i = 0; ok && i < n; ++i) {
       const ulonglong2* stat =
           reinterpret_cast<const ulonglong2*>(raw + Shape::kStats + (i & 1) * 2 * Shape::kStat + w * 256);
@@ -610,6 +618,19 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
+        if (splits > 1) {
+          // A part of a sum: 32-bit, put together by attention_join_kernel.
+          float* const part =
+              KV ? p.kv_part + (((static_cast<int64_t>(split) * 2 + (w == 0)) * p.keys + row) * p.hkv + xh) * p.d
+                 : p.q_part + ((static_cast<int64_t>(split) * p.tokens + row) * p.hq + xh) * p.d;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            if (live && col0 + c + e < p.d)
+              *reinterpret_cast<float4*>(part + col0 + c + e) =
+                  make_float4(__uint_as_float(o[e]) * factor, __uint_as_float(o[e + 1]) * factor,
+                              __uint_as_float(o[e + 2]) * factor, __uint_as_float(o[e + 3]) * factor);
+          continue;
+        }
         uint32_t bad = 0;  // bit e: a NaN in columns 8 e .. 8 e + 7
 #pragma unroll
         for (int e = 0; e < 32; e += 8) {
@@ -692,6 +713,60 @@ cudaError_t launch_tiles(const AttnBwdParams& p, const CUtensorMap* m, int64_t g
                     BwdShared<DP>::kSmem, st, p, m[0], m[1], m[2], m[3]);
 }
 
+// ---- sums in parts
+//
+// Few CTAs with many steps each (few heads that share their keys, one sequence) leave most
+// of the GPU idle: the steps of a tile go to several CTAs then, which write 32-bit parts,
+// and this kernel adds those up in order.  A thread takes eight columns of a row.  NaN:
+// computed pair by pair (see grad_again), which ends at once where it belongs there.
+template <typename T, int WHICH>
+__device__ __forceinline__ void join_rows(const AttnBwdParams& p, int block) {
+  const TilePlace place =
+      WHICH ? find_tile<kStatThreads, false>(p.cu_k, nullptr, p.batches, p.max_k, 0, 1, kStatTokens, block, nullptr)
+            : find_tile<kStatThreads, false>(p.cu, nullptr, p.batches, p.max_q, 0, 1, kStatTokens, block, nullptr);
+  if (place.tile < 0) return;
+  const int b = place.sequence, x0 = place.tile * kStatTokens;
+  const SeqRange s = bwd_range(p, b, false);
+  const int heads = WHICH ? p.hkv : p.hq, chunks = p.d / 8, splits = WHICH ? p.kv_splits : p.q_splits;
+  const int rows = min(kStatTokens, (WHICH ? s.kv : s.qlen) - x0);
+  const int64_t step = (WHICH ? 2 * static_cast<int64_t>(p.keys) * p.hkv : static_cast<int64_t>(p.tokens) * p.hq) * p.d;
+  for (int r = threadIdx.x; r < rows * heads * chunks; r += kStatThreads) {
+    const int col = r % chunks * 8, head = r / chunks % heads, x = x0 + r / chunks / heads;
+    const int64_t row = (WHICH ? s.k0 : s.q0) + static_cast<int64_t>(x);
+    const float* part = WHICH ? p.kv_part + (((WHICH == 1 ? 0 : 1) * static_cast<int64_t>(p.keys) + row) * p.hkv + head) * p.d + col
+                              : p.q_part + (row * p.hq + head) * p.d + col;
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < splits; ++i, part += step) {
+      const float4 a = *reinterpret_cast<const float4*>(part), c = *reinterpret_cast<const float4*>(part + 4);
+      f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w;
+      f[4] += c.x, f[5] += c.y, f[6] += c.z, f[7] += c.w;
+    }
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bad = bad || f[e] != f[e];
+    if (bad) grad_again<T, WHICH>(p, s, b, head, WHICH ? head : head / p.group, x, col, f);
+    uint32_t v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = narrow2<T>(p2(f[2 * q], f[2 * q + 1]));
+    T* const dst = static_cast<T*>(WHICH == 0 ? p.dq : WHICH == 1 ? p.dk : p.dv);
+    const int64_t at = WHICH == 0   ? row * p.dqt + head * p.dqh
+                       : WHICH == 1 ? row * p.dkt + head * p.dkh
+                                    : row * p.dvt + head * p.dvh;
+    *reinterpret_cast<uint4*>(dst + at + col) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+template <typename T>
+__global__ void __launch_bounds__(kStatThreads) attention_join_kernel(const AttnBwdParams p) {
+  pdl_begin();
+  const int block = blockIdx.x;
+  if (block >= p.kv_join_blocks) {
+    join_rows<T, 0>(p, block - p.kv_join_blocks);
+  } else {
+    join_rows<T, 1>(p, block);
+    join_rows<T, 2>(p, block);
+  }
+}
+
 template <typename T>
 cudaError_t launch_bwd(const AttnBwdParams& p, cudaStream_t st) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -710,7 +785,10 @@ cudaError_t launch_bwd(const AttnBwdParams& p, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const int64_t grid = p.kv_blocks + p.q_blocks;
   if (grid == 0) return cudaSuccess;
-  return p.d <= 64 ? launch_tiles<T, 64>(p, m, grid, st) : launch_tiles<T, 128>(p, m, grid, st);
+  e = p.d <= 64 ? launch_tiles<T, 64>(p, m, grid, st) : launch_tiles<T, 128>(p, m, grid, st);
+  if (e != cudaSuccess || p.join_blocks == 0) return e;
+  return launch_pdl(attention_join_kernel<T>, dim3(static_cast<unsigned>(p.join_blocks)), dim3(kStatThreads), 0,
+                    st, p);
 }
 
 // ---- host side
@@ -755,11 +833,45 @@ int64_t align_up(int64_t n, int64_t a) { return (n + a - 1) / a * a; }
 
 // Elements of one head's norms of `rows` rows: every sequence's runs behind the last one's.
 int64_t norm_elements(int64_t rows, int64_t batches) { return rows / kStatTokens + batches + 1; }
+int64_t norm_total(const AttnSizes& z, gbn_dtype dtype) {
+  return dtype != GBN_F16 ? 0
+                          : align_up(z.q_heads * norm_elements(z.tokens, z.batches) +
+                                         z.kv_heads * norm_elements(z.keys, z.batches), 4);
+}
 
 // Elements of one head's statistics: every sequence on a multiple of 4, and a whole tile
 // behind the last.
 int64_t stat_elements(const AttnSizes& z) {
   return align_up(z.tokens + 3 * z.batches + 3 + kBwdTile, 32);
+}
+
+// How many CTAs share a tile's steps.  A CTA's steps follow one another (about 1.2 us each for
+// dk and dv, 1 us for dq), so a launch takes at least as long as its longest one: where that
+// is more than a multiprocessor's share of the whole (152 of them, causal ones half full), it is
+// divided, down to 8 steps, below which beginning and end cost as much (one sequence of 4096
+// tokens, 8 / 2 heads of 128, causal: XXX us with one CTA a tile, XXX so).
+struct BwdPlan {
+  int kv_splits, q_splits;
+  int64_t kv_part, q_part;  // elements
+};
+BwdPlan plan_bwd(const AttnSizes& z, bool causal) {
+  const int64_t q_tiles = tiles(z.max_q, kBwdTile), k_tiles = tiles(z.max_k, kBwdTile);
+  const int64_t reach = causal && z.window > 0 ? tiles(z.window, kBwdTile) + 1 : kMaxRows;
+  const int64_t kv_steps = z.q_heads / z.kv_heads * std::min(q_tiles, reach), q_steps = std::min(k_tiles, reach);
+  const int64_t kv_ctas = std::min(k_tiles * z.batches, z.keys / kBwdTile + z.batches) * z.kv_heads;
+  const int64_t q_ctas = std::min(q_tiles * z.batches, z.tokens / kBwdTile + z.batches) * z.q_heads;
+  const double all = (causal ? 0.5 : 1.0) * (1.2 * static_cast<double>(kv_ctas) * static_cast<double>(kv_steps) +
+                                             static_cast<double>(q_ctas) * static_cast<double>(q_steps));
+  const int64_t most = std::max<int64_t>(8, static_cast<int64_t>(all / 152));
+  auto share = [&](int64_t steps) {
+    return steps * 4 <= most * 5 ? 1 : static_cast<int>(std::min<int64_t>(16, tiles(steps, most)));
+  };
+  BwdPlan r;
+  r.kv_splits = share(kv_steps);
+  r.q_splits = share(q_steps);
+  r.kv_part = r.kv_splits > 1 ? 2 * r.kv_splits * z.keys * z.kv_heads * z.head_dim : 0;
+  r.q_part = r.q_splits > 1 ? r.q_splits * z.tokens * z.q_heads * z.head_dim : 0;
+  return r;
 }
 
 bool scale_ok(float scale) { return scale > 0.f && std::isfinite(scale * kAttnLog2e); }
@@ -829,16 +941,15 @@ gbn_status gbn_attention_fwd(const gbn_attention_fwd_args* args, cudaStream_t st
 }
 
 gbn_status gbn_attention_bwd_workspace_size(int64_t tokens, int64_t keys, int64_t batches,
-                                            int64_t q_heads, int64_t kv_heads, gbn_dtype dtype,
-                                            size_t* bytes) {
+                                            int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                            int64_t max_q, int64_t max_k, int64_t window, int causal,
+                                            gbn_dtype dtype, size_t* bytes) {
   if (!bytes) return GBN_ERR_NULL;
-  AttnSizes z{tokens, keys, batches, q_heads, kv_heads, 8, 0, 0, 0, true, true};
+  const AttnSizes z{tokens, keys, batches, q_heads, kv_heads, head_dim, max_q, max_k, window, true, true};
   const gbn_status st = check_sizes(z, dtype);
   if (st != GBN_OK) return st;
-  const int64_t norms = dtype == GBN_F16 ? q_heads * norm_elements(tokens, batches) +
-                                               kv_heads * norm_elements(keys, batches)
-                                         : 0;
-  *bytes = static_cast<size_t>((2 * q_heads * stat_elements(z) + norms) * 4);
+  const BwdPlan a = plan_bwd(z, causal != 0);
+  *bytes = static_cast<size_t>(2 * q_heads * stat_elements(z) + norm_total(z, dtype) + a.kv_part + a.q_part) * 4;
   return GBN_OK;
 }
 
@@ -864,7 +975,8 @@ gbn_status gbn_attention_bwd(const gbn_attention_bwd_args* args, cudaStream_t st
       (st = check_tensor(c.dv, c.dv_strides, z.keys, z.kv_heads, false)) != GBN_OK)
     return st;
   size_t need = 0;
-  st = gbn_attention_bwd_workspace_size(z.tokens, z.keys, z.batches, z.q_heads, z.kv_heads, dtype, &need);
+  st = gbn_attention_bwd_workspace_size(z.tokens, z.keys, z.batches, z.q_heads, z.kv_heads, z.head_dim, z.max_q,
+                                        z.max_k, z.window, c.causal, dtype, &need);
   if (st != GBN_OK) return st;
   if (!c.workspace || c.workspace_bytes < need || (reinterpret_cast<uintptr_t>(c.workspace) & 15u))
     return GBN_ERR_WORKSPACE;
@@ -889,6 +1001,11 @@ gbn_status gbn_attention_bwd(const gbn_attention_bwd_args* args, cudaStream_t st
   p.v_norm_stride = norm_elements(z.keys, z.batches);
   p.q_norms = p.ndelta + z.q_heads * p.stat_stride;  // (f16 only)
   p.v_norms = p.q_norms + z.q_heads * p.q_norm_stride;
+  const BwdPlan a = plan_bwd(z, c.causal != 0);
+  p.kv_splits = a.kv_splits;
+  p.q_splits = a.q_splits;
+  p.kv_part = p.q_norms + norm_total(z, dtype);
+  p.q_part = p.kv_part + a.kv_part;
   p.qt = c.q_strides[0];
   p.qh = c.q_strides[1];
   p.kt = c.k_strides[0];
@@ -916,12 +1033,18 @@ gbn_status gbn_attention_bwd(const gbn_attention_bwd_args* args, cudaStream_t st
   p.max_k = static_cast<int>(z.max_k < z.keys ? z.max_k : z.keys);
   p.causal = c.causal != 0;
   p.window = static_cast<int>(z.window);
-  const int64_t kv_blocks = tile_blocks(p.cu_k, z.keys, z.batches, p.max_k, kBwdTile) * z.kv_heads;
-  const int64_t q_blocks = tile_blocks(p.cu, z.tokens, z.batches, p.max_q, kBwdTile) * z.q_heads;
+  const int64_t kv_blocks = tile_blocks(p.cu_k, z.keys, z.batches, p.max_k, kBwdTile) * z.kv_heads * a.kv_splits;
+  const int64_t q_blocks = tile_blocks(p.cu, z.tokens, z.batches, p.max_q, kBwdTile) * z.q_heads * a.q_splits;
   const int64_t q_stats = tile_blocks(p.cu, z.tokens, z.batches, p.max_q, kStatTokens, 1, false);
   const int64_t v_stats =
       dtype == GBN_F16 ? tile_blocks(p.cu_k, z.keys, z.batches, p.max_k, kStatTokens, 1, false) : 0;
-  if (kv_blocks + q_blocks > INT32_MAX || q_stats + v_stats > INT32_MAX) return GBN_ERR_SHAPE;
+  const int64_t kv_joins =
+      a.kv_splits > 1 ? tile_blocks(p.cu_k, z.keys, z.batches, p.max_k, kStatTokens, 1, false) : 0;
+  const int64_t q_joins = a.q_splits > 1 ? q_stats : 0;
+  if (kv_blocks + q_blocks > INT32_MAX || q_stats + v_stats > INT32_MAX || kv_joins + q_joins > INT32_MAX)
+    return GBN_ERR_SHAPE;
+  p.kv_join_blocks = static_cast<int>(kv_joins);
+  p.join_blocks = static_cast<int>(kv_joins + q_joins);
   p.q_stat_blocks = static_cast<int>(q_stats);
   p.stat_blocks = static_cast<int>(q_stats + v_stats);
   p.kv_blocks = static_cast<int>(kv_blocks);

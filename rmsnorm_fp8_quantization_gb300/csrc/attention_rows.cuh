@@ -25,6 +25,9 @@ struct AttnBwdParams {
   int64_t stat_stride, q_norm_stride, v_norm_stride;
   int tokens, keys, batches, hq, hkv, group, d, max_q, max_k;
   int causal, window;
+  float *kv_part, *q_part;  // sums in parts: [kv_splits][dk, dv][keys][hkv][d], [q_splits][tokens][hq][d]
+  int kv_splits, q_splits;         // CTAs that share a tile's steps
+  int kv_join_blocks, join_blocks;
   int kv_blocks, q_blocks;         // CTAs for dk and dv, and for dq
   int q_stat_blocks, stat_blocks;  // of the row statistics: for q's rows, and with v's
   float scale, scale_log2;

@@ -31,7 +31,8 @@ using BytesFn = gbn_status (*)(int64_t, int64_t, int64_t, int64_t, int64_t, int6
                                int64_t, int64_t, int64_t, int, gbn_dtype, gbn_dtype, size_t*);
 using AttnFwdFn = gbn_status (*)(const gbn_attention_fwd_args*, cudaStream_t);
 using AttnBwdFn = gbn_status (*)(const gbn_attention_bwd_args*, cudaStream_t);
-using AttnBwdBytesFn = gbn_status (*)(int64_t, int64_t, int64_t, int64_t, int64_t, gbn_dtype, size_t*);
+using AttnBwdBytesFn = gbn_status (*)(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
+                                      int64_t, int64_t, int, gbn_dtype, size_t*);
 using DropFwdFn = gbn_status (*)(const void*, const void*, void*, const int64_t*, int64_t, double,
                                  gbn_dtype, cudaStream_t);
 using DropBwdFn = gbn_status (*)(const void*, void*, const int64_t*, int64_t, double, gbn_dtype,
@@ -504,8 +505,8 @@ PyObject* attention_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       Py_RETURN_NONE;
     fill(s, &g);
     size_t bytes = 0;
-    gbn_status st = g_attn_bwd_bytes(g.tokens, g.keys, g.batches, g.q_heads, g.kv_heads,
-                                     static_cast<gbn_dtype>(g.dtype), &bytes);
+    gbn_status st = g_attn_bwd_bytes(g.tokens, g.keys, g.batches, g.q_heads, g.kv_heads, g.head_dim, g.max_q,
+                                     g.max_k, g.window, g.causal, static_cast<gbn_dtype>(g.dtype), &bytes);
     if (st != GBN_OK) return status(st);
     at::Tensor dq = at::empty(s.q->sizes(), s.q->options()), dk = at::empty(s.k->sizes(), s.k->options());
     at::Tensor dv = at::empty(s.v->sizes(), s.v->options());

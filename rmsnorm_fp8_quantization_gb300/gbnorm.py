@@ -83,7 +83,7 @@ def _load():
         f.restype = I
     lib.gbn_paged_attention_workspace_size.argtypes = [I64] * 10 + [I, I, I, ctypes.POINTER(SZ)]
     lib.gbn_paged_attention_workspace_size.restype = I
-    lib.gbn_attention_bwd_workspace_size.argtypes = [I64] * 5 + [I, ctypes.POINTER(SZ)]
+    lib.gbn_attention_bwd_workspace_size.argtypes = [I64] * 9 + [I, I, ctypes.POINTER(SZ)]
     lib.gbn_attention_bwd_workspace_size.restype = I
     lib.gbn_dropout_fwd.argtypes = [P, P, P, P, I64, ctypes.c_double, I, P]
     lib.gbn_dropout_fwd.restype = I
@@ -304,10 +304,12 @@ def gbn_attention_fwd(q, k, v, cu_q, cu_k, out, lse, tokens, keys, batches, q_he
                            1 if causal else 0, scale), _stream(stream))
 
 
-def gbn_attention_bwd_workspace_size(tokens, keys, batches, q_heads, kv_heads, dtype):
+def gbn_attention_bwd_workspace_size(tokens, keys, batches, q_heads, kv_heads, head_dim, max_q,
+                                     max_k, window, causal, dtype):
     """Returns (status, bytes)."""
     n = ctypes.c_size_t(0)
-    st = _lib.gbn_attention_bwd_workspace_size(tokens, keys, batches, q_heads, kv_heads, dtype,
+    st = _lib.gbn_attention_bwd_workspace_size(tokens, keys, batches, q_heads, kv_heads, head_dim,
+                                               max_q, max_k, window, 1 if causal else 0, dtype,
                                                ctypes.byref(n))
     return st, n.value
 

@@ -757,14 +757,17 @@ def attention_fwd(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, max_q=None, ma
     return out, lse
 
 
-def attention_bwd_workspace(q, k, cu_seqlens=None):
-    """A workspace for ``attention_bwd`` calls with these q, k and cu_seqlens."""
+def attention_bwd_workspace(q, k, *, cu_seqlens=None, max_q=None, max_k=None, causal=True, window=0):
+    """A workspace for ``attention_bwd`` calls with these arguments."""
     _on_gpu(q)
     tokens, keys = (t.shape[0] if t.dim() == 3 else t.shape[0] * t.shape[1] for t in (q, k))
-    batches = q.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    return torch.empty(_attention_bwd_bytes(tokens, keys, batches, q.shape[-2], k.shape[-2],
-                                            G.TORCH_DTYPE[q.dtype]), dtype=torch.uint8,
-                       device=q.device)
+    if cu_seqlens is None:
+        batches, max_q, max_k = q.shape[0], q.shape[1], k.shape[1]
+    else:
+        batches, max_k = cu_seqlens.shape[0] - 1, max_q if max_k is None else max_k
+    n = _attention_bwd_bytes(tokens, keys, batches, q.shape[-2], k.shape[-2], q.shape[-1], max_q,
+                             max_k, window, bool(causal), G.TORCH_DTYPE[q.dtype])
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -803,7 +806,7 @@ def attention_bwd(dout, q, k, v, out, lse, *, cu_seqlens=None, cu_seqlens_k=None
     y = tuple(_tokens(n, t, q) for n, t in (("dq", dq), ("dk", dk), ("dv", dv)))
     dt = G.TORCH_DTYPE[q.dtype]
     if workspace is None:
-        size = _attention_bwd_bytes(*sizes[:5], dt)
+        size = _attention_bwd_bytes(*sizes, window, bool(causal), dt)
         workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
     else:
         if workspace.device != q.device or not workspace.is_contiguous():

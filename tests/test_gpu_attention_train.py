@@ -60,6 +60,11 @@ CASES = {
     "large gradients f16": Case((300,), uniform=True, dtype=F16, dout_std=3000.0, dim=128),
     "small gradients": Case((300,), uniform=True, dout_std=1e-20, dim=128),
     "scale": Case((150,), uniform=True, scale=0.3),
+    # few CTAs of many steps: shared among several, added up afterwards
+    "shared steps": Case((1500,), uniform=True, heads=4, kv_heads=1, dim=128),
+    "shared steps, ragged f16": Case((900, 1, 0, 333), heads=6, kv_heads=1, dim=96, dtype=F16, lead=3, trail=5),
+    "shared steps of dq": Case((100,), (4100,), causal=False, heads=1, kv_heads=1, dim=72),
+    "shared steps, window": Case((3000,), uniform=True, heads=8, kv_heads=1, window=900),
     "long": Case((2500,), uniform=True, heads=2, kv_heads=1, dim=128),
     "long f16, not causal": Case((2500,), uniform=True, heads=2, kv_heads=1, dtype=F16, causal=False),
 }
@@ -124,13 +129,43 @@ def test_given_outputs_and_strides(gpu):
     wide[:, 1] = s["dout"]
     out, lse = gpu.attention_fwd(s["q"], s["k"], s["v"], **s["kw"])
     r = gpu.attention_bwd(wide[:, 1], s["q"], s["k"], s["v"], out, lse, dq=dq, dk=dk, dv=dv,
-                          workspace=gpu.attention_bwd_workspace(s["q"], s["k"], s["kw"]["cu_seqlens"]),
+                          workspace=gpu.attention_bwd_workspace(s["q"], s["k"], **s["kw"]),
                           **s["kw"])
     assert r[0] is dq and r[1] is dk and r[2] is dv
     assert (room[..., 80:] == 0).all()
     want = define(c, s)
     for n, t in (("dq", dq), ("dk", dk), ("dv", dv)):
         check(n, t, want[n])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("c", [Case((600,), dim=128, heads=8, kv_heads=4, window=20, lead=2),
+                               Case((130, 600), dim=64, dtype=F16, window=20),
+                               Case((2600,), dim=64, heads=8, kv_heads=1, window=700)], ids=str)
+def test_bad_values_in_pairs_that_are_not_kept(gpu, c, bad):
+    """A token's keys and values, and another's query and gradient, of no use: the rows that have no
+    kept pair with them come out as if they were 0, whatever else their tiles hold."""
+    s = make(c)
+    last = c.lead + sum(c.q_lens)
+    first = last - c.q_lens[-1]
+    m, i = (last - 5, first + 3) if c.window > 100 else (first + 300, first + 200)
+    clean = {n: t.clone() for n, t in s.items() if n != "kw"}
+    for n, at in (("k", m), ("v", m), ("q", i), ("dout", i)):
+        s[n][at] = bad
+        clean[n][at] = 0
+    got, want = both(gpu, s), define(c, dict(clean, kw=s["kw"]))
+    tokens = torch.arange(s["q"].shape[0], device="cuda")
+    w = c.window - 1
+    # query m .. m + w keeps key m; those keep keys m - w .. m + w; query i keeps keys i - w .. i
+    q_out = ((tokens >= m) & (tokens <= m + w)) | (tokens == i)
+    k_out = ((tokens >= m - w) & (tokens <= m + w)) | ((tokens >= i - w) & (tokens <= i))
+    for n, t in got.items():
+        out = k_out if n in ("dk", "dv") else q_out
+        value, off = (x.clone() for x in want[n])
+        value[out] = float("nan")
+        assert not value.isnan().all()
+        check(n, t, (value, off))
+    assert got["dq"][i].isnan().any() and got["dk"][m].isnan().any()
 
 
 def test_deterministic(gpu):
