@@ -234,7 +234,9 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
     if (tid == 0) flag_wait_timeout();
     return;
   }
-  if (tid == 0) {
+  // The warp of the loads sets the barriers up and goes ahead: the first tiles are on their way
+  // while the others are still setting up.
+  if (warp == kBwdLoadWarp && lane == 0) {
     for (int i = 0; i < Shape::kSlots; ++i) {
       mbar_init(&bars.full[i], 1);
       mbar_init(&bars.empty[i], 2);  // one arrival for each of the threads that issue
@@ -256,10 +258,16 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
     fence_mbar_init();
   }
   if (warp == kBwdMmaWarp) tc_alloc(&bars.tmem);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = bars.tmem;
+  uint32_t tmem = 0;
+  if (warp == kBwdLoadWarp) {
+    __syncwarp();
+    asm volatile("barrier.cta.arrive.aligned 1, %0;" ::"n"(Shape::kThreads) : "memory");
+  } else {
+    tc_fence_before();
+    asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(Shape::kThreads) : "memory");
+    tc_fence_after();
+    tmem = bars.tmem;
+  }
   // Columns (S: 0); kX: x as the products' first operand, 16-bit pairs.
   constexpr uint32_t kDp = 128, kAcc2 = 256, kAcc1 = KV ? 256 + DP : 256, kX = 384;
   constexpr bool kXInTmem = Shape::kXInTmem;
