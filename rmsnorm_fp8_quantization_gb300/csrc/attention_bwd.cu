@@ -29,7 +29,9 @@ __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const Att
   constexpr bool kNorms = Elem<T>::kDt == DT_F16;
   __shared__ float deltas[kStatHeads][kStatTokens + 1];
   __shared__ float norms[kStatHeads][kStatTokens + 1];
-  pdl_begin();
+  // The gradients' kernel may begin once everything before this one is complete (its first
+  // loads do not need the statistics).
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h0 = blockIdx.y * kStatHeads;
   // Lengths that do not fit are flagged here, a sequence by a thread.
@@ -45,38 +47,49 @@ __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const Att
   const int b = place.sequence, i0 = place.tile * kStatTokens;
   const SeqRange s = bwd_range(p, b, false);
   const int n = values ? s.kv : s.qlen, heads = values ? p.hkv : p.hq;
+  if (i0 >= n) return;  // (lengths that do not fit)
   const int c = lane % C;
   auto row_sum = [&](float v) {
 #pragma unroll
     for (int o = C / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
   };
-  constexpr int kStep = kStatThreads / C;  // rows the CTA reads at once
-#pragma unroll 4
-  for (int r = warp * (32 / C) + lane / C; r < kStatTokens * kStatHeads; r += kStep) {
-    const int t = r / kStatHeads, hh = r % kStatHeads;
-    float sum = 0.f, square = 0.f;
-    if (i0 + t < n && h0 + hh < heads && c * 8 < p.d) {
-      const int64_t at = (values ? s.k0 : s.q0) + static_cast<int64_t>(i0) + t, head = h0 + hh;
-      float x[8], y[8];
-      if (!values) {
-        eight<T>(p.out, at * p.ot + head * p.oh + c * 8, x);
-        eight<T>(p.dout, at * p.gt + head * p.gh + c * 8, y);
+  constexpr int kStep = kStatThreads / C, kAtOnce = 4;  // rows the CTA reads at once, times 4
+  const int count = min(heads - h0, kStatHeads), total = min(kStatTokens, n - i0) * count;
+  for (int from = warp * (32 / C) + lane / C, first = 0; first < total; first += kAtOnce * kStep) {
+    uint4 xw[kAtOnce], yw[kAtOnce];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
-      } else {
-        eight<T>(p.v, at * p.vt + head * p.vh + c * 8, y);
-      }
-      if (kNorms) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) square = fmaf(y[e], y[e], square);
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int r = first + u * kStep + from;
+      xw[u] = yw[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < total && c * 8 < p.d) {
+        const int64_t at = (values ? s.k0 : s.q0) + static_cast<int64_t>(i0) + r / count, head = h0 + r % count;
+        if (!values) {
+          xw[u] = ld_stream16(static_cast<const T*>(p.out) + at * p.ot + head * p.oh + c * 8);
+          yw[u] = ld_stream16(static_cast<const T*>(p.dout) + at * p.gt + head * p.gh + c * 8);
+        } else {
+          yw[u] = ld_stream16(static_cast<const T*>(p.v) + at * p.vt + head * p.vh + c * 8);
+        }
       }
     }
-    sum = row_sum(sum);
-    if (kNorms) square = row_sum(square);
-    if (c == 0) {
-      deltas[hh][t] = -sum;
-      if (kNorms) norms[hh][t] = square;
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int r = first + u * kStep + from;
+      const uint32_t xa[4] = {xw[u].x, xw[u].y, xw[u].z, xw[u].w}, ya[4] = {yw[u].x, yw[u].y, yw[u].z, yw[u].w};
+      float x[8], y[8], sum = 0.f, square = 0.f;
+      unpack<T, 8>(xa, x);
+      unpack<T, 8>(ya, y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum = fmaf(x[e], y[e], sum);
+        if (kNorms) square = fmaf(y[e], y[e], square);
+      }
+      sum = row_sum(sum);
+      if (kNorms) square = row_sum(square);
+      if (c == 0 && r < total) {
+        deltas[r % count][r / count] = -sum;
+        if (kNorms) norms[r % count][r / count] = square;
+      }
     }
   }
   __syncthreads();
@@ -92,7 +105,7 @@ __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const Att
   if (kNorms && tid < kStatHeads && h0 + tid < heads) {
     float most = 0.f;
 #pragma unroll
-    for (int t = 0; t < kStatTokens; ++t) most = fmax_nan(most, norms[tid][t]);
+    for (int t = 0; t < kStatTokens; ++t) most = i0 + t < n ? fmax_nan(most, norms[tid][t]) : most;
     const int64_t head = h0 + tid;
     if (values) p.v_norms[head * p.v_norm_stride + norm_base(s.k0, b) + place.tile] = most;
     else p.q_norms[head * p.q_norm_stride + norm_base(s.q0, b) + place.tile] = most;
@@ -188,6 +201,10 @@ __device__ __forceinline__ float ds_factor(const AttnBwdParams& p, const SeqRang
   return __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
 }
 
+// Until the kernel before has completed.  Every CTA gets here before it ends, so that what comes
+// after this kernel comes after the statistics too.
+__device__ __forceinline__ void wait_for_stats() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <typename T, int DP, bool KV>
 __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const CUtensorMap& x1map,
                                                    const CUtensorMap& x2map, const CUtensorMap& y1map,
@@ -208,12 +225,12 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
                                                          block, raw)
                              : find_tile<Shape::kThreads>(p.cu, p.cu_k, p.batches, p.max_q, p.max_k, 1, kBwdTile,
                                                          block, raw);
-  if (place.tile < 0) return;
+  if (place.tile < 0) return wait_for_stats();
   const int b = place.sequence, xt = KV ? place.tile : place.tiles - 1 - place.tile;
   const SeqRange s = bwd_range(p, b, false);
   const int nx = KV ? s.kv : s.qlen, ny = KV ? s.qlen : s.kv, x0 = xt * kBwdTile;
   const int rows = min(kBwdTile, nx - x0);
-  if (rows <= 0) return;
+  if (rows <= 0) return wait_for_stats();
   const int h = KV ? xh : xh / p.group;  // kv head
 
   // Rows of y that some row of x goes with, [y_lo, y_hi), in tiles from `base` on; for dk
@@ -232,7 +249,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
   const uint32_t ring = smem_u32(raw), xs = ring + Shape::kFirst * Shape::kSlot;
   if (ring & 1023u) {  // the swizzle goes by address bits; the compiler's alignment holds
     if (tid == 0) flag_wait_timeout();
-    return;
+    return wait_for_stats();
   }
   // The warp of the loads sets the barriers up and goes ahead: the first tiles are on their way
   // while the others are still setting up.
@@ -415,6 +432,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
             ++issued;
             if (++slot == Shape::kSlots) slot = 0, phase ^= 1;
             if (KV && w == 0) {
+              if (i == 0) wait_for_stats();
               const int st = i & 1;
               if (i >= 2) ok = mbar_wait(&bars.stat_empty[st], ((i >> 1) - 1) & 1);
               if (!ok) break;
@@ -468,6 +486,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
     // The rows of y that this thread's row goes with.
     const int lo = !live ? 0 : KV ? query_first(p, s, x) : key_first(p, s, x);
     const int hi = !live ? 0 : KV ? query_end(p, s, x) : key_end(p, s, x);
+    if (!KV || kType == 0 || n == 0) wait_for_stats();
     const float up = ds_factor<T, KV>(p, s, b, xh, h, x0, rows);
     const uint64_t sc2 = p2(p.scale_log2, p.scale_log2);
     const float back = ex2(-static_cast<float>(kWeightLog2<T>));  // P is 2^kWeightLog2 larger
@@ -705,7 +724,8 @@ __global__ void __launch_bounds__(BwdShape<DP, true>::kThreads, 1)
                          const __grid_constant__ CUtensorMap k, const __grid_constant__ CUtensorMap v,
                          const __grid_constant__ CUtensorMap dout) {
   extern __shared__ __align__(1024) uint8_t raw[];
-  pdl_begin();
+  // The statistics are waited for where they are read (see wait_for_stats).
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int block = blockIdx.x;
   if (block < p.kv_blocks) attention_bwd_tile<T, DP, true>(p, k, v, q, dout, block, raw);
   else attention_bwd_tile<T, DP, false>(p, q, dout, k, v, block - p.kv_blocks, raw);
@@ -717,8 +737,13 @@ cudaError_t launch_tiles(const AttnBwdParams& p, const CUtensorMap* m, int64_t g
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(k, BwdShared<DP>::kSmem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(BwdShape<DP, true>::kThreads),
-                    BwdShared<DP>::kSmem, st, p, m[0], m[1], m[2], m[3]);
+  const dim3 g(static_cast<unsigned>(grid)), t(BwdShape<DP, true>::kThreads);
+  // (without statistics before it, it must not begin before what comes before has ended)
+  if (p.stat_blocks == 0) {
+    k<<<g, t, BwdShared<DP>::kSmem, st>>>(p, m[0], m[1], m[2], m[3]);
+    return cudaGetLastError();
+  }
+  return launch_pdl(k, g, t, BwdShared<DP>::kSmem, st, p, m[0], m[1], m[2], m[3]);
 }
 
 // ---- sums in parts
@@ -934,12 +959,11 @@ gbn_status gbn_attention_fwd(const gbn_attention_fwd_args* args, cudaStream_t st
   p.hkv = static_cast<int>(z.kv_heads);
   p.group = p.hq / p.hkv;
   p.d = static_cast<int>(z.head_dim);
-  p.max_q = static_cast<int>(z.max_q);
-  p.max_kv = static_cast<int>(z.max_k);
+  p.max_q = static_cast<int>(std::min(z.max_q, z.tokens));
+  p.max_kv = static_cast<int>(std::min(z.max_k, z.keys));
   p.causal = c.causal != 0;
   p.window = static_cast<int>(z.window);
-  const int64_t blocks = tile_blocks(p.cu, z.tokens, z.batches, z.max_q < z.tokens ? z.max_q : z.tokens,
-                                     kPrefillRows, p.group);
+  const int64_t blocks = tile_blocks(p.cu, z.tokens, z.batches, p.max_q, kPrefillRows, p.group);
   if (blocks * z.kv_heads > INT32_MAX) return GBN_ERR_SHAPE;
   p.row_tiles = static_cast<int>(blocks);  // of all sequences
   p.splits = 1;
