@@ -14,9 +14,10 @@
  *     (sections Description, I/O Contract): the backward with the residual
  *     gradient added to the input gradient in the same kernel.
  * The softmax entry points follow "Migrate norms and softmax kernels to
- * NVRTC" (Description, JIT cost table), which names them.  Rotary positions
- * and the paged key/value cache (end of this file) have no page: they are what
- * stands between the norms and the softmax's use, in this library's manner.
+ * NVRTC" (Description, JIT cost table), which names them.  Rotary positions,
+ * the paged key/value cache, the attention over whole sequences and the
+ * dropout (end of this file) have no page: they are what stands between the
+ * norms in a network, in this library's manner.
  *
  * Arithmetic (x is one row of `hidden` elements; all device math in fp32):
  *   LayerNorm: mu = mean(x); var = mean((x - mu)^2); rsigma = 1/sqrt(var + eps)
@@ -108,7 +109,7 @@ typedef enum {
   GBN_ERR_NULL = 1,      /* a pointer the chosen mode needs is NULL */
   GBN_ERR_DTYPE = 2,     /* unsupported dtype or dtype combination */
   GBN_ERR_SHAPE = 3,     /* rows/hidden out of range, or MXFP8 blocks do not tile */
-  GBN_ERR_ALIGNMENT = 4, /* paged attention only: everything else takes a scalar path */
+  GBN_ERR_ALIGNMENT = 4, /* attention, and dropout off its element size: the rest takes a scalar path */
   GBN_ERR_WORKSPACE = 5, /* workspace NULL or smaller than the queried size */
   GBN_ERR_ENUM = 6,      /* norm type, scaling mode or layout out of range */
   GBN_ERR_CUDA = 7       /* a CUDA runtime call or a launch failed */
@@ -244,9 +245,10 @@ gbn_status gbn_norm_bwd_noalloc(const void* dz, const void* x, const float* mu,
  * reaches the host.  The query synchronizes with the device.  With clear != 0
  * the bits are reset after reading. */
 #define GBN_DEVICE_ERR_COPY_TIMEOUT 1u
-/*   bit 1 (GBN_DEVICE_ERR_BAD_INDEX): gbn_paged_append or gbn_paged_attention
- *   met lengths or a page index outside what the call's sizes allow (see
- *   there); what they point at was neither read nor written. */
+/*   bit 1 (GBN_DEVICE_ERR_BAD_INDEX): gbn_paged_append, gbn_paged_attention,
+ *   gbn_attention_fwd or gbn_attention_bwd met lengths or a page index outside
+ *   what the call's sizes allow (see there); what they point at was neither
+ *   read nor written. */
 #define GBN_DEVICE_ERR_BAD_INDEX 2u
 gbn_status gbn_device_error(unsigned int* flags, int clear);
 
@@ -311,7 +313,7 @@ typedef enum { GBN_ROPE_HALF = 0, GBN_ROPE_INTERLEAVED = 1 } gbn_rope_layout;
 
 #define GBN_ROPE_MAX_DIM 1024 /* largest head_dim */
 
-/* The calls from here on take their arguments as a struct (host memory, read
+/* The attention and rotary calls take their arguments as a struct (host memory, read
  * during the call): at thirty-odd of them it is what keeps the cost of a call
  * from another language near that of the launch.  Strides are in elements. */
 typedef struct {

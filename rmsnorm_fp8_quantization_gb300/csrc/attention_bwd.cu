@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const Att
 // head_dim 128.
 
 struct BwdBarriers {
-  uint64_t full[8], empty[8], s_full, p_full[2], dp_full, ds_full[2], x_full, x_ready, acc_full;
+  uint64_t full[8], empty[8], s_full, p_full[2], dp_full, ds_full[2], x_full[2], x_ready[2], acc_full;
   uint64_t turn[2], stat_full[2], stat_empty[2], cut[2], zeroed[2];
   uint32_t tmem;
 };
@@ -259,12 +259,12 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
       mbar_init(&bars.empty[i], 2);  // one arrival for each of the threads that issue
     }
     mbar_init(&bars.s_full, 1);
-    mbar_init(&bars.x_full, 1);
-    mbar_init(&bars.x_ready, 8);
     mbar_init(&bars.dp_full, 1);
     mbar_init(&bars.acc_full, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.turn[i], 1);
+      mbar_init(&bars.x_full[i], 1);
+      mbar_init(&bars.x_ready[i], 4);
       mbar_init(&bars.p_full[i], 8);  // one arrival per warp
       mbar_init(&bars.ds_full[i], 8);
       mbar_init(&bars.cut[i], 1);
@@ -343,7 +343,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
             }
           }
         };
-        ok = mbar_wait(kXInTmem ? &bars.x_ready : &bars.x_full, 0);
+        ok = mbar_wait(kXInTmem ? &bars.x_ready[first ? 0 : 1] : &bars.x_full[first ? 0 : 1], 0);
         const int own = first ? 0 : 1;  // y1 or y2: what this thread's product reads
         int y1 = 0, y2 = 0, left = nt - t0;  // slots of the step before; tiles up to the sequence's end
         uint32_t zeros = 0;
@@ -413,10 +413,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
           for (int pn = 0; pn < Shape::kPanels; ++pn)
             tma_box(dst + pn * Shape::kPanel, map, pn * 64, head, row, 0, bar);
         };
-        mbar_arrive_expect_tx(&bars.x_full, 2 * Shape::kSlot);
         const int xr = (KV ? s.k0 : s.q0) + x0;
-        tile(xs, &x1map, xh, xr, &bars.x_full);
-        tile(xs + Shape::kSlot, &x2map, xh, xr, &bars.x_full);
         const int64_t stat = stat_base(s.q0, b) + base;
         int slot = 0, issued = 0, t = t0, g = g0, i = 0;
         uint32_t phase = 0;
@@ -424,8 +421,13 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
           const int yr = (KV ? s.q0 : s.k0) + base + t * kBwdTile;
           const int yh = KV ? h * p.group + g : h;
           for (int w = 0; ok && w < 2; ++w) {
+            if (issued < 2) {  // x1 just ahead of the first y1, x2 of the first y2
+              mbar_arrive_expect_tx(&bars.x_full[w], Shape::kSlot);
+              tile(xs + w * Shape::kSlot, w ? &x2map : &x1map, xh, xr, &bars.x_full[w]);
+            }
             if (issued >= Shape::kSlots) ok = mbar_wait(&bars.empty[slot], phase ^ 1);
-            else if (issued == Shape::kFirst) ok = mbar_wait(&bars.x_ready, 0);  // (only where x's room is used)
+            else if (issued >= Shape::kFirst)  // (only where x's room is used)
+              ok = mbar_wait(&bars.x_ready[issued - Shape::kFirst], 0);
             if (!ok) break;
             mbar_arrive_expect_tx(&bars.full[slot], Shape::kSlot);
             tile(ring + slot * Shape::kSlot, w ? &y2map : &y1map, yh, yr, &bars.full[slot]);
@@ -447,7 +449,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
         }
         if (!ok) {
           // Leave no copy in flight behind.
-          mbar_wait(&bars.x_full, 0);
+          for (int j = 0; j < min(issued, 2); ++j) mbar_wait(&bars.x_full[j], 0);
           for (int j = max(0, issued - Shape::kSlots); j < issued; ++j)
             mbar_wait(&bars.full[j % Shape::kSlots], (j / Shape::kSlots) & 1);
           if (KV)
@@ -501,7 +503,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
     const uint32_t ts = tmem + lanes + w * 64;  // this warp's half of S
     if (kXInTmem && n > 0) {
       // x1 and x2 into tensor memory, a row by a thread.
-      ok = warp_wait(&bars.x_full, 0);
+      ok = warp_wait(&bars.x_full[w], 0);
       const uint8_t* from = raw + (Shape::kFirst + w) * Shape::kSlot + r * 128;
 #pragma unroll
       for (int pn = 0; pn < Shape::kPanels; ++pn) {
@@ -516,7 +518,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.x_ready);
+      if (lane == 0) mbar_arrive(&bars.x_ready[w]);
     }
     int t = t0;
     for (int i = 0; ok && i < n; ++i) {

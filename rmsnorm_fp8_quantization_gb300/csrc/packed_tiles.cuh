@@ -58,6 +58,23 @@ __device__ __forceinline__ TilePlace find_tile(const int32_t* cu, const int32_t*
     const int t = tiles_of(length(lo));
     return {lo, tile >= 0 && tile < t ? static_cast<int>(tile) : -1, t};
   }
+  if (n <= 32) {
+    // A sequence by a lane, every warp for itself.
+    const int lane = tid & 31, i = min(lane, n - 1);
+    const float pairs = static_cast<float>(length(i)) *
+                        static_cast<float>(cu_other ? static_cast<int64_t>(cu_other[i + 1]) - cu_other[i] : most_other);
+    const int t = lane < n ? tiles_of(length(i)) : 0;
+    int before = 0;  // tiles of the sequences taken before this one
+    for (int j = 0; j < n; ++j) {
+      const float w = __shfl_sync(0xFFFFFFFFu, pairs, j);
+      const int tj = __shfl_sync(0xFFFFFFFFu, t, j);
+      before += w > pairs || (w == pairs && j < lane) ? tj : 0;
+    }
+    const uint32_t mine = __ballot_sync(0xFFFFFFFFu, before <= index && index < before + t);
+    if (!mine) return {0, -1, 0};
+    const int at = __ffs(mine) - 1;
+    return {at, index - __shfl_sync(0xFFFFFFFFu, before, at), __shfl_sync(0xFFFFFFFFu, t, at)};
+  }
   float* const work = reinterpret_cast<float*>(scratch);
   int* const order = reinterpret_cast<int*>(scratch) + kSortSequences;
   for (int i = tid; i < n; i += THREADS)
