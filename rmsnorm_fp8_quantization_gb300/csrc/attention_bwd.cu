@@ -20,9 +20,9 @@ namespace {
 //
 // delta_i = dout_i.out_i for every query and head, and lse beside it in the form and order
 // that the kernel below reads: by head, then query.  f16 besides: the largest squared norms of
-// 16 rows of dout and v.  A CTA takes 16 tokens and 32 heads; a row is C lanes of 8
+// 16 rows of dout and v.  A CTA takes 16 tokens and 16 heads; a row is C lanes of 8
 // elements.  Bound by reading out and dout once.
-constexpr int kStatHeads = 32, kStatThreads = 256;
+constexpr int kStatHeads = 16, kStatThreads = 256;
 
 template <typename T, int C>
 __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const AttnBwdParams p) {

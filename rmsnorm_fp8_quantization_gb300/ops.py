@@ -724,7 +724,8 @@ def _lse(lse, q, new):
 
 def attention_fwd(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, max_q=None, max_k=None,
                   scale=None, causal=True, window=0, out=None, lse=None, stream=None):
-    """Attention over whole sequences; returns (out, lse), what ``attention_bwd`` needs.
+    """Attention over whole sequences (bf16 or f16, head_dim a multiple of 8 up to 128); returns
+    (out, lse), what ``attention_bwd`` needs.
 
     q [batch, seq, heads, head_dim] with k, v [batch, keys, kv_heads, head_dim]; or packed: q
     [tokens, heads, head_dim] whose rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (int32) are

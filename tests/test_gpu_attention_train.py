@@ -211,3 +211,22 @@ def test_against_differences(gpu):
         mine = (flat(got["d" + n]).double() * flat(way)).sum().item()
         # 2^-30: the difference's own error (h^2 and 1e-16 / h, times the sums)
         assert abs(mine - slope) <= (want[1] * flat(way).abs()).sum().item() + 2.0 ** -20 * abs(slope)
+
+
+def test_tensors_beyond_32_bits(gpu):
+    """The last of 2400 sequences, past 2^31 elements of every tensor, gives what it gives alone."""
+    b, n, h, d = 2400, 128, 64, 128
+    if torch.cuda.mem_get_info()[0] < 10 * b * n * h * d * 2:
+        pytest.skip("needs 50 GB")
+    x = [torch.empty(b, n, h, d, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    for t in x:
+        t[:-2].zero_()
+        t[-2:].normal_()
+    q, k, v, dout = x
+    out, lse = gpu.attention_fwd(q, k, v)
+    grads = gpu.attention_bwd(dout, q, k, v, out, lse)
+    q, k, v, dout = (t[-1:].clone() for t in x)
+    o1, l1 = gpu.attention_fwd(q, k, v)
+    assert torch.equal(out[-1:], o1) and torch.equal(lse[-1:], l1)
+    for a, c in zip(grads, gpu.attention_bwd(dout, q, k, v, o1, l1)):
+        assert torch.equal(a[-1:], c)
