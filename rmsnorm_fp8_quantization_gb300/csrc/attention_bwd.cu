@@ -21,7 +21,8 @@ namespace {
 // delta_i = dout_i.out_i for every query and head, and lse beside it in the form and order
 // that the kernel below reads: by head, then query.  f16 besides: the largest squared norms of
 // 16 rows of dout and v.  A CTA takes 16 tokens and 16 heads; a row is C lanes of 8
-// elements.  Bound by reading out and dout once.
+// elements.  Bound by reading out and dout once (cold, 4096 tokens of 32 heads of 128: 67 MB in
+// 23 us, a third of what memory gives: a warp has eight loads under way).
 constexpr int kStatHeads = 16, kStatThreads = 256;
 
 template <typename T, int C>
@@ -114,29 +115,37 @@ __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const Att
 
 // ---- the gradients on the tensor cores
 //
-// Both kernels hold one tile of 128 rows (x: keys for dk and dv, queries for dq) and stream
-// tiles of 128 rows of the other side (y) past it; with x1, x2 = k, v and y1, y2 = q, dout
-// (or the other way round) a step is
-//     S = x1 y1^T,  dP = x2 y2^T                    both operands in shared memory
+// A CTA holds one tile of 128 rows (x: keys for dk and dv, queries for dq) and streams tiles
+// of 128 rows of the other side (y) past it; with x1, x2 = k, v and y1, y2 = q, dout (or the
+// other way round) a step is
+//     S = x1 y1^T,  dP = x2 y2^T
 //     P = 2^(S scale log2(e) - lse log2(e)),  dS = P (dP - delta)
-//     acc1 += dS y1 (dk, or dq),  acc2 += P y2 (dv)   first operand in tensor memory
+//     acc1 += dS y1 (dk, or dq),  acc2 += P y2 (dv)
 // P and dS are transposed for dk and dv as they come, so neither passes through shared
-// memory: they go back into the columns of S and dP as 16-bit pairs.  One kernel for all
-// three gradients would need five products a step instead of the seven of both, but its dq
-// is a sum over CTAs: in memory, by additions in an order that changes from run to run, and
-// of as many bytes as the products read.  Two kernels add everything up in registers of the
-// tensor core, in a fixed order.
+// memory: they go back into the columns of S and dP as 16-bit pairs, and are the first
+// operand from there.  A pass for all three gradients would need five products a step
+// instead of the seven of two passes, but its dq is a sum over CTAs: in memory, by additions
+// in an order that changes from run to run, and of as many bytes as the products read.  Two
+// passes add everything up in the tensor core's accumulators, in a fixed order.
 //
 // Roles (as in the forward): warps 0-3 and 4-7 take the columns 0-63 and 64-127 of a step, a
 // thread per row; warps 8 and 9 issue the tcgen05.mma (one thread each), warp 10 the TMA
-// loads, warp 11 zeroes rows of y behind the sequence.  Order of the products, so that the
-// threads' work on one is hidden behind the next ones:
+// loads, warp 11 zeroes rows of y behind the sequence.  (16 warps of 32 columns were no
+// faster: 694 us against 690.)  Order of the products, so that the threads' work on one is
+// hidden behind the next ones:
 //     dk, dv:  dv(i)  S(i+1)  |  dk(i)  dP(i+1)
 //     dq:      S(i+1)  |  dq(i)  dP(i+1)
 // x goes to tensor memory too where there is room (for dq, and at head_dim 64): a product
 // reads 64 bytes of shared memory a cycle then instead of 128, all there are.
-// Bound by the tensor core: 2048 (dk, dv) and 1536 (dq) cycles a step of 128 x 128 at
-// head_dim 128.
+//
+// Bound at head_dim 128 by the tensor core: 2048 (dk, dv) and 1536 (dq) cycles a step.  Two
+// sequences of 4096 tokens, 32 / 8 heads: not causal 1131 us, causal 630; the seven products
+// run at 1700 TFLOP/s and 1530, and the same kernel without exponentials, conversions and
+// reads of the statistics was 2 % faster.  At 64 by the chain from one product over the rows'
+// threads to the next (2100 and 1700 cycles a step, 1230 and 870 of them products; causal 490
+// us): P and dS in columns of their own, which frees S and dP earlier, took 555, and two CTAs
+// a multiprocessor with steps of 64 rows 503, with ragged windows a third more.  A CTA takes
+// about 9000 cycles besides its steps: up to the first scores 5500, the output 3000.
 
 struct BwdBarriers {
   uint64_t full[8], empty[8], s_full, p_full[2], dp_full, ds_full[2], x_full[2], x_ready[2], acc_full;
@@ -619,6 +628,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
       }
     }
     // Output: dv by the warps 0-3, dk by 4-7; or half of dq's columns by each.
+    wait_for_stats();
     if (ok && n > 0) {
       ok = warp_wait(&bars.acc_full, 0);
       tc_fence_after();
@@ -884,7 +894,8 @@ int64_t stat_elements(const AttnSizes& z) {
 // dk and dv, 1 us for dq), so a launch takes at least as long as its longest one: where that
 // is more than a multiprocessor's share of the whole (152 of them, causal ones half full), it is
 // divided, down to 8 steps, below which beginning and end cost as much (one sequence of 4096
-// tokens, 8 / 2 heads of 128, causal: XXX us with one CTA a tile, XXX so).
+// tokens, 8 / 2 heads of 128, causal: 172 us with one CTA a tile, 104 so; 2048 tokens, 5 / 1 of
+// 64: 100, 36).
 struct BwdPlan {
   int kv_splits, q_splits;
   int64_t kv_part, q_part;  // elements

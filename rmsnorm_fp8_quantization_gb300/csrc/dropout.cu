@@ -8,8 +8,10 @@
 //
 //     out = (kept ? x / (1 - p) : 0) + residual
 //
-// Bound by memory: 6 bytes a 16-bit element with a residual against about 20
-// instructions, 16 of them the generator's.
+// 16384 x 4096 elements: fp32 and bf16 with a residual are bound by memory (6600 GB/s,
+// 60.7 us bf16); bf16 alone by the generator's twenty 32-bit products for four elements,
+// which the multiplier takes four cycles each for (54 us, 40 from memory; as separate low and
+// high products 62).
 #include <cmath>
 #include <cstdint>
 

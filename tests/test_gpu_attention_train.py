@@ -168,6 +168,17 @@ def test_bad_values_in_pairs_that_are_not_kept(gpu, c, bad):
     assert got["dq"][i].isnan().any() and got["dk"][m].isnan().any()
 
 
+def test_heads_outside_tokens(gpu):
+    """Tensors that are stored [heads, tokens, dim]."""
+    c = Case((150, 20), dim=128, heads=6, kv_heads=3)
+    s = make(c)
+    t = {n: s[n].transpose(0, 1).contiguous().transpose(0, 1) for n in ("q", "k", "v", "dout")}
+    assert t["q"].stride() == (128, 170 * 128, 1)
+    a, b = both(gpu, s), both(gpu, dict(t, kw=s["kw"]))
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
 def test_deterministic(gpu):
     c = Case((700, 300, 1), heads=8, kv_heads=2, dim=128)
     s = make(c)
