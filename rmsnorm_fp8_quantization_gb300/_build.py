@@ -25,7 +25,8 @@ FAST_STAMP = os.path.join(BUILD_DIR, "fastcall.txt")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "kernels_f32.cu", "kernels_bf16.cu", "kernels_f16.cu", "finalize.cu",
            "noalloc.cu", "softmax.cu", "rope.cu", "paged_attention.cu",
-           "paged_prefill.cu", "attention_bwd.cu", "dropout.cu"]
+           "paged_prefill.cu", "attention_bwd.cu",
+           "attention_bwd_bf16.cu", "attention_bwd_f16.cu", "dropout.cu"]
 
 
 def _nvcc() -> str:

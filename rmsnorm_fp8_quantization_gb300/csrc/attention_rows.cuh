@@ -27,6 +27,7 @@ struct AttnBwdParams {
   int causal, window;
   float *kv_part, *q_part;  // sums in parts: [kv_splits][dk, dv][keys][hkv][d], [q_splits][tokens][hq][d]
   int kv_splits, q_splits;         // CTAs that share a tile's steps
+  int kv_each, q_each;             // heads that a CTA takes one after another
   int kv_join_blocks, join_blocks;
   int kv_blocks, q_blocks;         // CTAs for dk and dv, and for dq
   int q_stat_blocks, stat_blocks;  // of the row statistics: for q's rows, and with v's
@@ -144,5 +145,10 @@ __device__ __noinline__ void grad_again(const AttnBwdParams& p, const SeqRange& 
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] *= f;
 }
+
+cudaError_t launch_attention_bwd_bf16(const AttnBwdParams& p, cudaStream_t stream);
+cudaError_t launch_attention_bwd_f16(const AttnBwdParams& p, cudaStream_t stream);
+cudaError_t read_attention_bwd_bf16_error(unsigned int* v, bool clear);
+cudaError_t read_attention_bwd_f16_error(unsigned int* v, bool clear);
 
 }  // namespace gbn

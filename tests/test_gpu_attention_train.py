@@ -65,6 +65,14 @@ CASES = {
     "shared steps, ragged f16": Case((900, 1, 0, 333), heads=6, kv_heads=1, dim=96, dtype=F16, lead=3, trail=5),
     "shared steps of dq": Case((100,), (4100,), causal=False, heads=1, kv_heads=1, dim=72),
     "shared steps, window": Case((3000,), uniform=True, heads=8, kv_heads=1, window=900),
+    # many CTAs of few steps: several heads of a tile in one, an odd number of them, lengths that differ
+    "heads in turn": Case((130,) * 40, uniform=True, heads=24, kv_heads=12),
+    "heads in turn, dim 128": Case((129,) * 40, uniform=True, heads=24, kv_heads=12, dim=128, dtype=F16),
+    "odd heads in turn": Case((200,) * 60, uniform=True, heads=9, kv_heads=9, dim=96, causal=False),
+    "heads in turn, window": Case((700,) * 16, uniform=True, heads=16, kv_heads=4, dim=72, window=100),
+    "heads in turn, ragged": Case(tuple(3 + 37 * i % 200 for i in range(100)), heads=16, kv_heads=16,
+                                  dim=40, dtype=F16, lead=2, trail=9),
+    "heads in turn, cross": Case((1, 140, 0) * 50, (300, 5, 64) * 50, heads=12, kv_heads=12, dim=128, causal=False),
     "long": Case((2500,), uniform=True, heads=2, kv_heads=1, dim=128),
     "long f16, not causal": Case((2500,), uniform=True, heads=2, kv_heads=1, dtype=F16, causal=False),
 }
@@ -141,7 +149,9 @@ def test_given_outputs_and_strides(gpu):
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 @pytest.mark.parametrize("c", [Case((600,), dim=128, heads=8, kv_heads=4, window=20, lead=2),
                                Case((130, 600), dim=64, dtype=F16, window=20),
-                               Case((2600,), dim=64, heads=8, kv_heads=1, window=700)], ids=str)
+                               Case((2600,), dim=64, heads=8, kv_heads=1, window=700),
+                               Case((130,) * 60 + (600,), dim=128, heads=16, kv_heads=16, window=20)],
+                         ids=lambda c: f"{len(c.q_lens)} sequences of {c.dim}")
 def test_bad_values_in_pairs_that_are_not_kept(gpu, c, bad):
     """A token's keys and values, and another's query and gradient, of no use: the rows that have no
     kept pair with them come out as if they were 0, whatever else their tiles hold."""
