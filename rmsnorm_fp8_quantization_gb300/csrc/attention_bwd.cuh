@@ -139,13 +139,15 @@ __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const Att
 // reads 64 bytes of shared memory a cycle then instead of 128, all there are.
 //
 // Bound at head_dim 128 by the tensor core: 2048 (dk, dv) and 1536 (dq) cycles a step.  Two
-// sequences of 4096 tokens, 32 / 8 heads: not causal 1131 us, causal 630; the seven products
-// run at 1700 TFLOP/s and 1530, and the same kernel without exponentials, conversions and
+// sequences of 4096 tokens, 32 / 8 heads: not causal 1131 us, causal 612; the seven products
+// run at 1700 TFLOP/s and 1570, and the same kernel without exponentials, conversions and
 // reads of the statistics was 2 % faster.  At 64 by the chain from one product over the rows'
 // threads to the next (2100 and 1700 cycles a step, 1230 and 870 of them products; causal 490
 // us): P and dS in columns of their own, which frees S and dP earlier, took 555, and two CTAs
 // a multiprocessor with steps of 64 rows 503, with ragged windows a third more.  A CTA takes
-// about 9000 cycles besides its steps: up to the first scores 5500, the output 3000.
+// about 9000 cycles besides its steps: up to the first scores 5500, the output 3000.  Where a
+// tile has few steps a CTA takes several heads of it in rounds: the next round's x goes to its
+// place, and its first products run, before the last one's output.
 
 struct BwdBarriers {
   uint64_t full[8], empty[8], s_full, p_full[2], dp_full, ds_full[2], x_full[2], x_ready[2], acc_full;
