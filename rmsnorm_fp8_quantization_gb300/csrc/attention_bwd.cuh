@@ -22,7 +22,7 @@ namespace {
 // that the kernel below reads: by head, then query.  f16 besides: the largest squared norms of
 // 16 rows of dout and v.  A CTA takes 16 tokens and 16 heads; a row is C lanes of 8
 // elements.  Bound by reading out and dout once (cold, 4096 tokens of 32 heads of 128: 67 MB in
-// 23 us, a third of what memory gives: a warp has eight loads under way).
+// 19 us, 44 % of what memory gives: a warp has eight loads under way).
 constexpr int kStatHeads = 16, kStatThreads = 256;
 
 template <typename T, int C>
