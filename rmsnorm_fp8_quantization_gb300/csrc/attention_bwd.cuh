@@ -687,10 +687,12 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
             put(e, v);
           }
           if (bad && dropped) {
-#pragma unroll 1
+#pragma unroll
             for (int e = 0; e < 4; ++e) {
               if (!(bad & (1u << e)) || col0 + c + 8 * e >= p.d) continue;
               float f[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q) f[q] = __uint_as_float(o[8 * e + q]) * factor;
               if (!KV) grad_again<T, 0>(p, s, b, xh, h, x, col0 + c + 8 * e, f);
               else if (w == 0) grad_again<T, 2>(p, s, b, 0, h, x, c + 8 * e, f);
               else grad_again<T, 1>(p, s, b, 0, h, x, c + 8 * e, f);
@@ -899,10 +901,7 @@ __device__ __forceinline__ void join_rows(const AttnBwdParams& p, int block) {
       f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w;
       f[4] += c.x, f[5] += c.y, f[6] += c.z, f[7] += c.w;
     }
-    bool bad = false;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) bad = bad || f[e] != f[e];
-    if (bad) grad_again<T, WHICH>(p, s, b, head, WHICH ? head : head / p.group, x, col, f);
+    if (nan_bits(f)) grad_again<T, WHICH>(p, s, b, head, WHICH ? head : head / p.group, x, col, f);
     uint32_t v[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) v[q] = narrow2<T>(p2(f[2 * q], f[2 * q + 1]));

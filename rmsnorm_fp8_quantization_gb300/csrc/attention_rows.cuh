@@ -93,11 +93,11 @@ __device__ __forceinline__ float row_dot(const void* a, int64_t at, const void* 
   }
   return s;
 }
-// All of them NaN: nothing that is added changes that.
-__device__ __forceinline__ bool all_nan(const float* f) {
-  bool r = true;
+// Bit e: f[e] is NaN.
+__device__ __forceinline__ uint32_t nan_bits(const float* f) {
+  uint32_t r = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) r = r && f[e] != f[e];
+  for (int e = 0; e < 8; ++e) r |= f[e] != f[e] ? 1u << e : 0u;
   return r;
 }
 
@@ -112,19 +112,40 @@ __device__ __forceinline__ float2 pair_again(const AttnBwdParams& p, const SeqRa
   return make_float2(w, w * (dp + p.ndelta[head * p.stat_stride + stat + i]));
 }
 
-// Eight columns of one row's gradient, pair by pair: dq of query `row` (of q head `head`), or
-// dk (WHICH 1) and dv (2) of key `row` of kv head h.  The products of whole tiles give a
-// pair that is not kept the weight 0, and 0 times an infinity or NaN is NaN: a row that came
-// out NaN next to such pairs is computed here, where they do not enter.  Rare, and slow.
+// Eight columns of one row's gradient, f: dq of query `row` (of q head `head`), or dk (WHICH 1)
+// and dv (2) of key `row` of kv head h.  The products of whole tiles give a pair that is not
+// kept the weight 0, and 0 times an infinity or NaN is NaN: columns that came out NaN next to
+// such pairs are computed here pair by pair, where those do not enter.  Rare, and slow; a NaN that
+// belongs there (a kept gradient's, or its row's delta) is looked for first, and ends it.
 template <typename T, int WHICH>
 __device__ __noinline__ void grad_again(const AttnBwdParams& p, const SeqRange& s, int b, int head,
-                                        int h, int row, int col, float* acc) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+                                        int h, int row, int col, float* f) {
+  const uint32_t need = nan_bits(f);
   const int64_t stat = stat_base(s.q0, b);
   const int lo = WHICH ? query_first(p, s, row) : key_first(p, s, row);
   const int hi = WHICH ? query_end(p, s, row) : key_end(p, s, row);
   const int heads = WHICH ? p.group : 1;
+  uint32_t sure = 0;
+#pragma unroll 1
+  for (int g = 0; g < heads; ++g) {
+    const int n = WHICH ? h * p.group + g : head;
+#pragma unroll 1
+    for (int o = lo; o < (WHICH ? hi : min(hi, lo + 1)); ++o) {
+      const int i = WHICH ? o : row;
+      if (WHICH != 2) {
+        const float nd = p.ndelta[n * p.stat_stride + stat + i];
+        if (nd != nd) return;
+      } else {
+        float x[8];
+        eight<T>(p.dout, (s.q0 + static_cast<int64_t>(i)) * p.gt + n * p.gh + col, x);
+        sure |= nan_bits(x);
+        if ((need & ~sure) == 0u) return;
+      }
+    }
+  }
+  float acc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 #pragma unroll 1
   for (int g = 0; g < heads; ++g) {
     const int n = WHICH ? h * p.group + g : head;
@@ -138,12 +159,13 @@ __device__ __noinline__ void grad_again(const AttnBwdParams& p, const SeqRange& 
       if (WHICH == 2) eight<T>(p.dout, (s.q0 + static_cast<int64_t>(i)) * p.gt + n * p.gh + col, x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] = fmaf(WHICH == 2 ? w.x : w.y, x[e], acc[e]);
-      if (all_nan(acc)) return;
+      if ((need & ~nan_bits(acc)) == 0u) return;  // (nothing that is added changes that)
     }
   }
-  const float f = ex2(-static_cast<float>(kWeightLog2<T>)) * (WHICH == 2 ? 1.f : p.scale);
+  const float factor = ex2(-static_cast<float>(kWeightLog2<T>)) * (WHICH == 2 ? 1.f : p.scale);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] *= f;
+  for (int e = 0; e < 8; ++e)
+    if (need & (1u << e)) f[e] = acc[e] * factor;
 }
 
 cudaError_t launch_attention_bwd_bf16(const AttnBwdParams& p, cudaStream_t stream);

@@ -178,6 +178,29 @@ def test_bad_values_in_pairs_that_are_not_kept(gpu, c, bad):
     assert got["dq"][i].isnan().any() and got["dk"][m].isnan().any()
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_one_bad_column(gpu, dim):
+    """A NaN in one column of a gradient: dv's column of the keys that keep it, dq's row and dk's rows; the
+    other columns of dv, and everything of rows that have no part in it, are numbers, and right."""
+    c = Case((600,), dim=dim, heads=2, kv_heads=1, window=50)
+    s = make(c)
+    i = 300
+    clean = dict(s, dout=s["dout"].clone())
+    s["dout"][i, 1, 5] = float("nan")
+    clean["dout"][i, 1] = 0
+    out, lse = gpu.attention_fwd(s["q"], s["k"], s["v"], **s["kw"])
+    dq, dk, dv = gpu.attention_bwd(s["dout"], s["q"], s["k"], s["v"], out, lse, **s["kw"])
+    hit = torch.zeros(600, dtype=torch.bool, device="cuda")
+    hit[i - 49:i + 1] = True
+    assert dv[hit, 0, 5].isnan().all() and not dv[hit, 0, :5].isnan().any() and not dv[hit, 0, 6:].isnan().any()
+    assert dk[hit].isnan().all() and dq[i, 1].isnan().all()
+    want = define(c, clean)
+    for n, t, out_ in (("dq", dq, (slice(i, i + 1), slice(1, 2))), ("dk", dk, (hit,)), ("dv", dv, (hit,))):
+        value, off = (x.clone() for x in want[n])
+        value[out_] = float("nan")
+        check(n, t, (value, off))
+
+
 def test_heads_outside_tokens(gpu):
     """Tensors that are stored [heads, tokens, dim]."""
     c = Case((150, 20), dim=128, heads=6, kv_heads=3)
