@@ -201,6 +201,33 @@ def test_one_bad_column(gpu, dim):
         check(n, t, (value, off))
 
 
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_an_overflowed_gradient(gpu, dtype, window):
+    """An infinity in a gradient, as a loss scale that is too large leaves: no gradient of a row that has a
+    part in it is finite (in dv: of its column), and every other one is right."""
+    c = Case((600,), heads=2, kv_heads=1, window=window, dtype=dtype)
+    s = make(c)
+    i = 300
+    clean = dict(s, dout=s["dout"].clone())
+    s["dout"][i, 1, 5] = float("inf")
+    clean["dout"][i, 1] = 0
+    out, lse = gpu.attention_fwd(s["q"], s["k"], s["v"], **s["kw"])
+    dq, dk, dv = gpu.attention_bwd(s["dout"], s["q"], s["k"], s["v"], out, lse, **s["kw"])
+    first = i - window + 1 if window else 0
+    hit = torch.zeros(600, dtype=torch.bool, device="cuda")
+    hit[first:i + 1] = True
+    assert not dk[hit].isfinite().any() and not dq[i, 1].isfinite().any()
+    assert not dv[hit, 0, 5].isfinite().any() and dv[hit, 0, :5].isfinite().all() and dv[hit, 0, 6:].isfinite().all()
+    want = define(c, clean)
+    for n, t, where in (("dq", dq, (slice(i, i + 1), slice(1, 2))), ("dk", dk, (hit,)), ("dv", dv, (hit,))):
+        value, off = (x.clone() for x in want[n])
+        value[where] = t[where].to(value.dtype) * float("nan")
+        t = t.clone()
+        t[where] = float("nan")
+        check(n, t, (value, off))
+
+
 def test_heads_outside_tokens(gpu):
     """Tensors that are stored [heads, tokens, dim]."""
     c = Case((150, 20), dim=128, heads=6, kv_heads=3)
