@@ -198,9 +198,10 @@ __device__ __forceinline__ float warp_largest(const float* at, int64_t stride, i
 }
 
 // What f16 ds is taken larger by: a power of two u with u |dout_i| |v_j| 2 < 2^15 for every
-// pair of this CTA (|ds| <= |dp| + |delta|, and |delta| is a mean of dp).  ds falls with the
-// number of keys and f16 ends early: without it, gradients of long sequences would be sums
-// of numbers without bits.
+// query of this CTA and every key of its sequence (|ds| <= |dp| + |delta|, and |delta| is a mean
+// of dp over all keys of the row: with the values of a tile's own keys alone, small ones among
+// larger, delta passes the bound and ds is infinite).  ds falls with the number of keys and f16
+// ends early: without it, gradients of long sequences would be sums of numbers without bits.
 template <typename T, bool KV>
 __device__ __forceinline__ float ds_factor(const AttnBwdParams& p, const SeqRange& s, int b, int xh, int h,
                                            int x0, int rows) {
@@ -210,7 +211,7 @@ __device__ __forceinline__ float ds_factor(const AttnBwdParams& p, const SeqRang
   const float* v = p.v_norms + h * p.v_norm_stride + norm_base(s.k0, b);
   const float mq = KV ? warp_largest(q, p.q_norm_stride, p.group, runs(s.qlen))
                       : warp_largest(q + x0 / kStatTokens, 0, 1, runs(rows));
-  const float mv = KV ? warp_largest(v + x0 / kStatTokens, 0, 1, runs(rows)) : warp_largest(v, 0, 1, runs(s.kv));
+  const float mv = warp_largest(v, 0, 1, runs(s.kv));
   const float most = 2.f * sqrtf(mq) * sqrtf(mv);
   if (!(most > 0.f) || !(most < INFINITY)) return 1.f;
   const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 100);
