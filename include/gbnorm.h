@@ -544,8 +544,8 @@ gbn_status gbn_attention_fwd(const gbn_attention_fwd_args* args, cudaStream_t st
  *     dv_j = sum_i p_ij dout_i
  * (over the queries of every head that shares the key).  fp32 scores, sums and
  * results; p and ds are rounded to dtype for their products: half a step
- * relative.  f16: probabilities below 2^-26 by up to 2^-37, ds below 2^-29 of
- * the largest |dout_i| |v_j| of a sequence and kv head by up to 2^-40 of it.
+ * relative.  f16: probabilities below 2^-26 by up to 2^-37, ds below 2^-28 of
+ * the largest |dout_i| |v_j| of a sequence and kv head by up to 2^-39 of it.
  * The rounding of lse itself (2^-24 relative) shows in p where |lse| is large.
  *   workspace  gbn_attention_bwd_workspace_size() bytes (same arguments), 16-byte
  *              aligned (else GBN_ERR_WORKSPACE); needs no initialization; calls that may

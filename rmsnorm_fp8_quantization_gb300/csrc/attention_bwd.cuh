@@ -197,11 +197,15 @@ __device__ __forceinline__ float warp_largest(const float* at, int64_t stride, i
   return warp_max_nan(most);
 }
 
-// What f16 ds is taken larger by: a power of two u with u |dout_i| |v_j| 2 < 2^15 for every
-// query of this CTA and every key of its sequence (|ds| <= |dp| + |delta|, and |delta| is a mean
-// of dp over all keys of the row: with the values of a tile's own keys alone, small ones among
-// larger, delta passes the bound and ds is infinite).  ds falls with the number of keys and f16
-// ends early: without it, gradients of long sequences would be sums of numbers without bits.
+// What f16 ds is taken larger by: a power of two u with 2^14 <= u M < 2^15, M the largest |dout_i|
+// of this CTA's queries times the largest |v_j| of the sequence.  delta is the mean of dp over
+// all keys of the row, so dp - delta is 1 - p times a difference of two that are within M, and
+// |ds| <= 2 M p (1 - p) <= M / 2: u |ds| stays below 2^14, a quarter of f16's range, which leaves
+// what p's and delta's rounding adds (2^-11 of M, and p relative) its room.  (With the values of a
+// tile's own keys alone, small ones among larger, delta passes the bound and ds is infinite.)
+// Its bits end at 2^-14 / u <= 2^-28 M, half a step there is 2^-25 / u <= 2^-39 M.  ds falls with the
+// number of keys and f16 ends early: without u, gradients of long sequences would be sums of
+// numbers without bits.
 template <typename T, bool KV>
 __device__ __forceinline__ float ds_factor(const AttnBwdParams& p, const SeqRange& s, int b, int xh, int h,
                                            int x0, int rows) {
@@ -212,7 +216,7 @@ __device__ __forceinline__ float ds_factor(const AttnBwdParams& p, const SeqRang
   const float mq = KV ? warp_largest(q, p.q_norm_stride, p.group, runs(s.qlen))
                       : warp_largest(q + x0 / kStatTokens, 0, 1, runs(rows));
   const float mv = warp_largest(v, 0, 1, runs(s.kv));
-  const float most = 2.f * sqrtf(mq) * sqrtf(mv);
+  const float most = sqrtf(mq) * sqrtf(mv);
   if (!(most > 0.f) || !(most < INFINITY)) return 1.f;
   const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 100);
   return __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);

@@ -81,3 +81,22 @@ def test_sequences_of_different_size(gpu, name, dtype):
     for n, lens in (("v", c.keys), ("dout", c.q_lens)):
         s = sized(c, s, n, -6 * (places(c, lens)[0] % 3))
     held(gpu, c, s)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_rounding_of_small_ds(gpu, dim):
+    """f16 ds that lie where the type ends, all rounded the same way: off by at most 2^-39 of the largest
+    |dout| |v| each, as documented.  Query 0 sets that (1) and has no part in dk (q_0 = 0); every other
+    one's ds is 9/8 2^-38 of either sign (p = 2^-7, dout 2^-24, v 9/8 2^-7, delta 0)."""
+    n = 128
+    c = Case((n,), uniform=True, heads=1, kv_heads=1, dim=dim, dtype=F16, causal=False, scale=2.0 ** 10)
+    q, k, v, dout = (torch.zeros(1, n, 1, dim, dtype=F16, device="cuda") for _ in range(4))
+    q[0, 1:, 0, 1] = 2.0 ** 10
+    dout[0, :, 0, 0] = 2.0 ** -24
+    dout[0, 0, 0, 0] = 1.0
+    v[0, 0::2, 0, 0], v[0, 1::2, 0, 0] = 1.125 * 2.0 ** -7, -1.125 * 2.0 ** -7
+    v[0, 0, 0, 0], v[0, 1, 0, 0] = 1.0, -1.0
+    s = dict(q=q, k=k, v=v, dout=dout, kw=dict(causal=False, scale=c.scale))
+    held(gpu, c, s)
+    dk = define(c, s)["dk"][0][:, 0, 1]
+    assert abs(dk[2].item() / (127 * 2.0 ** 20 * 1.125 * 2.0 ** -38) - 1) < 1e-6
