@@ -66,6 +66,18 @@ __device__ __forceinline__ T narrow(float v) {
   else return __float2half_rn(v);
 }
 
+// 16 bytes that are used once, by a coherent load: out may be x or residual, and what a kernel
+// writes must not be read on the read-only path, not even each thread its own bytes before it
+// writes them (half a sector is another thread's).
+__device__ __forceinline__ uint4 ld_once16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
 // VEC: pointers on 16 bytes; else element by element, four (one draw) at a time.
 template <typename T, int MODE, bool ADD, bool VEC>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p) {
@@ -85,14 +97,14 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p
   // A block's draws share their counter's high half (their number divides 2^32).
   const uint32_t high = static_cast<uint32_t>(
       (static_cast<int64_t>(blockIdx.x) * (kThreads * kVecs * kDraws)) >> 32);
-  uint32_t xw[kVecs][VEC ? 4 : 1], rw[kVecs][VEC ? 4 : 1];
+  uint4 xw[kVecs], rw[kVecs];
   if constexpr (VEC) {
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const int64_t e0 = (v0 + u * kThreads) * kElems;
       if (e0 + kElems > p.n) continue;
-      if (MODE != kDrop) ld_vec_raw<T, kElems, true>(x + e0, xw[u]);
-      if (ADD) ld_vec_raw<T, kElems, true>(res + e0, rw[u]);
+      if (MODE != kDrop) xw[u] = ld_once16(x + e0);
+      if (ADD) rw[u] = ld_once16(res + e0);
     }
   }
 #pragma unroll
@@ -114,8 +126,14 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p
     }
     if (VEC && e0 + kElems <= p.n) {
       float f[kElems] = {}, r[kElems];
-      if (MODE != kDrop) unpack<T, kElems>(xw[u], f);
-      if (ADD) unpack<T, kElems>(rw[u], r);
+      if (MODE != kDrop) {
+        const uint32_t h[4] = {xw[u].x, xw[u].y, xw[u].z, xw[u].w};
+        unpack<T, kElems>(h, f);
+      }
+      if (ADD) {
+        const uint32_t h[4] = {rw[u].x, rw[u].y, rw[u].z, rw[u].w};
+        unpack<T, kElems>(h, r);
+      }
       uint64_t o[kElems / 2];
 #pragma unroll
       for (int e = 0; e < kElems; e += 2) {

@@ -114,6 +114,22 @@ def test_in_place(gpu):
     assert torch.equal(gpu.dropout_bwd(d, 0.2, rng(), out=d), gpu.dropout_bwd(x, 0.2, rng()))
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("p", [0.0, 0.3, 1.0])
+def test_in_place_of_many_blocks(gpu, p, dtype):
+    """Whatever block runs first, each element is read before it is written."""
+    g = torch.Generator().manual_seed(2)
+    x, r = (torch.randn(3001, 1021, generator=g).to(dtype).cuda() for _ in range(2))
+    for residual in (None, r):
+        want = gpu.dropout_fwd(x, p, rng(8, 1), residual=residual)
+        for _ in range(3):
+            a = x.clone()
+            assert torch.equal(gpu.dropout_fwd(a, p, rng(8, 1), residual=residual, out=a), want)
+    for _ in range(3):
+        b = r.clone()
+        assert torch.equal(gpu.dropout_fwd(x, p, rng(8, 1), residual=b, out=b), want)
+
+
 def test_counter_beyond_32_bits(gpu):
     """Elements past 2^34: the counter's high half."""
     n = 2 ** 34 + 4096 + 5
