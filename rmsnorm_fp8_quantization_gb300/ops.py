@@ -758,16 +758,14 @@ def attention_fwd(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, max_q=None, ma
     return out, lse
 
 
-def attention_bwd_workspace(q, k, *, cu_seqlens=None, max_q=None, max_k=None, causal=True, window=0):
-    """A workspace for ``attention_bwd`` calls with these arguments."""
-    _on_gpu(q)
-    tokens, keys = (t.shape[0] if t.dim() == 3 else t.shape[0] * t.shape[1] for t in (q, k))
-    if cu_seqlens is None:
-        batches, max_q, max_k = q.shape[0], q.shape[1], k.shape[1]
-    else:
-        batches, max_k = cu_seqlens.shape[0] - 1, max_q if max_k is None else max_k
-    n = _attention_bwd_bytes(tokens, keys, batches, q.shape[-2], k.shape[-2], q.shape[-1], max_q,
-                             max_k, window, bool(causal), G.TORCH_DTYPE[q.dtype])
+def attention_bwd_workspace(q, k, *, cu_seqlens=None, cu_seqlens_k=None, max_q=None, max_k=None,
+                            scale=None, causal=True, window=0):
+    """A workspace for ``attention_bwd`` calls with these arguments (``scale`` does not matter to
+    it; neither do the lengths themselves: ``max_k`` alone stands for keys of their own)."""
+    if cu_seqlens is not None and max_k is not None and cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens
+    _, _, _, sizes = _attention_tensors(q, k, k, cu_seqlens, cu_seqlens_k, max_q, max_k)
+    n = _attention_bwd_bytes(*sizes, window, bool(causal), G.TORCH_DTYPE[q.dtype])
     return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 

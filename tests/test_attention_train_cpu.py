@@ -215,3 +215,24 @@ def test_dropout_keeps_its_own_numbers(fake):
     y = A.dropout(x.detach(), 0.5, rng, r)
     y.sum().backward()                         # nothing to draw for the residual alone
     assert len(calls) == 3
+
+
+def test_workspace_wrapper_refusals(ops):
+    b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)
+    q, k, cu, cu_k = b(6, 4, 16), b(9, 2, 16), i32(0, 2, 6), i32(0, 4, 9)
+    for match, a, kw in (
+            ("needs max_q", (q, k), dict(cu_seqlens=cu)),
+            ("needs max_k", (q, k), dict(cu_seqlens=cu, max_q=4, cu_seqlens_k=cu_k)),
+            ("entries", (q, k), dict(cu_seqlens=cu, max_q=4, cu_seqlens_k=i32(0, 9), max_k=9)),
+            ("tokens", (q, k), dict(cu_seqlens=cu, max_q=4)),
+            ("cu_seqlens", (q, k), {}),
+            ("head_dim", (q, b(6, 2, 24)), dict(cu_seqlens=cu, max_q=4)),
+            ("dtype", (q.float(), k.float()), dict(cu_seqlens=cu, max_q=4))):
+        with pytest.raises(ValueError, match=match):
+            ops.attention_bwd_workspace(*a, **kw)
+    # what attention_bwd takes is taken, up to the tensors' device
+    for kw in (dict(cu_seqlens=cu, max_q=4, cu_seqlens_k=cu_k, max_k=5, scale=0.3, causal=False, window=3),
+               dict(cu_seqlens=cu, max_q=4, max_k=5)):
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            ops.attention_bwd_workspace(q, k, **kw)

@@ -146,6 +146,23 @@ def test_given_outputs_and_strides(gpu):
         check(n, t, want[n])
 
 
+@pytest.mark.parametrize("c", [Case((3, 140, 1), (211, 1, 300), causal=False, dim=96, scale=0.07),
+                               Case((1500,), (1400,), heads=8, kv_heads=1, dim=128, scale=0.2, dtype=F16),
+                               Case((130, 130), uniform=True, window=40, scale=0.3)],
+                         ids=["cross", "cross, shared steps", "uniform"])
+def test_workspace_of_the_callers(gpu, c):
+    """Keys of their own and a scale: the workspace takes what the call takes, and its size is the call's."""
+    s = make(c)
+    out, lse = gpu.attention_fwd(s["q"], s["k"], s["v"], **s["kw"])
+    w = gpu.attention_bwd_workspace(s["q"], s["k"], **s["kw"])
+    want = gpu.attention_bwd(s["dout"], s["q"], s["k"], s["v"], out, lse, **s["kw"])
+    for _ in range(2):
+        got = gpu.attention_bwd(s["dout"], s["q"], s["k"], s["v"], out, lse, workspace=w, **s["kw"])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with pytest.raises(RuntimeError, match="WORKSPACE|workspace"):
+        gpu.attention_bwd(s["dout"], s["q"], s["k"], s["v"], out, lse, workspace=w[:-1], **s["kw"])
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 @pytest.mark.parametrize("c", [Case((600,), dim=128, heads=8, kv_heads=4, window=20, lead=2),
                                Case((130, 600), dim=64, dtype=F16, window=20),
