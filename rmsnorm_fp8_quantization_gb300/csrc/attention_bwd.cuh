@@ -158,6 +158,7 @@ struct BwdBarriers {
     SeqRange range;
     int sequence, head0, rounds, x0, rows;
   } kept;
+  uint4 again[8];  // by warp of the rows: those with a NaN, a word a round
 };
 
 template <int DP, bool KV>
@@ -225,6 +226,28 @@ __device__ __forceinline__ float ds_factor(const AttnBwdParams& p, const SeqRang
 // Until the kernel before has completed.  Every CTA gets here before it ends, so that what comes
 // after this kernel comes after the statistics too.
 __device__ __forceinline__ void wait_for_stats() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The rows of a warp's gradients that have a NaN, when its outputs are written: no other role waits
+// then, and what this needs in registers costs the steps nothing.
+template <typename T, bool KV>
+__device__ __noinline__ void tile_again(const AttnBwdParams& p, const BwdBarriers& bars) {
+  const auto kept = bars.kept;
+  const int warp = threadIdx.x >> 5, w = warp >> 2, half = p.d <= 64 ? 32 : 64;
+  for (int round = 0; round < kept.rounds; ++round) {
+    const int xh = kept.head0 + round;
+    for (uint32_t todo = (&bars.again[warp].x)[round]; todo; todo &= todo - 1) {
+      const int x = kept.x0 + (warp & 3) * 32 + __ffs(todo) - 1;
+      const int64_t row = (KV ? kept.range.k0 : kept.range.q0) + static_cast<int64_t>(x);
+      if constexpr (!KV)
+        grad_again<T, 0>(p, kept.range, kept.sequence, xh, xh / p.group, x, w * half, half,
+                         static_cast<T*>(p.dq) + row * p.dqt + xh * p.dqh);
+      else if (w == 0)
+        grad_again<T, 2>(p, kept.range, kept.sequence, 0, xh, x, 0, p.d, static_cast<T*>(p.dv) + row * p.dvt + xh * p.dvh);
+      else
+        grad_again<T, 1>(p, kept.range, kept.sequence, 0, xh, x, 0, p.d, static_cast<T*>(p.dk) + row * p.dkt + xh * p.dkh);
+    }
+  }
+}
 
 // SEVERAL: a CTA may take several heads of its tile one after another, in rounds (a kernel of its
 // own: with one round the code for more costs 3 to 6 % of a call).
@@ -556,6 +579,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
   } else {
     // -------------------------------------------------- probabilities and their gradients
     set_regs_inc<Shape::kRegsSoftmax>();
+    if (lane == 0) bars.again[warp] = make_uint4(0u, 0u, 0u, 0u);
     const int w = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
     int lo = 0, hi = 0;  // the rows of y that this thread's row goes with
@@ -625,7 +649,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
       }
       // Output: dv by the warps 0-3, dk by 4-7; or half of dq's columns by each.
       if (!kFirstRound && ok) {
-        const int xh = xh0 + round - 1, h = KV ? xh : xh / p.group;  // h: kv head
+        const int xh = xh0 + round - 1;
         constexpr int kCols = KV ? DP : DP / 2;
         const int col0 = KV ? 0 : w * kCols;
         const uint32_t from = tmem + lanes + (KV && w == 0 ? kAcc2 : kAcc1 + col0);
@@ -635,8 +659,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
         const int64_t at = KV ? (w == 0 ? row * p.dvt + xh * p.dvh : row * p.dkt + xh * p.dkh)
                               : row * p.dqt + xh * p.dqh;
         const uint32_t some = __ballot_sync(0xFFFFFFFFu, live);
-        // Next to pairs of its tiles that it dropped.
-        const bool dropped = live && n > 0 && (lo > base || hi < min(base + nt * kBwdTile, KV ? s.qlen : s.kv));
+        bool nan = false;
         // Through shared memory, so that a store writes whole sectors, where the ring is used up; a
         // lane to a row otherwise.
         uint8_t* const stage = raw + warp * 32 * 64;
@@ -663,7 +686,6 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
                                 __uint_as_float(o[e + 2]) * factor, __uint_as_float(o[e + 3]) * factor);
             continue;
           }
-          uint32_t bad = 0;  // bit e: a NaN in columns 8 e .. 8 e + 7
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             float f = __uint_as_float(o[e]);
@@ -671,7 +693,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
             for (int q = 1; q < 7; q += 2)
               f = max3_nan(f, __uint_as_float(o[e + q]), __uint_as_float(o[e + q + 1]));
             f = max3_nan(f, f, __uint_as_float(o[e + 7]));
-            bad |= f != f ? 1u << (e / 8) : 0u;
+            nan |= f != f;
           }
           auto put = [&](int e, const uint32_t* v) {
             if (more) {
@@ -691,22 +713,6 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
                                      p2(factor, factor)));
             put(e, v);
           }
-          if (bad && dropped) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (!(bad & (1u << e)) || col0 + c + 8 * e >= p.d) continue;
-              float f[8];
-#pragma unroll
-              for (int q = 0; q < 8; ++q) f[q] = __uint_as_float(o[8 * e + q]) * factor;
-              if (!KV) grad_again<T, 0>(p, s, b, xh, h, x, col0 + c + 8 * e, f);
-              else if (w == 0) grad_again<T, 2>(p, s, b, 0, h, x, c + 8 * e, f);
-              else grad_again<T, 1>(p, s, b, 0, h, x, c + 8 * e, f);
-              uint32_t v[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) v[q] = narrow2<T>(p2(f[2 * q], f[2 * q + 1]));
-              put(e, v);
-            }
-          }
           __syncwarp();
           if (more) continue;
           const int e = lane & 3;
@@ -721,6 +727,8 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
           __syncwarp();
         }
         if (more) tc_fence_before();  // (read before the next round's sums)
+        const uint32_t again = __ballot_sync(0xFFFFFFFFu, nan && live);
+        if (again != 0u && lane == 0) (&bars.again[warp].x)[round - 1] = again;
       }
       return more;
     };
@@ -833,6 +841,10 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
     if (ok) steps_of(0);
 #pragma unroll 1
     for (int round = 1; ok && between(std::false_type(), round) && ok; ++round) steps_of(round);
+    if (splits == 1) {
+      const uint4 again = bars.again[warp];
+      if ((again.x | again.y | again.z | again.w) != 0u) tile_again<T, KV>(p, bars);
+    }
   }
 
   if (!ok) flag_wait_timeout();
@@ -882,8 +894,8 @@ cudaError_t launch_dim(const AttnBwdParams& p, const CUtensorMap* m, int64_t gri
 //
 // Few CTAs with many steps each (few heads that share their keys, one sequence) leave most
 // of the GPU idle: the steps of a tile go to several CTAs then, which write 32-bit parts,
-// and this kernel adds those up in order.  A thread takes eight columns of a row.  NaN:
-// computed pair by pair (see grad_again), which ends at once where it belongs there.
+// and this kernel adds those up in order.  A thread takes eight columns of a row; rows with a NaN
+// are looked at again (grad_again).
 template <typename T, int WHICH>
 __device__ __forceinline__ void join_rows(const AttnBwdParams& p, int block) {
   const TilePlace place =
@@ -895,6 +907,12 @@ __device__ __forceinline__ void join_rows(const AttnBwdParams& p, int block) {
   const int heads = WHICH ? p.hkv : p.hq, chunks = p.d / 8, splits = WHICH ? p.kv_splits : p.q_splits;
   const int rows = min(kStatTokens, (WHICH ? s.kv : s.qlen) - x0);
   const int64_t step = (WHICH ? 2 * static_cast<int64_t>(p.keys) * p.hkv : static_cast<int64_t>(p.tokens) * p.hq) * p.d;
+  T* const dst = static_cast<T*>(WHICH == 0 ? p.dq : WHICH == 1 ? p.dk : p.dv);
+  auto place_of = [&](int x, int head) {  // a row's in the output
+    const int64_t row = (WHICH ? s.k0 : s.q0) + static_cast<int64_t>(x);
+    return WHICH == 0 ? row * p.dqt + head * p.dqh : WHICH == 1 ? row * p.dkt + head * p.dkh : row * p.dvt + head * p.dvh;
+  };
+  bool nan = false;
   for (int r = threadIdx.x; r < rows * heads * chunks; r += kStatThreads) {
     const int col = r % chunks * 8, head = r / chunks % heads, x = x0 + r / chunks / heads;
     const int64_t row = (WHICH ? s.k0 : s.q0) + static_cast<int64_t>(x);
@@ -906,19 +924,21 @@ __device__ __forceinline__ void join_rows(const AttnBwdParams& p, int block) {
       f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w;
       f[4] += c.x, f[5] += c.y, f[6] += c.z, f[7] += c.w;
     }
-    if (nan_bits(f)) grad_again<T, WHICH>(p, s, b, head, WHICH ? head : head / p.group, x, col, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) nan |= f[e] != f[e];
     uint32_t v[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) v[q] = narrow2<T>(p2(f[2 * q], f[2 * q + 1]));
-    T* const dst = static_cast<T*>(WHICH == 0 ? p.dq : WHICH == 1 ? p.dk : p.dv);
-    const int64_t at = WHICH == 0   ? row * p.dqt + head * p.dqh
-                       : WHICH == 1 ? row * p.dkt + head * p.dkh
-                                    : row * p.dvt + head * p.dvh;
-    *reinterpret_cast<uint4*>(dst + at + col) = make_uint4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<uint4*>(dst + place_of(x, head) + col) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  if (!__syncthreads_or(nan)) return;
+  for (int r = threadIdx.x >> 5; r < rows * heads; r += kStatThreads / 32) {
+    const int head = r % heads, x = x0 + r / heads;
+    grad_again<T, WHICH>(p, s, b, head, WHICH ? head : head / p.group, x, 0, p.d, dst + place_of(x, head));
   }
 }
 template <typename T>
-__global__ void __launch_bounds__(kStatThreads) attention_join_kernel(const AttnBwdParams p) {
+__global__ void __launch_bounds__(kStatThreads, 2) attention_join_kernel(const AttnBwdParams p) {
   pdl_begin();
   const int block = blockIdx.x;
   if (block >= p.kv_join_blocks) {

@@ -1,4 +1,4 @@
-// Parameters, masks and the key-by-key gradients of the attention's backward pass.
+// Parameters, masks and the gradients pair by pair of the attention's backward pass.
 //
 // With p_ij = 2^(scale log2(e) q_i.k_j - lse_i log2(e)) (kept pairs), dp_ij = dout_i.v_j
 // and delta_i = dout_i.out_i:
@@ -75,110 +75,250 @@ __device__ __forceinline__ int query_end(const AttnBwdParams& p, const SeqRange&
   return e > 0 ? static_cast<int>(min(e, static_cast<int64_t>(s.qlen))) : 0;
 }
 
+__device__ __forceinline__ bool finite32(float f) { return fabsf(f) < INFINITY; }
+// Four elements; beyond the head 0.
 template <typename T>
-__device__ __forceinline__ void eight(const void* base, int64_t at, float* f) {
-  const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + at);
-  const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-  unpack<T, 8>(h, f);
+__device__ __forceinline__ uint2 four_words(const T* row, int col, int d) {
+  return col < d ? *reinterpret_cast<const uint2*>(row + col) : make_uint2(0u, 0u);
 }
 template <typename T>
-__device__ __forceinline__ float row_dot(const void* a, int64_t at, const void* b, int64_t bt, int d) {
-  float s = 0.f;
-  for (int c = 0; c < d; c += 8) {
-    float x[8], y[8];
-    eight<T>(a, at + c, x);
-    eight<T>(b, bt + c, y);
+__device__ __forceinline__ void four_floats(uint2 w, float* f) {
+  const uint32_t a[2] = {w.x, w.y};
+  unpack<T, 4>(a, f);
+}
+
+// v[i] summed over the warp, in lanes 32 / N i and the next 32 / N - 1.
+template <int N>
+__device__ __forceinline__ float sum_of_pairs(float* v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(x[e], y[e], s);
+  for (int n = N / 2, o = 16; n > 0; n >>= 1, o >>= 1) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+    }
   }
-  return s;
-}
-// Bit e: f[e] is NaN.
-__device__ __forceinline__ uint32_t nan_bits(const float* f) {
-  uint32_t r = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) r |= f[e] != f[e] ? 1u << e : 0u;
-  return r;
+  for (int o = 16 / N; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+  return v[0];
 }
 
-// (p, ds) of one kept pair: query i of `head`, key j of kv head h; p 2^kWeightLog2 larger.
-template <typename T>
-__device__ __forceinline__ float2 pair_again(const AttnBwdParams& p, const SeqRange& s, int64_t stat,
-                                             int head, int h, int i, int j) {
-  const int64_t qi = s.q0 + i, kj = s.k0 + j;
-  const float z = row_dot<T>(p.q, qi * p.qt + head * p.qh, p.k, kj * p.kt + h * p.kh, p.d);
-  const float w = ex2(fmaf(z, p.scale_log2, p.nlse[head * p.stat_stride + stat + i]));
-  const float dp = row_dot<T>(p.dout, qi * p.gt + head * p.gh, p.v, kj * p.vt + h * p.vh, p.d);
-  return make_float2(w, w * (dp + p.ndelta[head * p.stat_stride + stat + i]));
-}
-
-// Eight columns of one row's gradient, f: dq of query `row` (of q head `head`), or dk (WHICH 1)
-// and dv (2) of key `row` of kv head h.  The products of whole tiles give a pair that is not
-// kept the weight 0, and 0 times an infinity or NaN is NaN: columns that came out NaN next to
-// such pairs are computed here pair by pair, where those do not enter.  Rare, and slow; a NaN that
-// belongs there (a kept gradient's, its row's delta, or what an infinite delta makes of its row) is
-// looked for first, and ends it (4096 tokens, 8 / 2 heads of 128, f16: one such gradient 31 ms a call, an
-// infinity in every seventh 62).
+// The columns from `first` on of one row's gradient that came out NaN, by a whole warp: dq of query x (WHICH 0,
+// of q head `head`), or dk (1) and dv (2) of key x of kv head h; dst: the row.
+//
+// The products of whole tiles give a pair that is not kept the weight 0, and 0 times an infinity or NaN
+// is NaN.  So a NaN either belongs there or comes from a row of the other side that x's tiles hold and
+// x dropped; then the sum is taken again pair by pair, over the kept pairs alone.  That costs a pass over
+// the range for a row, so what can be told from less is told from less:
+//  * a query's -lse or -delta that is NaN makes every kept pair's share NaN;
+//  * the rows that x dropped, at most two tiles of them, hold nothing infinite or NaN (queries: their lse and
+//    delta are numbers; lse is not where a kept score is not, delta is not where dout is not): it belongs;
+//  * kept pairs whose share is infinite or NaN alone decide the sum, if there are any: dk and dv take them
+//    first, dq looks for columns of kept keys that are not finite (lse is, so their weight is 0, and 0
+//    times them NaN).
+// A lane takes four columns; every sum in a fixed order.
 template <typename T, int WHICH>
-__device__ __noinline__ void grad_again(const AttnBwdParams& p, const SeqRange& s, int b, int head,
-                                        int h, int row, int col, float* f) {
-  const uint32_t need = nan_bits(f);
-  const int64_t stat = stat_base(s.q0, b);
-  const int lo = WHICH ? query_first(p, s, row) : key_first(p, s, row);
-  const int hi = WHICH ? query_end(p, s, row) : key_end(p, s, row);
-  const int heads = WHICH ? p.group : 1;
-  uint32_t sure = 0;
-  float acc[8];
+__device__ __noinline__ void grad_again(const AttnBwdParams& p, const SeqRange& s, int b, int head, int h, int x,
+                                        int first, int columns, T* dst) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  constexpr bool kv = WHICH != 0;
+  constexpr int kAtOnce = 8;  // pairs under way
+  const int lane = threadIdx.x & 31, col = lane * 4;
+  const int heads = kv ? p.group : 1;
+  const int lo = kv ? query_first(p, s, x) : key_first(p, s, x);
+  const int hi = kv ? query_end(p, s, x) : key_end(p, s, x);
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  uint32_t need = 0;  // bit e: column col + e
+  if (col >= first && col < min(first + columns, p.d)) {
+    float f[4];
+    four_floats<T>(four_words(dst, col, p.d), f);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-#pragma unroll 1
-  for (int g = 0; g < heads; ++g) {
-    const int n = WHICH ? h * p.group + g : head;
-#pragma unroll 1
-    for (int o = lo; o < (WHICH ? hi : min(hi, lo + 1)); ++o) {
-      const int i = WHICH ? o : row;
-      if (WHICH != 2) {
-        const float nd = p.ndelta[n * p.stat_stride + stat + i];
-        if (nd != nd) return;
-        if (WHICH == 1 && fabsf(nd) == INFINITY) {
-          // (what these pairs alone make NaN, the whole sum has NaN)
-          const float2 w = pair_again<T>(p, s, stat, n, h, i, row);
-          float x[8];
-          eight<T>(p.q, (s.q0 + static_cast<int64_t>(i)) * p.qt + n * p.qh + col, x);
+    for (int e = 0; e < 4; ++e) need |= f[e] != f[e] ? 1u << e : 0u;
+  }
+  if (!__any_sync(kAll, need != 0u)) return;
+  auto write = [&](uint32_t which) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] = fmaf(w.y, x[e], acc[e]);
-          if ((need & ~nan_bits(acc)) == 0u) return;
-        }
-      } else {
-        float x[8];
-        eight<T>(p.dout, (s.q0 + static_cast<int64_t>(i)) * p.gt + n * p.gh + col, x);
-        sure |= nan_bits(x);
-        if ((need & ~sure) == 0u) return;
+    for (int e = 0; e < 4; ++e)
+      if ((which >> e) & 1u)
+        reinterpret_cast<uint16_t*>(dst)[col + e] = static_cast<uint16_t>(narrow2<T>(p2(acc[e], acc[e])));
+  };
+  if (hi <= lo) return write(need);
+
+  const int64_t stat = stat_base(s.q0, b) + static_cast<int64_t>(kv ? h * p.group : head) * p.stat_stride;
+  const float* const nlse = p.nlse + stat;
+  const float* const ndelta = p.ndelta + stat;
+  float own_nl = 0.f, own_nd = 0.f;
+  if constexpr (!kv) {
+    own_nl = nlse[x];
+    own_nd = ndelta[x];
+    if (own_nl != own_nl || own_nd != own_nd) return;
+  }
+  // Rows of the other side, this lane's columns: q or k, dout or v.  (What a row needs, out of the
+  // parameters once: read there for every row it is what the passes below wait for.)
+  const bool has = col < p.d;
+  const int64_t row0 = kv ? s.q0 : s.k0, step1 = kv ? p.qt : p.kt, step2 = kv ? p.gt : p.vt;
+  const int64_t head1 = kv ? p.qh : p.kh, head2 = kv ? p.gh : p.vh, stats = p.stat_stride;
+  const T* const base1 = static_cast<const T*>(kv ? p.q : p.k) + row0 * step1 + (kv ? h * p.group : h) * head1 + col;
+  const T* const base2 = static_cast<const T*>(kv ? p.dout : p.v) + row0 * step2 + (kv ? h * p.group : h) * head2 + col;
+  const float scale_log2 = p.scale_log2;
+  auto four = [&](const T* at) { return has ? *reinterpret_cast<const uint2*>(at) : make_uint2(0u, 0u); };
+  auto not_finite = [&](int y) {  // of k's columns (dq)
+    float f[4];
+    four_floats<T>(four(base1 + y * step1), f);
+    uint32_t r = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r |= finite32(f[e]) ? 0u : 1u << e;
+    return r;
+  };
+
+  // The rows of x's tiles that x dropped.
+  {
+    const int x0 = x & ~(kBwdTile - 1), last = min(x0 + kBwdTile, kv ? s.kv : s.qlen) - 1;
+    const int from = (kv ? query_first(p, s, x0) : key_first(p, s, x0)) & ~(kBwdTile - 1);
+    const int end = kv ? query_end(p, s, last) : key_end(p, s, last);
+    const int to = min((end + kBwdTile - 1) & ~(kBwdTile - 1), kv ? s.qlen : s.kv);
+    const int count = to - from - (hi - lo);
+    auto dropped = [&](int o) { return from + o < lo ? from + o : from + o + hi - lo; };
+    if constexpr (kv) {
+      bool any = false;
+      for (int g = 0; g < heads && !any; ++g) {
+        const float* const nl = nlse + g * stats;
+        const float* const nd = ndelta + g * stats;
+        bool bad = false;
+#pragma unroll 4
+        for (int o = lane; o < count; o += 32) bad |= !finite32(nl[dropped(o)]) || !finite32(nd[dropped(o)]);
+        any = __any_sync(kAll, bad);
       }
+      if (!any) return;
+    } else {
+      uint32_t bad = 0;
+#pragma unroll 8
+      for (int o = 0; o < count; ++o) bad |= not_finite(dropped(o));
+      need &= bad;
+      if (!__any_sync(kAll, need != 0u)) return;
     }
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-#pragma unroll 1
-  for (int g = 0; g < heads; ++g) {
-    const int n = WHICH ? h * p.group + g : head;
-#pragma unroll 1
-    for (int o = lo; o < hi; ++o) {
-      const int i = WHICH ? o : row, j = WHICH ? row : o;
-      const float2 w = pair_again<T>(p, s, stat, n, h, i, j);
-      float x[8];
-      if (WHICH == 0) eight<T>(p.k, (s.k0 + static_cast<int64_t>(j)) * p.kt + h * p.kh + col, x);
-      if (WHICH == 1) eight<T>(p.q, (s.q0 + static_cast<int64_t>(i)) * p.qt + n * p.qh + col, x);
-      if (WHICH == 2) eight<T>(p.dout, (s.q0 + static_cast<int64_t>(i)) * p.gt + n * p.gh + col, x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(WHICH == 2 ? w.x : w.y, x[e], acc[e]);
-      if ((need & ~nan_bits(acc)) == 0u) return;  // (nothing that is added changes that)
-    }
+
+  float a[4], c[4];  // x's own row: k or q, v or dout
+  {
+    const int64_t row = static_cast<int64_t>(kv ? s.k0 : s.q0) + x;
+    four_floats<T>(four_words(static_cast<const T*>(kv ? p.k : p.q) + (kv ? row * p.kt + h * p.kh : row * p.qt + head * p.qh),
+                              col, p.d), a);
+    four_floats<T>(four_words(static_cast<const T*>(kv ? p.v : p.dout) + (kv ? row * p.vt + h * p.vh : row * p.gt + head * p.gh),
+                              col, p.d), c);
   }
+  // Adds the shares of the pairs with rows y[0 ..] of the group's head g (negative: none).
+  auto add = [&](int g, const int* y) {
+    uint2 w1[kAtOnce], w2[kAtOnce];
+    // The pair whose weight this lane computes.
+    const int which = lane / (32 / kAtOnce);
+    int mine = -1;
+    const T* const from1 = base1 + g * head1;
+    const T* const from2 = base2 + g * head2;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      w1[i] = w2[i] = make_uint2(0u, 0u);
+      if (i == which) mine = y[i];
+      if (y[i] < 0) continue;
+      w1[i] = four(from1 + y[i] * step1);
+      w2[i] = four(from2 + y[i] * step2);
+    }
+    float nl = own_nl, nd = own_nd, z[kAtOnce], dp[kAtOnce];
+    if (kv && mine >= 0) {
+      nl = nlse[g * stats + mine];
+      nd = ndelta[g * stats + mine];
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      float f[4];
+      four_floats<T>(w1[i], f);
+      z[i] = fmaf(a[3], f[3], fmaf(a[2], f[2], fmaf(a[1], f[1], a[0] * f[0])));
+      four_floats<T>(w2[i], f);
+      dp[i] = fmaf(c[3], f[3], fmaf(c[2], f[2], fmaf(c[1], f[1], c[0] * f[0])));
+    }
+    const float zs = sum_of_pairs<kAtOnce>(z), dps = WHICH == 2 ? 0.f : sum_of_pairs<kAtOnce>(dp);
+    const float w = ex2(fmaf(zs, scale_log2, nl));
+    const float weight = mine < 0 ? 0.f : WHICH == 2 ? w : w * (dps + nd);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      float f[4];
+      four_floats<T>(WHICH == 2 ? w2[i] : w1[i], f);
+      const float v = __shfl_sync(kAll, weight, i * (32 / kAtOnce));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = fmaf(v, f[e], acc[e]);
+    }
+  };
+  // Nothing that is added changes what is NaN already.
+  auto settled = [&] {
+    uint32_t nan = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) nan |= acc[e] != acc[e] ? 1u << e : 0u;
+    return __all_sync(kAll, (need & ~nan) == 0u);
+  };
+
+  if constexpr (kv) {
+    bool some = false;
+#pragma unroll 1
+    for (int g = 0; g < heads; ++g)
+#pragma unroll 1
+      for (int o = lo; o < hi; o += 32) {
+        float nl = 0.f, nd = 0.f;
+        if (o + lane < hi) {
+          nl = nlse[g * stats + o + lane];
+          nd = ndelta[g * stats + o + lane];
+        }
+        if (__any_sync(kAll, nl != nl || (WHICH == 1 && nd != nd))) return;
+        uint32_t bad = __ballot_sync(kAll, !finite32(nl) || !finite32(nd));
+        if (!bad) continue;
+        some = true;
+#pragma unroll 1
+        while (bad) {
+          int y[kAtOnce];
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            y[i] = bad ? o + __ffs(bad) - 1 : -1;
+            bad &= bad - 1;  // (0 stays 0)
+          }
+          add(g, y);
+        }
+        if (settled()) return;
+      }
+    if (some) {
+      uint32_t nan = 0, inf = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        nan |= acc[e] != acc[e] ? 1u << e : 0u;
+        inf |= fabsf(acc[e]) == INFINITY ? 1u << e : 0u;
+      }
+      write(need & inf);
+      need &= ~(nan | inf);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = 0.f;
+    }
+  } else if (finite32(own_nl)) {
+    uint32_t bad = 0;
+#pragma unroll 8
+    for (int o = lo; o < hi; ++o) bad |= not_finite(o);
+    need &= ~bad;
+  }
+  if (!__any_sync(kAll, need != 0u)) return;
+
+#pragma unroll 1
+  for (int g = 0; g < heads; ++g)
+#pragma unroll 1
+    for (int o = lo; o < hi; o += kAtOnce) {
+      int y[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) y[i] = o + i < hi ? o + i : -1;
+      add(g, y);
+      if ((o - lo) % 64 == 0 && settled()) return;
+    }
   const float factor = ex2(-static_cast<float>(kWeightLog2<T>)) * (WHICH == 2 ? 1.f : p.scale);
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (need & (1u << e)) f[e] = acc[e] * factor;
+  for (int e = 0; e < 4; ++e) acc[e] *= factor;
+  write(need);
 }
 
 cudaError_t launch_attention_bwd_bf16(const AttnBwdParams& p, cudaStream_t stream);
