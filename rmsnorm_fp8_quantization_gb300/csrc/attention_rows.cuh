@@ -75,7 +75,6 @@ __device__ __forceinline__ int query_end(const AttnBwdParams& p, const SeqRange&
   return e > 0 ? static_cast<int>(min(e, static_cast<int64_t>(s.qlen))) : 0;
 }
 
-__device__ __forceinline__ bool finite32(float f) { return fabsf(f) < INFINITY; }
 // Four elements; beyond the head 0.
 template <typename T>
 __device__ __forceinline__ uint2 four_words(const T* row, int col, int d) {
@@ -85,24 +84,6 @@ template <typename T>
 __device__ __forceinline__ void four_floats(uint2 w, float* f) {
   const uint32_t a[2] = {w.x, w.y};
   unpack<T, 4>(a, f);
-}
-
-// v[i] summed over the warp, in lanes 32 / N i and the next 32 / N - 1.
-template <int N>
-__device__ __forceinline__ float sum_of_pairs(float* v) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int n = N / 2, o = 16; n > 0; n >>= 1, o >>= 1) {
-    const bool upper = lane & o;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float give = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
-    }
-  }
-#pragma unroll
-  for (int o = 16 / N; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
-  return v[0];
 }
 
 // The columns from `first` on of one row's gradient that came out NaN, by a whole warp: dq of query x (WHICH 0,

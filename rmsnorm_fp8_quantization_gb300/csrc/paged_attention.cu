@@ -599,9 +599,14 @@ __global__ void __launch_bounds__(kStepThreads + 32, MT <= 2 ? StepShape<T, FP8,
     for (int e = 0; e < 8; ++e) nan |= acc[e] != acc[e];
     if (nan && ll == ll) {  // (a NaN sum: a kept score is NaN, and so is the row)
       const int low = max(row_low(p, s, gr / p.group), k0), high = min(row_high(p, s, gr / p.group), k1);
-      if (low > k0 || high < k1)  // it dropped keys that others of its tile keep
-        row_again<T, FP8>(p, b, 0, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
-                          FP8 ? p.scale_log2 * *p.k_scale_inv : p.scale_log2, ll, low, high, c, acc);
+      if (low > k0 || high < k1) {  // it dropped keys that others of its tile keep
+        float f[8];
+        const uint32_t other =
+            row_again<T, FP8>(p, b, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
+                              FP8 ? p.scale_log2 * *p.k_scale_inv : p.scale_log2, ll, k0, k1, low, high, c, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = (other >> e) & 1u ? f[e] : acc[e];
+      }
     }
     if (p.cluster) {
       float* dst = s_part + r * DP + c;

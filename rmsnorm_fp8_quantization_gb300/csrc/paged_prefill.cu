@@ -110,6 +110,67 @@ __device__ __forceinline__ float large_factor(float scale) {
   return __uint_as_float(__float_as_uint(scale) & 0xFF800000u);
 }
 
+// A row's columns that came out NaN (bad: bit c: among 8 c .. 8 c + 7), after it has been written, in 32 bits
+// where it is a part of several (see columns_to_sum; l = 0: nothing has a weight, and they are 0).  By the row's
+// thread: the rows of a warp go through the same keys, and read them once.  Whole warps that took one row after
+// another were slower (34 ms against 23: 2 x 4096 tokens, 32 / 8 heads of 128, causal, with a NaN among the values of
+// one token), and a call of all lanes together costs every call of this kernel 3 %.
+template <typename T, bool FP8, bool PACKED>
+__device__ __noinline__ void columns_again(const AttnParams& p, int b, int first, int h, const T* q, float scale,
+                                           float l, float inv, int k0, int k1, int lo, int hi, uint32_t bad,
+                                           uint8_t* row) {
+  const Keys<T, FP8, PACKED> keys = {p, b, first, h};
+  auto write = [&](int col, float f) {
+    if (p.splits > 1) reinterpret_cast<float*>(row)[col] = f;
+    else reinterpret_cast<uint16_t*>(row)[col] = static_cast<uint16_t>(narrow2<T>(p2(f * inv, f * inv)));
+  };
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+  for (int group = 0; group < p.d; group += 32) {
+    uint32_t open = 0;  // bit e: column group + e
+#pragma unroll 1
+    for (int c = 0; c < 32 && group + c < p.d; c += 8) {
+      if (!((bad >> ((group + c) / 8)) & 1u)) continue;
+      uint32_t up = 0, down = 0, zero = 0;
+      if (l != 0.f) open |= columns_to_sum(keys, q, scale, k0, k1, lo, hi, group + c, &up, &down) << c;
+      else zero = 0xFFu;
+      for (int e = 0; e < 8; ++e)
+        if (((up | down | zero) >> e) & 1u) write(group + c + e, (up >> e) & 1u ? INFINITY : (down >> e) & 1u ? -INFINITY : 0.f);
+    }
+    if (open == 0u) continue;
+    if (sum == 0.f) {
+#pragma unroll 1
+      for (int j = lo; j < hi; ++j) {
+        float s;
+        if (!keys.score(q, scale, j, &s) || s == -INFINITY) continue;
+        if (s > top) sum = top == -INFINITY ? 0.f : sum * ex2(top - s);
+        top = fmaxf(top, s);
+        sum += ex2(s - top);
+      }
+    }
+    float acc[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+#pragma unroll 1
+    for (int j = lo; j < hi; ++j) {
+      float s;
+      if (!keys.score(q, scale, j, &s)) continue;
+      const float w = ex2(s - (top == -INFINITY ? 0.f : top));
+#pragma unroll
+      for (int c = 0; c < 32; c += 8) {
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (((open >> c) & 0xFFu) != 0u) keys.value(j, group + c, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[c + e] = fmaf(w, f[e], acc[c + e]);
+      }
+    }
+    const float back = sum == 0.f ? 0.f : l / sum;
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if ((open >> e) & 1u) write(group + e, acc[e] * back);
+  }
+}
+
 template <typename T, bool FP8, int DP, bool PACKED>
 __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ AttnParams p,
@@ -711,12 +772,12 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
         if (part) p.part_ml[ro * p.splits + split] = make_float2(ref, l);
         else if (p.lse) p.lse[ro] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
       }
+      uint32_t bad = 0;  // bit c: a NaN in columns 8 c .. 8 c + 7
       // (one copy of the code: a CTA runs it once, and fetching it is what it costs)
 #pragma unroll 1
       for (int q4 = 0; q4 < DP / 32; ++q4) {
         const int col = q4 * 32;
         uint32_t o[32];
-        uint32_t bad = 0;  // bit i: a NaN in columns col + 8 i .. + 7
         if (n > 0) {
           tc_ld32(to + col, o);
           tc_wait_ld<32>(o);
@@ -731,7 +792,7 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
           for (int e = 1; e < 7; e += 2)
             x = max3_nan(x, __uint_as_float(o[i + e]), __uint_as_float(o[i + e + 1]));
           x = max3_nan(x, x, __uint_as_float(o[i + 7]));
-          bad |= x != x ? 1u << (i / 8) : 0u;
+          bad |= x != x ? 1u << (q4 * 4 + i / 8) : 0u;
         }
         auto narrow = [&](float x, float y) { return narrow2<T>(mul2(p2(x, y), p2(inv, inv))); };
         if (part) {
@@ -747,32 +808,16 @@ __global__ void __launch_bounds__(PrefillShape<FP8, DP>::kThreads, 1)
             put((q4 & 1) * 4 + i / 8, w[0], w[1], w[2], w[3]);
           }
         }
-        if (bad && live && l == l && (l == 0.f || rlo > k0 || rhi < k1)) {
-          // It dropped keys that other rows of its tiles keep (a NaN sum: a kept
-          // score is NaN, and so is the row).  A sum of 0: nothing has a weight.
-#pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            if (!(bad & (1u << i)) || col + 8 * i >= p.d) continue;
-            float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (l != 0.f)
-              row_again<T, FP8, PACKED>(p, b, s.k0, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
-                                FP8 ? p.scale_log2 * kscale : p.scale_log2, l, rlo, rhi, col + 8 * i,
-                                f);
-            if (part) {
-#pragma unroll
-              for (int e = 0; e < 8; e += 4)
-                put(2 * i + e / 4, __float_as_uint(f[e]), __float_as_uint(f[e + 1]),
-                    __float_as_uint(f[e + 2]), __float_as_uint(f[e + 3]));
-            } else {
-              put((q4 & 1) * 4 + i, narrow(f[0], f[1]), narrow(f[2], f[3]), narrow(f[4], f[5]),
-                  narrow(f[6], f[7]));
-            }
-          }
-        }
         if (part) flush(col * 4, (p.d - col) / 4);
         else if (q4 & 1) flush((col - 32) * 2, (p.d - (col - 32)) / 8);
         else __syncwarp();  // the loads of tensor memory take the whole warp
       }
+      // NaN next to keys that the row dropped and others of its tiles keep, or where nothing has a weight.  (A NaN
+      // sum: a kept score is NaN, and so is the row.)
+      if (bad && ((some >> lane) & 1u) && l == l && (l == 0.f || rlo > k0 || rhi < k1))
+        columns_again<T, FP8, PACKED>(p, b, s.k0, h, reinterpret_cast<const T*>(p.q) + token * p.qt + head * p.qh,
+                                      FP8 ? p.scale_log2 * kscale : p.scale_log2, l, inv, k0, k1, rlo, rhi, bad,
+                                      dst + at);
     }
   }
 

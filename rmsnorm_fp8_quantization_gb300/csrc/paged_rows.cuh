@@ -176,54 +176,157 @@ __device__ __forceinline__ void cache_values(const void* cache, int64_t at, floa
   }
 }
 
-// Eight output columns of one row again, key by key, over j in [lo, hi) alone:
-// l times the mean of v_j with the weights 2^(scale q.k_j), l the row's sum.  The
-// products of whole tiles give a dropped key the weight 0, and 0 times an infinity
-// or NaN among its values is NaN; a row that dropped keys of its tiles and came out
-// NaN is computed here, where dropped keys do not enter (a NaN that belongs there
-// comes out again).  Against its own maximum and sum: of large scores the rounding,
-// which goes by the order of summation, exceeds one.  Rare, and slow.
-template <typename T, bool FP8, bool PACKED = false>
-__device__ __noinline__ void row_again(const AttnParams& p, int b, int first, int h, const T* q,
-                                       float scale, float l, int lo, int hi, int col, float* acc) {
+__device__ __forceinline__ bool finite32(float f) { return fabsf(f) < INFINITY; }
+
+// v[i] summed over the warp, in lanes 32 / N i and the next 32 / N - 1.
+template <int N>
+__device__ __forceinline__ float sum_of_pairs(float* v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = N / 2, o = 16; n > 0; n >>= 1, o >>= 1) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+    }
+  }
+#pragma unroll
+  for (int o = 16 / N; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+  return v[0];
+}
+
+// Keys and values of one sequence and kv head.
+template <typename T, bool FP8, bool PACKED>
+struct Keys {
+  const AttnParams& p;
+  int b, first, h;  // first: row of the first key (contiguous keys)
+
+  __device__ __forceinline__ bool place(int j, int64_t* pg, int64_t* slot) const {  // false: no such page
+    *pg = 0;
+    *slot = first + j;
+    if constexpr (!PACKED) {
+      *pg = p.table[b * p.table_stride + (j >> p.page_shift)];
+      *slot = j & ((1 << p.page_shift) - 1);
+      return *pg >= 0 && *pg < p.num_pages;
+    }
+    return true;
+  }
+  __device__ __forceinline__ void value(int j, int col, float* f) const {  // eight columns; 0: no such page
+    int64_t pg, slot;
+    if (place(j, &pg, &slot)) {
+      cache_values<T, FP8>(p.v, pg * p.vp + slot * p.vs + h * p.vh + col, f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = 0.f;
+    }
+  }
+  __device__ __forceinline__ bool score(const T* q, float scale, int j, float* s) const {
+    int64_t pg, slot;
+    if (!place(j, &pg, &slot)) return false;
+    const int64_t ko = pg * p.kp + slot * p.ks + h * p.kh;
+    float sum = 0.f;
+    for (int c = 0; c < p.d; c += 8) {
+      float qf[8], kf[8];
+      const uint4 w = *reinterpret_cast<const uint4*>(q + c);
+      const uint32_t qw[4] = {w.x, w.y, w.z, w.w};
+      unpack<T, 8>(qw, qf);
+      cache_values<T, FP8>(p.k, ko + c, kf);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(qf[e], kf[e], sum);
+    }
+    *s = __fmul_rn(sum, scale);  // (not into a subtraction: its rounding is the maximum's)
+    return true;
+  }
+};
+
+// Eight columns of a row's output, some of them NaN, next to keys of [k0, k1) that the row dropped; it keeps
+// [lo, hi).  Returns the columns (bits) that have to be summed again, and those that are infinite.
+//
+// The products of whole tiles give a dropped key the weight 0, and 0 times an infinity or NaN among its
+// values is NaN.  A column in which no dropped key has one is right as it is.  In the others kept values
+// that are not finite decide: NaN, or infinities of both signs, are NaN; of one sign that infinity (a
+// kept key's weight is not 0, unless its score is -inf).  They are looked for from the row's own token
+// on, and found next to it where there are many.  What is left is summed again key by key, over the
+// kept keys alone: against their own maximum and sum, because of large scores the rounding, which goes by
+// the order of summation, exceeds one.  Rare, and slow.
+template <typename T, bool FP8, bool PACKED>
+__device__ __forceinline__ uint32_t columns_to_sum(const Keys<T, FP8, PACKED>& keys, const T* q, float scale, int k0,
+                                                   int k1, int lo, int hi, int col, uint32_t* up, uint32_t* down) {
+  uint32_t open = 0;
+  const int dropped = k1 - k0 - (hi - lo);
+#pragma unroll 4
+  for (int o = 0; o < dropped; ++o) {
+    float f[8];
+    keys.value(k0 + o < lo ? k0 + o : k0 + o + hi - lo, col, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) open |= finite32(f[e]) ? 0u : 1u << e;
+  }
+  *up = *down = 0;
+#pragma unroll 1
+  for (int j = hi - 1; j >= lo && open != 0u; j -= 4) {
+    float f[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) keys.value(max(j - i, lo), col, f[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t nan = 0, pos = 0, neg = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        nan |= f[i][e] != f[i][e] ? 1u << e : 0u;
+        pos |= f[i][e] == INFINITY ? 1u << e : 0u;
+        neg |= f[i][e] == -INFINITY ? 1u << e : 0u;
+      }
+      if (open & ((pos & ~*up) | (neg & ~*down))) {
+        float s;
+        if (keys.score(q, scale, max(j - i, lo), &s) && s == -INFINITY) nan |= pos | neg;
+        *up |= pos;
+        *down |= neg;
+      }
+      open &= ~(nan | (*up & *down));
+    }
+  }
+  *up &= open;
+  *down &= open;
+  return open & ~(*up | *down);
+}
+
+// Those of one thread's eight columns: returns the ones that belong otherwise than they are, in acc l times the
+// mean of v_j with the weights 2^(scale q.k_j), l the row's sum.
+template <typename T, bool FP8>
+__device__ __noinline__ uint32_t row_again(const AttnParams& p, int b, int h, const T* q, float scale, float l,
+                                           int k0, int k1, int lo, int hi, int col, float* acc) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  float top = -INFINITY, sum = 0.f;
+  if (hi <= lo) return 0xFFu;
+  const Keys<T, FP8, false> keys = {p, b, 0, h};
+  uint32_t up, down;
+  const uint32_t open = columns_to_sum(keys, q, scale, k0, k1, lo, hi, col, &up, &down);
+  if (open != 0u) {
+    float top = -INFINITY, sum = 0.f;
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass)
-    for (int j = lo; j < hi; ++j) {
-      int64_t pg = 0, slot = first + j;
-      if constexpr (!PACKED) {
-        pg = p.table[b * p.table_stride + (j >> p.page_shift)];
-        if (pg < 0 || pg >= p.num_pages) continue;
-        slot = j & ((1 << p.page_shift) - 1);
-      }
-      const int64_t ko = pg * p.kp + slot * p.ks + h * p.kh, vo = pg * p.vp + slot * p.vs + h * p.vh;
-      float s = 0.f;
-      for (int c = 0; c < p.d; c += 8) {
-        float qf[8], kf[8];
-        const uint4 w = *reinterpret_cast<const uint4*>(q + c);
-        const uint32_t qw[4] = {w.x, w.y, w.z, w.w};
-        unpack<T, 8>(qw, qf);
-        cache_values<T, FP8>(p.k, ko + c, kf);
+    for (int pass = 0; pass < 2; ++pass)
+      for (int j = lo; j < hi; ++j) {
+        float s;
+        if (!keys.score(q, scale, j, &s)) continue;
+        if (pass == 0) {
+          top = fmaxf(top, s);
+          continue;
+        }
+        const float w = ex2(s - (top == -INFINITY ? 0.f : top));
+        sum += w;
+        float vf[8];
+        keys.value(j, col, vf);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(qf[e], kf[e], s);
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, vf[e], acc[e]);
       }
-      s = __fmul_rn(s, scale);  // (not into the subtraction below: its rounding is the maximum's)
-      if (pass == 0) {
-        top = fmaxf(top, s);
-        continue;
-      }
-      const float w = ex2(s - (top == -INFINITY ? 0.f : top));
-      sum += w;
-      float vf[8];
-      cache_values<T, FP8>(p.v, vo + col, vf);
+    const float back = sum == 0.f ? 0.f : l / sum;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, vf[e], acc[e]);
-    }
-  const float back = sum == 0.f ? 0.f : l / sum;
+    for (int e = 0; e < 8; ++e) acc[e] *= back;
+  }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] *= back;
+  for (int e = 0; e < 8; ++e) acc[e] = (up >> e) & 1u ? INFINITY : (down >> e) & 1u ? -INFINITY : acc[e];
+  return open | up | down;
 }
 
 constexpr float kLn2 = 0.6931471805599453f;
