@@ -98,6 +98,11 @@ def rms_norm_with_residual(x, gamma, eps=1e-6, zero_centered_gamma=False, sm_mar
     return _Norm.apply(x, gamma, None, "rmsnorm", eps, zero_centered_gamma, sm_margin, True)
 
 
+def _no_gradient(name, value, where):
+    if isinstance(value, torch.Tensor) and value.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, and {where} has none for it")
+
+
 class _Rope(torch.autograd.Function):
     """(q, k) rotated; k may be None."""
 
@@ -126,8 +131,7 @@ def rope(q, k, inv_freq, positions=None, layout="half", mscale=1.0):
     """Rotary positions of q and k [batch, seq, heads, head_dim] (k may be
     None): ``ops.rope_fwd`` with its gradient, for q and k alone (inv_freq is refused
     where it requires one)."""
-    if inv_freq.requires_grad and torch.is_grad_enabled():
-        raise ValueError("inv_freq requires a gradient, and rope has none for it")
+    _no_gradient("inv_freq", inv_freq, "rope")
     return _Rope.apply(q, k, inv_freq, positions, layout, mscale)
 
 
@@ -169,7 +173,9 @@ def attention(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, max_q=None, max_k=
               causal=True, window=0):
     """``ops.attention_fwd`` with its gradient, for q, k and v; returns its output.  Padding rows
     of packed tensors get 0, in the output and in the gradients.  Tensors whose strides the
-    kernels do not take are copied."""
+    kernels do not take are copied.  ``scale`` gets no gradient (a tensor that requires one is
+    refused: multiply q by it)."""
+    _no_gradient("scale", scale, "attention")
     kw = dict(max_q=max_q, max_k=max_k, scale=scale, causal=causal, window=window)
     return _Attention.apply(q, k, v, cu_seqlens, cu_seqlens_k, kw)
 
@@ -196,4 +202,5 @@ class _Dropout(torch.autograd.Function):
 def dropout(x, p, rng, residual=None):
     """``ops.dropout_fwd`` with its gradient, for x and residual.  rng (seed, offset) is copied:
     the caller may advance it in place."""
+    _no_gradient("p", p, "dropout")
     return _Dropout.apply(x, p, rng, residual)

@@ -236,3 +236,20 @@ def test_workspace_wrapper_refusals(ops):
                dict(cu_seqlens=cu, max_q=4, max_k=5)):
         with pytest.raises(ValueError, match="CUDA tensors"):
             ops.attention_bwd_workspace(q, k, **kw)
+
+
+def test_numbers_that_require_a_gradient(ops):
+    """A learnable scale (or p) would come out without a gradient: refused, as a rotation's frequencies are."""
+    from rmsnorm_fp8_quantization_gb300 import autograd as A
+    q, k = torch.zeros(2, 3, 4, 16, dtype=torch.bfloat16), torch.zeros(2, 5, 2, 16, dtype=torch.bfloat16)
+    x, rng = torch.zeros(8), torch.zeros(2, dtype=torch.int64)
+    number = torch.nn.Parameter(torch.tensor(0.5))
+    with pytest.raises(ValueError, match="scale requires a gradient"):
+        A.attention(q, k, k, scale=number)
+    with pytest.raises(ValueError, match="p requires a gradient"):
+        A.dropout(x, number, rng)
+    for call in (lambda: A.attention(q, k, k, scale=number.detach()), lambda: A.dropout(x, number.detach(), rng)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        A.attention(q, k, k, scale=number)
