@@ -137,7 +137,8 @@ gbn_status gbn_attention_fwd(const gbn_attention_fwd_args* args, cudaStream_t st
   gbn_status st = check_sizes(z, dtype);
   if (st != GBN_OK) return st;
   if (!scale_ok(c.scale)) return GBN_ERR_SHAPE;
-  if (z.tokens == 0 || z.batches == 0 || z.max_q == 0) return GBN_OK;
+  // (a bound of 0 leaves no rows, but lengths that do not fit it are flagged)
+  if (z.tokens == 0 || z.batches == 0 || (z.max_q == 0 && !z.packed_q)) return GBN_OK;
   if (!c.q || !c.out || (z.keys > 0 && (!c.k || !c.v))) return GBN_ERR_NULL;
   if ((st = check_tensor(c.q, c.q_strides, z.tokens, z.q_heads, false)) != GBN_OK ||
       (st = check_tensor(c.out, c.out_strides, z.tokens, z.q_heads, false)) != GBN_OK ||
@@ -172,7 +173,8 @@ gbn_status gbn_attention_fwd(const gbn_attention_fwd_args* args, cudaStream_t st
   p.max_kv = static_cast<int>(std::min(z.max_k, z.keys));
   p.causal = c.causal != 0;
   p.window = static_cast<int>(z.window);
-  const int64_t blocks = tile_blocks(p.cu, z.tokens, z.batches, p.max_q, kPrefillRows, p.group);
+  const int64_t blocks = z.max_q > 0 ? tile_blocks(p.cu, z.tokens, z.batches, p.max_q, kPrefillRows, p.group)
+                                     : tiles(z.batches, kPrefillRows);
   if (blocks * z.kv_heads > INT32_MAX) return GBN_ERR_SHAPE;
   p.row_tiles = static_cast<int>(blocks);  // of all sequences
   p.splits = 1;

@@ -127,6 +127,23 @@ def test_neighbours_do_not_matter(gpu):
         assert torch.equal(got[n][70:203], one[n]), n
 
 
+@pytest.mark.parametrize("batches", [1, 20, 200, 700])
+def test_lengths_beyond_the_bounds_are_flagged(gpu, batches):
+    """Bounds of 0 and of too little, in both passes; lengths of 0 fit a bound of 0."""
+    from rmsnorm_fp8_quantization_gb300 import gbnorm as G
+    c = Case((3,) * batches, dim=16)
+    s = make(c)
+    out, lse = gpu.attention_fwd(s["q"], s["k"], s["v"], **s["kw"])
+    flags()
+    for cu, bound, bad in ((s["kw"]["cu_seqlens"], 0, True), (s["kw"]["cu_seqlens"], 2, True),
+                           (s["kw"]["cu_seqlens"], 3, False), (torch.zeros_like(s["kw"]["cu_seqlens"]), 0, False)):
+        want = G.GBN_DEVICE_ERR_BAD_INDEX if bad else 0
+        o, l = gpu.attention_fwd(s["q"], s["k"], s["v"], cu_seqlens=cu, max_q=bound)
+        assert flags() == want, ("forward", bound)
+        gpu.attention_bwd(s["dout"], s["q"], s["k"], s["v"], out, lse, cu_seqlens=cu, max_q=bound)
+        assert flags() == want, ("backward", bound)
+
+
 def test_given_outputs_and_strides(gpu):
     """Outputs that are views of one tensor, a gradient whose tokens lie apart."""
     c = Case((150, 20), dim=80, heads=6, kv_heads=3)
