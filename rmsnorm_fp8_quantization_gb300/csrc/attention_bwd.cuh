@@ -21,8 +21,9 @@ namespace {
 // delta_i = dout_i.out_i for every query and head, and lse beside it in the form and order
 // that the kernel below reads: by head, then query.  f16 besides: the largest squared norms of
 // 16 rows of dout and v.  A CTA takes 16 tokens and 16 heads; a row is C lanes of 8
-// elements.  Bound by reading out and dout once (cold, 4096 tokens of 32 heads of 128: 67 MB in
-// 19 us, 44 % of what memory gives: a warp has eight loads under way).
+// elements.  It reads out and dout once (cold, 4096 tokens of 32 heads of 128: 67 MB in 19 us, 44 %
+// of what memory gives); neither that nor the issue slots (57 %) are full: a warp has eight loads
+// under way and 38 % of the warps a multiprocessor can hold are there.
 constexpr int kStatHeads = 16, kStatThreads = 256;
 
 template <typename T, int C>
@@ -139,7 +140,8 @@ __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const Att
 // reads 64 bytes of shared memory a cycle then instead of 128, all there are.
 //
 // Bound at head_dim 128 by the tensor core: 2048 (dk, dv) and 1536 (dq) cycles a step.  Two
-// sequences of 4096 tokens, 32 / 8 heads: not causal 1131 us, causal 612; the seven products
+// sequences of 4096 tokens, 32 / 8 heads: not causal 1131 us, causal 612 with the same inputs
+// again and again (650 to 661 with inputs that alternate); the seven products
 // run at 1700 TFLOP/s and 1570, and the same kernel without exponentials, conversions and
 // reads of the statistics was 2 % faster.  At 64 by the chain from one product over the rows'
 // threads to the next (2100 and 1700 cycles a step, 1230 and 870 of them products; causal 490
@@ -158,7 +160,7 @@ struct BwdBarriers {
     SeqRange range;
     int sequence, head0, rounds, x0, rows;
   } kept;
-  uint4 again[8];  // by warp of the rows: those with a NaN, a word a round
+  uint32_t again[8][4];  // by warp of the rows: those with a NaN, a word a round
 };
 
 template <int DP, bool KV>
@@ -235,7 +237,7 @@ __device__ __noinline__ void tile_again(const AttnBwdParams& p, const BwdBarrier
   const int warp = threadIdx.x >> 5, w = warp >> 2, half = p.d <= 64 ? 32 : 64;
   for (int round = 0; round < kept.rounds; ++round) {
     const int xh = kept.head0 + round;
-    for (uint32_t todo = (&bars.again[warp].x)[round]; todo; todo &= todo - 1) {
+    for (uint32_t todo = bars.again[warp][round]; todo; todo &= todo - 1) {
       const int x = kept.x0 + (warp & 3) * 32 + __ffs(todo) - 1;
       const int64_t row = (KV ? kept.range.k0 : kept.range.q0) + static_cast<int64_t>(x);
       if constexpr (!KV)
@@ -579,7 +581,8 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
   } else {
     // -------------------------------------------------- probabilities and their gradients
     set_regs_inc<Shape::kRegsSoftmax>();
-    if (lane == 0) bars.again[warp] = make_uint4(0u, 0u, 0u, 0u);
+    if (lane < 4) bars.again[warp][lane] = 0u;
+    __syncwarp();
     const int w = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
     int lo = 0, hi = 0;  // the rows of y that this thread's row goes with
@@ -728,7 +731,7 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
         }
         if (more) tc_fence_before();  // (read before the next round's sums)
         const uint32_t again = __ballot_sync(0xFFFFFFFFu, nan && live);
-        if (again != 0u && lane == 0) (&bars.again[warp].x)[round - 1] = again;
+        if (again != 0u && lane == 0) bars.again[warp][round - 1] = again;
       }
       return more;
     };
@@ -842,8 +845,9 @@ __device__ __forceinline__ void attention_bwd_tile(const AttnBwdParams& p, const
 #pragma unroll 1
     for (int round = 1; ok && between(std::false_type(), round) && ok; ++round) steps_of(round);
     if (splits == 1) {
-      const uint4 again = bars.again[warp];
-      if ((again.x | again.y | again.z | again.w) != 0u) tile_again<T, KV>(p, bars);
+      __syncwarp();
+      const uint32_t* const again = bars.again[warp];
+      if ((again[0] | again[1] | again[2] | again[3]) != 0u) tile_again<T, KV>(p, bars);
     }
   }
 
