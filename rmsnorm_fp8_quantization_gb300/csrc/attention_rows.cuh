@@ -99,7 +99,9 @@ __device__ __forceinline__ void four_floats(uint2 w, float* f) {
 //  * kept pairs whose share is infinite or NaN alone decide the sum, if there are any: dk and dv take them
 //    first, dq looks for columns of kept keys that are not finite (lse is, so their weight is 0, and 0
 //    times them NaN).
-// A lane takes four columns; every sum in a fixed order.
+// A lane takes four columns; every sum in a fixed order.  (2 x 4096 tokens, 32 / 8 heads of 128, causal, 0.61 ms
+// without such values: a NaN in a gradient, inside a tile, 26 ms; infinities of either sign in every seventh 1.1;
+// nothing but one infinity 105, where no share decides.)
 template <typename T, int WHICH>
 __device__ __noinline__ void grad_again(const AttnBwdParams& p, const SeqRange& s, int b, int head, int h, int x,
                                         int first, int columns, T* dst) {
