@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const Att
 //
 // Bound at head_dim 128 by the tensor core: 2048 (dk, dv) and 1536 (dq) cycles a step.  Two
 // sequences of 4096 tokens, 32 / 8 heads: not causal 1131 us, causal 612 with the same inputs
-// again and again (650 to 661 with inputs that alternate); the seven products
+// again and again (637 to 661 with inputs that alternate); the seven products
 // run at 1700 TFLOP/s and 1570, and the same kernel without exponentials, conversions and
 // reads of the statistics was 2 % faster.  At 64 by the chain from one product over the rows'
 // threads to the next (2100 and 1700 cycles a step, 1230 and 870 of them products; causal 490
